@@ -115,6 +115,12 @@ enum { FP8_GROUPED_JAGGED_M = 0, FP8_GROUPED_JAGGED_K = 1 };
 /* weight-gradient recipe of fp8_linear_bwd */
 enum { FP8_WGRAD_FP8 = 0, FP8_WGRAD_BF16 = 1 };
 
+/* score function of the router (fp8_moe_route) */
+enum { FP8_SCORE_SOFTMAX = 0, FP8_SCORE_SIGMOID = 1 };
+
+/* most tokens of one fp8_moe_tokens call */
+#define FP8_MOE_MAX_TOKENS 64
+
 /* operations for fp8_workspace_size */
 enum { FP8_OP_QUANTIZE = 0, FP8_OP_LINEAR_FWD = 1, FP8_OP_LINEAR_BWD = 2 };
 
@@ -133,8 +139,9 @@ enum {
 /* device status bits (OR-ed into *d_status) */
 enum {
   FP8_DEV_BAD_OFFSETS = 1 << 8, /* offsets not non-decreasing, or last entry != total rows */
-  FP8_DEV_TIMEOUT = 1 << 9      /* a bounded on-device wait ran out; the kernel drained and
+  FP8_DEV_TIMEOUT = 1 << 9,     /* a bounded on-device wait ran out; the kernel drained and
                                    returned */
+  FP8_DEV_BAD_IDS = 1 << 10     /* an expert id outside -1 .. E - 1; its slot counts as unused */
 };
 
 typedef struct fp8_tensor {
@@ -340,6 +347,102 @@ int fp8_linear_bwd(const fp8_tensor* dy, const fp8_linear_saved* saved, const fp
                    const fp8_tensor* w, int granularity, int wgrad_mode, fp8_tensor* dx,
                    fp8_tensor* dw, void* workspace, size_t workspace_bytes, int32_t* d_status,
                    void* stream);
+
+/*
+ * fp8_add_rmsnorm — root-mean-square norm with the residual's addition and the quantization of its
+ * result, one pass over the data:
+ *   s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight   (all in fp32)
+ *  x           bf16 [T, H], H % 8 == 0, H <= 16384.
+ *  residual    bf16 [T, H], or NULL (s = x).
+ *  weight      bf16 or fp32 [H].
+ *  h           bf16 [T, H] or NULL: s rounded once (the residual stream's new value). The norm takes
+ *              the unrounded s.
+ *  y           bf16 [T, H] or NULL: y rounded once.
+ *  q           FP8 (E4M3 or E5M2) [T, H] or NULL: y quantized from its fp32 value by the recipe [Q] with
+ *              fp32 divisions; inv_scales, given with q, by granularity as for fp8_quantize ROW_MAJOR:
+ *              FP8_GRAN_ROW fp32 [T]; FP8_GRAN_BLOCK_1x128 fp32 [T, H / 128] (H % 128 == 0);
+ *              FP8_GRAN_MX E8M0 [fp8_mx_scale_bytes(T, H)] (H % 128 == 0). Other granularities:
+ *              FP8_ERR_UNSUPPORTED. amax is that of the unrounded y, so the codes are those of y in
+ *              one rounding, not of y's bf16 value.
+ *  rstd        fp32 [T] or NULL (for the backward pass).
+ * At least one output is given. h or y may be x's or residual's own buffer. A row with a NaN or an
+ * infinity gives what the formula gives: NaN scales and codes. No workspace.
+ */
+int fp8_add_rmsnorm(const fp8_tensor* x, const fp8_tensor* residual, const fp8_tensor* weight, float eps,
+                    int granularity, fp8_tensor* h, fp8_tensor* y, fp8_tensor* q, fp8_tensor* inv_scales,
+                    fp8_tensor* rstd, void* stream);
+
+/*
+ * fp8_add_rmsnorm_bwd — gradients of fp8_add_rmsnorm (its 8-bit cast counts as the identity):
+ *   g = dy * weight,  xhat = h * rstd,
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dh,   dw = sum over rows of dy * xhat
+ *  dy, h       bf16 [T, H]; h is the forward's output (its x where there was no residual); rstd fp32
+ *              [T] from the forward pass; weight as there.
+ *  dh          bf16 [T, H] or NULL: the gradient that reaches h itself (the residual stream).
+ *  dx          bf16 [T, H] or NULL: the gradient of x and of residual alike; may be dy's, h's or dh's
+ *              own buffer.
+ *  dw          bf16 or fp32 [H] or NULL. Summed in fp32 in an order that depends on T and H only:
+ *              the same bits on every run. T == 0 gives zeros.
+ *  workspace   fp8_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, when dw is given.
+ */
+int fp8_add_rmsnorm_bwd(const fp8_tensor* dy, const fp8_tensor* h, const fp8_tensor* weight,
+                        const fp8_tensor* rstd, const fp8_tensor* dh, fp8_tensor* dx, fp8_tensor* dw,
+                        void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8_rmsnorm_bwd_workspace_size(int64_t T, int64_t H);
+
+/*
+ * fp8_moe_route — the router of a mixture-of-experts layer: the top k experts of each token, their
+ * weights, and the table that fp8_grouped_mm's offsets need.
+ *  logits      bf16 or fp32 [T, E], E <= 1024. k = ids->shape[1], 1 <= k <= 16, k <= E.
+ *  bias        fp32 [E] or NULL: added to the logits (in fp32) for the choice only, not for the weights.
+ *  The k experts with the largest logit + bias are taken, in falling order, ties by the lowest
+ *  index. One whose sum is -inf or NaN is never taken: where fewer than k are left, the slot's id
+ *  is -1 and its weight 0.
+ *  score       FP8_SCORE_SOFTMAX: v = softmax(logits) over all E; FP8_SCORE_SIGMOID: v = sigmoid(logit).
+ *  renormalize 0: weight = scale * v. Else over the experts taken: softmax: weight = scale * softmax of
+ *              their logits; sigmoid: weight = scale * v / (sum of their v + 1e-20).
+ *  ids         int32 [T, k]; weights fp32 [T, k].
+ *  order, pos, ends   all given or all NULL. ends int32 [E]: cumulative counts of the slots of each
+ *              expert (the offsets of fp8_grouped_mm); order int32 [T k]: the slots t * k + j sorted by
+ *              expert, in slot order within an expert, -1 past ends[E - 1]; pos int32 [T, k]: each
+ *              slot's place in order (the row of its product), -1 for an unused slot.
+ *  workspace   fp8_moe_route_workspace_size(T, E) bytes, 16-byte aligned, with the table.
+ */
+int fp8_moe_route(const fp8_tensor* logits, const fp8_tensor* bias, int score, int renormalize, float scale,
+                  fp8_tensor* ids, fp8_tensor* weights, fp8_tensor* order, fp8_tensor* pos,
+                  fp8_tensor* ends, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                  void* stream);
+size_t fp8_moe_route_workspace_size(int64_t T, int64_t E);
+
+/*
+ * fp8_moe_route_bwd — gradient of the logits from the gradient dweights (fp32 [T, k]) of the weights,
+ * the choice held fixed. logits, ids, score, renormalize and scale as in fp8_moe_route; a slot with
+ * id -1 has no gradient. dlogits [T, E] in logits' type, every element written.
+ */
+int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids, const fp8_tensor* dweights,
+                      int score, int renormalize, float scale, fp8_tensor* dlogits, int32_t* d_status,
+                      void* stream);
+
+/*
+ * fp8_moe_tokens — the experts of a few tokens (decode), from the hidden state to the weighted sum:
+ *   out[t] = sum_j weights[t, j] * W2[e] (silu(W1[e] x[t]) * (W3[e] x[t])),   e = ids[t, j],
+ * with W[e, n, k] = code * scale of its row. Only the experts named are read, each once.
+ *  x           bf16 [T, H], T <= FP8_MOE_MAX_TOKENS; H and I multiples of 16, <= 65536.
+ *  ids         int32 [T, k], k <= 16: -1 marks an unused slot (its weight is not read); a token
+ *              without any used slot gives zeros. Other ids outside 0 .. E - 1 set FP8_DEV_BAD_IDS and
+ *              count as unused. weights fp32 [T, k].
+ *  w13, s13    E4M3 [E, 2 I, H] and fp32 [E, 2 I]: rows 0 .. I - 1 are W1 (gate), rows I .. 2 I - 1 W3
+ *              (up), as fp8_quantize with FP8_GRAN_ROW writes them; E <= 1024.
+ *  w2, s2      E4M3 [E, H, I] and fp32 [E, H].
+ *  out         bf16 [T, H].
+ *  workspace   fp8_moe_tokens_workspace_size(T, k, H, I) bytes, 16-byte aligned.
+ * The activations are not rounded to 8 bits: products and sums are fp32, the result is rounded once.
+ */
+int fp8_moe_tokens(const fp8_tensor* x, const fp8_tensor* ids, const fp8_tensor* weights,
+                   const fp8_tensor* w13, const fp8_tensor* s13, const fp8_tensor* w2, const fp8_tensor* s2,
+                   fp8_tensor* out, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                   void* stream);
+size_t fp8_moe_tokens_workspace_size(int64_t T, int64_t top_k, int64_t H, int64_t I);
 
 /* Test hook for failure detection: while enabled, every GEMM launch first waits on a barrier
  * that nothing signals, the grid barrier of the tensorwise quantize waits for one arrival more

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -29,6 +30,9 @@ OP_QUANTIZE, OP_LINEAR_FWD, OP_LINEAR_BWD = 0, 1, 2
 OK = 0
 DEV_BAD_OFFSETS = 1 << 8
 DEV_TIMEOUT = 1 << 9
+DEV_BAD_IDS = 1 << 10
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MOE_MAX_TOKENS = 64
 
 _TORCH_DT = {
     torch.bfloat16: DT_BF16,
@@ -87,6 +91,16 @@ def _load():
     L.fp8_test_cast_bits.argtypes = [ctypes.c_uint32, ctypes.c_int64, ctypes.c_int, P, P]
     L.fp8_scaled_mm_quant.argtypes = [T, T, T, T, ctypes.c_int, ctypes.c_int, T, T, P, P]
     L.fp8_set_test_stall.restype = ctypes.c_int
+    # descriptors of the calls below travel as the packed bytes of an fp8_tensor (see _pack)
+    I, Z, F, L64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
+    L.fp8_add_rmsnorm.argtypes = [P, P, P, F, I, P, P, P, P, P, P]
+    L.fp8_add_rmsnorm_bwd.argtypes = [P, P, P, P, P, P, P, P, Z, P]
+    L.fp8_moe_route.argtypes = [P, P, I, I, F, P, P, P, P, P, P, Z, P, P]
+    L.fp8_moe_route_bwd.argtypes = [P, P, P, I, I, F, P, P, P]
+    L.fp8_moe_tokens.argtypes = [P, P, P, P, P, P, P, P, P, Z, P, P]
+    for name, n in (("rmsnorm_bwd", 2), ("moe_route", 2), ("moe_tokens", 4)):
+        f = getattr(L, f"fp8_{name}_workspace_size")
+        f.argtypes, f.restype = [L64] * n, Z
     return L
 
 
@@ -96,7 +110,9 @@ lib = _load()
 EXPORTS = ("fp8_quantize", "fp8_scaled_mm", "fp8_grouped_mm", "fp8_linear_fwd", "fp8_linear_bwd",
            "fp8_workspace_size", "fp8_jagged_padded_rows", "fp8_status_string", "fp8_set_wait_limit_ns",
            "fp8_quantize_tensor_noalloc", "fp8_set_test_stall", "fp8_mx_scale_bytes", "fp8_scaled_mm_amax",
-           "fp8_quantize_from_amax", "fp8_test_cast_bits", "fp8_scaled_mm_quant")
+           "fp8_quantize_from_amax", "fp8_test_cast_bits", "fp8_scaled_mm_quant", "fp8_add_rmsnorm",
+           "fp8_add_rmsnorm_bwd", "fp8_rmsnorm_bwd_workspace_size", "fp8_moe_route", "fp8_moe_route_bwd",
+           "fp8_moe_route_workspace_size", "fp8_moe_tokens", "fp8_moe_tokens_workspace_size")
 
 
 def status_string(code: int) -> str:
@@ -118,6 +134,32 @@ def desc(t: torch.Tensor | None, dtype: int | None = None):
     for i, s in enumerate(t.shape):
         d.shape[i] = s
     return d
+
+
+_PACK = struct.Struct("=Qii3q").pack  # the bytes of an fp8_tensor
+
+
+def _pack(t: torch.Tensor | None):
+    """desc() as bytes: the short calls around a mixture-of-experts layer take a few microseconds on
+    the GPU, and a ctypes structure per tensor would take longer on the host."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to fp8lin must be contiguous")
+    s = t.shape
+    n = len(s)
+    dt = _TORCH_DT[t.dtype]
+    if n == 2:
+        return _PACK(t.data_ptr(), dt, 2, s[0], s[1], 0)
+    if n == 1:
+        return _PACK(t.data_ptr(), dt, 1, s[0], 0, 0)
+    if n == 3:
+        return _PACK(t.data_ptr(), dt, 3, s[0], s[1], s[2])
+    raise ValueError("fp8lin tensors have 1 to 3 dimensions")
+
+
+def _ws(t):
+    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
 
 
 def _ref(d):
@@ -252,6 +294,56 @@ def fp8_quantize_tensor_noalloc(x, out_dtype, layout, out=None, out_t=None, inv_
     _check(rc, "fp8_quantize_tensor_noalloc")
 
 
+def fp8_add_rmsnorm(x, weight, eps, residual=None, h=None, y=None, q=None, inv_scales=None, granularity=GRAN_ROW,
+                    rstd=None, stream=None):
+    """s = x + residual, h = bf16(s), y = s / sqrt(mean(s^2) + eps) * weight, q / inv_scales = y in 8 bits
+    (GRAN_ROW, GRAN_BLOCK_1x128 or GRAN_MX), rstd for the backward pass; any of the outputs may be None."""
+    _check(lib.fp8_add_rmsnorm(_pack(x), _pack(residual), _pack(weight), eps, granularity, _pack(h), _pack(y), _pack(q),
+                               _pack(inv_scales), _pack(rstd), _stream(stream)), "fp8_add_rmsnorm")
+
+
+def fp8_add_rmsnorm_bwd(dy, h, weight, rstd, dx=None, dw=None, dh=None, workspace=None, stream=None):
+    """Gradients of fp8_add_rmsnorm: dx (of x and of residual alike) and dw, from dy and from dh, the gradient that
+    reaches h itself. dw needs a workspace (rmsnorm_bwd_workspace)."""
+    _check(lib.fp8_add_rmsnorm_bwd(_pack(dy), _pack(h), _pack(weight), _pack(rstd), _pack(dh), _pack(dx), _pack(dw),
+                                   *_ws(workspace), _stream(stream)), "fp8_add_rmsnorm_bwd")
+
+
+def fp8_moe_route(logits, ids, weights, order=None, pos=None, ends=None, bias=None, score=SCORE_SOFTMAX,
+                  renormalize=True, scale=1.0, workspace=None, status=None, stream=None):
+    """Top-k experts (k = ids.shape[1]) and their weights for each row of logits; with order, pos and ends also the
+    slots sorted by expert (needs a workspace, route_workspace)."""
+    _check(lib.fp8_moe_route(_pack(logits), _pack(bias), score, bool(renormalize), scale, _pack(ids), _pack(weights),
+                             _pack(order), _pack(pos), _pack(ends), *_ws(workspace), _ptr(status), _stream(stream)),
+           "fp8_moe_route")
+
+
+def fp8_moe_route_bwd(logits, ids, dweights, dlogits, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, status=None,
+                      stream=None):
+    """Gradient of the logits from the gradient of fp8_moe_route's weights, the choice of experts held fixed."""
+    _check(lib.fp8_moe_route_bwd(_pack(logits), _pack(ids), _pack(dweights), score, bool(renormalize), scale,
+                                 _pack(dlogits), _ptr(status), _stream(stream)), "fp8_moe_route_bwd")
+
+
+def fp8_moe_tokens(x, ids, weights, w13, s13, w2, s2, out, workspace=None, status=None, stream=None):
+    """The experts of up to MOE_MAX_TOKENS tokens on FP8 weights with a scale per row: out[t] = sum_j weights[t, j] *
+    W2[e] (silu(W1[e] x[t]) * (W3[e] x[t])), e = ids[t, j]; id -1 is an unused slot. Workspace: moe_tokens_workspace."""
+    _check(lib.fp8_moe_tokens(_pack(x), _pack(ids), _pack(weights), _pack(w13), _pack(s13), _pack(w2), _pack(s2),
+                              _pack(out), *_ws(workspace), _ptr(status), _stream(stream)), "fp8_moe_tokens")
+
+
+def fp8_rmsnorm_bwd_workspace_size(T, H) -> int:
+    return int(lib.fp8_rmsnorm_bwd_workspace_size(T, H))
+
+
+def fp8_moe_route_workspace_size(T, E) -> int:
+    return int(lib.fp8_moe_route_workspace_size(T, E))
+
+
+def fp8_moe_tokens_workspace_size(T, top_k, H, I) -> int:
+    return int(lib.fp8_moe_tokens_workspace_size(T, top_k, H, I))
+
+
 def fp8_workspace_size(op, d0=0, d1=0, d2=0, granularity=0, wgrad_mode=0) -> int:
     return int(lib.fp8_workspace_size(op, d0, d1, d2, granularity, wgrad_mode))
 
@@ -279,6 +371,62 @@ def col_workspace(groups: int, cols: int, rows: int, device) -> torch.Tensor:
     """Workspace of a column-granularity fp8_quantize of `rows` rows (all groups) x `cols` columns."""
     n = fp8_workspace_size(OP_QUANTIZE, groups, cols, rows, granularity=GRAN_COL)
     return torch.empty(max(n // 4, 4), dtype=torch.int32, device=device)
+
+
+def rmsnorm_bwd_workspace(T: int, H: int, device) -> torch.Tensor:
+    return torch.empty(max(fp8_rmsnorm_bwd_workspace_size(T, H), 16), dtype=torch.uint8, device=device)
+
+
+def route_workspace(T: int, E: int, device) -> torch.Tensor:
+    return torch.empty(max(fp8_moe_route_workspace_size(T, E), 16), dtype=torch.uint8, device=device)
+
+
+def moe_tokens_workspace(T: int, top_k: int, H: int, I: int, device) -> torch.Tensor:
+    return torch.empty(max(fp8_moe_tokens_workspace_size(T, top_k, H, I), 16), dtype=torch.uint8, device=device)
+
+
+def add_rmsnorm_alloc(x, weight, eps, residual=None, granularity=None, out_dtype=DT_E4M3, want_y=False, want_rstd=False,
+                      stream=None):
+    """Returns (h, y, q, inv_scales, rstd), None for what was not asked: h with a residual (x itself without one), q and
+    inv_scales with a granularity, y with want_y or without a granularity."""
+    T, H = x.shape
+    dev = x.device
+    h = torch.empty_like(x) if residual is not None else None
+    y = torch.empty_like(x) if want_y or granularity is None else None
+    q = inv = None
+    if granularity is not None:
+        q = torch.empty((T, H), dtype=FP8_TORCH[out_dtype], device=dev)
+        if granularity == GRAN_MX:
+            inv = torch.empty(max(fp8_mx_scale_bytes(T, H), 0), dtype=torch.uint8, device=dev)
+        else:
+            inv = torch.empty((T, H // 128) if granularity == GRAN_BLOCK_1x128 else (T,), dtype=torch.float32, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if want_rstd else None
+    fp8_add_rmsnorm(x, weight, eps, residual, h, y, q, inv, granularity if granularity is not None else GRAN_ROW, rstd,
+                    stream)
+    return (h if h is not None else x), y, q, inv, rstd
+
+
+def moe_route_alloc(logits, top_k, bias=None, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, table=True, status=None,
+                    stream=None):
+    """Returns (ids, weights, order, pos, ends); the last three None without the table."""
+    T, E = logits.shape
+    dev, i32 = logits.device, torch.int32
+    ids = torch.empty((T, top_k), dtype=i32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    order = pos = ends = ws = None
+    if table:
+        order = torch.empty(T * top_k, dtype=i32, device=dev)
+        pos, ends = torch.empty((T, top_k), dtype=i32, device=dev), torch.empty(E, dtype=i32, device=dev)
+        ws = route_workspace(T, E, dev)
+    fp8_moe_route(logits, ids, weights, order, pos, ends, bias, score, renormalize, scale, ws, status, stream)
+    return ids, weights, order, pos, ends
+
+
+def moe_tokens_alloc(x, ids, weights, w13, s13, w2, s2, status=None, stream=None):
+    out = torch.empty_like(x)
+    ws = moe_tokens_workspace(x.shape[0], ids.shape[1], x.shape[1], w13.shape[1] // 2, x.device)
+    fp8_moe_tokens(x, ids, weights, w13, s13, w2, s2, out, ws, status, stream)
+    return out
 
 
 def quantize_alloc(x, granularity, out_dtype, layout=None, offsets=None, padded_rows=None, status=None,

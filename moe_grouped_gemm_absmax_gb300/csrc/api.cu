@@ -7,6 +7,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "args.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -111,42 +112,6 @@ int make_tmap(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int ra
 using namespace fp8lin;
 
 // ------------------------------------------------------------------------------------------
-// argument helpers
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-static bool is_fp8(int dt) { return dt == FP8_DT_E4M3 || dt == FP8_DT_E5M2; }
-static bool is_out(int dt) { return dt == FP8_DT_BF16 || dt == FP8_DT_F32; }
-static int64_t numel(const fp8_tensor* t) {
-  int64_t n = 1;
-  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-  return n;
-}
-static bool valid_desc(const fp8_tensor* t) {
-  if (!t || t->ndim < 1 || t->ndim > 3) return false;
-  for (int i = 0; i < t->ndim; ++i)
-    if (t->shape[i] < 0) return false;
-  return t->ptr != nullptr || numel(t) == 0;
-}
-static bool shape_is(const fp8_tensor* t, int nd, int64_t a, int64_t b = -1, int64_t c = -1) {
-  if (t->ndim != nd) return false;
-  const int64_t s[3] = {a, b, c};
-  for (int i = 0; i < nd; ++i)
-    if (t->shape[i] != s[i]) return false;
-  return true;
-}
-static int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
-
-#define FP8_CHECK(cond, code) \
-  do {                        \
-    if (!(cond)) return (code); \
-  } while (0)
-#define FP8_TRY(expr)        \
-  do {                       \
-    int rc_ = (expr);        \
-    if (rc_ != FP8_OK) return rc_; \
-  } while (0)
-
-// ------------------------------------------------------------------------------------------
 
 extern "C" int64_t fp8_mx_scale_bytes(int64_t rows, int64_t k) { return mx_scale_bytes(rows, k); }
 
@@ -179,6 +144,8 @@ extern "C" const char* fp8_status_string(int code) {
     case FP8_ERR_DEVICE: return "no sm_103 device current";
     case FP8_DEV_BAD_OFFSETS: return "device: offsets not non-decreasing or last != total rows";
     case FP8_DEV_TIMEOUT: return "device: a bounded wait ran out";
+    case FP8_DEV_BAD_IDS: return "device: expert ids outside -1 .. E - 1";
+    case FP8_DEV_BAD_IDS | FP8_DEV_TIMEOUT: return "device: bad expert ids and a wait ran out";
     case FP8_DEV_BAD_OFFSETS | FP8_DEV_TIMEOUT: return "device: bad offsets and a wait ran out";
     default: return "unknown status";
   }

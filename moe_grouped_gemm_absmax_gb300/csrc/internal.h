@@ -78,6 +78,30 @@ int launch_mx_quant(const void* x, int64_t batches, int64_t R, int64_t C, int fm
 int launch_blk_quant(const void* x, int64_t R, int64_t C, int fmt, bool tile128, void* q, void* qt, float* inv,
                      float* inv_t, const Ctx& c);
 
+// --- norm with the residual's addition (norm.cu) ---
+// x, res (may be null), h, y bf16 [T, H]; w [H] bf16 or fp32; q FP8 [T, H] with inv in the layout of
+// gran (row, 1 x 128 or MX); h, y, q and rstd [T] may be null. H % 8 == 0, H <= 16384.
+int launch_add_rmsnorm(const void* x, const void* res, const void* w, int w_f32, float eps, int64_t T, int64_t H,
+                       int gran, int fmt, void* h, void* y, void* q, void* inv, float* rstd, const Ctx& c);
+int64_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t H);
+int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, const float* rstd, const void* dh,
+                       int64_t T, int64_t H, void* dx, void* dw, int dw_bf16, float* ws, const Ctx& c);
+
+// --- router (route.cu) ---
+// logits [T, E] bf16 or fp32; order, pos and ends all given or all null. E <= 1024, k <= 16.
+int64_t route_ws_bytes(int64_t T, int64_t E);
+int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int64_t E, int64_t k, int softmax,
+                 int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,
+                 void* ws, const Ctx& c);
+int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const float* dw, int64_t T, int64_t E,
+                     int64_t k, int softmax, int renorm, float scale, void* dlogits, const Ctx& c);
+
+// --- experts of a few tokens (moe.cu) ---
+int64_t moe_tokens_ws_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
+int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, const void* w13, const float* s13,
+                      const void* w2, const float* s2, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* out,
+                      void* ws, const Ctx& c);
+
 // --- GEMM launchers (gemm.cu) ---
 struct GemmArgs {
   // operands
