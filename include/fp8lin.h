@@ -444,8 +444,8 @@ int fp8_moe_tokens(const fp8_tensor* x, const fp8_tensor* ids, const fp8_tensor*
                    void* stream);
 size_t fp8_moe_tokens_workspace_size(int64_t T, int64_t top_k, int64_t H, int64_t I);
 
-/* Test hook for failure detection: while enabled, every GEMM launch first waits on a barrier
- * that nothing signals, the grid barrier of the tensorwise quantize waits for one arrival more
+/* Test hook for failure detection: while enabled, every GEMM launch (and fp8_moe_tokens) first waits
+ * on a barrier that nothing signals, the grid barrier of the tensorwise quantize waits for one arrival more
  * than there are CTAs, the column-wise quantize sees no tile maxima as written, and the MX
  * quantize with a column-major output of a dense tensor loads no tile into its ring; the wait
  * runs out after the wait limit (fp8_set_wait_limit_ns), the kernel reports FP8_DEV_TIMEOUT,

@@ -2,6 +2,30 @@
 //   out[t] = sum_j weight[t, j] * W2[e] (silu(W1[e] x[t]) * (W3[e] x[t])),  e = ids[t, j],
 // on FP8 weights with one inverse scale per row: w13 [E, 2 I, H] holds W1 (gate) and below it W3
 // (up), w2 [E, H, I].
+//
+// With a few tokens the work is reading the named experts' weights once; everything here serves to
+// keep that stream going. One persistent cooperative launch, one CTA per SM:
+//  - The weights are the MMA's A operand (tcgen05.mma kind::f8f6f4, M = 128 weight rows), so they go
+//    from HBM by TMA into a shared-memory ring and from there into the tensor cores without
+//    passing through registers. The tokens are its N.
+//  - The activations keep their precision although the MMA takes 8-bit operands: a value v, scaled
+//    by a power of two so that its row's largest lies in [128, 256), is split into e4m3 parts
+//    v = p0 + p1 / 16 + p2 / 256, each part the rounding of 16 times what the ones before left. e4m3
+//    has 4 significant bits, so two parts hold a bf16 value's 8 bits exactly (to 2^-21 of the row's
+//    largest for the smallest values) and three hold the hidden layer to 2^-13 or better. The parts
+//    are neighbouring columns of N; the epilogue adds the columns up. That costs columns of N,
+//    which an MMA this narrow has to spare.
+//  - Both products are cut into units of 128 rows x 128 K bytes (16 KB), in a fixed order, and each
+//    CTA takes an equal contiguous run of them, whatever tile it ends in (the tail is at most one
+//    unit). A tile that several CTAs share leaves fp32 partial sums in the workspace; the last to
+//    arrive adds them in CTA order, so the result does not depend on who was last.
+//  - Between the two products all CTAs meet at a grid barrier (the hidden layer is complete); the
+//    weight ring is filled for the second product meanwhile.
+//
+// Warps: 0 the weights' TMA producer; 1 the MMA issuer; 2-5 build the activation operand, each its
+// own stage of a 4-stage ring; 6-9 the epilogue, a thread per row of the tile.
+// Every wait is bounded; on a timeout the kernel raises FP8_DEV_TIMEOUT, drains its loads and MMAs,
+// frees its tensor memory and returns.
 #include "common.cuh"
 #include "internal.h"
 
@@ -9,20 +33,69 @@ namespace fp8lin {
 
 namespace {
 
+constexpr int kRows = 128;             // weight rows of a tile (64 gate + 64 up rows in the first product)
+constexpr int kUnitBytes = kRows * 128;
+constexpr int kBStages = 4;            // one per builder warp
+constexpr int kMaxA = 12;
+constexpr int kThreads = 320;
+constexpr int kSmemMax = 232448;       // 227 KB
+constexpr uint64_t kDrainNs = 2000000000ull;
+// columns of N: groups of 16 hold 8 tokens in two parts, or 5 in three
+constexpr int kPerGroup1 = 8, kPerGroup2 = 5;
+
 struct MoeArgs {
   const uint16_t* x;  // bf16 [T, H]
   const int32_t* ids;
   const float* weights;
-  const uint8_t* w13;
   const float* s13;
-  const uint8_t* w2;
   const float* s2;
-  uint16_t* out;
-  float* act;  // workspace [T k][I]
-  int T, k, E;
-  int64_t H, I;
+  __nv_bfloat16* out;
+  int T, k, E, H, I;
+  int a_stages, b_bytes;  // ring sizes: weight stages; bytes of an activation stage
+  int tiles1, nk1, tiles2, nk2;
+  // workspace
+  uint32_t* counters;     // [0] the grid barrier, [1 + ph * grid + c] arrivals at the tile that CTA c starts and leaves
+  float* act;             // hidden layer [slots sorted by expert][I]
+  uint32_t* amax;         // |hidden| maxima as bit patterns [slots][2 tiles1]
+  float* part;            // partial sums [CTA][2][T][128]
   int32_t* status;
+  uint64_t wait_ns;
+  int test_stall;
 };
+
+struct Shared {
+  uint64_t afull[kMaxA], aempty[kMaxA];
+  uint64_t bfull[kBStages], bempty[kBStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t drain, never, scales;
+  uint32_t tmem_base;
+  int abort;
+  int n_act;
+  int last;
+};
+
+// Shared memory after the rings: offsets in bytes (n = T k slots).
+struct Layout {
+  int acc, xch, shared, wt, mult2, inv2, hist, xbits, ids, ent, slot, total;
+};
+__host__ __device__ inline Layout layout(int T, int k, int E) {
+  const int n = T * k;
+  Layout L;
+  int o = 0;
+  L.acc = o, o += T * kRows * 4;
+  L.xch = o, o += kPerGroup1 * 64 * 4;
+  L.shared = o, o += (int)sizeof(Shared);
+  L.wt = o, o += n * 4;
+  L.mult2 = o, o += n * 4;
+  L.inv2 = o, o += n * 4;
+  L.hist = o, o += E * 4;
+  L.xbits = o, o += T * 4;
+  L.ids = o, o += n * 4;
+  L.ent = o, o += n * 4;   // per entry: expert, first slot
+  L.slot = o, o += n * 4;  // per entry: slots; per sorted slot: slot index
+  L.total = o;
+  return L;
+}
 
 FP8_DEVI float2 e4m3x2_to_f32(uint32_t two) {
   uint32_t h;
@@ -33,91 +106,618 @@ FP8_DEVI float2 e4m3x2_to_f32(uint32_t two) {
       : "r"(h));
   return r;
 }
-FP8_DEVI float warp_sum(float v) {
+FP8_DEVI void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int32_t y, int32_t z,
+                               uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(pol)
+      : "memory");
+}
+FP8_DEVI uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
+  return r;
+}
+
+// The power of two that brings a row's largest magnitude (bit pattern of an fp32) into [128, 256), and
+// its inverse. A row with an infinity or a NaN gets NaN, which makes all of its values NaN.
+FP8_DEVI void row_scale(uint32_t amax_bits, float* mult, float* inv) {
+  const int ef = (int)(amax_bits >> 23);
+  const int s = min(134 - ef, 126);
+  *mult = ef == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 + s) << 23);
+  *inv = ef == 255 ? 1.0f : __uint_as_float((uint32_t)(127 - s) << 23);
+}
+
+// Four values, already scaled, into PARTS words of e4m3 codes.
+template <int PARTS>
+FP8_DEVI void split4(float4 v, uint32_t* out) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-FP8_DEVI int slot_expert(const MoeArgs& p, int slot) {
-  const int e = p.ids[slot];
-  if (e < -1 || e >= p.E) {
-    set_status(p.status, FP8_DEV_BAD_IDS);
-    return -1;
-  }
-  return e;
-}
-
-// A warp per (slot, row of the hidden layer).
-__global__ void __launch_bounds__(256) moe_up_kernel(const MoeArgs p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int slot = blockIdx.y;
-  const int e = slot_expert(p, slot);
-  if (e < 0 || i >= p.I) return;
-  const uint16_t* x = p.x + (int64_t)(slot / p.k) * p.H;
-  const int64_t r1 = (int64_t)e * 2 * p.I + i, r3 = r1 + p.I;
-  float g = 0.f, u = 0.f;
-  for (int64_t c = lane * 2; c < p.H; c += 64) {
-    const float x0 = __uint_as_float((uint32_t)x[c] << 16), x1 = __uint_as_float((uint32_t)x[c + 1] << 16);
-    const float2 a = e4m3x2_to_f32(*reinterpret_cast<const uint16_t*>(p.w13 + r1 * p.H + c));
-    const float2 b = e4m3x2_to_f32(*reinterpret_cast<const uint16_t*>(p.w13 + r3 * p.H + c));
-    g = fmaf(a.x, x0, fmaf(a.y, x1, g));
-    u = fmaf(b.x, x0, fmaf(b.y, x1, u));
-  }
-  g = warp_sum(g) * p.s13[r1];
-  u = warp_sum(u) * p.s13[r3];
-  if (lane == 0) p.act[slot * p.I + i] = g / (1.0f + expf(-g)) * u;
-}
-
-// A warp per (token, output column), its experts in slot order.
-__global__ void __launch_bounds__(256) moe_down_kernel(const MoeArgs p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = blockIdx.y;
-  if (n >= p.H) return;
-  float y = 0.f;
-  for (int j = 0; j < p.k; ++j) {
-    const int slot = t * p.k + j;
-    const int e = slot_expert(p, slot);
-    if (e < 0) continue;
-    const int64_t r = (int64_t)e * p.H + n;
-    const float* a = p.act + slot * p.I;
-    float d = 0.f;
-    for (int64_t c = lane * 2; c < p.I; c += 64) {
-      const float2 w = e4m3x2_to_f32(*reinterpret_cast<const uint16_t*>(p.w2 + r * p.I + c));
-      d = fmaf(w.x, a[c], fmaf(w.y, a[c + 1], d));
+  for (int p = 0; p < PARTS; ++p) {
+    const uint32_t lo = cvt_fp8x2<FP8_DT_E4M3>(v.x, v.y), hi = cvt_fp8x2<FP8_DT_E4M3>(v.z, v.w);
+    out[p] = lo | (hi << 16);
+    if (p + 1 < PARTS) {
+      const float2 a = e4m3x2_to_f32(lo), b = e4m3x2_to_f32(hi);
+      v = make_float4((v.x - a.x) * 16.f, (v.y - a.y) * 16.f, (v.z - b.x) * 16.f, (v.w - b.y) * 16.f);
     }
-    y += p.weights[slot] * (warp_sum(d) * p.s2[r]);
   }
-  if (lane == 0) reinterpret_cast<__nv_bfloat16*>(p.out)[t * p.H + n] = __float2bfloat16_rn(y);
+}
+
+// One product's share of a CTA: units [it0, it1) of `total`, tile after tile of nk units each.
+struct Run {
+  int total, nk, it0, it1, grid;  // grid: CTAs with a share
+  FP8_DEVI int owner(int64_t it) const { return (int)(((it + 1) * grid - 1) / total); }
+  FP8_DEVI int first(int c) const { return (int)((int64_t)c * total / grid); }
+};
+FP8_DEVI Run make_run(int tiles, int nk, int cta, int grid) {
+  Run r;
+  r.total = tiles * nk;
+  r.nk = nk;
+  r.grid = min(grid, r.total);
+  r.it0 = cta < r.grid ? r.first(cta) : 0;
+  r.it1 = cta < r.grid ? r.first(cta + 1) : 0;
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_tokens_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2, const MoeArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Layout L = layout(p.T, p.k, p.E);
+  uint8_t* a_ring = smem;
+  uint8_t* b_ring = smem + p.a_stages * kUnitBytes;
+  uint8_t* rest = b_ring + kBStages * p.b_bytes;
+  float* acc = reinterpret_cast<float*>(rest + L.acc);
+  float* xch = reinterpret_cast<float*>(rest + L.xch);
+  Shared& S = *reinterpret_cast<Shared*>(rest + L.shared);
+  float* wt = reinterpret_cast<float*>(rest + L.wt);
+  float* mult2 = reinterpret_cast<float*>(rest + L.mult2);
+  float* inv2 = reinterpret_cast<float*>(rest + L.inv2);
+  int* hist = reinterpret_cast<int*>(rest + L.hist);
+  uint32_t* xbits = reinterpret_cast<uint32_t*>(rest + L.xbits);
+  int* ids = reinterpret_cast<int*>(rest + L.ids);
+  uint16_t* ent_e = reinterpret_cast<uint16_t*>(rest + L.ent);
+  const int n = p.T * p.k;
+  uint16_t* ent_start = ent_e + n;
+  uint16_t* ent_cnt = reinterpret_cast<uint16_t*>(rest + L.slot);
+  uint16_t* slot_of = ent_cnt + n;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, grid = gridDim.x;
+  volatile int* abort_flag = &S.abort;
+  auto fail = [&]() {
+    if (!*abort_flag) {
+      *abort_flag = 1;
+      set_status(p.status, FP8_DEV_TIMEOUT);
+    }
+  };
+
+  // ---- slots by expert: each entry is an expert with up to T of its slots ----
+  for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
+  for (int t = tid; t < p.T; t += kThreads) xbits[t] = 0;
+  if (tid == 0) {
+    for (int s = 0; s < p.a_stages; ++s) {
+      mbar_init(&S.afull[s], 1);
+      mbar_init(&S.aempty[s], 1);
+    }
+    for (int s = 0; s < kBStages; ++s) {
+      mbar_init(&S.bfull[s], 1);
+      mbar_init(&S.bempty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&S.tfull[b], 1);
+      mbar_init(&S.tempty[b], 4);
+    }
+    mbar_init(&S.drain, 1);
+    mbar_init(&S.never, 1);
+    mbar_init(&S.scales, 4);
+    S.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm13);
+    tma_prefetch_desc(&tm2);
+  }
+  if (warp == 1) {
+    tmem_alloc(&S.tmem_base, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  for (int s = tid; s < n; s += kThreads) {
+    int id = p.ids[s];
+    if (id < -1 || id >= p.E) {
+      if (cta == 0) set_status(p.status, FP8_DEV_BAD_IDS);
+      id = -1;
+    }
+    ids[s] = id;
+    if (id >= 0) atomicAdd(hist + id, 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int slots = 0, ents = 0;
+    for (int b = 0; b < p.E; b += 32) {
+      const int e = b + lane;
+      const int cnt = e < p.E ? hist[e] : 0;
+      const int ne = (cnt + p.T - 1) / p.T;
+      int xs = cnt, xe = ne;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int ys = __shfl_up_sync(0xffffffffu, xs, o), ye = __shfl_up_sync(0xffffffffu, xe, o);
+        if (lane >= o) xs += ys, xe += ye;
+      }
+      const int s0 = slots + xs - cnt, a0 = ents + xe - ne;
+      if (e < p.E) hist[e] = s0;
+      for (int q = 0; q < ne; ++q) {
+        ent_e[a0 + q] = (uint16_t)e;
+        ent_start[a0 + q] = (uint16_t)(s0 + q * p.T);
+        ent_cnt[a0 + q] = (uint16_t)min(p.T, cnt - q * p.T);
+      }
+      slots += __shfl_sync(0xffffffffu, xs, 31);
+      ents += __shfl_sync(0xffffffffu, xe, 31);
+    }
+    if (lane == 0) S.n_act = ents;
+    __syncwarp();
+    for (int b = 0; b < n; b += 32) {  // in slot order, so that every CTA has the same order
+      const int s = b + lane;
+      const int id = s < n ? ids[s] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      const int before = __popc(same & ((1u << lane) - 1));
+      const int at = id >= 0 ? hist[id] + before : 0;
+      __syncwarp();
+      if (id >= 0) {
+        slot_of[at] = (uint16_t)s;
+        if (before == 0) hist[id] += __popc(same);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = S.tmem_base;
+  const int n_act = S.n_act;
+
+  if (n_act == 0) {  // nothing to read: zeros
+    for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
+      p.out[i] = __float2bfloat16_rn(0.f);
+    if (warp == 1) tmem_dealloc(tmem_base, 512);
+    return;
+  }
+  // first product: tiles by entry, then rows; second: tiles by rows, each over all entries
+  const Run R1 = make_run(n_act * p.tiles1, p.nk1, cta, grid);
+  const Run R2 = make_run(p.tiles2 * n_act, p.nk2, cta, grid);
+  const int units1 = R1.it1 - R1.it0, units = units1 + R2.it1 - R2.it0;
+
+  if (warp == 0) {
+    // ============================== weights: TMA producer ==============================
+    if (lane == 0) {
+      const uint64_t pol = l2_evict_first();
+      int li = 0;
+      for (; li < units; ++li) {
+        const int s = li % p.a_stages;
+        if (!mbar_wait(&S.aempty[s], (uint32_t)(((li / p.a_stages) & 1) ^ 1), abort_flag, p.wait_ns)) {
+          fail();
+          break;
+        }
+        mbar_arrive_expect_tx(&S.afull[s], kUnitBytes);
+        if (li < units1) {
+          const int it = R1.it0 + li, X = it / p.nk1, kk = it - X * p.nk1;
+          const int a = X / p.tiles1, tile = X - a * p.tiles1;
+          tma_load_3d_hint(a_ring + s * kUnitBytes, &tm13, &S.afull[s], kk * 128, tile * 64, 2 * ent_e[a], pol);
+        } else {
+          const int it = R2.it0 + li - units1, X = it / p.nk2, kk = it - X * p.nk2;
+          const int tile = X / n_act, a = X - tile * n_act;
+          tma_load_3d_hint(a_ring + s * kUnitBytes, &tm2, &S.afull[s], kk * 128, tile * kRows, ent_e[a], pol);
+        }
+      }
+      for (int i = li > p.a_stages ? li - p.a_stages : 0; i < li; ++i)  // loads in flight land before exit
+        mbar_wait(&S.afull[i % p.a_stages], (uint32_t)((i / p.a_stages) & 1), nullptr, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================================== MMA issuer ==================================
+    if (lane == 0) {
+      const uint32_t idesc0 = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kRows, 0);
+      bool ok = true;
+      if (p.test_stall && !mbar_wait(&S.never, 0, abort_flag, p.wait_ns)) {
+        fail();
+        ok = false;
+      }
+      int li = 0, seg = 0;
+      while (li < units && ok) {
+        const bool one = li < units1;
+        const int it = one ? R1.it0 + li : R2.it0 + li - units1;
+        const int nk = one ? p.nk1 : p.nk2;
+        const int X = it / nk, left = min(nk - (it - X * nk), (one ? R1.it1 : R2.it1) - it);
+        const int cnt = ent_cnt[one ? X / p.tiles1 : X % n_act];
+        const int groups = one ? (cnt + kPerGroup1 - 1) / kPerGroup1 : (cnt + kPerGroup2 - 1) / kPerGroup2;
+        const uint32_t idesc = idesc0 | ((uint32_t)(2 * groups) << 17);
+        const int buf = seg & 1;
+        if (!mbar_wait(&S.tempty[buf], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, p.wait_ns)) {
+          fail();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+        for (int i = 0; i < left; ++i, ++li) {
+          const int sa = li % p.a_stages, sb = li % kBStages;
+          if (!mbar_wait(&S.afull[sa], (uint32_t)((li / p.a_stages) & 1), abort_flag, p.wait_ns) ||
+              !mbar_wait(&S.bfull[sb], (uint32_t)((li / kBStages) & 1), abort_flag, p.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = smem_desc(smem_u32(a_ring + sa * kUnitBytes), 16, 1024);
+          const uint64_t bd = smem_desc(smem_u32(b_ring + sb * p.b_bytes), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f8f6f4(d, ad + 2 * kk, bd + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&S.aempty[sa]);
+          umma_commit(&S.bempty[sb]);
+        }
+        if (!ok) break;
+        umma_commit(&S.tfull[buf]);
+        ++seg;
+      }
+      umma_commit(&S.drain);
+    }
+    __syncwarp();
+  } else {
+    // ---- each token's largest |x|: builders and epilogue warps together ----
+    {
+      const int w = warp - 2, nvec = p.H / 8;
+      const int chunks = (nvec + 31) / 32;
+      for (int64_t j = w; j < (int64_t)p.T * chunks; j += 8) {
+        const int t = (int)(j / chunks), c = (int)(j - (int64_t)t * chunks) * 32 + lane;
+        uint32_t m = 0;
+        if (c < nvec) m = absmax_fold(absmax_vec8(0u, __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.H) + c)));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) atomicMax(xbits + t, m << 16);
+      }
+      named_bar_sync(1, 256);
+    }
+    if (warp < 6) {
+      // ============================ activations: B operand ============================
+      const int w = warp - 2;
+      bool ok = true;
+      uint8_t* stage = b_ring + w * p.b_bytes;
+      const uint32_t col = 4u * (uint32_t)lane;  // this lane's 4 of the unit's 128 K values
+      int use = 0;
+      int li = w;
+      auto wait_empty = [&]() {
+        if (mbar_wait(&S.bempty[w], (uint32_t)((use & 1) ^ 1), abort_flag, p.wait_ns)) return true;
+        if (lane == 0) fail();
+        return false;
+      };
+      auto put = [&](int row, uint32_t word) {  // 128-byte swizzled row
+        *reinterpret_cast<uint32_t*>(stage + row * 128 + (col ^ ((uint32_t)(row & 7) << 4))) = word;
+      };
+      auto publish = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.bfull[w]);
+        ++use;
+      };
+      for (; li < units1; li += kBStages) {
+        const int it = R1.it0 + li, X = it / p.nk1;
+        const int k0 = (it - X * p.nk1) * 128 + (int)col;
+        const int a = X / p.tiles1, cnt = ent_cnt[a], start = ent_start[a];
+        if (!__all_sync(0xffffffffu, wait_empty())) {
+          ok = false;
+          break;
+        }
+#pragma unroll 4
+        for (int j = 0; j < cnt; ++j) {
+          const int t = slot_of[start + j] / p.k;
+          float mult, inv;
+          row_scale(xbits[t], &mult, &inv);
+          uint2 v = make_uint2(0, 0);
+          if (k0 < p.H) v = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)t * p.H + k0));
+          uint32_t o[2];
+          split4<2>(make_float4(__uint_as_float(v.x << 16) * mult, __uint_as_float(v.x & 0xFFFF0000u) * mult,
+                                __uint_as_float(v.y << 16) * mult, __uint_as_float(v.y & 0xFFFF0000u) * mult),
+                    o);
+          const int row = 16 * (j / kPerGroup1) + 2 * (j % kPerGroup1);
+          put(row, o[0]);
+          put(row + 1, o[1]);
+        }
+        publish();
+      }
+      // ---- the hidden layer is complete once every CTA has arrived ----
+      if (ok) {
+        bool there = true;
+        if (lane == 0) there = wait_count_geq(p.counters, (uint32_t)grid, p.wait_ns);
+        ok = __shfl_sync(0xffffffffu, (int)there, 0);
+        if (!ok && lane == 0) fail();
+      }
+      if (ok) {
+        const int used = ent_start[n_act - 1] + ent_cnt[n_act - 1];
+        for (int pos = w; pos < used; pos += 4) {
+          uint32_t m = 0;
+          for (int i = lane; i < 2 * p.tiles1; i += 32) m = max(m, __ldcg(p.amax + (int64_t)pos * 2 * p.tiles1 + i));
+          m = __reduce_max_sync(0xffffffffu, m);
+          if (lane == 0) {
+            row_scale(m, mult2 + pos, inv2 + pos);
+            wt[pos] = p.weights[slot_of[pos]];
+          }
+        }
+        named_bar_sync(3, 128);
+        if (lane == 0) mbar_arrive(&S.scales);
+      } else {
+        named_bar_sync(3, 128);
+      }
+      for (; li < units && ok; li += kBStages) {
+        const int it = R2.it0 + li - units1, X = it / p.nk2;
+        const int k0 = (it - X * p.nk2) * 128 + (int)col;
+        const int a = X % n_act, cnt = ent_cnt[a], start = ent_start[a];
+        if (!__all_sync(0xffffffffu, wait_empty())) break;
+#pragma unroll 2
+        for (int j = 0; j < cnt; ++j) {
+          const float mult = mult2[start + j];
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 < p.I) v = __ldcg(reinterpret_cast<const float4*>(p.act + (int64_t)(start + j) * p.I + k0));
+          uint32_t o[3];
+          split4<3>(make_float4(v.x * mult, v.y * mult, v.z * mult, v.w * mult), o);
+          const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
+          put(row, o[0]);
+          put(row + 1, o[1]);
+          put(row + 2, o[2]);
+        }
+        publish();
+      }
+    } else {
+      // ================================== epilogue ==================================
+      const int q = warp & 3, r = q * 32 + lane;  // tensor-memory lane quarter, row of the tile
+      const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+      bool ok = true;
+      int seg = 0;
+      float* my_part = p.part + (int64_t)cta * 2 * p.T * kRows;
+      auto part_of = [&](int c, int which) { return p.part + ((int64_t)c * 2 + which) * p.T * kRows; };
+      // the four warps go on or stop together: they meet at named barriers further down
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = mbar_wait(bar, parity, abort_flag, p.wait_ns);
+        if (!got) fail();
+        return named_bar_and(2, 128, got);
+      };
+      auto wait_tile = [&](int buf) {
+        if (!wait_all(&S.tfull[buf], (uint32_t)((seg >> 1) & 1))) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto release_tile = [&](int buf) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(&S.tempty[buf]);
+        ++seg;
+      };
+      // this CTA's partial sums of a shared tile are written: true for the CTA that came last
+      auto came_last = [&](int ph, int c_first, int c_last) {
+        named_bar_sync(2, 128);
+        if (tid == 192) S.last = atom_add_acq_rel(p.counters + 1 + ph * grid + c_first, 1u) == (uint32_t)(c_last - c_first);
+        named_bar_sync(2, 128);
+        return S.last != 0;
+      };
+
+      // ---- first product: hidden = silu(gate) * up ----
+      for (int it = R1.it0; it < R1.it1;) {
+        const int X = it / p.nk1, first = X * p.nk1, len = min(first + p.nk1, R1.it1) - it;
+        const int a = X / p.tiles1, tile = X - a * p.tiles1;
+        const int cnt = ent_cnt[a], start = ent_start[a];
+        const int i = tile * 64 + (r & 63);
+        const float s = i < p.I ? __ldg(p.s13 + ((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i) : 0.f;
+        const bool whole = len == p.nk1;
+        // gate and up of 8 tokens' row r -> the hidden layer and its maxima
+        auto finish = [&](int g, const float* v) {
+          if (r >= 64) {
+#pragma unroll
+            for (int j = 0; j < kPerGroup1; ++j) xch[j * 64 + r - 64] = v[j] * s;
+          }
+          named_bar_sync(2, 128);
+          if (r < 64) {
+#pragma unroll
+            for (int j = 0; j < kPerGroup1; ++j) {
+              if (g * kPerGroup1 + j >= cnt) break;
+              const int64_t pos = start + g * kPerGroup1 + j;
+              const float gate = v[j] * s;
+              const float h = gate / (1.0f + expf(-gate)) * xch[j * 64 + r];
+              if (i < p.I) p.act[pos * p.I + i] = h;
+              const uint32_t m = __reduce_max_sync(0xffffffffu, i < p.I ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
+              if (lane == 0) p.amax[pos * 2 * p.tiles1 + 2 * tile + q] = m;
+            }
+          }
+          named_bar_sync(2, 128);
+        };
+        const int buf = seg & 1;
+        if (!wait_tile(buf)) {
+          ok = false;
+          break;
+        }
+        float* mine = my_part + (it == R1.it0 ? 0 : p.T * kRows);
+        for (int g = 0; g * kPerGroup1 < cnt; ++g) {
+          uint32_t d[16];
+          tmem_ld16(lanes + (uint32_t)(buf * 256 + 16 * g), d);
+          tmem_ld_wait_regs16(d);
+          float v[kPerGroup1];
+#pragma unroll
+          for (int j = 0; j < kPerGroup1; ++j) {
+            const int idx = g * kPerGroup1 + j;
+            float mult, inv = 0.f;
+            if (idx < cnt) row_scale(xbits[slot_of[start + idx] / p.k], &mult, &inv);
+            v[j] = (__uint_as_float(d[2 * j]) + __uint_as_float(d[2 * j + 1]) * 0.0625f) * inv;
+            if (!whole && idx < cnt) mine[idx * kRows + r] = v[j];
+          }
+          if (whole) finish(g, v);
+        }
+        release_tile(buf);
+        if (!whole) {
+          const int c0 = R1.owner(first), c1 = R1.owner(first + p.nk1 - 1);
+          if (came_last(0, c0, c1)) {
+            for (int g = 0; g * kPerGroup1 < cnt; ++g) {
+              float v[kPerGroup1];
+#pragma unroll
+              for (int j = 0; j < kPerGroup1; ++j) v[j] = 0.f;
+              for (int c = c0; c <= c1; ++c) {
+                const float* o = part_of(c, R1.first(c) >= first ? 0 : 1) + r;
+#pragma unroll
+                for (int j = 0; j < kPerGroup1; ++j)
+                  if (g * kPerGroup1 + j < cnt) v[j] += __ldcg(o + (g * kPerGroup1 + j) * kRows);
+              }
+              finish(g, v);
+            }
+          }
+        }
+        it += len;
+      }
+      named_bar_sync(2, 128);
+      if (ok && tid == 192) red_add_release_gpu(p.counters, 1u);
+
+      // ---- second product: the weighted sum over a token's experts, in entry order ----
+      if (ok) ok = wait_all(&S.scales, 0);
+      const int per = n_act * p.nk2;  // units of a tile of the output
+      for (int it = R2.it0; it < R2.it1 && ok;) {
+        const int tile = it / per, first = tile * per, end = min(first + per, R2.it1);
+        const int nrow = tile * kRows + r;
+        const bool whole = it == first && end == first + per;
+        float* mine = my_part + (it == R2.it0 ? 0 : p.T * kRows);
+        for (int t = 0; t < p.T; ++t) acc[t * kRows + r] = 0.f;
+        while (it < end) {
+          const int X = it / p.nk2, len = min((X + 1) * p.nk2, end) - it;
+          const int a = X - tile * n_act, cnt = ent_cnt[a], start = ent_start[a];
+          const float s = nrow < p.H ? __ldg(p.s2 + (int64_t)ent_e[a] * p.H + nrow) : 0.f;
+          const int buf = seg & 1;
+          if (!wait_tile(buf)) {
+            ok = false;
+            break;
+          }
+          for (int g = 0; g * kPerGroup2 < cnt; ++g) {
+            uint32_t d[16];
+            tmem_ld16(lanes + (uint32_t)(buf * 256 + 16 * g), d);
+            tmem_ld_wait_regs16(d);
+#pragma unroll
+            for (int j = 0; j < kPerGroup2; ++j) {
+              if (g * kPerGroup2 + j >= cnt) break;
+              const int pos = start + g * kPerGroup2 + j;
+              const float v = __uint_as_float(d[3 * j]) + __uint_as_float(d[3 * j + 1]) * 0.0625f +
+                              __uint_as_float(d[3 * j + 2]) * 0.00390625f;
+              acc[(slot_of[pos] / p.k) * kRows + r] += wt[pos] * (v * inv2[pos] * s);
+            }
+          }
+          release_tile(buf);
+          it += len;
+        }
+        if (!ok) break;
+        if (whole) {
+          if (nrow < p.H)
+            for (int t = 0; t < p.T; ++t) p.out[(int64_t)t * p.H + nrow] = __float2bfloat16_rn(acc[t * kRows + r]);
+          continue;
+        }
+        for (int t = 0; t < p.T; ++t) mine[t * kRows + r] = acc[t * kRows + r];
+        const int c0 = R2.owner(first), c1 = R2.owner(first + per - 1);
+        if (came_last(1, c0, c1)) {
+          for (int t = 0; t < p.T; ++t) {
+            float v = 0.f;
+            for (int c = c0; c <= c1; ++c) v += __ldcg(part_of(c, R2.first(c) >= first ? 0 : 1) + t * kRows + r);
+            if (nrow < p.H) p.out[(int64_t)t * p.H + nrow] = __float2bfloat16_rn(v);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait(&S.drain, 0, nullptr, kDrainNs);  // the MMAs that write tensor memory
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// The workspace: counters (cleared by each call), hidden layer, its maxima, partial sums.
+struct WsLayout {
+  int64_t act, amax, part, total;
+};
+constexpr int64_t kMaxGrid = 160;  // CTAs that the workspace holds partial sums for
+WsLayout ws_layout(int64_t T, int64_t k, int64_t I) {
+  WsLayout L;
+  const int64_t n = T * k, tiles1 = ceil_div64(I, 64);
+  int64_t o = round_up64((1 + 2 * kMaxGrid) * 4, 256);
+  L.act = o, o += round_up64(n * I * 4, 256);
+  L.amax = o, o += round_up64(n * 2 * tiles1 * 4, 256);
+  L.part = o, o += kMaxGrid * 2 * T * kRows * 4;
+  L.total = o;
+  return L;
 }
 
 }  // namespace
 
-int64_t moe_tokens_ws_bytes(int64_t T, int64_t k, int64_t H, int64_t I) { return round_up64(T * k * I * 4, 16); }
+int64_t moe_tokens_ws_bytes(int64_t T, int64_t k, int64_t H, int64_t I) {
+  (void)H;
+  return ws_layout(T, k, I).total;
+}
 
 int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, const void* w13, const float* s13,
                       const void* w2, const float* s2, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* out,
                       void* ws, const Ctx& c) {
-  if (T == 0 || H == 0) return FP8_OK;
-  const MoeArgs a = {static_cast<const uint16_t*>(x),
-                     ids,
-                     weights,
-                     static_cast<const uint8_t*>(w13),
-                     s13,
-                     static_cast<const uint8_t*>(w2),
-                     s2,
-                     static_cast<uint16_t*>(out),
-                     static_cast<float*>(ws),
-                     (int)T,
-                     (int)k,
-                     (int)E,
-                     H,
-                     I,
-                     c.status};
-  if (I > 0) moe_up_kernel<<<dim3((unsigned)ceil_div64(I, 8), (unsigned)(T * k)), 256, 0, c.stream>>>(a);
-  moe_down_kernel<<<dim3((unsigned)ceil_div64(H, 8), (unsigned)T), 256, 0, c.stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  if (T == 0) return FP8_OK;
+  const WsLayout W = ws_layout(T, k, I);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  MoeArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ids = ids;
+  a.weights = weights;
+  a.s13 = s13;
+  a.s2 = s2;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.T = (int)T, a.k = (int)k, a.E = (int)E, a.H = (int)H, a.I = (int)I;
+  a.tiles1 = (int)ceil_div64(I, 64);
+  a.nk1 = (int)ceil_div64(H, 128);
+  a.tiles2 = (int)ceil_div64(H, kRows);
+  a.nk2 = (int)ceil_div64(I, 128);
+  a.counters = reinterpret_cast<uint32_t*>(base);
+  a.act = reinterpret_cast<float*>(base + W.act);
+  a.amax = reinterpret_cast<uint32_t*>(base + W.amax);
+  a.part = reinterpret_cast<float*>(base + W.part);
+  a.status = c.status;
+  a.wait_ns = c.wait_ns;
+  a.test_stall = c.test_stall;
+  // columns of N for T slots of one expert, in the layout that needs more of them (5 to a group)
+  a.b_bytes = (int)ceil_div64(T, kPerGroup2) * 16 * 128;
+  const Layout L = layout((int)T, (int)k, (int)E);
+  const int room = kSmemMax - 1024 - kBStages * a.b_bytes - L.total;
+  a.a_stages = room / kUnitBytes < kMaxA ? room / kUnitBytes : kMaxA;
+  if (a.a_stages < 2) return FP8_ERR_UNSUPPORTED;
+  const int grid = (int)(c.sm_count < kMaxGrid ? c.sm_count : kMaxGrid);
+  const size_t smem = 1024 + (size_t)a.a_stages * kUnitBytes + (size_t)kBStages * a.b_bytes + L.total;
+
+  CUtensorMap t13, t2;
+  {
+    // [2 E][I][H]: a box of 64 rows of the gate and the same 64 rows of the up projection
+    const uint64_t dims[3] = {(uint64_t)H, (uint64_t)I, (uint64_t)(2 * E)};
+    const uint64_t strides[2] = {(uint64_t)H, (uint64_t)(H * I)};
+    const uint32_t box[3] = {128, 64, 2};
+    const int rc = make_tmap(&t13, w13, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != FP8_OK) return rc;
+  }
+  {
+    const uint64_t dims[3] = {(uint64_t)I, (uint64_t)H, (uint64_t)E};
+    const uint64_t strides[2] = {(uint64_t)I, (uint64_t)(H * I)};
+    const uint32_t box[3] = {128, kRows, 1};
+    const int rc = make_tmap(&t2, w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != FP8_OK) return rc;
+  }
+  if (cudaMemsetAsync(ws, 0, (1 + 2 * (size_t)grid) * 4, c.stream) != cudaSuccess) return FP8_ERR_CUDA;
+  if (cudaFuncSetAttribute(moe_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return FP8_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs resident: they meet at the grid barrier
+  attr[0].val.cooperative = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_tokens_kernel, t13, t2, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
 }  // namespace fp8lin

@@ -188,3 +188,22 @@ def test_no_tokens(fp8):
     out = fp8.moe_tokens_alloc(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"),
                                torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda"), *layer)
     assert out.shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 4, 2, 256, 128), (20, 8, 4, 2048, 1024)])
+def test_wait_limit_expiry_reports_timeout_and_context_survives(fp8, T, E, k, H, I):
+    """The MMA issuer waits on a barrier that nothing signals; the wait runs out, the kernel reports it, drains and
+    returns, and the next call is right."""
+    layer, g = _layer(E, H, I, 8)
+    x, ids, wt = _tokens(g, T, H, E, k)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    old = fp8.fp8_set_wait_limit_ns(2_000_000)  # 2 ms
+    fp8.fp8_set_test_stall(True)
+    try:
+        fp8.moe_tokens_alloc(x, ids, wt, *layer, status=st)
+        torch.cuda.synchronize()
+    finally:
+        fp8.fp8_set_test_stall(False)
+        fp8.fp8_set_wait_limit_ns(old)
+    assert int(st) & fp8.DEV_TIMEOUT
+    _check(fp8, x, ids, wt, layer)
