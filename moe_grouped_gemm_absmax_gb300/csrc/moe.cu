@@ -22,8 +22,11 @@
 //  - Between the two products all CTAs meet at a grid barrier (the hidden layer is complete); the
 //    weight ring is filled for the second product meanwhile.
 //
-// Warps: 0 the weights' TMA producer; 1 the MMA issuer; 2-5 build the activation operand, each its
-// own stage of a 4-stage ring; 6-9 the epilogue, a thread per row of the tile.
+// Warps: 0 the weights' TMA producer; 1 the MMA issuer; 2-9 build the activation operand, every
+// eighth unit each, into the weights' ring stages; 10-13 the epilogue, a thread per row of
+// the tile. The MMA issuer's loop runs warp-uniform (elect.sync picks the issuing lane), with one
+// commit a unit: with a lane's own control flow and a ring of its own for the activations a unit took
+// 980 cycles, above the 700 that its 16 KB take to arrive.
 // Every wait is bounded; on a timeout the kernel raises FP8_DEV_TIMEOUT, drains its loads and MMAs,
 // frees its tensor memory and returns.
 #include "common.cuh"
@@ -35,9 +38,11 @@ namespace {
 
 constexpr int kRows = 128;             // weight rows of a tile (64 gate + 64 up rows in the first product)
 constexpr int kUnitBytes = kRows * 128;
-constexpr int kBStages = 4;            // one per builder warp
-constexpr int kMaxA = 12;
-constexpr int kThreads = 320;
+constexpr int kMaxStages = 12;
+constexpr int kBuilders = 8;           // warps 2 .. 9
+constexpr int kEpi0 = 2 + kBuilders;   // first epilogue warp
+constexpr int kThreads = 32 * (kEpi0 + 4);
+constexpr int kMaxEntry = 40;          // slots of an entry at most: 128 columns of N in three parts
 constexpr int kSmemMax = 232448;       // 227 KB
 constexpr uint64_t kDrainNs = 2000000000ull;
 // columns of N: groups of 16 hold 8 tokens in two parts, or 5 in three
@@ -51,7 +56,8 @@ struct MoeArgs {
   const float* s2;
   __nv_bfloat16* out;
   int T, k, E, H, I;
-  int a_stages, b_bytes;  // ring sizes: weight stages; bytes of an activation stage
+  int cap;                // slots of an entry at most
+  int stages, b_bytes;    // ring stages; bytes of a stage's activations, after its weights
   int tiles1, nk1, tiles2, nk2;
   // workspace
   uint32_t* counters;     // [0] the grid barrier, [1 + ph * grid + c] arrivals at the tile that CTA c starts and leaves
@@ -64,8 +70,7 @@ struct MoeArgs {
 };
 
 struct Shared {
-  uint64_t afull[kMaxA], aempty[kMaxA];
-  uint64_t bfull[kBStages], bempty[kBStages];
+  uint64_t full[kMaxStages], built[kMaxStages], empty[kMaxStages];  // weights landed; activations written; both read
   uint64_t tfull[2], tempty[2];
   uint64_t drain, never, scales;
   uint32_t tmem_base;
@@ -114,6 +119,15 @@ FP8_DEVI void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, i
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(pol)
       : "memory");
 }
+FP8_DEVI bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 FP8_DEVI uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
   uint32_t r;
   asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
@@ -159,14 +173,34 @@ FP8_DEVI Run make_run(int tiles, int nk, int cta, int grid) {
   return r;
 }
 
+// A place in a CTA's share, stepped without divisions: unit kk of the nk of a (tile, entry).
+struct Walk {
+  int kk, nk, tile, a;
+  FP8_DEVI void step1(int by, int tiles1) {  // first product: tiles of an entry are consecutive
+    for (kk += by; kk >= nk; kk -= nk)
+      if (++tile == tiles1) tile = 0, ++a;
+  }
+  FP8_DEVI void step2(int by, int n_act) {  // second: entries of a tile are consecutive
+    for (kk += by; kk >= nk; kk -= nk)
+      if (++a == n_act) a = 0, ++tile;
+  }
+};
+FP8_DEVI Walk walk1(int it, int nk, int tiles1) {
+  const int X = it / nk;
+  return {it - X * nk, nk, X % tiles1, X / tiles1};
+}
+FP8_DEVI Walk walk2(int it, int nk, int n_act) {
+  const int X = it / nk;
+  return {it - X * nk, nk, X / n_act, X % n_act};
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     moe_tokens_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2, const MoeArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Layout L = layout(p.T, p.k, p.E);
-  uint8_t* a_ring = smem;
-  uint8_t* b_ring = smem + p.a_stages * kUnitBytes;
-  uint8_t* rest = b_ring + kBStages * p.b_bytes;
+  const int stage_bytes = kUnitBytes + p.b_bytes;
+  uint8_t* rest = smem + p.stages * stage_bytes;
   float* acc = reinterpret_cast<float*>(rest + L.acc);
   float* xch = reinterpret_cast<float*>(rest + L.xch);
   Shared& S = *reinterpret_cast<Shared*>(rest + L.shared);
@@ -191,17 +225,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  // ---- slots by expert: each entry is an expert with up to T of its slots ----
+  // ---- slots by expert: each entry is an expert with up to `cap` of its slots ----
   for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
   for (int t = tid; t < p.T; t += kThreads) xbits[t] = 0;
   if (tid == 0) {
-    for (int s = 0; s < p.a_stages; ++s) {
-      mbar_init(&S.afull[s], 1);
-      mbar_init(&S.aempty[s], 1);
-    }
-    for (int s = 0; s < kBStages; ++s) {
-      mbar_init(&S.bfull[s], 1);
-      mbar_init(&S.bempty[s], 1);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.built[s], 1);
+      mbar_init(&S.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S.tfull[b], 1);
@@ -209,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&S.drain, 1);
     mbar_init(&S.never, 1);
-    mbar_init(&S.scales, 4);
+    mbar_init(&S.scales, kBuilders);
     S.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm13);
@@ -235,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < p.E; b += 32) {
       const int e = b + lane;
       const int cnt = e < p.E ? hist[e] : 0;
-      const int ne = (cnt + p.T - 1) / p.T;
+      const int ne = (cnt + p.cap - 1) / p.cap;
       int xs = cnt, xe = ne;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -246,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e < p.E) hist[e] = s0;
       for (int q = 0; q < ne; ++q) {
         ent_e[a0 + q] = (uint16_t)e;
-        ent_start[a0 + q] = (uint16_t)(s0 + q * p.T);
-        ent_cnt[a0 + q] = (uint16_t)min(p.T, cnt - q * p.T);
+        ent_start[a0 + q] = (uint16_t)(s0 + q * p.cap);
+        ent_cnt[a0 + q] = (uint16_t)min(p.cap, cnt - q * p.cap);
       }
       slots += __shfl_sync(0xffffffffu, xs, 31);
       ents += __shfl_sync(0xffffffffu, xe, 31);
@@ -289,136 +320,175 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================== weights: TMA producer ==============================
     if (lane == 0) {
       const uint64_t pol = l2_evict_first();
-      int li = 0;
+      int li = 0, s = 0;
+      uint32_t phase = 0;
+      Walk w1 = walk1(R1.it0, p.nk1, p.tiles1), w2 = walk2(R2.it0, p.nk2, n_act);
       for (; li < units; ++li) {
-        const int s = li % p.a_stages;
-        if (!mbar_wait(&S.aempty[s], (uint32_t)(((li / p.a_stages) & 1) ^ 1), abort_flag, p.wait_ns)) {
+        if (!mbar_wait(&S.empty[s], phase ^ 1, abort_flag, p.wait_ns)) {
           fail();
           break;
         }
-        mbar_arrive_expect_tx(&S.afull[s], kUnitBytes);
+        uint8_t* dst = smem + s * stage_bytes;
+        mbar_arrive_expect_tx(&S.full[s], kUnitBytes);
         if (li < units1) {
-          const int it = R1.it0 + li, X = it / p.nk1, kk = it - X * p.nk1;
-          const int a = X / p.tiles1, tile = X - a * p.tiles1;
-          tma_load_3d_hint(a_ring + s * kUnitBytes, &tm13, &S.afull[s], kk * 128, tile * 64, 2 * ent_e[a], pol);
+          tma_load_3d_hint(dst, &tm13, &S.full[s], w1.kk * 128, w1.tile * 64, 2 * ent_e[w1.a], pol);
+          w1.step1(1, p.tiles1);
         } else {
-          const int it = R2.it0 + li - units1, X = it / p.nk2, kk = it - X * p.nk2;
-          const int tile = X / n_act, a = X - tile * n_act;
-          tma_load_3d_hint(a_ring + s * kUnitBytes, &tm2, &S.afull[s], kk * 128, tile * kRows, ent_e[a], pol);
+          tma_load_3d_hint(dst, &tm2, &S.full[s], w2.kk * 128, w2.tile * kRows, ent_e[w2.a], pol);
+          w2.step2(1, n_act);
         }
+        if (++s == p.stages) s = 0, phase ^= 1;
       }
-      for (int i = li > p.a_stages ? li - p.a_stages : 0; i < li; ++i)  // loads in flight land before exit
-        mbar_wait(&S.afull[i % p.a_stages], (uint32_t)((i / p.a_stages) & 1), nullptr, kDrainNs);
+      for (int i = li > p.stages ? li - p.stages : 0; i < li; ++i)  // loads in flight land before exit
+        mbar_wait(&S.full[i % p.stages], (uint32_t)((i / p.stages) & 1), nullptr, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ================================== MMA issuer ==================================
-    if (lane == 0) {
-      const uint32_t idesc0 = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kRows, 0);
-      bool ok = true;
-      if (p.test_stall && !mbar_wait(&S.never, 0, abort_flag, p.wait_ns)) {
+    const bool leader = elect_one();
+    const uint32_t idesc0 = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kRows, 0);
+    const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024);
+    const uint32_t stage16 = (uint32_t)stage_bytes >> 4;
+    bool ok = true;
+    if (p.test_stall && !mbar_wait(&S.never, 0, abort_flag, p.wait_ns)) {
+      fail();
+      ok = false;
+    }
+    int li = 0, seg = 0, s = 0;
+    uint32_t phase = 0;
+    Walk w = walk1(R1.it0, p.nk1, p.tiles1);
+    if (units1 == 0) w = walk2(R2.it0, p.nk2, n_act);
+    while (li < units && ok) {
+      const bool one = li < units1;
+      const int left = min(w.nk - w.kk, (one ? units1 : units) - li);
+      const int cnt = ent_cnt[w.a];
+      const int groups = one ? (cnt + kPerGroup1 - 1) / kPerGroup1 : (cnt + kPerGroup2 - 1) / kPerGroup2;
+      const uint32_t idesc = idesc0 | ((uint32_t)(2 * groups) << 17);
+      const int buf = seg & 1;
+      if (!mbar_wait(&S.tempty[buf], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, p.wait_ns)) {
         fail();
-        ok = false;
+        break;
       }
-      int li = 0, seg = 0;
-      while (li < units && ok) {
-        const bool one = li < units1;
-        const int it = one ? R1.it0 + li : R2.it0 + li - units1;
-        const int nk = one ? p.nk1 : p.nk2;
-        const int X = it / nk, left = min(nk - (it - X * nk), (one ? R1.it1 : R2.it1) - it);
-        const int cnt = ent_cnt[one ? X / p.tiles1 : X % n_act];
-        const int groups = one ? (cnt + kPerGroup1 - 1) / kPerGroup1 : (cnt + kPerGroup2 - 1) / kPerGroup2;
-        const uint32_t idesc = idesc0 | ((uint32_t)(2 * groups) << 17);
-        const int buf = seg & 1;
-        if (!mbar_wait(&S.tempty[buf], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, p.wait_ns)) {
+      tc_fence_after();
+      const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+      for (int i = 0; i < left; ++i) {
+        if (!mbar_wait(&S.full[s], phase, abort_flag, p.wait_ns) || !mbar_wait(&S.built[s], phase, abort_flag, p.wait_ns)) {
           fail();
+          ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(buf * 256);
-        for (int i = 0; i < left; ++i, ++li) {
-          const int sa = li % p.a_stages, sb = li % kBStages;
-          if (!mbar_wait(&S.afull[sa], (uint32_t)((li / p.a_stages) & 1), abort_flag, p.wait_ns) ||
-              !mbar_wait(&S.bfull[sb], (uint32_t)((li / kBStages) & 1), abort_flag, p.wait_ns)) {
-            fail();
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = smem_desc(smem_u32(a_ring + sa * kUnitBytes), 16, 1024);
-          const uint64_t bd = smem_desc(smem_u32(b_ring + sb * p.b_bytes), 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) umma_f8f6f4(d, ad + 2 * kk, bd + 2 * kk, idesc, (i > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&S.aempty[sa]);
-          umma_commit(&S.bempty[sb]);
+        const uint64_t ad = desc0 + (uint64_t)((uint32_t)s * stage16);
+        const uint64_t bd = ad + (kUnitBytes >> 4);
+        if (leader) {
+          umma_f8f6f4(d, ad, bd, idesc, i > 0 ? 1u : 0u);
+          umma_f8f6f4(d, ad + 2, bd + 2, idesc, 1u);
+          umma_f8f6f4(d, ad + 4, bd + 4, idesc, 1u);
+          umma_f8f6f4(d, ad + 6, bd + 6, idesc, 1u);
+          umma_commit(&S.empty[s]);
+          if (i + 1 == left) umma_commit(&S.tfull[buf]);
         }
-        if (!ok) break;
-        umma_commit(&S.tfull[buf]);
-        ++seg;
+        __syncwarp();
+        if (++s == p.stages) s = 0, phase ^= 1;
       }
-      umma_commit(&S.drain);
+      li += left;
+      ++seg;
+      if (one) {
+        w.step1(left, p.tiles1);
+        if (li == units1) w = walk2(R2.it0, p.nk2, n_act);
+      } else {
+        w.step2(left, n_act);
+      }
     }
+    if (leader) umma_commit(&S.drain);
     __syncwarp();
   } else {
     // ---- each token's largest |x|: builders and epilogue warps together ----
     {
       const int w = warp - 2, nvec = p.H / 8;
       const int chunks = (nvec + 31) / 32;
-      for (int64_t j = w; j < (int64_t)p.T * chunks; j += 8) {
+      for (int64_t j = w; j < (int64_t)p.T * chunks; j += kBuilders + 4) {
         const int t = (int)(j / chunks), c = (int)(j - (int64_t)t * chunks) * 32 + lane;
         uint32_t m = 0;
         if (c < nvec) m = absmax_fold(absmax_vec8(0u, __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.H) + c)));
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) atomicMax(xbits + t, m << 16);
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 32 * (kBuilders + 4));
     }
-    if (warp < 6) {
+    if (warp < kEpi0) {
       // ============================ activations: B operand ============================
       const int w = warp - 2;
       bool ok = true;
-      uint8_t* stage = b_ring + w * p.b_bytes;
       const uint32_t col = 4u * (uint32_t)lane;  // this lane's 4 of the unit's 128 K values
-      int use = 0;
-      int li = w;
-      auto wait_empty = [&]() {
-        if (mbar_wait(&S.bempty[w], (uint32_t)((use & 1) ^ 1), abort_flag, p.wait_ns)) return true;
-        if (lane == 0) fail();
-        return false;
+      // A builder waits for the use of its stage before its own. It must not get two uses ahead (their
+      // parities are the same), so no more builders work than there are stages.
+      const int builders = min(kBuilders, p.stages);
+      int li = w < builders ? w : units, s = w;
+      uint32_t phase = 0;
+      uint8_t* stage = nullptr;
+      auto enter = [&]() {
+        const bool got = mbar_wait(&S.empty[s], phase ^ 1, abort_flag, p.wait_ns);
+        if (!got) fail();
+        stage = smem + s * stage_bytes + kUnitBytes;
+        return __all_sync(0xffffffffu, got) != 0;
       };
       auto put = [&](int row, uint32_t word) {  // 128-byte swizzled row
         *reinterpret_cast<uint32_t*>(stage + row * 128 + (col ^ ((uint32_t)(row & 7) << 4))) = word;
       };
-      auto publish = [&]() {
+      auto leave = [&]() {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.bfull[w]);
-        ++use;
+        if (lane == 0) mbar_arrive(&S.built[s]);
+        for (s += builders; s >= p.stages; s -= p.stages) phase ^= 1;
+        li += builders;
       };
-      for (; li < units1; li += kBStages) {
-        const int it = R1.it0 + li, X = it / p.nk1;
-        const int k0 = (it - X * p.nk1) * 128 + (int)col;
-        const int a = X / p.tiles1, cnt = ent_cnt[a], start = ent_start[a];
-        if (!__all_sync(0xffffffffu, wait_empty())) {
-          ok = false;
-          break;
+      // Rows are loaded four at a time, the first ones before the wait for the stage.
+      constexpr int kBatch = 4;
+      {
+        Walk at = walk1(R1.it0, p.nk1, p.tiles1);
+        at.step1(w, p.tiles1);
+        while (li < units1) {
+          const int k0 = at.kk * 128 + (int)col;
+          const int cnt = ent_cnt[at.a], start = ent_start[at.a];
+          uint2 v[kBatch];
+          float mult[kBatch];
+          auto fetch = [&](int j0) {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              v[b] = make_uint2(0, 0);
+              mult[b] = 0.f;
+              if (j0 + b < cnt) {
+                const int t = slot_of[start + j0 + b] / p.k;
+                float inv;
+                row_scale(xbits[t], &mult[b], &inv);
+                if (k0 < p.H) v[b] = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)t * p.H + k0));
+              }
+            }
+          };
+          fetch(0);
+          if (!enter()) {
+            ok = false;
+            break;
+          }
+          for (int j0 = 0; j0 < cnt; j0 += kBatch) {
+            if (j0) fetch(j0);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              const int j = j0 + b;
+              if (j >= cnt) break;
+              uint32_t o[2];
+              split4<2>(make_float4(__uint_as_float(v[b].x << 16) * mult[b], __uint_as_float(v[b].x & 0xFFFF0000u) * mult[b],
+                                    __uint_as_float(v[b].y << 16) * mult[b], __uint_as_float(v[b].y & 0xFFFF0000u) * mult[b]),
+                        o);
+              const int row = 16 * (j / kPerGroup1) + 2 * (j % kPerGroup1);
+              put(row, o[0]);
+              put(row + 1, o[1]);
+            }
+          }
+          leave();
+          at.step1(builders, p.tiles1);
         }
-#pragma unroll 4
-        for (int j = 0; j < cnt; ++j) {
-          const int t = slot_of[start + j] / p.k;
-          float mult, inv;
-          row_scale(xbits[t], &mult, &inv);
-          uint2 v = make_uint2(0, 0);
-          if (k0 < p.H) v = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)t * p.H + k0));
-          uint32_t o[2];
-          split4<2>(make_float4(__uint_as_float(v.x << 16) * mult, __uint_as_float(v.x & 0xFFFF0000u) * mult,
-                                __uint_as_float(v.y << 16) * mult, __uint_as_float(v.y & 0xFFFF0000u) * mult),
-                    o);
-          const int row = 16 * (j / kPerGroup1) + 2 * (j % kPerGroup1);
-          put(row, o[0]);
-          put(row + 1, o[1]);
-        }
-        publish();
       }
       // ---- the hidden layer is complete once every CTA has arrived ----
       if (ok) {
@@ -429,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) {
         const int used = ent_start[n_act - 1] + ent_cnt[n_act - 1];
-        for (int pos = w; pos < used; pos += 4) {
+        for (int pos = w; pos < used; pos += kBuilders) {
           uint32_t m = 0;
           for (int i = lane; i < 2 * p.tiles1; i += 32) m = max(m, __ldcg(p.amax + (int64_t)pos * 2 * p.tiles1 + i));
           m = __reduce_max_sync(0xffffffffu, m);
@@ -438,29 +508,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             wt[pos] = p.weights[slot_of[pos]];
           }
         }
-        named_bar_sync(3, 128);
-        if (lane == 0) mbar_arrive(&S.scales);
-      } else {
-        named_bar_sync(3, 128);
       }
-      for (; li < units && ok; li += kBStages) {
-        const int it = R2.it0 + li - units1, X = it / p.nk2;
-        const int k0 = (it - X * p.nk2) * 128 + (int)col;
-        const int a = X % n_act, cnt = ent_cnt[a], start = ent_start[a];
-        if (!__all_sync(0xffffffffu, wait_empty())) break;
-#pragma unroll 2
-        for (int j = 0; j < cnt; ++j) {
-          const float mult = mult2[start + j];
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k0 < p.I) v = __ldcg(reinterpret_cast<const float4*>(p.act + (int64_t)(start + j) * p.I + k0));
-          uint32_t o[3];
-          split4<3>(make_float4(v.x * mult, v.y * mult, v.z * mult, v.w * mult), o);
-          const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
-          put(row, o[0]);
-          put(row + 1, o[1]);
-          put(row + 2, o[2]);
+      named_bar_sync(3, 32 * kBuilders);
+      if (ok && lane == 0) mbar_arrive(&S.scales);
+      if (ok && li < units) {
+        Walk at = walk2(R2.it0, p.nk2, n_act);
+        at.step2(li - units1, n_act);
+        while (li < units) {
+          const int k0 = at.kk * 128 + (int)col;
+          const int cnt = ent_cnt[at.a], start = ent_start[at.a];
+          float4 v[kBatch];
+          auto fetch = [&](int j0) {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (j0 + b < cnt && k0 < p.I)
+                v[b] = __ldcg(reinterpret_cast<const float4*>(p.act + (int64_t)(start + j0 + b) * p.I + k0));
+            }
+          };
+          fetch(0);
+          if (!enter()) break;
+          for (int j0 = 0; j0 < cnt; j0 += kBatch) {
+            if (j0) fetch(j0);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+              const int j = j0 + b;
+              if (j >= cnt) break;
+              const float mult = mult2[start + j];
+              uint32_t o[3];
+              split4<3>(make_float4(v[b].x * mult, v[b].y * mult, v[b].z * mult, v[b].w * mult), o);
+              const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
+              put(row, o[0]);
+              put(row + 1, o[1]);
+              put(row + 2, o[2]);
+            }
+          }
+          leave();
+          at.step2(builders, n_act);
         }
-        publish();
       }
     } else {
       // ================================== epilogue ==================================
@@ -490,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this CTA's partial sums of a shared tile are written: true for the CTA that came last
       auto came_last = [&](int ph, int c_first, int c_last) {
         named_bar_sync(2, 128);
-        if (tid == 192) S.last = atom_add_acq_rel(p.counters + 1 + ph * grid + c_first, 1u) == (uint32_t)(c_last - c_first);
+        if (tid == 32 * kEpi0) S.last = atom_add_acq_rel(p.counters + 1 + ph * grid + c_first, 1u) == (uint32_t)(c_last - c_first);
         named_bar_sync(2, 128);
         return S.last != 0;
       };
@@ -566,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it += len;
       }
       named_bar_sync(2, 128);
-      if (ok && tid == 192) red_add_release_gpu(p.counters, 1u);
+      if (ok && tid == 32 * kEpi0) red_add_release_gpu(p.counters, 1u);
 
       // ---- second product: the weighted sum over a token's experts, in entry order ----
       if (ok) ok = wait_all(&S.scales, 0);
@@ -679,14 +764,15 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   a.status = c.status;
   a.wait_ns = c.wait_ns;
   a.test_stall = c.test_stall;
-  // columns of N for T slots of one expert, in the layout that needs more of them (5 to a group)
-  a.b_bytes = (int)ceil_div64(T, kPerGroup2) * 16 * 128;
+  a.cap = (int)(T < kMaxEntry ? T : kMaxEntry);
+  // columns of N for an entry, in the layout that needs more of them (5 slots to a group of 16)
+  a.b_bytes = (int)ceil_div64(a.cap, kPerGroup2) * 16 * 128;
   const Layout L = layout((int)T, (int)k, (int)E);
-  const int room = kSmemMax - 1024 - kBStages * a.b_bytes - L.total;
-  a.a_stages = room / kUnitBytes < kMaxA ? room / kUnitBytes : kMaxA;
-  if (a.a_stages < 2) return FP8_ERR_UNSUPPORTED;
+  const int stage_bytes = kUnitBytes + a.b_bytes;
+  const int fit = (kSmemMax - 1024 - L.total) / stage_bytes;  // at least 4: T, k and E are bounded
+  a.stages = fit < kMaxStages ? fit : kMaxStages;
   const int grid = (int)(c.sm_count < kMaxGrid ? c.sm_count : kMaxGrid);
-  const size_t smem = 1024 + (size_t)a.a_stages * kUnitBytes + (size_t)kBStages * a.b_bytes + L.total;
+  const size_t smem = 1024 + (size_t)a.stages * stage_bytes + L.total;
 
   CUtensorMap t13, t2;
   {
