@@ -49,7 +49,6 @@ constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr int kPerGroup1 = 8, kPerGroup2 = 5;
 
 struct MoeArgs {
-  const uint16_t* x;  // bf16 [T, H]
   const int32_t* ids;
   const float* weights;
   const float* s13;
@@ -61,6 +60,8 @@ struct MoeArgs {
   int tiles1, nk1, tiles2, nk2;
   // workspace
   uint32_t* counters;     // [0] the grid barrier, [1 + ph * grid + c] arrivals at the tile that CTA c starts and leaves
+  const uint8_t* xq;      // the tokens' parts [T][2][128 nk1], zeros past H
+  const float* xinv;      // [T]: their powers of two
   float* act;             // hidden layer [slots sorted by expert][I]
   uint32_t* amax;         // |hidden| maxima as bit patterns [slots][2 tiles1]
   float* part;            // partial sums [CTA][2][T][128]
@@ -81,7 +82,7 @@ struct Shared {
 
 // Shared memory after the rings: offsets in bytes (n = T k slots).
 struct Layout {
-  int acc, xch, shared, wt, mult2, inv2, hist, xbits, ids, ent, slot, total;
+  int acc, xch, shared, wt, inv1, mult2, inv2, hist, ids, ent, slot, total;
 };
 __host__ __device__ inline Layout layout(int T, int k, int E) {
   const int n = T * k;
@@ -91,13 +92,13 @@ __host__ __device__ inline Layout layout(int T, int k, int E) {
   L.xch = o, o += kPerGroup1 * 64 * 4;
   L.shared = o, o += (int)sizeof(Shared);
   L.wt = o, o += n * 4;
+  L.inv1 = o, o += n * 4;
   L.mult2 = o, o += n * 4;
   L.inv2 = o, o += n * 4;
   L.hist = o, o += E * 4;
-  L.xbits = o, o += T * 4;
   L.ids = o, o += n * 4;
   L.ent = o, o += n * 4;   // per entry: expert, first slot
-  L.slot = o, o += n * 4;  // per entry: slots; per sorted slot: slot index
+  L.slot = o, o += n * 4;  // per entry: slots; per sorted slot: token
   L.total = o;
   return L;
 }
@@ -194,6 +195,45 @@ FP8_DEVI Walk walk2(int it, int nk, int n_act) {
   return {it - X * nk, nk, X / n_act, X % n_act};
 }
 
+// The tokens' parts, a CTA per token, and the counters' zeros. The product kernel is launched while
+// this one runs (programmatic dependent launch) and waits for it where it first needs the parts: by
+// then it has sorted the slots and filled its ring with weights.
+constexpr int kSplitThreads = 512;
+__global__ void __launch_bounds__(kSplitThreads) moe_split_kernel(const uint16_t* __restrict__ x, int H, int Hp,
+                                                                  uint8_t* __restrict__ xq, float* __restrict__ xinv,
+                                                                  uint32_t* __restrict__ counters, int n_counters) {
+  __shared__ uint32_t red[kSplitThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (t == 0)
+    for (int i = tid; i < n_counters; i += kSplitThreads) counters[i] = 0;
+  const uint4* row = reinterpret_cast<const uint4*>(x + (int64_t)t * H);
+  uint32_t m = 0;
+  for (int c = tid; c < H / 8; c += kSplitThreads) m = absmax_vec8(m, row[c]);
+  m = __reduce_max_sync(0xffffffffu, absmax_fold(m));
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  __syncthreads();
+  m = 0;
+#pragma unroll
+  for (int w = 0; w < kSplitThreads / 32; ++w) m = max(m, red[w]);
+  float mult, inv;
+  row_scale(m << 16, &mult, &inv);
+  if (tid == 0) xinv[t] = inv;
+  for (int c = tid; c < Hp / 8; c += kSplitThreads) {
+    const uint4 v = c < H / 8 ? row[c] : make_uint4(0, 0, 0, 0);
+    uint32_t a[2] = {0, 0}, b[2] = {0, 0};
+    if (c < H / 8) {
+      split4<2>(make_float4(__uint_as_float(v.x << 16) * mult, __uint_as_float(v.x & 0xFFFF0000u) * mult,
+                            __uint_as_float(v.y << 16) * mult, __uint_as_float(v.y & 0xFFFF0000u) * mult), a);
+      split4<2>(make_float4(__uint_as_float(v.z << 16) * mult, __uint_as_float(v.z & 0xFFFF0000u) * mult,
+                            __uint_as_float(v.w << 16) * mult, __uint_as_float(v.w & 0xFFFF0000u) * mult), b);
+    }
+    uint2* o = reinterpret_cast<uint2*>(xq + (int64_t)t * 2 * Hp) + c;
+    o[0] = make_uint2(a[0], b[0]);
+    o[Hp / 8] = make_uint2(a[1], b[1]);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     moe_tokens_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2, const MoeArgs p) {
   extern __shared__ uint8_t smem_raw[];
@@ -205,16 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* xch = reinterpret_cast<float*>(rest + L.xch);
   Shared& S = *reinterpret_cast<Shared*>(rest + L.shared);
   float* wt = reinterpret_cast<float*>(rest + L.wt);
+  float* inv1 = reinterpret_cast<float*>(rest + L.inv1);
   float* mult2 = reinterpret_cast<float*>(rest + L.mult2);
   float* inv2 = reinterpret_cast<float*>(rest + L.inv2);
   int* hist = reinterpret_cast<int*>(rest + L.hist);
-  uint32_t* xbits = reinterpret_cast<uint32_t*>(rest + L.xbits);
   int* ids = reinterpret_cast<int*>(rest + L.ids);
   uint16_t* ent_e = reinterpret_cast<uint16_t*>(rest + L.ent);
   const int n = p.T * p.k;
   uint16_t* ent_start = ent_e + n;
   uint16_t* ent_cnt = reinterpret_cast<uint16_t*>(rest + L.slot);
-  uint16_t* slot_of = ent_cnt + n;
+  uint16_t* tok = ent_cnt + n;
+  int* slot_tmp = reinterpret_cast<int*>(wt);  // a sorted slot's index, until its weight takes the place
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
   volatile int* abort_flag = &S.abort;
@@ -227,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- slots by expert: each entry is an expert with up to `cap` of its slots ----
   for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
-  for (int t = tid; t < p.T; t += kThreads) xbits[t] = 0;
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&S.full[s], 1);
@@ -293,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = id >= 0 ? hist[id] + before : 0;
       __syncwarp();
       if (id >= 0) {
-        slot_of[at] = (uint16_t)s;
+        slot_tmp[at] = s;
+        tok[at] = (uint16_t)(s / p.k);
         if (before == 0) hist[id] += __popc(same);
       }
       __syncwarp();
@@ -306,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_act = S.n_act;
 
   if (n_act == 0) {  // nothing to read: zeros
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // not done before the kernel before it is
     for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
       p.out[i] = __float2bfloat16_rn(0.f);
     if (warp == 1) tmem_dealloc(tmem_base, 512);
@@ -403,19 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) umma_commit(&S.drain);
     __syncwarp();
   } else {
-    // ---- each token's largest |x|: builders and epilogue warps together ----
-    {
-      const int w = warp - 2, nvec = p.H / 8;
-      const int chunks = (nvec + 31) / 32;
-      for (int64_t j = w; j < (int64_t)p.T * chunks; j += kBuilders + 4) {
-        const int t = (int)(j / chunks), c = (int)(j - (int64_t)t * chunks) * 32 + lane;
-        uint32_t m = 0;
-        if (c < nvec) m = absmax_fold(absmax_vec8(0u, __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.H) + c)));
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(xbits + t, m << 16);
-      }
-      named_bar_sync(1, 32 * (kBuilders + 4));
+    // ---- each slot's weight and its token's power of two: builders and epilogue warps together ----
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' parts and the counters are there
+    const int used = ent_start[n_act - 1] + ent_cnt[n_act - 1];
+    for (int i = tid - 64; i < used; i += 32 * (kBuilders + 4)) {
+      wt[i] = __ldg(p.weights + slot_tmp[i]);
+      inv1[i] = __ldcg(p.xinv + tok[i]);
     }
+    named_bar_sync(1, 32 * (kBuilders + 4));
     if (warp < kEpi0) {
       // ============================ activations: B operand ============================
       const int w = warp - 2;
@@ -449,21 +486,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk at = walk1(R1.it0, p.nk1, p.tiles1);
         at.step1(w, p.tiles1);
         while (li < units1) {
-          const int k0 = at.kk * 128 + (int)col;
-          const int cnt = ent_cnt[at.a], start = ent_start[at.a];
-          uint2 v[kBatch];
-          float mult[kBatch];
-          auto fetch = [&](int j0) {
+          // the entry's 2 cnt rows of 128 codes: 8 lanes a row, 4 rows a step
+          const int rows = 2 * ent_cnt[at.a], start = ent_start[at.a];
+          const uint8_t* src = p.xq + at.kk * 128 + (lane & 7) * 16;
+          uint4 v[kBatch];
+          auto fetch = [&](int r0) {
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-              v[b] = make_uint2(0, 0);
-              mult[b] = 0.f;
-              if (j0 + b < cnt) {
-                const int t = slot_of[start + j0 + b] / p.k;
-                float inv;
-                row_scale(xbits[t], &mult[b], &inv);
-                if (k0 < p.H) v[b] = __ldg(reinterpret_cast<const uint2*>(p.x + (int64_t)t * p.H + k0));
-              }
+              const int row = r0 + 4 * b + (lane >> 3);
+              if (row < rows) v[b] = __ldcg(reinterpret_cast<const uint4*>(src + (int64_t)(2 * tok[start + (row >> 1)] + (row & 1)) * (p.nk1 * 128)));
             }
           };
           fetch(0);
@@ -471,19 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          for (int j0 = 0; j0 < cnt; j0 += kBatch) {
-            if (j0) fetch(j0);
+          for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
+            if (r0) fetch(r0);
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-              const int j = j0 + b;
-              if (j >= cnt) break;
-              uint32_t o[2];
-              split4<2>(make_float4(__uint_as_float(v[b].x << 16) * mult[b], __uint_as_float(v[b].x & 0xFFFF0000u) * mult[b],
-                                    __uint_as_float(v[b].y << 16) * mult[b], __uint_as_float(v[b].y & 0xFFFF0000u) * mult[b]),
-                        o);
-              const int row = 16 * (j / kPerGroup1) + 2 * (j % kPerGroup1);
-              put(row, o[0]);
-              put(row + 1, o[1]);
+              const int row = r0 + 4 * b + (lane >> 3);
+              if (row < rows) *reinterpret_cast<uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) = v[b];
             }
           }
           leave();
@@ -498,15 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) fail();
       }
       if (ok) {
-        const int used = ent_start[n_act - 1] + ent_cnt[n_act - 1];
         for (int pos = w; pos < used; pos += kBuilders) {
           uint32_t m = 0;
           for (int i = lane; i < 2 * p.tiles1; i += 32) m = max(m, __ldcg(p.amax + (int64_t)pos * 2 * p.tiles1 + i));
           m = __reduce_max_sync(0xffffffffu, m);
-          if (lane == 0) {
-            row_scale(m, mult2 + pos, inv2 + pos);
-            wt[pos] = p.weights[slot_of[pos]];
-          }
+          if (lane == 0) row_scale(m, mult2 + pos, inv2 + pos);
         }
       }
       named_bar_sync(3, 32 * kBuilders);
@@ -623,9 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kPerGroup1; ++j) {
             const int idx = g * kPerGroup1 + j;
-            float mult, inv = 0.f;
-            if (idx < cnt) row_scale(xbits[slot_of[start + idx] / p.k], &mult, &inv);
-            v[j] = (__uint_as_float(d[2 * j]) + __uint_as_float(d[2 * j + 1]) * 0.0625f) * inv;
+            v[j] = (__uint_as_float(d[2 * j]) + __uint_as_float(d[2 * j + 1]) * 0.0625f) * (idx < cnt ? inv1[start + idx] : 0.f);
             if (!whole && idx < cnt) mine[idx * kRows + r] = v[j];
           }
           if (whole) finish(g, v);
@@ -681,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int pos = start + g * kPerGroup2 + j;
               const float v = __uint_as_float(d[3 * j]) + __uint_as_float(d[3 * j + 1]) * 0.0625f +
                               __uint_as_float(d[3 * j + 2]) * 0.00390625f;
-              acc[(slot_of[pos] / p.k) * kRows + r] += wt[pos] * (v * inv2[pos] * s);
+              acc[tok[pos] * kRows + r] += wt[pos] * (v * inv2[pos] * s);
             }
           }
           release_tile(buf);
@@ -716,15 +734,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The workspace: counters (cleared by each call), hidden layer, its maxima, partial sums.
+// The workspace: counters (cleared by each call), the tokens' parts, hidden layer, its maxima, partial
+// sums.
 struct WsLayout {
-  int64_t act, amax, part, total;
+  int64_t xq, xinv, act, amax, part, total;
 };
 constexpr int64_t kMaxGrid = 160;  // CTAs that the workspace holds partial sums for
-WsLayout ws_layout(int64_t T, int64_t k, int64_t I) {
+WsLayout ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   WsLayout L;
   const int64_t n = T * k, tiles1 = ceil_div64(I, 64);
   int64_t o = round_up64((1 + 2 * kMaxGrid) * 4, 256);
+  L.xq = o, o += T * 2 * round_up64(H, 128);
+  L.xinv = o, o += round_up64(T * 4, 256);
   L.act = o, o += round_up64(n * I * 4, 256);
   L.amax = o, o += round_up64(n * 2 * tiles1 * 4, 256);
   L.part = o, o += kMaxGrid * 2 * T * kRows * 4;
@@ -735,18 +756,18 @@ WsLayout ws_layout(int64_t T, int64_t k, int64_t I) {
 }  // namespace
 
 int64_t moe_tokens_ws_bytes(int64_t T, int64_t k, int64_t H, int64_t I) {
-  (void)H;
-  return ws_layout(T, k, I).total;
+  return ws_layout(T, k, H, I).total;
 }
 
 int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, const void* w13, const float* s13,
                       const void* w2, const float* s2, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* out,
                       void* ws, const Ctx& c) {
   if (T == 0) return FP8_OK;
-  const WsLayout W = ws_layout(T, k, I);
+  const WsLayout W = ws_layout(T, k, H, I);
   uint8_t* base = static_cast<uint8_t*>(ws);
   MoeArgs a;
-  a.x = static_cast<const uint16_t*>(x);
+  a.xq = base + W.xq;
+  a.xinv = reinterpret_cast<const float*>(base + W.xinv);
   a.ids = ids;
   a.weights = weights;
   a.s13 = s13;
@@ -790,19 +811,24 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
     const int rc = make_tmap(&t2, w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc != FP8_OK) return rc;
   }
-  if (cudaMemsetAsync(ws, 0, (1 + 2 * (size_t)grid) * 4, c.stream) != cudaSuccess) return FP8_ERR_CUDA;
   if (cudaFuncSetAttribute(moe_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return FP8_ERR_CUDA;
+  moe_split_kernel<<<(unsigned)T, kSplitThreads, 0, c.stream>>>(
+      static_cast<const uint16_t*>(x), a.H, a.nk1 * 128, base + W.xq, reinterpret_cast<float*>(base + W.xinv), a.counters,
+      1 + 2 * grid);
+  if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs resident: they meet at the grid barrier
   attr[0].val.cooperative = 1;
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, moe_tokens_kernel, t13, t2, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
