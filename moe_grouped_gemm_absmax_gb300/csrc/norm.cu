@@ -9,6 +9,8 @@
 //
 // Everything between the loads and the stores is fp32: s is not rounded to bf16 on its way into
 // the statistics or into y, and y is rounded once, into each of its outputs.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -240,11 +242,15 @@ int launch_add_rmsnorm(const void* x, const void* res, const void* w, int w_f32,
 }
 
 // ==========================================================================================
-// Backward. A CTA walks rows with a grid stride; a thread owns VPT vectors of every row, so its
-// share of dw stays in registers from row to row and leaves once, as one of `parts` partial rows
-// in the workspace. A second kernel adds the partial rows in a fixed order: no atomics, the same
-// bits on every run.
+// Backward. Persistent CTAs walk groups of `rows` rows with a grid stride, a team of threads a row. A
+// group's inputs arrive by bulk copies into a ring in shared memory, several groups ahead, so memory
+// never waits for a row's reduction and its barrier. A thread owns VPT vectors of every row of its team,
+// so its share of dw stays in registers from row to row; a CTA's teams add theirs up at the end, and it
+// leaves as one of `grid` partial rows in the workspace. A second kernel adds the partial rows in a
+// fixed order: no atomics, the same bits on every run.
 namespace {
+
+constexpr int kBwdStages = 5;
 
 struct NormBwdArgs {
   const uint4* dy;
@@ -253,97 +259,159 @@ struct NormBwdArgs {
   int w_f32;
   const float* rstd;
   const uint4* dh;  // may be null
-  uint4* dx;
+  uint4* dx;        // may be null
   float* part;      // [grid][H], null without dw
   int64_t T;
   int nvec;
   float H;
+  int rows, stages;
+  uint64_t wait_ns;
 };
+
+FP8_DEVI void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 template <int VPT>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs p) {
+  extern __shared__ uint4 ring[];  // [stages][dy, h, dh][rows][nvec]
   __shared__ float red[2][16];
+  __shared__ uint64_t full[kBwdStages];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = threadIdx.x, team = blockDim.x;
-  float dw[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-  int par = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, par ^= 1) {
-    const float rstd = __ldg(p.rstd + row);
-    uint4 vdy[VPT], vh[VPT], vdh[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * team;
-      const bool in = c < p.nvec;
-      vdy[i] = in ? ld_stream(p.dy + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
-      vh[i] = in ? ld_stream(p.h + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
-      vdh[i] = p.dh && in ? ld_stream(p.dh + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
+  const int team_size = blockDim.x / p.rows, team = threadIdx.x / team_size, t = threadIdx.x % team_size;
+  const int team_warps = team_size / 32, warp0 = team * team_warps;
+  const int tensors = p.dh ? 3 : 2;
+  const int slab = p.rows * p.nvec;  // vectors of a tensor in a stage
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int64_t groups = ceil_div64(p.T, p.rows);
+  auto load = [&](int64_t g, int s) {
+    const int64_t row = g * p.rows;
+    const uint32_t bytes = (uint32_t)min((int64_t)p.rows, p.T - row) * (uint32_t)p.nvec * 16;
+    uint4* d = ring + s * tensors * slab;
+    mbar_arrive_expect_tx(&full[s], bytes * tensors);
+    bulk_load(d, p.dy + row * p.nvec, bytes, &full[s]);
+    bulk_load(d + slab, p.h + row * p.nvec, bytes, &full[s]);
+    if (p.dh) bulk_load(d + 2 * slab, p.dh + row * p.nvec, bytes, &full[s]);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < p.stages; ++s) {
+      const int64_t g = blockIdx.x + (int64_t)s * gridDim.x;
+      if (g < groups) load(g, s);
     }
+  float dw[VPT][8], w8[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = w8[i][j] = 0.f;
+    if (t + i * team_size < p.nvec) load_w(p.w, p.w_f32, t + i * team_size, w8[i]);
+  }
+  int s = 0, prev = 0, par = 0;
+  uint32_t phase = 0;
+  auto row_rstd = [&](int64_t g) {
+    const int64_t row = g * p.rows + team;
+    return row < p.T ? __ldg(p.rstd + row) : 0.f;
+  };
+  float rstd_next = row_rstd(blockIdx.x);
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x, par ^= 1) {
+    const int64_t row = g * p.rows + team;
+    const bool active = row < p.T;
+    float rstd = rstd_next;
+    rstd_next = row_rstd(g + gridDim.x);
+    // a wait that ran out would show as NaN in everything that the row reaches
+    if (!mbar_wait(&full[s], phase, nullptr, p.wait_ns)) rstd = __uint_as_float(0x7FC00000u);
+    const uint4* d = ring + s * tensors * slab + team * p.nvec;
     float sum = 0.f;
+    if (active) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * team;
-      float d8[8], h8[8], w8[8];
-      unpack8(vdy[i], d8);
-      unpack8(vh[i], h8);
+      for (int i = 0; i < VPT; ++i) {
+        const int c = t + i * team_size;
+        if (c >= p.nvec) continue;
+        float d8[8], h8[8];
+        unpack8(d[c], d8);
+        unpack8(d[slab + c], h8);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w8[j] = 0.f;
-      if (c < p.nvec) load_w(p.w, p.w_f32, c, w8);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xhat = h8[j] * rstd;
-        const float dyx = d8[j] * xhat;
-        dw[i][j] += dyx;
-        sum = fmaf(dyx, w8[j], sum);
+        for (int j = 0; j < 8; ++j) {
+          const float dyx = d8[j] * (h8[j] * rstd);
+          dw[i][j] += dyx;
+          sum = fmaf(dyx, w8[i][j], sum);
+        }
       }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) red[par][warp] = sum;  // two buffers: a row's values are read while the next row's are written
     __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < team / 32; ++w) sum += red[par][w];
-    const float mean = sum / p.H;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * team;
-      if (c >= p.nvec) continue;
-      float d8[8], h8[8], w8[8], g8[8];
-      unpack8(vdy[i], d8);
-      unpack8(vh[i], h8);
-      unpack8(vdh[i], g8);
-      load_w(p.w, p.w_f32, c, w8);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d8[j] = rstd * (d8[j] * w8[j] - h8[j] * rstd * mean) + g8[j];
-      if (p.dx) p.dx[row * p.nvec + c] = pack8(d8);
+    // every thread is done with the group before this one: its stage takes the group `stages` further on
+    if (threadIdx.x == 0 && g != blockIdx.x) {
+      const int64_t next = g + (int64_t)(p.stages - 1) * gridDim.x;
+      if (next < groups) load(next, prev);
     }
+    if (p.dx && active) {
+      sum = 0.f;
+      for (int w = 0; w < team_warps; ++w) sum += red[par][warp0 + w];
+      const float mean = sum / p.H;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = t + i * team_size;
+        if (c >= p.nvec) continue;
+        float d8[8], h8[8], g8[8];
+        unpack8(d[c], d8);
+        unpack8(d[slab + c], h8);
+        unpack8(p.dh ? d[2 * slab + c] : make_uint4(0, 0, 0, 0), g8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d8[j] = rstd * (d8[j] * w8[i][j] - h8[j] * rstd * mean) + g8[j];
+        p.dx[row * p.nvec + c] = pack8(d8);
+      }
+    }
+    prev = s;
+    if (++s == p.stages) s = 0, phase ^= 1;
   }
   if (p.part) {
+    float4* out = reinterpret_cast<float4*>(p.part) + (int64_t)blockIdx.x * p.nvec * 2;
+    float4* sh = reinterpret_cast<float4*>(ring);  // [rows][2 nvec], after the last group
+    if (p.rows > 1) __syncthreads();
+    if (p.rows > 1) out = sh + team * p.nvec * 2;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * team;
+      const int c = t + i * team_size;
       if (c >= p.nvec) continue;
-      float4* o = reinterpret_cast<float4*>(p.part) + ((int64_t)blockIdx.x * p.nvec + c) * 2;
-      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      out[2 * c] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+      out[2 * c + 1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
+    if (p.rows > 1) {
+      __syncthreads();
+      out = reinterpret_cast<float4*>(p.part) + (int64_t)blockIdx.x * p.nvec * 2;
+      for (int c = threadIdx.x; c < 2 * p.nvec; c += blockDim.x) {
+        float4 a = sh[c];
+        for (int r = 1; r < p.rows; ++r) {
+          const float4 v = sh[r * 2 * p.nvec + c];
+          a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+        }
+        out[c] = a;
+      }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // dw[c] = sum of `parts` partial rows: 32 float4 columns a CTA, the rows split over 16 thread rows
 // that are then added in order.
-__global__ void __launch_bounds__(512) dw_sum_kernel(const float4* __restrict__ part, int parts, int n4, void* dw,
-                                                     int dw_bf16) {
+__global__ void __launch_bounds__(512) dw_sum_kernel(const float4* part, int parts, int n4, void* dw, int dw_bf16) {
   __shared__ float4 sh[16][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x * 32 + threadIdx.x;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < n4) {
-#pragma unroll 4
+#pragma unroll 8
     for (int r = threadIdx.y; r < parts; r += 16) {
-      const float4 v = part[(int64_t)r * n4 + c];
+      const float4 v = __ldcg(part + (int64_t)r * n4 + c);
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
   }
@@ -360,22 +428,55 @@ __global__ void __launch_bounds__(512) dw_sum_kernel(const float4* __restrict__ 
     static_cast<float4*>(dw)[c] = a;
 }
 
+// Shape of the backward kernel for rows of nvec vectors: two vectors a thread up to 8192 columns, four
+// beyond; teams for several short rows, up to 512 threads a CTA; two CTAs an SM where each then has a ring of three
+// groups, else one with as many as fit (two for the widest rows).
+struct BwdShape {
+  int vpt, team, rows, ctas, stages;
+};
+BwdShape bwd_shape(int nvec, bool dh) {
+  constexpr int kRoom = 220 * 1024;
+  BwdShape b;
+  b.vpt = nvec <= 1024 ? 2 : 4;
+  b.team = (int)round_up64(ceil_div64(nvec, b.vpt), 32);
+  b.rows = 512 / b.team;
+  const int group = (dh ? 3 : 2) * b.rows * nvec * 16;
+  b.ctas = kRoom / 2 / group >= 3 ? 2 : 1;
+  const int fit = kRoom / b.ctas / group;
+  b.stages = fit < kBwdStages ? fit : kBwdStages;
+  return b;
+}
+constexpr int64_t kBwdSms = 152;
+int64_t bwd_grid(int64_t T, const BwdShape& b) {
+  const int64_t groups = ceil_div64(T, b.rows);
+  return groups < kBwdSms * b.ctas ? groups : kBwdSms * b.ctas;
+}
+
 template <int VPT>
-int run_norm_bwd(const NormBwdArgs& a, int grid, const Ctx& c) {
-  rmsnorm_bwd_kernel<VPT><<<grid, (int)round_up64(ceil_div64(a.nvec, VPT), 32), 0, c.stream>>>(a);
+int run_norm_bwd(const NormBwdArgs& a, const BwdShape& b, int grid, const Ctx& c) {
+  const size_t smem = (size_t)b.stages * (a.dh ? 3 : 2) * b.rows * a.nvec * 16;
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(rmsnorm_bwd_kernel<VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+      return FP8_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  rmsnorm_bwd_kernel<VPT><<<grid, b.team * b.rows, smem, c.stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
-constexpr int64_t kBwdParts = 304;  // partial rows of dw at most: two CTAs on each of 152 SMs
-
 }  // namespace
 
-int64_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t H) { return (T < kBwdParts ? T : kBwdParts) * H * 4; }
+int64_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t H) {
+  // without dh the ring is shorter and more CTAs may fit: room for those
+  return bwd_grid(T, bwd_shape((int)(H / 8), false)) * H * 4;
+}
 
 int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, const float* rstd, const void* dh,
                        int64_t T, int64_t H, void* dx, void* dw, int dw_bf16, float* ws, const Ctx& c) {
-  if (H == 0) return FP8_OK;
-  const int64_t grid = T < kBwdParts ? T : kBwdParts;
+  const BwdShape b = bwd_shape((int)(H / 8), dh != nullptr);
+  const int64_t grid = bwd_grid(T, b);
   if (grid > 0) {
     NormBwdArgs a;
     a.dy = static_cast<const uint4*>(dy);
@@ -389,16 +490,29 @@ int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, 
     a.T = T;
     a.nvec = (int)(H / 8);
     a.H = (float)H;
-    const int rc = a.nvec <= 1024 ? run_norm_bwd<2>(a, (int)grid, c) : run_norm_bwd<4>(a, (int)grid, c);
+    a.rows = b.rows;
+    a.stages = b.stages;
+    a.wait_ns = c.wait_ns;
+    const int rc = b.vpt == 2 ? run_norm_bwd<2>(a, b, (int)grid, c) : run_norm_bwd<4>(a, b, (int)grid, c);
     if (rc != FP8_OK) return rc;
   }
-  if (dw) {  // no rows: an empty sum
-    const int n4 = (int)(H / 4);
-    dw_sum_kernel<<<(unsigned)ceil_div64(n4, 32), dim3(32, 16), 0, c.stream>>>(reinterpret_cast<const float4*>(ws),
-                                                                              (int)grid, n4, dw, dw_bf16);
-    if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
-  }
-  return FP8_OK;
+  if (!dw) return FP8_OK;
+  if (grid == 0)  // no rows: an empty sum
+    return cudaMemsetAsync(dw, 0, (size_t)H * (dw_bf16 ? 2 : 4), c.stream) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  const int n4 = (int)(H / 4);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)ceil_div64(n4, 32));
+  cfg.blockDim = dim3(32, 16);
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dw_sum_kernel, static_cast<const float4*>(static_cast<const void*>(ws)), (int)grid, n4,
+                            dw, dw_bf16) == cudaSuccess
+             ? FP8_OK
+             : FP8_ERR_CUDA;
 }
 
 }  // namespace fp8lin

@@ -5,6 +5,9 @@
 //   sel[e] = logit[e] + bias[e] decides the k experts (ties: the lowest index; -inf and NaN are
 //   never taken); v[e] = softmax(logits)[e] or sigmoid(logit[e]); w_j = scale * v[e_j], or with
 //   renormalization scale * v[e_j] / sum_i v[e_i].
+//
+// Up to 64 tokens one CTA chooses, counts and places; more take two launches, the second started while
+// the first runs (programmatic dependent launch).
 #include "common.cuh"
 #include "internal.h"
 
@@ -12,7 +15,7 @@ namespace fp8lin {
 
 namespace {
 
-constexpr int kRouteWarps = 8;
+constexpr int kBwdWarps = 8;
 
 FP8_DEVI float load_logit(const void* p, int bf16, int64_t i) {
   return bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16)
@@ -57,12 +60,15 @@ struct RouteArgs {
   int32_t* order;  // the table's outputs: all or none
   int32_t* pos;
   int32_t* ends;
-  int32_t* hist;       // workspace [chunks][E]: slots of each chunk of tokens by expert, then their places
+  uint16_t* hist;      // workspace [chunks][E2]: slots of each chunk of tokens by expert
+  int E2;              // E rounded up to even
   int64_t per_chunk;   // tokens of a chunk (one CTA's)
   int chunks;
 };
 
-// A warp per token: lane l holds experts l + 32 i.
+// A warp per token: lane l holds experts l + 32 i. Each step takes the largest key left: the lanes'
+// maxima meet in one warp reduction, a second one settles ties by the lowest expert, and the lane that
+// holds it drops it.
 template <int VPL>
 FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, int32_t* hist) {
   float v[VPL];
@@ -71,29 +77,32 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, int32_t* hist
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
     v[i] = e < p.E ? load_logit(p.logits, p.bf16, t * p.E + e) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
     key[i] = e < p.E ? order_key(p.bias ? v[i] + __ldg(p.bias + e) : v[i]) : 0u;
   }
-  int my_id = -1;
-  float my_v = 0.f;  // lane j: the j-th expert taken and its logit
+  int my_id = -1;  // lane j: the j-th expert taken
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0;
-    int at = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] > best) best = key[i], at = i;
+    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     if (top <= kKeyMasked) break;  // nothing left that may be taken
-    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
-    float val = 0.f;
+    uint32_t mine = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if ((int)e == lane + 32 * i) {
-        key[i] = 0;
-        val = v[i];
-      }
-    val = __shfl_sync(0xffffffffu, val, e & 31);
-    if (lane == j) my_id = (int)e, my_v = val;
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == top) mine = (uint32_t)(lane + 32 * i);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
+    if (e == mine) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if ((int)e == lane + 32 * i) key[i] = 0;
+    }
+    if (lane == j) my_id = (int)e;
   }
+  const float my_v = my_id >= 0 ? load_logit(p.logits, p.bf16, t * p.E + my_id) : 0.f;
   float w = 0.f;
   if (p.softmax) {
     if (p.renorm) {  // softmax over the experts taken
@@ -122,76 +131,41 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, int32_t* hist
   }
 }
 
-template <int VPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs p) {
-  extern __shared__ int32_t hist[];
+// Exclusive sums over the CTA's threads (blockDim.x of them, a multiple of 32).
+FP8_DEVI int block_scan(int x, int32_t* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (p.order)
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
-  __syncthreads();
-  const int64_t t0 = blockIdx.x * p.per_chunk;
-  const int64_t t1 = t0 + p.per_chunk < p.T ? t0 + p.per_chunk : p.T;
-  for (int64_t t = t0 + warp; t < t1; t += kRouteWarps) route_token<VPL>(p, t, lane, p.order ? hist : nullptr);
-  if (!p.order) return;
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(int64_t)blockIdx.x * p.E + e] = hist[e];
-}
-
-// The places where each chunk's slots of each expert begin, and the experts' ends. One CTA, a
-// thread per expert.
-__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs p) {
-  __shared__ int32_t wsum[32];
-  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
-  int n = 0;
-  if (e < p.E)
-    for (int c = 0; c < p.chunks; ++c) n += p.hist[(int64_t)c * p.E + e];
-  int x = n;
+  int s = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  if (lane == 31) wsum[warp] = x;
+  if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    int s = lane < (int)blockDim.x / 32 ? wsum[lane] : 0;
+    int w = lane < (int)blockDim.x / 32 ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
     }
-    wsum[lane] = s;
+    warp_sums[lane] = w;
   }
   __syncthreads();
-  const int end = x + (warp ? wsum[warp - 1] : 0);
-  if (e >= p.E) return;
-  p.ends[e] = end;
-  int at = end - n;
-  for (int c = 0; c < p.chunks; ++c) {
-    int32_t* h = p.hist + (int64_t)c * p.E + e;
-    const int m = *h;
-    *h = at;
-    at += m;
-  }
+  return s - x + (warp ? warp_sums[warp - 1] : 0);
 }
 
-// Each slot's place: its chunk's place of its expert plus the slots of that expert before it in the
-// chunk, counted by one warp in slot order.
-__global__ void __launch_bounds__(32 * kRouteWarps) route_place_kernel(const RouteArgs p) {
-  extern __shared__ int32_t at[];
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) at[e] = p.hist[(int64_t)blockIdx.x * p.E + e];
-  __syncthreads();
-  const int64_t n = p.T * p.k;
-  const int64_t valid = p.ends[p.E - 1];
-  for (int64_t i = valid + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
-    p.order[i] = -1;
-  if (threadIdx.x >= 32) return;
+// Each slot's place: `at` holds the chunk's first place of each expert; the slots are counted in slot
+// order by one warp.
+FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at) {
   const int lane = threadIdx.x;
-  const int64_t s0 = blockIdx.x * p.per_chunk * p.k;
-  const int64_t s1 = s0 + p.per_chunk * p.k < n ? s0 + p.per_chunk * p.k : n;
+  const int64_t n = p.T * p.k, len = p.per_chunk * p.k;
+  const int64_t s0 = chunk * len, s1 = s0 + len < n ? s0 + len : n;
+  int next = s0 + lane < s1 ? p.ids[s0 + lane] : -1;
   for (int64_t b = s0; b < s1; b += 32) {
     const int64_t s = b + lane;
-    const int id = s < s1 ? p.ids[s] : -1;
+    const int id = next;
+    next = s + 32 < s1 ? p.ids[s + 32] : -1;
     const uint32_t same = __match_any_sync(0xffffffffu, id);
     const int before = __popc(same & ((1u << lane) - 1));
     int32_t place = -1;
@@ -204,6 +178,92 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_place_kernel(const Rou
       if (id >= 0) p.order[place] = (int32_t)s;
     }
   }
+}
+// Unused slots leave the end of `order` without a slot.
+FP8_DEVI void fill_order(const RouteArgs& p, int64_t valid) {
+  for (int64_t i = valid + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.T * p.k;
+       i += (int64_t)gridDim.x * blockDim.x)
+    p.order[i] = -1;
+}
+
+// The choice for a chunk of tokens, and the chunk's slots of each expert; with one chunk the table too.
+template <int VPL, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
+  extern __shared__ int32_t hist[];
+  __shared__ int32_t warp_sums[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (p.order) {
+    for (int e = threadIdx.x; e < p.E2; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
+  const int64_t t0 = blockIdx.x * p.per_chunk;
+  const int64_t t1 = t0 + p.per_chunk < p.T ? t0 + p.per_chunk : p.T;
+  for (int64_t t = t0 + warp; t < t1; t += WARPS) route_token<VPL>(p, t, lane, p.order ? hist : nullptr);
+  if (!p.order) return;
+  __syncthreads();
+  if (p.chunks > 1) {
+    for (int e = threadIdx.x; e < p.E2; e += blockDim.x) p.hist[(int64_t)blockIdx.x * p.E2 + e] = (uint16_t)hist[e];
+    return;
+  }
+  int before = 0;
+  for (int b = 0; b < p.E; b += blockDim.x) {
+    const int e = b + threadIdx.x;
+    const int n = e < p.E ? hist[e] : 0;
+    const int start = before + block_scan(n, warp_sums);
+    before += warp_sums[blockDim.x / 32 - 1];
+    if (e < p.E) {
+      p.ends[e] = start + n;
+      hist[e] = start;
+    }
+    __syncthreads();
+  }
+  fill_order(p, before);
+  if (warp == 0) place_chunk(p, 0, hist);
+}
+
+// The table from the chunks' counts. Each CTA sums the whole matrix of counts (16 bits each, 78 KB for 152
+// chunks and 256 experts, from L2) into its own first places, so that no launch is spent on a scan.
+constexpr int kPlaceThreads = 1024;
+__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs p) {
+  extern __shared__ int32_t sh[];  // [E2] slots, [E2] slots in the chunks before this one
+  __shared__ int32_t warp_sums[32];
+  int32_t* total = sh;
+  int32_t* prior = sh + p.E2;
+  for (int e = threadIdx.x; e < 2 * p.E2; e += kPlaceThreads) sh[e] = 0;
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int pairs = p.E2 / 2;
+  const int lanes = pairs < kPlaceThreads ? pairs : kPlaceThreads;  // threads on a row of counts
+  const int split = kPlaceThreads / lanes;
+  const int grp = threadIdx.x / lanes;
+  if (grp < split) {
+    const uint32_t* h = reinterpret_cast<const uint32_t*>(p.hist);
+    const int x = threadIdx.x % lanes;
+    int a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+#pragma unroll 8
+    for (int c = grp; c < p.chunks; c += split) {
+      const uint32_t v = __ldcg(h + (int64_t)c * pairs + x);
+      const int lo = v & 0xFFFF, hi = v >> 16;
+      a0 += lo, a1 += hi;
+      if (c < (int)blockIdx.x) b0 += lo, b1 += hi;
+    }
+    atomicAdd(total + 2 * x, a0), atomicAdd(total + 2 * x + 1, a1);
+    atomicAdd(prior + 2 * x, b0), atomicAdd(prior + 2 * x + 1, b1);
+  }
+  __syncthreads();
+  // E <= kPlaceThreads: an expert a thread
+  const int e = threadIdx.x;
+  const int n = e < p.E ? total[e] : 0;
+  const int start = block_scan(n, warp_sums);
+  if (e < p.E) {
+    if (blockIdx.x == 0) p.ends[e] = start + n;
+    prior[e] += start;
+  }
+  const int64_t valid = warp_sums[31];
+  __syncthreads();
+  fill_order(p, valid);
+  if (threadIdx.x < 32) place_chunk(p, blockIdx.x, prior);
 }
 
 // Gradient of the logits, a warp per token. With g_j = scale * dweights_j:
@@ -225,9 +285,9 @@ struct RouteBwdArgs {
 };
 
 template <int VPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const RouteBwdArgs p) {
+__global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBwdArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  const int64_t t = (int64_t)blockIdx.x * kBwdWarps + warp;
   if (t >= p.T) return;
   int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
   float g = lane < p.k ? p.dw[t * p.k + lane] * p.scale : 0.f;
@@ -239,7 +299,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const Route
   const float l = id >= 0 ? load_logit(p.logits, p.bf16, t * p.E + id) : 0.f;
   float d = 0.f;
   float v[VPL];
-  float base = 0.f;
+  float base = 0.f, pe = 0.f;
   if (p.softmax && !p.renorm) {
     float m = -INFINITY, z = 0.f;
 #pragma unroll
@@ -258,7 +318,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const Route
     z = warp_sum(z);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = none ? 0.f : v[i] / z;
-    d = id >= 0 && !none ? g * (expf(l - m) / z) : 0.f;
+    pe = id >= 0 && !none ? expf(l - m) / z : 0.f;
+    d = g * pe;
     base = -warp_sum(d);
   } else if (p.softmax) {
     const float m = warp_max(id >= 0 ? l : -INFINITY);
@@ -286,27 +347,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const Route
     const float dj = __shfl_sync(0xffffffffu, d, j);
     if (idj == id) all += dj;
   }
-  if (p.softmax && !p.renorm) {
-    float pe = 0.f;
-    for (int j = 0; j < p.k; ++j) {  // the expert's probability, from the lane that holds it
-      const int idj = __shfl_sync(0xffffffffu, id, j);
-      float mine = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (idj == lane + 32 * i) mine = v[i];
-      const float got = __shfl_sync(0xffffffffu, mine, idj & 31);
-      if (lane == j) pe = got;
-    }
-    all += base * pe;
-  }
+  all += base * pe;
   __syncwarp();  // the row's stores above come first
   if (id >= 0) store_logit(p.dlogits, p.bf16, t * p.E + id, all);
 }
 
-constexpr int64_t kRouteChunks = 304;
+// Chunks of tokens: one CTA does it all for as many tokens as its warps have twice over; else a chunk
+// for each of 152 SMs, and not above what 16-bit counts hold.
 int64_t chunk_tokens(int64_t T) {
-  const int64_t n = ceil_div64(T, kRouteChunks);
-  return round_up64(n < 1 ? 1 : n, kRouteWarps);
+  if (T <= 64) return T < 1 ? 1 : T;
+  const int64_t n = round_up64(ceil_div64(T, 152), 8);
+  return n < 65528 ? n : 65528;
 }
 
 #define FP8_BY_EXPERTS(E, CALL)      \
@@ -321,7 +372,7 @@ int64_t chunk_tokens(int64_t T) {
 
 }  // namespace
 
-int64_t route_ws_bytes(int64_t T, int64_t E) { return ceil_div64(T, chunk_tokens(T)) * E * 4; }
+int64_t route_ws_bytes(int64_t T, int64_t E) { return round_up64(ceil_div64(T, chunk_tokens(T)) * round_up64(E, 2) * 2, 16); }
 
 int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int64_t E, int64_t k, int softmax,
                  int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,
@@ -331,25 +382,34 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
     return FP8_OK;
   }
   RouteArgs a = {logits, bf16, bias, T,    (int)E, (int)k, softmax, renorm, scale, ids, weights,
-                 order,  pos,  ends, static_cast<int32_t*>(ws), chunk_tokens(T), 0};
+                 order,  pos,  ends, static_cast<uint16_t*>(ws), (int)round_up64(E, 2), chunk_tokens(T), 0};
   a.chunks = (int)ceil_div64(T, a.per_chunk);
-  const size_t smem = (size_t)E * 4;
-#define FP8_ROUTE(V) route_kernel<V><<<(unsigned)a.chunks, 32 * kRouteWarps, smem, c.stream>>>(a)
+  // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers
+#define FP8_ROUTE(V) \
+  route_kernel<V, (V <= 8 ? 32 : 16)><<<(unsigned)a.chunks, V <= 8 ? 1024 : 512, (size_t)a.E2 * 4, c.stream>>>(a)
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
-  if (order) {
-    route_scan_kernel<<<1, (unsigned)round_up64(E, 32), 0, c.stream>>>(a);
-    route_place_kernel<<<(unsigned)a.chunks, 32 * kRouteWarps, smem, c.stream>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
+  if (!order || a.chunks == 1) return FP8_OK;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)a.chunks);
+  cfg.blockDim = dim3(kPlaceThreads);
+  cfg.dynamicSmemBytes = (size_t)a.E2 * 8;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, route_place_kernel, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
 int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const float* dw, int64_t T, int64_t E,
                      int64_t k, int softmax, int renorm, float scale, void* dlogits, const Ctx& c) {
   if (T == 0) return FP8_OK;
   const RouteBwdArgs a = {logits, bf16, ids, dw, dlogits, T, (int)E, (int)k, softmax, renorm, scale, c.status};
-  const unsigned grid = (unsigned)ceil_div64(T, kRouteWarps);
-#define FP8_ROUTE(V) route_bwd_kernel<V><<<grid, 32 * kRouteWarps, 0, c.stream>>>(a)
+  const unsigned grid = (unsigned)ceil_div64(T, kBwdWarps);
+#define FP8_ROUTE(V) route_bwd_kernel<V><<<grid, 32 * kBwdWarps, 0, c.stream>>>(a)
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
   return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
