@@ -358,8 +358,8 @@ int fp8_linear_bwd(const fp8_tensor* dy, const fp8_linear_saved* saved, const fp
  *  h           bf16 [T, H] or NULL: s rounded once (the residual stream's new value). The norm takes
  *              the unrounded s.
  *  y           bf16 [T, H] or NULL: y rounded once.
- *  q           FP8 (E4M3 or E5M2) [T, H] or NULL: y quantized from its fp32 value by the recipe [Q] with
- *              fp32 divisions; inv_scales, given with q, by granularity as for fp8_quantize ROW_MAJOR:
+ *  q           FP8 (E4M3 or E5M2) [T, H] or NULL: y quantized from its fp32 value by the recipe [Q] in
+ *              fp32 (scale and inverse to 4 units in the last place); inv_scales, given with q, by granularity as for fp8_quantize ROW_MAJOR:
  *              FP8_GRAN_ROW fp32 [T]; FP8_GRAN_BLOCK_1x128 fp32 [T, H / 128] (H % 128 == 0);
  *              FP8_GRAN_MX E8M0 [fp8_mx_scale_bytes(T, H)] (H % 128 == 0). Other granularities:
  *              FP8_ERR_UNSUPPORTED. amax is that of the unrounded y, so the codes are those of y in

@@ -18,17 +18,43 @@ namespace fp8lin {
 
 namespace {
 
-FP8_DEVI float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
-FP8_DEVI float bf_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-FP8_DEVI uint32_t pack_bf16(float lo, float hi) {
+// Two fp32 operations in one instruction, each rounded as the scalar one. The kernels here move 7 to 8
+// bytes an element and run into the issue rate before the memory's with scalar arithmetic (221
+// instructions for 8 elements forward, 266 backward, at 2.5-2.9 of 4 a cycle), so all of it is paired.
+FP8_DEVI float2 fadd2_rn(float2 a, float2 b) {
+  uint64_t ra, rb, rd;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
+}
+FP8_DEVI float2 ffma2_rn(float2 a, float2 b, float2 c) {
+  uint64_t ra, rb, rc, rd;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rc) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rd) : "l"(ra), "l"(rb), "l"(rc));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
+}
+FP8_DEVI float2 both(float v) { return make_float2(v, v); }
+FP8_DEVI uint32_t pack_bf16(float2 v) {
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
   return r;
 }
-// max that keeps a NaN, so that a NaN reaches the scale as it does in fp8_quantize
+// Maxima that keep a NaN, so that a NaN reaches the scale as it does in fp8_quantize.
 FP8_DEVI float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+FP8_DEVI float absmax3_nan(float m, float2 v) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(v.x), "f"(v.y));
   return r;
 }
 // 16 bytes through L2 only: each row is read once. Not ld.nc: an output may be one of the inputs.
@@ -41,21 +67,47 @@ FP8_DEVI uint4 ld_stream(const uint4* p) {
   return r;
 }
 
-FP8_DEVI void unpack8(uint4 v, float* f) {
-  f[0] = bf_lo(v.x), f[1] = bf_hi(v.x), f[2] = bf_lo(v.y), f[3] = bf_hi(v.y);
-  f[4] = bf_lo(v.z), f[5] = bf_hi(v.z), f[6] = bf_lo(v.w), f[7] = bf_hi(v.w);
+FP8_DEVI float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+FP8_DEVI uint32_t word(uint4 v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+// 8 elements as 4 pairs
+FP8_DEVI void unpack8(uint4 v, float2* f) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = unpack2(word(v, j));
 }
-FP8_DEVI uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+FP8_DEVI uint4 pack8(const float2* f) {
+  return make_uint4(pack_bf16(f[0]), pack_bf16(f[1]), pack_bf16(f[2]), pack_bf16(f[3]));
 }
 // 8 weights from bf16 or fp32
-FP8_DEVI void load_w(const void* w, int w_f32, int c, float* f) {
+FP8_DEVI void load_w(const void* w, int w_f32, int c, float2* f) {
   if (w_f32) {
     const float4 a = __ldg(static_cast<const float4*>(w) + 2 * c), b = __ldg(static_cast<const float4*>(w) + 2 * c + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
   } else {
     unpack8(__ldg(static_cast<const uint4*>(w) + c), f);
   }
+}
+
+// A team's values from its warps, 32 slots; the slots past its warps hold zeros. Written by the team's first warp
+// and by each warp's lane 0, before the barrier.
+FP8_DEVI void team_put(float* slots, int t, int warps, float v) {
+  if ((t & 31) == 0) slots[t >> 5] = v;
+  if (t < 32 && t >= warps) slots[t] = 0.f;
+}
+FP8_DEVI float team_sum(const float* slots, int warps) {
+  float4 a = *reinterpret_cast<const float4*>(slots);
+  for (int i = 4; i < warps; i += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(slots + i);
+    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+  }
+  return (a.x + a.y) + (a.z + a.w);
+}
+FP8_DEVI float team_max(const float* slots, int warps) {
+  float m = 0.f;
+  for (int i = 0; i < warps; i += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(slots + i);
+    m = absmax3_nan(absmax3_nan(m, make_float2(b.x, b.y)), make_float2(b.z, b.w));
+  }
+  return m;
 }
 
 struct NormArgs {
@@ -64,7 +116,7 @@ struct NormArgs {
   const void* w;
   int w_f32;
   float eps;
-  float H;
+  float inv_H;
   int64_t T;
   int nvec;          // 16-byte vectors of a row
   uint4* h;          // the outputs may be null
@@ -76,135 +128,147 @@ struct NormArgs {
 
 constexpr int kNone = -1;  // no 8-bit output
 
-// One row per team: one warp (WARP; eight rows a CTA, no barrier), or the whole CTA. A thread holds
-// VPT vectors of its row, vector t + i * team, as fp32 sums. The sum of squares and the largest
-// |s * w| are reduced together, behind one barrier: y = (s * w) * rstd, and rounding keeps order,
-// so rstd * max |s * w| is the largest |y| exactly and the scale needs no second pass.
+// ------------------------------------------------------------------------------------------
+// Forward, 8 elements at a time. y = (s * w) * rstd, and rounding keeps order, so rstd times the largest
+// |s * w| is the largest |y| exactly: both reductions of a row meet at one barrier.
+
+// s = x + r, its part of the sum of squares, then s * w in its place; returns the largest |s * w|
+FP8_DEVI float norm_in(uint4 x, uint4 r, bool has_r, const float2* w, uint4* h, float2* s, float2* sum) {
+  unpack8(x, s);
+  if (has_r) {
+    float2 r8[4];
+    unpack8(r, r8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = fadd2_rn(s[j], r8[j]);
+  }
+  if (h) *h = pack8(s);
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    *sum = ffma2_rn(s[j], s[j], *sum);
+    s[j] = fmul2_rn(s[j], w[j]);
+    m = absmax3_nan(m, s[j]);
+  }
+  return m;
+}
+// the block's maximum: 16 (128 elements) or 4 (32 elements) consecutive lanes' vectors
+template <int GRAN>
+FP8_DEVI float block_max(float m) {
+#pragma unroll
+  for (int o = 1; o < (GRAN == FP8_GRAN_MX ? 4 : 16); o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+FP8_DEVI float amax_floor(float a) { return a < 1e-12f ? 1e-12f : a; }  // a NaN stays
+// y and its codes of vector c of a row; f: rstd times the row's scale, with row scales
+template <int GRAN, int FMT>
+FP8_DEVI void norm_out(const NormArgs& p, int64_t row, int c, const float2* s, float rstd, float f, float bm) {
+  constexpr float FMAX = FmtMax<FMT>::v;
+  if (p.y) {
+    float2 y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = fmul2_rn(s[j], both(rstd));
+    p.y[row * p.nvec + c] = pack8(y);
+  }
+  if (GRAN == kNone) return;
+  if (GRAN == FP8_GRAN_BLOCK_1x128) {
+    const float a = amax_floor(bm * rstd);
+    f = rstd * __fdividef(FMAX, a);
+    if ((c & 15) == 0) static_cast<float*>(p.inv)[row * (p.nvec / 16) + c / 16] = a * (1.0f / FMAX);
+  }
+  if (GRAN == FP8_GRAN_MX) {
+    // the block's exponent field, as the rule takes it from a bf16 amax, here from the fp32 one
+    const uint32_t code = mx_code<FMT>(__float_as_uint(bm * rstd) >> 16);
+    const int j = c / 4;  // block of 32 along the row
+    if ((c & 3) == 0)
+      static_cast<uint8_t*>(p.inv)[((row >> 7) * (p.nvec / 16) + (j >> 2)) * 512 + (row & 31) * 16 +
+                                   ((row >> 5) & 3) * 4 + (j & 3)] = (uint8_t)code;
+    f = rstd * mx_inv(code);
+  }
+  float2 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = fmul2_rn(s[j], both(f));
+  uint2 o;
+  o.x = cvt_fp8x2<FMT>(v[0].x, v[0].y) | (cvt_fp8x2<FMT>(v[1].x, v[1].y) << 16);
+  o.y = cvt_fp8x2<FMT>(v[2].x, v[2].y) | (cvt_fp8x2<FMT>(v[3].x, v[3].y) << 16);
+  p.q[row * p.nvec + c] = o;
+}
+
+// One row per team: one warp (WARP; eight rows a CTA, no barrier) or the whole CTA, VPT vectors a thread.
+// A CTA ends with its row: while some of an SM's CTAs reduce or store, others load. Persistent CTAs that
+// asked for the next row ahead had fewer warps an SM and took 43 us instead of 40 for 8192 x 4096; one that
+// took rows through shared memory 53 us.
 template <int VPT, int GRAN, int FMT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const NormArgs p) {
   constexpr float FMAX = FmtMax<FMT>::v;
-  __shared__ float red_s[16], red_m[16];
+  __shared__ __align__(16) float red_s[32], red_m[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
   const int t = WARP ? lane : threadIdx.x;
   const int team = WARP ? 32 : blockDim.x;
   if (WARP && row >= p.T) return;
-  const uint4* xr = p.x + row * p.nvec;
-  const uint4* rr = p.res ? p.res + row * p.nvec : nullptr;
-
   uint4 vx[VPT], vr[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = t + i * team;
-    vx[i] = c < p.nvec ? ld_stream(xr + c) : make_uint4(0, 0, 0, 0);
-    vr[i] = rr && c < p.nvec ? ld_stream(rr + c) : make_uint4(0, 0, 0, 0);
+    vx[i] = c < p.nvec ? ld_stream(p.x + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
+    vr[i] = p.res && c < p.nvec ? ld_stream(p.res + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
   }
-  float s[VPT][8];
-  float sum = 0.f, mx = 0.f;
+  float2 s[VPT][4];
+  float2 sum2 = both(0.f);
+  float mx = 0.f;
   float bm[VPT];  // block scales: the block's largest |s * w|
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = t + i * team;
-    float r8[8], w8[8];
-    unpack8(vx[i], s[i]);
-    if (rr) {
-      unpack8(vr[i], r8);
+    float2 w8[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] += r8[j];
-    }
-    if (p.h && c < p.nvec) p.h[row * p.nvec + c] = pack8(s[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w8[j] = 0.f;
+    for (int j = 0; j < 4; ++j) w8[j] = both(0.f);
     if (c < p.nvec) load_w(p.w, p.w_f32, c, w8);
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sum = fmaf(s[i][j], s[i][j], sum);
-      s[i][j] *= w8[j];
-      m = max_nan(m, fabsf(s[i][j]));
-    }
+    const float m = norm_in(vx[i], vr[i], p.res != nullptr, w8, p.h && c < p.nvec ? p.h + row * p.nvec + c : nullptr,
+                            s[i], &sum2);
     if (GRAN == FP8_GRAN_ROW) mx = max_nan(mx, m);
-    if (GRAN == FP8_GRAN_BLOCK_1x128 || GRAN == FP8_GRAN_MX) {
-      // a block is 16 (128 elements) or 4 (32 elements) consecutive lanes' vectors
-#pragma unroll
-      for (int o = 1; o < (GRAN == FP8_GRAN_MX ? 4 : 16); o <<= 1)
-        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      bm[i] = m;
-    }
+    if (GRAN == FP8_GRAN_BLOCK_1x128 || GRAN == FP8_GRAN_MX) bm[i] = block_max<GRAN>(m);
   }
+  float sum = sum2.x + sum2.y;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (GRAN == FP8_GRAN_ROW) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
   if (!WARP) {
-    if (lane == 0) {
-      red_s[warp] = sum;
-      red_m[warp] = mx;
-    }
+    team_put(red_s, t, team / 32, sum);
+    if (GRAN == FP8_GRAN_ROW) team_put(red_m, t, team / 32, mx);
     __syncthreads();
-    sum = 0.f;
-    mx = 0.f;
-    for (int w = 0; w < team / 32; ++w) {
-      sum += red_s[w];
-      if (GRAN == FP8_GRAN_ROW) mx = max_nan(mx, red_m[w]);
-    }
+    sum = team_sum(red_s, team / 32);
+    if (GRAN == FP8_GRAN_ROW) mx = team_max(red_m, team / 32);
   }
-  const float rstd = 1.0f / sqrtf(sum / p.H + p.eps);
+  const float rstd = rsqrtf(fmaf(sum, p.inv_H, p.eps));
   if (p.rstd && t == 0) p.rstd[row] = rstd;
-  float scale = 1.f;
+  float f = 1.f;
   if (GRAN == FP8_GRAN_ROW) {
-    float a = mx * rstd;
-    a = a < 1e-12f ? 1e-12f : a;  // a NaN stays
-    scale = FMAX / a;
-    if (t == 0) static_cast<float*>(p.inv)[row] = a / FMAX;
+    const float a = amax_floor(mx * rstd);
+    f = rstd * __fdividef(FMAX, a);
+    if (t == 0) static_cast<float*>(p.inv)[row] = a * (1.0f / FMAX);
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = t + i * team;
-    if (c >= p.nvec) continue;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[i][j] *= rstd;
-    if (p.y) p.y[row * p.nvec + c] = pack8(s[i]);
-    if (GRAN == kNone) continue;
-    if (GRAN == FP8_GRAN_BLOCK_1x128) {
-      float a = bm[i] * rstd;
-      a = a < 1e-12f ? 1e-12f : a;
-      scale = FMAX / a;
-      if ((t & 15) == 0) static_cast<float*>(p.inv)[row * (p.nvec / 16) + c / 16] = a / FMAX;
-    }
-    if (GRAN == FP8_GRAN_MX) {
-      // the block's exponent field, as the rule takes it from a bf16 amax, here from the fp32 one
-      const uint32_t code = mx_code<FMT>(__float_as_uint(bm[i] * rstd) >> 16);
-      scale = mx_inv(code);
-      const int j = c / 4;  // block of 32 along the row
-      if ((t & 3) == 0)
-        static_cast<uint8_t*>(p.inv)[((row >> 7) * (p.nvec / 16) + (j >> 2)) * 512 + (row & 31) * 16 +
-                                     ((row >> 5) & 3) * 4 + (j & 3)] = (uint8_t)code;
-    }
-    uint2 o;
-    o.x = cvt_fp8x2<FMT>(s[i][0] * scale, s[i][1] * scale) | (cvt_fp8x2<FMT>(s[i][2] * scale, s[i][3] * scale) << 16);
-    o.y = cvt_fp8x2<FMT>(s[i][4] * scale, s[i][5] * scale) | (cvt_fp8x2<FMT>(s[i][6] * scale, s[i][7] * scale) << 16);
-    p.q[row * p.nvec + c] = o;
+    if (c < p.nvec) norm_out<GRAN, FMT>(p, row, c, s[i], rstd, f, bm[i]);
   }
 }
 
-template <int VPT, int GRAN, int FMT>
-int run_norm(const NormArgs& a, const Ctx& c) {
-  if (a.nvec <= 32 * VPT) {
-    add_rmsnorm_kernel<VPT, GRAN, FMT, true><<<(unsigned)ceil_div64(a.T, 8), 256, 0, c.stream>>>(a);
-  } else {
-    const int team = (int)round_up64(ceil_div64(a.nvec, VPT), 32);
-    add_rmsnorm_kernel<VPT, GRAN, FMT, false><<<(unsigned)a.T, team, 0, c.stream>>>(a);
-  }
+template <int VPT, int GRAN, int FMT, bool WARP>
+int run_norm(const NormArgs& a, int threads, const Ctx& c) {
+  add_rmsnorm_kernel<VPT, GRAN, FMT, WARP><<<(unsigned)ceil_div64(a.T, WARP ? 8 : 1), threads, 0, c.stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
 template <int GRAN, int FMT>
 int norm_dispatch(const NormArgs& a, const Ctx& c) {
   // two vectors a thread while a CTA of 512 threads covers the row, four for the widest rows
-  if (a.nvec <= 1024) return run_norm<2, GRAN, FMT>(a, c);
-  return run_norm<4, GRAN, FMT>(a, c);
+  if (a.nvec <= 64) return run_norm<2, GRAN, FMT, true>(a, 256, c);
+  if (a.nvec <= 1024) return run_norm<2, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 2), 32), c);
+  return run_norm<4, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 4), 32), c);
 }
 
 }  // namespace
@@ -218,7 +282,7 @@ int launch_add_rmsnorm(const void* x, const void* res, const void* w, int w_f32,
   a.w = w;
   a.w_f32 = w_f32;
   a.eps = eps;
-  a.H = (float)H;
+  a.inv_H = 1.0f / (float)H;
   a.T = T;
   a.nvec = (int)(H / 8);
   a.h = static_cast<uint4*>(h);
@@ -242,31 +306,17 @@ int launch_add_rmsnorm(const void* x, const void* res, const void* w, int w_f32,
 }
 
 // ==========================================================================================
-// Backward. Persistent CTAs walk groups of `rows` rows with a grid stride, a team of threads a row. A
-// group's inputs arrive by bulk copies into a ring in shared memory, several groups ahead, so memory
-// never waits for a row's reduction and its barrier. A thread owns VPT vectors of every row of its team,
-// so its share of dw stays in registers from row to row; a CTA's teams add theirs up at the end, and it
-// leaves as one of `grid` partial rows in the workspace. A second kernel adds the partial rows in a
-// fixed order: no atomics, the same bits on every run.
+// Backward. Rows pass in order through shared memory. A persistent CTA takes groups of `rows` consecutive rows
+// with a grid stride, a team of threads a row. A group's inputs arrive by bulk copies, a tensor each, a group
+// or more ahead, so that memory does not wait for a row's reduction and its barrier; a thread has its
+// vectors in registers before the group's barrier, behind which the stage is loaded anew. A thread owns VPT vectors of every row of its team, so its share of dw stays
+// in registers from row to row; a CTA's teams add theirs up at the end, and it leaves as one of `grid`
+// partial rows in the workspace. A second kernel adds the partial rows in a fixed order: no atomics, the
+// same bits on every run.
 namespace {
 
-constexpr int kBwdStages = 5;
-
-struct NormBwdArgs {
-  const uint4* dy;
-  const uint4* h;
-  const void* w;
-  int w_f32;
-  const float* rstd;
-  const uint4* dh;  // may be null
-  uint4* dx;        // may be null
-  float* part;      // [grid][H], null without dw
-  int64_t T;
-  int nvec;
-  float H;
-  int rows, stages;
-  uint64_t wait_ns;
-};
+constexpr int kRingStages = 3;
+constexpr int kRingRoom = 220 * 1024;  // of an SM, for its CTAs' rings together
 
 FP8_DEVI void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -275,126 +325,182 @@ FP8_DEVI void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* ba
                : "memory");
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs p) {
-  extern __shared__ uint4 ring[];  // [stages][dy, h, dh][rows][nvec]
-  __shared__ float red[2][16];
-  __shared__ uint64_t full[kBwdStages];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int team_size = blockDim.x / p.rows, team = threadIdx.x / team_size, t = threadIdx.x % team_size;
-  const int team_warps = team_size / 32, warp0 = team * team_warps;
-  const int tensors = p.dh ? 3 : 2;
-  const int slab = p.rows * p.nvec;  // vectors of a tensor in a stage
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
-    fence_mbar_init();
+struct RingShape {
+  int vpt, team, rows, ctas, stages, tensors;
+};
+// One vector a thread up to 8192 columns (four beyond), teams for several short rows up to 512 threads a CTA,
+// as many CTAs an SM as make 1024 threads with one vector each (one CTA with four: it needs the registers),
+// and up to three groups in a CTA's ring. Measured for 8192 x 7168, 470 MB: 76 us; with the weights read from L1
+// row by row instead of kept in registers 93 us, with two vectors a thread and two CTAs an SM (spills) 91 us,
+// with a ring of five groups 78 us, without any arithmetic 75 us.
+inline RingShape ring_shape(int nvec, int tensors) {
+  RingShape r;
+  r.vpt = nvec <= 1024 ? 1 : 4;
+  r.team = (int)round_up64(ceil_div64(nvec, r.vpt), 32);
+  r.rows = r.team > 512 ? 1 : 512 / r.team < 8 ? 512 / r.team : 8;
+  r.ctas = r.vpt == 1 && r.team * r.rows <= 512 ? 2 : 1;
+  r.tensors = tensors;
+  const int fit = kRingRoom / r.ctas / (tensors * r.rows * nvec * 16);
+  r.stages = fit < kRingStages ? fit : kRingStages;
+  return r;
+}
+// CTAs: by the shape with three tensors, so that the partial rows do not depend on dh
+inline int64_t ring_grid(int64_t T, int64_t H) {
+  const RingShape r = ring_shape((int)(H / 8), 3);
+  const int64_t groups = ceil_div64(T, r.rows);
+  return groups < 152 * r.ctas ? groups : 152 * r.ctas;
+}
+
+struct Ring {
+  const uint4* src[3];
+  int64_t T, groups;
+  int nvec, slab;  // vectors of a row, of a tensor's part of a stage
+  RingShape r;
+  FP8_DEVI void load(uint4* ring, uint64_t* full, int64_t g, int s) const {
+    if (g >= groups) return;
+    const int64_t row = g * r.rows;
+    const uint32_t bytes = (uint32_t)min((int64_t)r.rows, T - row) * (uint32_t)nvec * 16;
+    mbar_arrive_expect_tx(&full[s], bytes * r.tensors);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < r.tensors) bulk_load(ring + (s * r.tensors + i) * slab, src[i] + row * nvec, bytes, &full[s]);
   }
-  __syncthreads();
-  const int64_t groups = ceil_div64(p.T, p.rows);
-  auto load = [&](int64_t g, int s) {
-    const int64_t row = g * p.rows;
-    const uint32_t bytes = (uint32_t)min((int64_t)p.rows, p.T - row) * (uint32_t)p.nvec * 16;
-    uint4* d = ring + s * tensors * slab;
-    mbar_arrive_expect_tx(&full[s], bytes * tensors);
-    bulk_load(d, p.dy + row * p.nvec, bytes, &full[s]);
-    bulk_load(d + slab, p.h + row * p.nvec, bytes, &full[s]);
-    if (p.dh) bulk_load(d + 2 * slab, p.dh + row * p.nvec, bytes, &full[s]);
-  };
-  if (threadIdx.x == 0)
-    for (int s = 0; s < p.stages; ++s) {
-      const int64_t g = blockIdx.x + (int64_t)s * gridDim.x;
-      if (g < groups) load(g, s);
+  FP8_DEVI void start(uint4* ring, uint64_t* full) const {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < r.stages; ++s) mbar_init(&full[s], 1);
+      fence_mbar_init();
+      for (int s = 0; s < r.stages; ++s) load(ring, full, blockIdx.x + (int64_t)s * gridDim.x, s);
     }
-  float dw[VPT][8], w8[VPT][8];
+    __syncthreads();
+  }
+};
+inline Ring make_ring(const void* a, const void* b, const void* c, int64_t T, int64_t H) {
+  Ring q = {};
+  int n = 0;
+  for (const void* t : {a, b, c})
+    if (t) q.src[n++] = static_cast<const uint4*>(t);
+  q.nvec = (int)(H / 8);
+  q.r = ring_shape(q.nvec, n);
+  q.T = T;
+  q.groups = ceil_div64(T, q.r.rows);
+  q.slab = q.r.rows * q.nvec;
+  return q;
+}
+inline size_t ring_bytes(const Ring& q) { return (size_t)q.r.stages * q.r.tensors * q.slab * 16; }
+
+// Once for each device: the ring's shared memory.
+template <typename K>
+int allow_ring(K kern, std::atomic<uint64_t>& done, const Ctx& c) {
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (done.load(std::memory_order_acquire) & bit) return FP8_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingRoom) != cudaSuccess)
+    return FP8_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_release);
+  return FP8_OK;
+}
+
+struct NormBwdArgs {
+  const void* w;
+  const float* rstd;
+  uint4* dx;        // may be null
+  float* part;      // [grid][H], null without dw
+  float inv_H;
+  uint64_t wait_ns;
+};
+
+template <int VPT, bool WF32>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, 1) rmsnorm_bwd_kernel(const NormBwdArgs p, const Ring q) {
+  extern __shared__ uint4 ring[];  // [stages][dy, h, dh][rows][nvec]
+  __shared__ uint64_t full[kRingStages];
+  __shared__ __align__(16) float red[2][8][32];
+  const int nvec = q.nvec;
+  const int team = threadIdx.x / q.r.team, t = threadIdx.x % q.r.team;
+  const bool has_dh = q.r.tensors == 3;
+  q.start(ring, full);
+  float2 dw[VPT][4];
+  uint4 wv[VPT];  // bf16 weights stay in registers; fp32 ones, twice as many, come from L1
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
+    const int c = t + i * q.r.team;
+    wv[i] = !WF32 && c < nvec ? ld_stream(static_cast<const uint4*>(p.w) + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = w8[i][j] = 0.f;
-    if (t + i * team_size < p.nvec) load_w(p.w, p.w_f32, t + i * team_size, w8[i]);
+    for (int j = 0; j < 4; ++j) dw[i][j] = both(0.f);
   }
-  int s = 0, prev = 0, par = 0;
+  int st = 0, par = 0;
   uint32_t phase = 0;
   auto row_rstd = [&](int64_t g) {
-    const int64_t row = g * p.rows + team;
-    return row < p.T ? __ldg(p.rstd + row) : 0.f;
+    const int64_t row = g * q.r.rows + team;
+    return row < q.T ? __ldg(p.rstd + row) : 0.f;
   };
   float rstd_next = row_rstd(blockIdx.x);
-  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x, par ^= 1) {
-    const int64_t row = g * p.rows + team;
-    const bool active = row < p.T;
+  for (int64_t g = blockIdx.x; g < q.groups; g += gridDim.x, par ^= 1) {
+    const int64_t row = g * q.r.rows + team;
+    const bool active = row < q.T;
     float rstd = rstd_next;
     rstd_next = row_rstd(g + gridDim.x);
     // a wait that ran out would show as NaN in everything that the row reaches
-    if (!mbar_wait(&full[s], phase, nullptr, p.wait_ns)) rstd = __uint_as_float(0x7FC00000u);
-    const uint4* d = ring + s * tensors * slab + team * p.nvec;
-    float sum = 0.f;
-    if (active) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * team_size;
-        if (c >= p.nvec) continue;
-        float d8[8], h8[8];
-        unpack8(d[c], d8);
-        unpack8(d[slab + c], h8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float dyx = d8[j] * (h8[j] * rstd);
-          dw[i][j] += dyx;
-          sum = fmaf(dyx, w8[i][j], sum);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red[par][warp] = sum;  // two buffers: a row's values are read while the next row's are written
-    __syncthreads();
-    // every thread is done with the group before this one: its stage takes the group `stages` further on
-    if (threadIdx.x == 0 && g != blockIdx.x) {
-      const int64_t next = g + (int64_t)(p.stages - 1) * gridDim.x;
-      if (next < groups) load(next, prev);
-    }
-    if (p.dx && active) {
-      sum = 0.f;
-      for (int w = 0; w < team_warps; ++w) sum += red[par][warp0 + w];
-      const float mean = sum / p.H;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * team_size;
-        if (c >= p.nvec) continue;
-        float d8[8], h8[8], g8[8];
-        unpack8(d[c], d8);
-        unpack8(d[slab + c], h8);
-        unpack8(p.dh ? d[2 * slab + c] : make_uint4(0, 0, 0, 0), g8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d8[j] = rstd * (d8[j] * w8[i][j] - h8[j] * rstd * mean) + g8[j];
-        p.dx[row * p.nvec + c] = pack8(d8);
-      }
-    }
-    prev = s;
-    if (++s == p.stages) s = 0, phase ^= 1;
-  }
-  if (p.part) {
-    float4* out = reinterpret_cast<float4*>(p.part) + (int64_t)blockIdx.x * p.nvec * 2;
-    float4* sh = reinterpret_cast<float4*>(ring);  // [rows][2 nvec], after the last group
-    if (p.rows > 1) __syncthreads();
-    if (p.rows > 1) out = sh + team * p.nvec * 2;
+    if (!mbar_wait(&full[st], phase, nullptr, p.wait_ns)) rstd = __uint_as_float(0x7FC00000u);
+    const uint4* in = ring + st * q.r.tensors * q.slab + team * nvec;
+    uint4 vdy[VPT], vh[VPT], vdh[VPT];
+    float2 sum2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * team_size;
-      if (c >= p.nvec) continue;
-      out[2 * c] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      out[2 * c + 1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      const int c = t + i * q.r.team;
+      if (!active || c >= nvec) continue;
+      vdy[i] = in[c];
+      vh[i] = in[q.slab + c];
+      vdh[i] = has_dh ? in[2 * q.slab + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 dyh = fmul2_rn(unpack2(word(vdy[i], j)), unpack2(word(vh[i], j)));
+        dw[i][j] = ffma2_rn(dyh, both(rstd), dw[i][j]);
+        sum2 = ffma2_rn(dyh, WF32 ? __ldg(static_cast<const float2*>(p.w) + 4 * c + j) : unpack2(word(wv[i], j)), sum2);
+      }
     }
-    if (p.rows > 1) {
+    float sum = sum2.x + sum2.y;  // of dy * w * h: rstd comes in below
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    team_put(red[par][team], t, q.r.team / 32, sum);  // two buffers: a group's are read while the next one's are written
+    __syncthreads();
+    if (threadIdx.x == 0) q.load(ring, full, g + (int64_t)q.r.stages * gridDim.x, st);
+    if (++st == q.r.stages) st = 0, phase ^= 1;
+    if (!p.dx || !active) continue;
+    const float c1 = rstd * rstd * (rstd * team_sum(red[par][team], q.r.team / 32) * p.inv_H);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = t + i * q.r.team;
+      if (c >= nvec) continue;
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 w2 = WF32 ? __ldg(static_cast<const float2*>(p.w) + 4 * c + j) : unpack2(word(wv[i], j));
+        const float2 g2 = ffma2_rn(unpack2(word(vh[i], j)), both(-c1), unpack2(word(vdh[i], j)));
+        o[j] = pack_bf16(ffma2_rn(fmul2_rn(unpack2(word(vdy[i], j)), w2), both(rstd), g2));
+      }
+      p.dx[row * nvec + c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (p.part) {
+    float4* mine = reinterpret_cast<float4*>(p.part) + (int64_t)blockIdx.x * nvec * 2;
+    float4* sh = reinterpret_cast<float4*>(ring);  // [rows][2 nvec]: every load has landed and been read
+    if (q.r.rows > 1) __syncthreads();
+    float4* out = q.r.rows > 1 ? sh + team * nvec * 2 : mine;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = t + i * q.r.team;
+      if (c >= nvec) continue;
+      out[2 * c] = make_float4(dw[i][0].x, dw[i][0].y, dw[i][1].x, dw[i][1].y);
+      out[2 * c + 1] = make_float4(dw[i][2].x, dw[i][2].y, dw[i][3].x, dw[i][3].y);
+    }
+    if (q.r.rows > 1) {
       __syncthreads();
-      out = reinterpret_cast<float4*>(p.part) + (int64_t)blockIdx.x * p.nvec * 2;
-      for (int c = threadIdx.x; c < 2 * p.nvec; c += blockDim.x) {
+      for (int c = threadIdx.x; c < 2 * nvec; c += blockDim.x) {
         float4 a = sh[c];
-        for (int r = 1; r < p.rows; ++r) {
-          const float4 v = sh[r * 2 * p.nvec + c];
+        for (int r = 1; r < q.r.rows; ++r) {
+          const float4 v = sh[r * 2 * nvec + c];
           a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
         }
-        out[c] = a;
+        mine[c] = a;
       }
     }
   }
@@ -423,77 +529,41 @@ __global__ void __launch_bounds__(512) dw_sum_kernel(const float4* part, int par
     a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
   }
   if (dw_bf16)
-    static_cast<uint2*>(dw)[c] = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+    static_cast<uint2*>(dw)[c] = make_uint2(pack_bf16(make_float2(a.x, a.y)), pack_bf16(make_float2(a.z, a.w)));
   else
     static_cast<float4*>(dw)[c] = a;
 }
 
-// Shape of the backward kernel for rows of nvec vectors: two vectors a thread up to 8192 columns, four
-// beyond; teams for several short rows, up to 512 threads a CTA; two CTAs an SM where each then has a ring of three
-// groups, else one with as many as fit (two for the widest rows).
-struct BwdShape {
-  int vpt, team, rows, ctas, stages;
-};
-BwdShape bwd_shape(int nvec, bool dh) {
-  constexpr int kRoom = 220 * 1024;
-  BwdShape b;
-  b.vpt = nvec <= 1024 ? 2 : 4;
-  b.team = (int)round_up64(ceil_div64(nvec, b.vpt), 32);
-  b.rows = 512 / b.team;
-  const int group = (dh ? 3 : 2) * b.rows * nvec * 16;
-  b.ctas = kRoom / 2 / group >= 3 ? 2 : 1;
-  const int fit = kRoom / b.ctas / group;
-  b.stages = fit < kBwdStages ? fit : kBwdStages;
-  return b;
-}
-constexpr int64_t kBwdSms = 152;
-int64_t bwd_grid(int64_t T, const BwdShape& b) {
-  const int64_t groups = ceil_div64(T, b.rows);
-  return groups < kBwdSms * b.ctas ? groups : kBwdSms * b.ctas;
-}
-
-template <int VPT>
-int run_norm_bwd(const NormBwdArgs& a, const BwdShape& b, int grid, const Ctx& c) {
-  const size_t smem = (size_t)b.stages * (a.dh ? 3 : 2) * b.rows * a.nvec * 16;
+template <int VPT, bool WF32>
+int run_norm_bwd(const NormBwdArgs& a, const Ring& q, int grid, const Ctx& c) {
   static std::atomic<uint64_t> done{0};
-  const uint64_t bit = 1ull << (c.device & 63);
-  if (!(done.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(rmsnorm_bwd_kernel<VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
-      return FP8_ERR_CUDA;
-    done.fetch_or(bit, std::memory_order_release);
-  }
-  rmsnorm_bwd_kernel<VPT><<<grid, b.team * b.rows, smem, c.stream>>>(a);
+  const int rc = allow_ring(rmsnorm_bwd_kernel<VPT, WF32>, done, c);
+  if (rc != FP8_OK) return rc;
+  rmsnorm_bwd_kernel<VPT, WF32><<<grid, q.r.team * q.r.rows, ring_bytes(q), c.stream>>>(a, q);
   return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
 }  // namespace
 
-int64_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t H) {
-  // without dh the ring is shorter and more CTAs may fit: room for those
-  return bwd_grid(T, bwd_shape((int)(H / 8), false)) * H * 4;
-}
+int64_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t H) { return ring_grid(T, H) * H * 4; }
 
 int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, const float* rstd, const void* dh,
                        int64_t T, int64_t H, void* dx, void* dw, int dw_bf16, float* ws, const Ctx& c) {
-  const BwdShape b = bwd_shape((int)(H / 8), dh != nullptr);
-  const int64_t grid = bwd_grid(T, b);
+  const Ring q = make_ring(dy, h, dh, T, H);
+  const int64_t grid = ring_grid(T, H);
   if (grid > 0) {
     NormBwdArgs a;
-    a.dy = static_cast<const uint4*>(dy);
-    a.h = static_cast<const uint4*>(h);
     a.w = w;
-    a.w_f32 = w_f32;
     a.rstd = rstd;
-    a.dh = static_cast<const uint4*>(dh);
     a.dx = static_cast<uint4*>(dx);
     a.part = dw ? ws : nullptr;
-    a.T = T;
-    a.nvec = (int)(H / 8);
-    a.H = (float)H;
-    a.rows = b.rows;
-    a.stages = b.stages;
+    a.inv_H = 1.0f / (float)H;
     a.wait_ns = c.wait_ns;
-    const int rc = b.vpt == 2 ? run_norm_bwd<2>(a, b, (int)grid, c) : run_norm_bwd<4>(a, b, (int)grid, c);
+    int rc;
+    if (q.r.vpt == 1)
+      rc = w_f32 ? run_norm_bwd<1, true>(a, q, (int)grid, c) : run_norm_bwd<1, false>(a, q, (int)grid, c);
+    else
+      rc = w_f32 ? run_norm_bwd<4, true>(a, q, (int)grid, c) : run_norm_bwd<4, false>(a, q, (int)grid, c);
     if (rc != FP8_OK) return rc;
   }
   if (!dw) return FP8_OK;

@@ -212,3 +212,56 @@ def test_no_rows(fp8):
     dw = torch.full((H,), 3.0, device="cuda")
     fp8.fp8_add_rmsnorm_bwd(e, e, w, torch.empty(0, device="cuda"), e, dw, workspace=fp8.rmsnorm_bwd_workspace(0, H, "cuda"))
     assert not dw.any()
+
+
+# ------------------------------------------------------------------------------------------ many rows
+
+@pytest.mark.parametrize("T,H,gran", [(5000, 264, "row"), (2500, 1024, "block"), (1300, 4096, "row"), (1217, 2056, "row"),
+                                      (1300, 4096, "mx"), (700, 7168, "row"), (700, 7168, "block"), (650, 8200, "row"),
+                                      (615, 16384, "block"), (615, 16384, "mx"), (700, 7168, "none")])
+@pytest.mark.parametrize("residual", [True, False])
+def test_many_rows(fp8, T, H, gran, residual):
+    """Enough rows that each CTA takes several groups of them, the last group short: every row as the formula gives it,
+    and the same bits as in a call with that row among few."""
+    x, r, w = _inputs(T, H, T + 2 * H, residual)
+    g = {"row": fp8.GRAN_ROW, "block": fp8.GRAN_BLOCK_1x128, "mx": fp8.GRAN_MX, "none": None}[gran]
+    h, y, q, inv, rstd = fp8.add_rmsnorm_alloc(x, w, EPS, r, g, want_y=True, want_rstd=True)
+    s, rs, yr = _reference(x, r, w)
+    if residual:
+        assert torch.equal(h, (x.float() + r.float()).bfloat16())
+    assert ((rstd.double() - rs).abs() <= 64 * U * rs).all()
+    assert ((y.double() - yr).abs() <= (2.0 ** -8 + 64 * U) * yr.abs()).all()
+    if gran == "row":
+        want = yr.abs().amax(1).clamp_min(1e-12) / 448
+        assert ((inv.double() - want).abs() <= 80 * U * want).all()
+        _check_codes(q.double() * inv.double()[:, None], yr, inv.double()[:, None], 3)
+    elif gran == "block":
+        yb = yr.view(T, H // 128, 128)
+        want = yb.abs().amax(2).clamp_min(1e-12) / 448
+        assert ((inv.double() - want).abs() <= 80 * U * want).all()
+        _check_codes(q.double().view_as(yb) * inv.double()[..., None], yb, inv.double()[..., None], 3)
+    elif gran == "mx":
+        yb = yr.view(T, H // 32, 32)
+        X = torch.exp2(torch.from_numpy(mx_unblock_rows(inv, np.arange(T), H).astype(np.float64)).cuda() - 127)
+        amax = yb.abs().amax(2)
+        assert (X * 2.0 ** 8 <= amax * (1 + 1e-5)).all() and (amax * (1 - 1e-5) < X * 2.0 ** 9).all()
+        clipped = yb.clamp(-448 * X[..., None], 448 * X[..., None])
+        _check_codes(q.double().view_as(yb) * X[..., None], clipped, X[..., None], 3)
+
+
+@pytest.mark.parametrize("T,H", [(5000, 264), (1300, 4096), (700, 7168), (320, 8200), (315, 16384), (9000, 1024)])
+def test_many_rows_backward_in_place(fp8, T, H):
+    """dx over dy's own buffer, rows loaded ahead of the ones being written."""
+    x, r, w = _inputs(T, H, 7 * T + H)
+    h, _, _, _, rstd = fp8.add_rmsnorm_alloc(x, w, EPS, r, want_rstd=True)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dy, dh = (torch.randn(T, H, generator=g, device="cuda").bfloat16() for _ in range(2))
+    rx, rw = _bwd_reference(dy, h, w, rstd, dh)
+    xhat = h.double().abs() * rstd.double()[:, None]
+    gabs = dy.double().abs() * w.double().abs()
+    terms = rstd.double()[:, None] * (gabs + xhat * (gabs * xhat).mean(1, keepdim=True))
+    bound = (T / 152 + 60) * U * (dy.double().abs() * xhat).sum(0) + 1e-30
+    dw = torch.empty(H, device="cuda")
+    fp8.fp8_add_rmsnorm_bwd(dy, h, w, rstd, dy, dw, dh=dh, workspace=fp8.rmsnorm_bwd_workspace(T, H, "cuda"))
+    assert ((dy.double() - rx).abs() <= 2.0 ** -8 * rx.abs() + 64 * U * terms + 1e-30).all()
+    assert ((dw.double() - rw).abs() <= bound).all()
