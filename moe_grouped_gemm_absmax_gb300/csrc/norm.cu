@@ -265,9 +265,12 @@ int run_norm(const NormArgs& a, int threads, const Ctx& c) {
 
 template <int GRAN, int FMT>
 int norm_dispatch(const NormArgs& a, const Ctx& c) {
-  // two vectors a thread while a CTA of 512 threads covers the row, four for the widest rows
+  // Two vectors a thread while a CTA of 512 threads covers the row: with few rows a row's latency counts (1021 x
+  // 5120 4.7 us, with four 5.4). Four for wider rows, and for many rows above 4096 columns, where two
+  // leave a third of an SM's threads without a CTA (8192 x 7168 with block scales 76 us, with two 82).
   if (a.nvec <= 64) return run_norm<2, GRAN, FMT, true>(a, 256, c);
-  if (a.nvec <= 1024) return run_norm<2, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 2), 32), c);
+  if (a.nvec <= 512 || (a.nvec <= 1024 && a.T < 2048))
+    return run_norm<2, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 2), 32), c);
   return run_norm<4, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 4), 32), c);
 }
 

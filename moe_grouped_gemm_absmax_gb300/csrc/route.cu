@@ -38,13 +38,73 @@ FP8_DEVI float warp_max(float v) {
   return v;
 }
 
-// Unsigned keys in the order of the values: -inf is kKeyMasked, a NaN counts as -inf, 0 is below
-// every value (an expert already taken).
-constexpr uint32_t kKeyMasked = 0x007FFFFFu;
+// Which experts a lane holds: VEC, where E % 4 == 0, four neighbours at a time (16- or 8-byte loads),
+// else one of each 32.
+template <bool VEC>
+FP8_DEVI int expert_of(int lane, int i) {
+  return VEC ? (i >> 2) * 128 + lane * 4 + (i & 3) : lane + 32 * i;
+}
+template <bool VEC>
+FP8_DEVI int index_of(int e) {
+  return VEC ? (e >> 7) * 4 + (e & 3) : e >> 5;
+}
+// A row's logits (or a row of fp32 values); experts past E get `none`.
+template <int VPL, bool VEC>
+FP8_DEVI void load_row(const void* p, int bf16, int64_t row, int E, int lane, float none, float* v) {
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4) {
+      const int e = expert_of<true>(lane, i);
+      float4 q = make_float4(none, none, none, none);
+      if (e < E) {
+        if (bf16) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + row * E + e));
+          q = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                          __uint_as_float(w.y & 0xFFFF0000u));
+        } else {
+          q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + row * E + e));
+        }
+      }
+      v[i] = q.x;
+      if (VPL > 1) v[(i + 1) % VPL] = q.y, v[(i + 2) % VPL] = q.z, v[(i + 3) % VPL] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = lane + 32 * i < E ? load_logit(p, bf16, row * E + lane + 32 * i) : none;
+  }
+}
+template <int VPL, bool VEC>
+FP8_DEVI void store_row(void* p, int bf16, int64_t row, int E, int lane, const float* v) {
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4) {
+      const int e = expert_of<true>(lane, i);
+      if (e >= E) continue;
+      const float4 q = make_float4(v[i], v[(i + 1) % VPL], v[(i + 2) % VPL], v[(i + 3) % VPL]);
+      if (bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(q.x, q.y), hi = __floats2bfloat162_rn(q.z, q.w);
+        __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + row * E + e);
+        o[0] = lo;
+        o[1] = hi;
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + row * E + e) = q;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 32 * i < E) store_logit(p, bf16, row * E + lane + 32 * i, v[i]);
+  }
+}
+
+// Unsigned keys in the order of the values: -inf is kKeyMasked, a NaN counts as -inf. Below every
+// value: kKeyNone, no expert, and kKeyUnknown, one that has to be looked for.
+constexpr uint32_t kKeyMasked = 0x007FFFFFu, kKeyUnknown = 1u, kKeyNone = 0u;
 FP8_DEVI uint32_t order_key(float v) {
+  v = v + 0.0f;  // -0 and +0 are level
   const uint32_t b = __float_as_uint(v);
-  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return v != v ? kKeyMasked : (v == 0.0f ? 0x80000000u : k);  // -0 and +0 are level
+  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return v != v ? kKeyMasked : k;
 }
 
 struct RouteArgs {
@@ -66,39 +126,43 @@ struct RouteArgs {
   int chunks;
 };
 
-// A warp per token: lane l holds experts l + 32 i. Each step takes the largest key left: the lanes'
-// maxima meet in one warp reduction, a second one settles ties by the lowest expert, and the lane that
-// holds it drops it.
-template <int VPL>
-FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, int32_t* hist) {
+// A warp per token. Each lane knows the best two of its experts that are left. A step takes the largest
+// key of all lanes' best (one warp reduction; a second one settles ties by the lowest expert); its lane
+// moves on to its second, and only when a lane's second is gone too are the keys looked through again.
+// Looking through them at every step took 950 instructions a token of 256 experts and k = 8.
+template <int VPL, bool VEC>
+FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* bias, int32_t* hist) {
   float v[VPL];
   uint32_t key[VPL];
+  load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, 0.f, v);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < p.E ? load_logit(p.logits, p.bf16, t * p.E + e) : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e < p.E ? order_key(p.bias ? v[i] + __ldg(p.bias + e) : v[i]) : 0u;
-  }
+  for (int i = 0; i < VPL; ++i)
+    key[i] = expert_of<VEC>(lane, i) < p.E ? order_key(p.bias ? v[i] + bias[i] : v[i]) : kKeyNone;
+  uint32_t taken = 0, best = kKeyUnknown, second = kKeyNone;
+  int best_i = 0, second_i = 0;
   int my_id = -1;  // lane j: the j-th expert taken
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = key[0];
+    if (__any_sync(0xffffffffu, best == kKeyUnknown)) {
+      best = second = kKeyNone;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
+      for (int i = 0; i < VPL; ++i) {  // strict comparisons: of level keys the lower expert is first
+        const uint32_t x = taken >> i & 1u ? kKeyNone : key[i];
+        const bool c1 = x > best, c2 = x > second;
+        second_i = c1 ? best_i : (c2 ? i : second_i);
+        second = max(second, min(best, x));
+        best_i = c1 ? i : best_i;
+        best = max(best, x);
+      }
+    }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     if (top <= kKeyMasked) break;  // nothing left that may be taken
-    uint32_t mine = 0xffffffffu;
-#pragma unroll
-    for (int i = VPL - 1; i >= 0; --i)
-      if (key[i] == top) mine = (uint32_t)(lane + 32 * i);
+    const uint32_t mine = best == top ? (uint32_t)expert_of<VEC>(lane, best_i) : 0xffffffffu;
     const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
-    if (e == mine) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if ((int)e == lane + 32 * i) key[i] = 0;
+    if (mine == e) {
+      taken |= 1u << best_i;
+      best = second;
+      best_i = second_i;
+      second = kKeyUnknown;
     }
     if (lane == j) my_id = (int)e;
   }
@@ -113,11 +177,11 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, int32_t* hist
       float m = -INFINITY, z = 0.f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < p.E) m = fmaxf(m, v[i]);
+        if (expert_of<VEC>(lane, i) < p.E) m = fmaxf(m, v[i]);
       m = warp_max(m);
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < p.E) z += expf(v[i] - m);
+        if (expert_of<VEC>(lane, i) < p.E) z += expf(v[i] - m);
       w = expf(my_v - m) / warp_sum(z);
     }
   } else {
@@ -155,28 +219,48 @@ FP8_DEVI int block_scan(int x, int32_t* warp_sums) {
   return s - x + (warp ? warp_sums[warp - 1] : 0);
 }
 
-// Each slot's place: `at` holds the chunk's first place of each expert; the slots are counted in slot
-// order by one warp.
-FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at) {
-  const int lane = threadIdx.x;
+// Each slot's place: `at` holds the chunk's first place of each expert. kRankWarps warps take 32 slots each;
+// a slot's place is its expert's, plus the slots of that expert in the warps before (`count`, a row of E2
+// counts a warp) and in the lanes before.
+constexpr int kRankWarps = 16;
+FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, int32_t* total, uint16_t* count) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n = p.T * p.k, len = p.per_chunk * p.k;
   const int64_t s0 = chunk * len, s1 = s0 + len < n ? s0 + len : n;
-  int next = s0 + lane < s1 ? p.ids[s0 + lane] : -1;
-  for (int64_t b = s0; b < s1; b += 32) {
-    const int64_t s = b + lane;
-    const int id = next;
-    next = s + 32 < s1 ? p.ids[s + 32] : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    const int before = __popc(same & ((1u << lane) - 1));
-    int32_t place = -1;
-    if (id >= 0) place = at[id] + before;
-    __syncwarp();
-    if (id >= 0 && before == 0) at[id] += __popc(same);
-    __syncwarp();
-    if (s < s1) {
-      p.pos[s] = place;
-      if (id >= 0) p.order[place] = (int32_t)s;
+  for (int64_t b = s0; b < s1; b += 32 * kRankWarps) {
+    for (int i = threadIdx.x; i < kRankWarps * p.E2 / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    __syncthreads();
+    const int64_t s = b + threadIdx.x;
+    int id = -1, before = 0;
+    if (warp < kRankWarps) {
+      id = s < s1 ? p.ids[s] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      before = __popc(same & ((1u << lane) - 1));
+      if (id >= 0 && before == 0) count[warp * p.E2 + id] = (uint16_t)__popc(same);
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < kRankWarps; ++w) {
+        const int c = count[w * p.E2 + e];
+        count[w * p.E2 + e] = (uint16_t)sum;
+        sum += c;
+      }
+      total[e] = sum;
+    }
+    __syncthreads();
+    if (warp < kRankWarps && s < s1) {
+      int32_t place = -1;
+      if (id >= 0) {
+        place = at[id] + count[warp * p.E2 + id];
+        place += before;
+        p.order[place] = (int32_t)s;
+      }
+      p.pos[s] = place;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) at[e] += total[e];  // the next batch's first places
   }
 }
 // Unused slots leave the end of `order` without a slot.
@@ -187,9 +271,9 @@ FP8_DEVI void fill_order(const RouteArgs& p, int64_t valid) {
 }
 
 // The choice for a chunk of tokens, and the chunk's slots of each expert; with one chunk the table too.
-template <int VPL, int WARPS>
+template <int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
-  extern __shared__ int32_t hist[];
+  extern __shared__ int32_t hist[];  // [E2]; with one chunk also place_chunk's arrays
   __shared__ int32_t warp_sums[32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -199,7 +283,11 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
   }
   const int64_t t0 = blockIdx.x * p.per_chunk;
   const int64_t t1 = t0 + p.per_chunk < p.T ? t0 + p.per_chunk : p.T;
-  for (int64_t t = t0 + warp; t < t1; t += WARPS) route_token<VPL>(p, t, lane, p.order ? hist : nullptr);
+  float bias[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) bias[i] = 0.f;
+  if (p.bias) load_row<VPL, VEC>(p.bias, 0, 0, p.E, lane, 0.f, bias);
+  for (int64_t t = t0 + warp; t < t1; t += WARPS) route_token<VPL, VEC>(p, t, lane, bias, p.order ? hist : nullptr);
   if (!p.order) return;
   __syncthreads();
   if (p.chunks > 1) {
@@ -219,14 +307,14 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
     __syncthreads();
   }
   fill_order(p, before);
-  if (warp == 0) place_chunk(p, 0, hist);
+  place_chunk(p, 0, hist, hist + p.E2, reinterpret_cast<uint16_t*>(hist + 2 * p.E2));
 }
 
 // The table from the chunks' counts. Each CTA sums the whole matrix of counts (16 bits each, 78 KB for 152
 // chunks and 256 experts, from L2) into its own first places, so that no launch is spent on a scan.
 constexpr int kPlaceThreads = 1024;
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs p) {
-  extern __shared__ int32_t sh[];  // [E2] slots, [E2] slots in the chunks before this one
+  extern __shared__ int32_t sh[];  // [E2] slots, [E2] slots in the chunks before this one, place_chunk's counts
   __shared__ int32_t warp_sums[32];
   int32_t* total = sh;
   int32_t* prior = sh + p.E2;
@@ -263,7 +351,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   const int64_t valid = warp_sums[31];
   __syncthreads();
   fill_order(p, valid);
-  if (threadIdx.x < 32) place_chunk(p, blockIdx.x, prior);
+  place_chunk(p, blockIdx.x, prior, total, reinterpret_cast<uint16_t*>(sh + 2 * p.E2));
 }
 
 // Gradient of the logits, a warp per token. With g_j = scale * dweights_j:
@@ -284,7 +372,7 @@ struct RouteBwdArgs {
   int32_t* status;
 };
 
-template <int VPL>
+template <int VPL, bool VEC>
 __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBwdArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kBwdWarps + warp;
@@ -302,25 +390,22 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
   float base = 0.f, pe = 0.f;
   if (p.softmax && !p.renorm) {
     float m = -INFINITY, z = 0.f;
+    load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, -INFINITY, v);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < p.E ? load_logit(p.logits, p.bf16, t * p.E + e) : -INFINITY;
-      m = fmaxf(m, v[i]);
-    }
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
     m = warp_max(m);
     const bool none = m == -INFINITY;  // a row of masked logits: no probabilities, no gradient
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = none || lane + 32 * i >= p.E ? 0.f : expf(v[i] - m);
+      v[i] = none ? 0.f : expf(v[i] - m);
       z += v[i];
     }
-    z = warp_sum(z);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = none ? 0.f : v[i] / z;
-    pe = id >= 0 && !none ? expf(l - m) / z : 0.f;
+    z = none ? 0.f : 1.0f / warp_sum(z);
+    pe = id >= 0 && !none ? expf(l - m) * z : 0.f;
     d = g * pe;
     base = -warp_sum(d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] *= base * z;
   } else if (p.softmax) {
     const float m = warp_max(id >= 0 ? l : -INFINITY);
     float u = id >= 0 && m > -INFINITY ? expf(l - m) : 0.f;
@@ -335,11 +420,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
     }
     d = g * s * (1.0f - s);
   }
+  if (!(p.softmax && !p.renorm)) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    if (e < p.E) store_logit(p.dlogits, p.bf16, t * p.E + e, p.softmax && !p.renorm ? base * v[i] : 0.f);
+    for (int i = 0; i < VPL; ++i) v[i] = 0.f;
   }
+  store_row<VPL, VEC>(p.dlogits, p.bf16, t, p.E, lane, v);
   // an expert named twice gets the sum of its slots
   float all = 0.f;
   for (int j = 0; j < p.k; ++j) {
@@ -360,15 +445,19 @@ int64_t chunk_tokens(int64_t T) {
   return n < 65528 ? n : 65528;
 }
 
-#define FP8_BY_EXPERTS(E, CALL)      \
-  do {                               \
-    if ((E) <= 32) { CALL(1); }      \
-    else if ((E) <= 64) { CALL(2); } \
-    else if ((E) <= 128) { CALL(4); } \
-    else if ((E) <= 256) { CALL(8); } \
-    else if ((E) <= 512) { CALL(16); } \
-    else { CALL(32); }               \
+// CALL(vectors a lane, VEC) by the number of experts
+#define FP8_BY_EXPERTS(E, CALL)                                                        \
+  do {                                                                                 \
+    if ((E) <= 32) { CALL(1, false); }                                                 \
+    else if ((E) <= 64) { CALL(2, false); }                                            \
+    else if ((E) <= 128) { if ((E) % 4 == 0) { CALL(4, true); } else { CALL(4, false); } }   \
+    else if ((E) <= 256) { if ((E) % 4 == 0) { CALL(8, true); } else { CALL(8, false); } }   \
+    else if ((E) <= 512) { if ((E) % 4 == 0) { CALL(16, true); } else { CALL(16, false); } } \
+    else { if ((E) % 4 == 0) { CALL(32, true); } else { CALL(32, false); } }                 \
   } while (0)
+
+// Shared memory of place_chunk: first places and totals, a row of counts a warp.
+size_t place_bytes(int E2) { return (size_t)E2 * (8 + 2 * kRankWarps); }
 
 }  // namespace
 
@@ -384,9 +473,10 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   RouteArgs a = {logits, bf16, bias, T,    (int)E, (int)k, softmax, renorm, scale, ids, weights,
                  order,  pos,  ends, static_cast<uint16_t*>(ws), (int)round_up64(E, 2), chunk_tokens(T), 0};
   a.chunks = (int)ceil_div64(T, a.per_chunk);
+  const size_t smem = a.chunks == 1 ? place_bytes(a.E2) : (size_t)a.E2 * 4;
   // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers
-#define FP8_ROUTE(V) \
-  route_kernel<V, (V <= 8 ? 32 : 16)><<<(unsigned)a.chunks, V <= 8 ? 1024 : 512, (size_t)a.E2 * 4, c.stream>>>(a)
+#define FP8_ROUTE(V, X) \
+  route_kernel<V, X, (V <= 8 ? 32 : 16)><<<(unsigned)a.chunks, V <= 8 ? 1024 : 512, smem, c.stream>>>(a)
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
   if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
@@ -397,7 +487,7 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)a.chunks);
   cfg.blockDim = dim3(kPlaceThreads);
-  cfg.dynamicSmemBytes = (size_t)a.E2 * 8;
+  cfg.dynamicSmemBytes = place_bytes(a.E2);
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -409,7 +499,7 @@ int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const flo
   if (T == 0) return FP8_OK;
   const RouteBwdArgs a = {logits, bf16, ids, dw, dlogits, T, (int)E, (int)k, softmax, renorm, scale, c.status};
   const unsigned grid = (unsigned)ceil_div64(T, kBwdWarps);
-#define FP8_ROUTE(V) route_bwd_kernel<V><<<grid, 32 * kBwdWarps, 0, c.stream>>>(a)
+#define FP8_ROUTE(V, X) route_bwd_kernel<V, X><<<grid, 32 * kBwdWarps, 0, c.stream>>>(a)
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
   return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
