@@ -97,14 +97,11 @@ FP8_DEVI void store_row(void* p, int bf16, int64_t row, int E, int lane, const f
   }
 }
 
-// Unsigned keys in the order of the values: -inf is kKeyMasked, a NaN counts as -inf. Below every
-// value: kKeyNone, no expert, and kKeyUnknown, one that has to be looked for.
-constexpr uint32_t kKeyMasked = 0x007FFFFFu, kKeyUnknown = 1u, kKeyNone = 0u;
-FP8_DEVI uint32_t order_key(float v) {
-  v = v + 0.0f;  // -0 and +0 are level
-  const uint32_t b = __float_as_uint(v);
-  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  return v != v ? kKeyMasked : k;
+// The largest value of the warp's lanes; none is a NaN.
+FP8_DEVI float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 struct RouteArgs {
@@ -126,72 +123,96 @@ struct RouteArgs {
   int chunks;
 };
 
-// A warp per token. Each lane knows the best two of its experts that are left. A step takes the largest
-// key of all lanes' best (one warp reduction; a second one settles ties by the lowest expert); its lane
-// moves on to its second, and only when a lane's second is gone too are the keys looked through again.
-// Looking through them at every step took 950 instructions a token of 256 experts and k = 8.
+// A warp per token. The k-th largest of the lanes' maxima is a bound that at least k experts reach, and
+// few more do (9 of 256 on average for k = 8): those are gathered, one a lane, and each counts the ones
+// before it. Where more than 32 reach it (level values, rows with most experts masked), k steps each take
+// the largest one left. All rows by such steps took 950 instructions a token of 256 experts and k = 8, with
+// each lane's best two kept 780.
+struct Cand {
+  float sel;
+  int e;
+};
 template <int VPL, bool VEC>
-FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* bias, int32_t* hist) {
-  float v[VPL];
-  uint32_t key[VPL];
-  load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, 0.f, v);
+FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* bias, Cand* cand, int32_t* hist) {
+  float v[VPL], sel[VPL];
+  load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, -INFINITY, v);
+  float best = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    key[i] = expert_of<VEC>(lane, i) < p.E ? order_key(p.bias ? v[i] + bias[i] : v[i]) : kKeyNone;
-  uint32_t taken = 0, best = kKeyUnknown, second = kKeyNone;
-  int best_i = 0, second_i = 0;
-  int my_id = -1;  // lane j: the j-th expert taken
-  for (int j = 0; j < p.k; ++j) {
-    if (__any_sync(0xffffffffu, best == kKeyUnknown)) {
-      best = second = kKeyNone;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {  // strict comparisons: of level keys the lower expert is first
-        const uint32_t x = taken >> i & 1u ? kKeyNone : key[i];
-        const bool c1 = x > best, c2 = x > second;
-        second_i = c1 ? best_i : (c2 ? i : second_i);
-        second = max(second, min(best, x));
-        best_i = c1 ? i : best_i;
-        best = max(best, x);
-      }
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    if (top <= kKeyMasked) break;  // nothing left that may be taken
-    const uint32_t mine = best == top ? (uint32_t)expert_of<VEC>(lane, best_i) : 0xffffffffu;
-    const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
-    if (mine == e) {
-      taken |= 1u << best_i;
-      best = second;
-      best_i = second_i;
-      second = kKeyUnknown;
-    }
-    if (lane == j) my_id = (int)e;
+  for (int i = 0; i < VPL; ++i) {  // a NaN becomes -inf; experts past E are -inf
+    sel[i] = fmaxf(v[i] + bias[i], -INFINITY);
+    best = fmaxf(best, sel[i]);
   }
-  const float my_v = my_id >= 0 ? load_logit(p.logits, p.bf16, t * p.E + my_id) : 0.f;
+  float bound = -INFINITY;
+  for (int j = 0; j < p.k; ++j) {
+    bound = redux_max(best);
+    if (best == bound) best = -INFINITY;
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool in = sel[i] >= bound && sel[i] > -INFINITY;
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    const int at = n + __popc(m & ((1u << lane) - 1));
+    if (in && at < 32) cand[at] = {sel[i], expert_of<VEC>(lane, i)};
+    n += __popc(m);
+  }
+  __syncwarp();
+  int id = -1, rank = lane;  // this lane's expert and its place among the k
+  if (n <= 32) {
+    if (lane < n) {
+      const Cand mine = cand[lane];
+      rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const Cand c = cand[j];
+        rank += c.sel > mine.sel || (c.sel == mine.sel && c.e < mine.e);
+      }
+      if (rank < p.k) id = mine.e;
+    }
+  } else {
+    uint32_t taken = 0;
+    for (int j = 0; j < p.k; ++j) {
+      float b = -INFINITY;
+      int bi = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!(taken >> i & 1u) && sel[i] > b) b = sel[i], bi = i;
+      const float top = redux_max(b);
+      if (top == -INFINITY) break;  // nothing left that may be taken
+      const uint32_t mine = b == top ? (uint32_t)expert_of<VEC>(lane, bi) : 0xffffffffu;
+      const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
+      if (mine == e) taken |= 1u << bi;
+      if (lane == j) id = (int)e;
+    }
+  }
+  __syncwarp();  // the candidates are read before the next token's are written
+  const float l = id >= 0 ? load_logit(p.logits, p.bf16, t * p.E + id) : 0.f;
   float w = 0.f;
   if (p.softmax) {
     if (p.renorm) {  // softmax over the experts taken
-      const float m = warp_max(my_id >= 0 ? my_v : -INFINITY);
-      w = my_id >= 0 ? expf(my_v - m) : 0.f;
+      const float m = warp_max(id >= 0 ? l : -INFINITY);
+      w = id >= 0 ? expf(l - m) : 0.f;
       w = w / warp_sum(w);
     } else {
       float m = -INFINITY, z = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (expert_of<VEC>(lane, i) < p.E) m = fmaxf(m, v[i]);
+      for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
       m = warp_max(m);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (expert_of<VEC>(lane, i) < p.E) z += expf(v[i] - m);
-      w = expf(my_v - m) / warp_sum(z);
+      for (int i = 0; i < VPL; ++i) z += expert_of<VEC>(lane, i) < p.E ? expf(v[i] - m) : 0.f;
+      w = expf(l - m) / warp_sum(z);
     }
   } else {
-    w = my_id >= 0 ? 1.0f / (1.0f + expf(-my_v)) : 0.f;
+    w = id >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.f;
     if (p.renorm) w = w / (warp_sum(w) + 1e-20f);
   }
-  if (lane < p.k) {
-    p.ids[t * p.k + lane] = my_id;
-    p.weights[t * p.k + lane] = my_id >= 0 ? w * p.scale : 0.f;
-    if (hist && my_id >= 0) atomicAdd(hist + my_id, 1);
+  if (id >= 0) {
+    p.ids[t * p.k + rank] = id;
+    p.weights[t * p.k + rank] = w * p.scale;
+    if (hist) atomicAdd(hist + id, 1);
+  } else if (n < p.k && lane >= n && lane < p.k) {  // fewer than k: the last slots are unused
+    p.ids[t * p.k + lane] = -1;
+    p.weights[t * p.k + lane] = 0.f;
   }
 }
 
@@ -219,21 +240,21 @@ FP8_DEVI int block_scan(int x, int32_t* warp_sums) {
   return s - x + (warp ? warp_sums[warp - 1] : 0);
 }
 
-// Each slot's place: `at` holds the chunk's first place of each expert. kRankWarps warps take 32 slots each;
-// a slot's place is its expert's, plus the slots of that expert in the warps before (`count`, a row of E2
-// counts a warp) and in the lanes before.
-constexpr int kRankWarps = 16;
+// Each slot's place: `at` holds the chunk's first place of each expert. Warps take 32 slots each; a slot's
+// place is its expert's, plus the slots of that expert in the warps before (`count`, a row of E2 counts a
+// warp) and in the lanes before. Up to 32 warps, as many as the CTA has and 32 KB of counts allow.
+FP8_DEVI int rank_warps(int E2) { return min((int)blockDim.x / 32, E2 <= 512 ? 32 : 16); }
 FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, int32_t* total, uint16_t* count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = rank_warps(p.E2);
   const int64_t n = p.T * p.k, len = p.per_chunk * p.k;
   const int64_t s0 = chunk * len, s1 = s0 + len < n ? s0 + len : n;
-  for (int64_t b = s0; b < s1; b += 32 * kRankWarps) {
-    for (int i = threadIdx.x; i < kRankWarps * p.E2 / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
-    __syncthreads();
+  for (int64_t b = s0; b < s1; b += 32 * warps) {
     const int64_t s = b + threadIdx.x;
-    int id = -1, before = 0;
-    if (warp < kRankWarps) {
-      id = s < s1 ? p.ids[s] : -1;
+    int id = warp < warps && s < s1 ? p.ids[s] : -1, before = 0;
+    for (int i = threadIdx.x; i < warps * p.E2 / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    __syncthreads();
+    if (warp < warps) {
       const uint32_t same = __match_any_sync(0xffffffffu, id);
       before = __popc(same & ((1u << lane) - 1));
       if (id >= 0 && before == 0) count[warp * p.E2 + id] = (uint16_t)__popc(same);
@@ -241,8 +262,8 @@ FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, int32_
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       int sum = 0;
-#pragma unroll
-      for (int w = 0; w < kRankWarps; ++w) {
+#pragma unroll 8
+      for (int w = 0; w < warps; ++w) {
         const int c = count[w * p.E2 + e];
         count[w * p.E2 + e] = (uint16_t)sum;
         sum += c;
@@ -250,7 +271,7 @@ FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, int32_
       total[e] = sum;
     }
     __syncthreads();
-    if (warp < kRankWarps && s < s1) {
+    if (warp < warps && s < s1) {
       int32_t place = -1;
       if (id >= 0) {
         place = at[id] + count[warp * p.E2 + id];
@@ -275,6 +296,7 @@ template <int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
   extern __shared__ int32_t hist[];  // [E2]; with one chunk also place_chunk's arrays
   __shared__ int32_t warp_sums[32];
+  __shared__ Cand cand[WARPS][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (p.order) {
@@ -287,7 +309,7 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
 #pragma unroll
   for (int i = 0; i < VPL; ++i) bias[i] = 0.f;
   if (p.bias) load_row<VPL, VEC>(p.bias, 0, 0, p.E, lane, 0.f, bias);
-  for (int64_t t = t0 + warp; t < t1; t += WARPS) route_token<VPL, VEC>(p, t, lane, bias, p.order ? hist : nullptr);
+  for (int64_t t = t0 + warp; t < t1; t += WARPS) route_token<VPL, VEC>(p, t, lane, bias, cand[warp], p.order ? hist : nullptr);
   if (!p.order) return;
   __syncthreads();
   if (p.chunks > 1) {
@@ -457,7 +479,7 @@ int64_t chunk_tokens(int64_t T) {
   } while (0)
 
 // Shared memory of place_chunk: first places and totals, a row of counts a warp.
-size_t place_bytes(int E2) { return (size_t)E2 * (8 + 2 * kRankWarps); }
+size_t place_bytes(int E2) { return (size_t)E2 * (8 + 2 * (E2 <= 512 ? 32 : 16)); }
 
 }  // namespace
 
