@@ -59,7 +59,6 @@ constexpr int kSmemPair = 115712;      // two CTAs an SM: half of 228 KB less th
 constexpr uint64_t kDrainNs = 2000000000ull;
 // columns of N: groups of 16 hold 8 slots in two parts (columns 2 j, 2 j + 1), or 5 in three
 constexpr int kPerGroup1 = 8, kPerGroup2 = 5;
-constexpr int kMinUnits = 2;           // units a CTA takes at least, so that small tiles have few partial sums
 constexpr int kPrefetchUnits = 8;      // units a CTA brings into L2 for the second product
 
 struct MoeArgs {
@@ -182,10 +181,14 @@ struct Run {
   FP8_DEVI int owner(int64_t it) const { return (int)(((it + 1) * grid - 1) / total); }
   FP8_DEVI int first(int c) const { return (int)((int64_t)c * total / grid); }
 };
-FP8_DEVI Run make_run(int total, int cta, int grid) {
+// A tile shared by CTAs costs its joining, about 3 us of stores, an atomic and loads one after the other; a unit
+// takes an SM 0.15 us. So where there are fewer tiles than CTAs and a whole tile takes no longer than that
+// above an equal share, each CTA takes one tile (one token of a 1040 x 528 layer 15.2 us, shared 16.4).
+constexpr int kJoinUnits = 20;
+FP8_DEVI Run make_run(int tiles, int per, int cta, int grid) {  // per: units of a tile
   Run r;
-  r.total = total;
-  r.grid = min(grid, (total + kMinUnits - 1) / kMinUnits);
+  r.total = tiles * per;
+  r.grid = tiles <= grid && per - r.total / grid <= kJoinUnits ? tiles : min(grid, r.total);
   r.it0 = cta < r.grid ? r.first(cta) : 0;
   r.it1 = cta < r.grid ? r.first(cta + 1) : 0;
   return r;
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     return;
   }
   const int nk = PH == 1 ? p.nk1 : p.nk2;
-  const Run R = make_run(n_act * nk * (PH == 1 ? p.tiles1 : p.tiles2), cta, grid);
+  const Run R = PH == 1 ? make_run(n_act * p.tiles1, nk, cta, grid) : make_run(p.tiles2, n_act * nk, cta, grid);
   const int units = R.it1 - R.it0;
 
   if (warp == 0) {
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       // first units of its weights past its ring go to L2 meanwhile (64.7 us against 66.6 for one token
       // of the 7168 x 2048 layer; asking for them before the last loads have landed delays those).
       if (PH == 1 && !*abort_flag) {
-        const Run R2 = make_run(n_act * p.nk2 * p.tiles2, cta, grid);
+        const Run R2 = make_run(p.tiles2, n_act * p.nk2, cta, grid);
         Walk<2> at2(R2.it0, p, n_act);
         for (int i = R2.it0; i < min(R2.it1, R2.it0 + kPrefetchUnits); ++i, at2.step(1))
           tma_prefetch_3d(&tm_next, at2.kk * 128, at2.tile * kRows, ent_e[at2.a]);
