@@ -9,8 +9,10 @@ them into autograd. No bias: the pages' hot path is the bias-free matmul, and a 
 non-FP8 step."""
 import torch
 
-from . import (GRAN_BLOCK_1x128, GRAN_MX, GRAN_ROW, GRAN_TENSOR, MM_FAST_ACCUM, OP_LINEAR_BWD, OP_LINEAR_FWD, WGRAD_BF16,
-               WGRAD_FP8, fp8_linear_bwd, fp8_linear_fwd, fp8_workspace_size, linear_saved_alloc, make_saved)
+from . import (GRAN_BLOCK_1x128, GRAN_MX, GRAN_ROW, GRAN_TENSOR, MM_FAST_ACCUM, OP_LINEAR_BWD, OP_LINEAR_FWD,
+               SCORE_SOFTMAX, WGRAD_BF16, WGRAD_FP8, add_rmsnorm_alloc, fp8_add_rmsnorm_bwd, fp8_linear_bwd,
+               fp8_linear_fwd, fp8_moe_route_bwd, fp8_workspace_size, linear_saved_alloc, make_saved, moe_route_alloc,
+               rmsnorm_bwd_workspace)
 
 
 def _workspace(nbytes, device):
@@ -103,3 +105,58 @@ def swap_linears(module, granularity=GRAN_ROW, wgrad_mode=WGRAD_BF16, module_fil
 
     visit(module, "")
     return swapped
+
+
+class AddRmsNormFunction(torch.autograd.Function):
+    """(y, h) = norm(x + residual) * weight and the new residual stream; x, residual [..., H] bf16, weight [H] bf16 or
+    fp32. Without a residual (None), h is x. Gradients of x, residual and weight."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps=1e-6):
+        if x.dtype != torch.bfloat16:
+            raise TypeError("AddRmsNormFunction takes bf16 x")
+        H = x.shape[-1]
+        x2 = x.reshape(-1, H).contiguous()
+        r2 = residual.reshape(-1, H).contiguous() if residual is not None else None
+        w = weight.contiguous()
+        h, y, _, _, rstd = add_rmsnorm_alloc(x2, w, eps, r2, want_rstd=True)
+        ctx.save_for_backward(h, w, rstd)
+        ctx.shape, ctx.has_residual = x.shape, residual is not None
+        return y.reshape(x.shape), (h.reshape(x.shape) if residual is not None else x.view_as(x))
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        h, w, rstd = ctx.saved_tensors
+        T, H = h.shape
+        dy2 = dy.reshape(T, H).to(torch.bfloat16).contiguous()
+        dh2 = dh.reshape(T, H).to(torch.bfloat16).contiguous() if dh is not None else None
+        need_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[1]
+        dx = torch.empty_like(h) if need_x else None
+        dw = torch.empty_like(w) if ctx.needs_input_grad[2] else None
+        if need_x or dw is not None:
+            fp8_add_rmsnorm_bwd(dy2, h, w, rstd, dx, dw, dh2,
+                                rmsnorm_bwd_workspace(T, H, h.device) if dw is not None else None)
+        g = dx.reshape(ctx.shape) if need_x else None
+        return (g if ctx.needs_input_grad[0] else None,
+                g if ctx.has_residual and ctx.needs_input_grad[1] else None, dw, None)
+
+
+class MoERouteFunction(torch.autograd.Function):
+    """(weights fp32 [T, k], ids int32 [T, k]) of fp8_moe_route; the gradient of the weights reaches the logits, the
+    choice and its bias get none."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, bias=None, score=SCORE_SOFTMAX, renormalize=True, scale=1.0):
+        logits = logits.contiguous()
+        ids, weights, _, _, _ = moe_route_alloc(logits, top_k, bias, score, renormalize, scale, table=False)
+        ctx.save_for_backward(logits, ids)
+        ctx.args = (score, renormalize, scale)
+        ctx.mark_non_differentiable(ids)
+        return weights, ids
+
+    @staticmethod
+    def backward(ctx, dweights, _):
+        logits, ids = ctx.saved_tensors
+        dlogits = torch.empty_like(logits)
+        fp8_moe_route_bwd(logits, ids, dweights.float().contiguous(), dlogits, *ctx.args)
+        return dlogits, None, None, None, None, None
