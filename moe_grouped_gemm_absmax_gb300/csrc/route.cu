@@ -241,47 +241,63 @@ FP8_DEVI int block_scan(int x, int32_t* warp_sums) {
 }
 
 // Each slot's place: `at` holds the chunk's first place of each expert. Warps take 32 slots each; a slot's
-// place is its expert's, plus the slots of that expert in the warps before (`count`, a row of E2 counts a
-// warp) and in the lanes before. Up to 32 warps, as many as the CTA has and 32 KB of counts allow.
+// place is its expert's, plus the slots of that expert in the warps before and in the lanes before. The
+// warps' counts (`count`, a row of E2 a warp) are summed by two experts a thread, the warps split over up to
+// 8 groups of threads whose totals (`total`, a row of E2 a group) the slots then add up.
 FP8_DEVI int rank_warps(int E2) { return min((int)blockDim.x / 32, E2 <= 512 ? 32 : 16); }
-FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, int32_t* total, uint16_t* count) {
+__host__ __device__ constexpr int most_groups(int E2) { return E2 <= 512 ? 8 : 2; }
+FP8_DEVI int rank_groups(int E2) {
+  int g = most_groups(E2);
+  while (g > 1 && g * (E2 / 2) > (int)blockDim.x) g >>= 1;
+  return g;
+}
+FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, uint16_t* total, uint16_t* count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = rank_warps(p.E2);
+  const int warps = rank_warps(p.E2), groups = rank_groups(p.E2), per = warps / groups, pairs = p.E2 / 2;
   const int64_t n = p.T * p.k, len = p.per_chunk * p.k;
   const int64_t s0 = chunk * len, s1 = s0 + len < n ? s0 + len : n;
+  uint32_t* count2 = reinterpret_cast<uint32_t*>(count);
+  uint32_t* total2 = reinterpret_cast<uint32_t*>(total);
   for (int64_t b = s0; b < s1; b += 32 * warps) {
     const int64_t s = b + threadIdx.x;
-    int id = warp < warps && s < s1 ? p.ids[s] : -1, before = 0;
-    for (int i = threadIdx.x; i < warps * p.E2 / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    const int id = warp < warps && s < s1 ? p.ids[s] : -1;
+    for (int i = threadIdx.x; i < warps * pairs; i += blockDim.x) count2[i] = 0;
     __syncthreads();
+    int before = 0;
     if (warp < warps) {
       const uint32_t same = __match_any_sync(0xffffffffu, id);
       before = __popc(same & ((1u << lane) - 1));
       if (id >= 0 && before == 0) count[warp * p.E2 + id] = (uint16_t)__popc(same);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-      int sum = 0;
-#pragma unroll 8
-      for (int w = 0; w < warps; ++w) {
-        const int c = count[w * p.E2 + e];
-        count[w * p.E2 + e] = (uint16_t)sum;
+    for (int i = threadIdx.x; i < groups * pairs; i += blockDim.x) {
+      const int g = i / pairs, x = i - g * pairs;
+      uint32_t sum = 0;  // two 16-bit sums: at most 1024 slots in all
+#pragma unroll 4
+      for (int w = g * per; w < (g + 1) * per; ++w) {
+        const uint32_t c = count2[w * pairs + x];
+        count2[w * pairs + x] = sum;
         sum += c;
       }
-      total[e] = sum;
+      total2[g * pairs + x] = sum;
     }
     __syncthreads();
     if (warp < warps && s < s1) {
       int32_t place = -1;
       if (id >= 0) {
-        place = at[id] + count[warp * p.E2 + id];
-        place += before;
+        place = at[id] + count[warp * p.E2 + id] + before;
+        for (int g = 0; g < warp / per; ++g) place += total[g * p.E2 + id];
         p.order[place] = (int32_t)s;
       }
       p.pos[s] = place;
     }
+    if (b + 32 * warps >= s1) break;
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) at[e] += total[e];  // the next batch's first places
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {  // the next batch's first places
+      int sum = 0;
+      for (int g = 0; g < groups; ++g) sum += total[g * p.E2 + e];
+      at[e] += sum;
+    }
   }
 }
 // Unused slots leave the end of `order` without a slot.
@@ -329,34 +345,41 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
     __syncthreads();
   }
   fill_order(p, before);
-  place_chunk(p, 0, hist, hist + p.E2, reinterpret_cast<uint16_t*>(hist + 2 * p.E2));
+  place_chunk(p, 0, hist, reinterpret_cast<uint16_t*>(hist + p.E2), reinterpret_cast<uint16_t*>(hist + p.E2) + most_groups(p.E2) * p.E2);
 }
 
 // The table from the chunks' counts. Each CTA sums the whole matrix of counts (16 bits each, 78 KB for 152
 // chunks and 256 experts, from L2) into its own first places, so that no launch is spent on a scan.
 constexpr int kPlaceThreads = 1024;
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs p) {
-  extern __shared__ int32_t sh[];  // [E2] slots, [E2] slots in the chunks before this one, place_chunk's counts
+  extern __shared__ int32_t sh[];  // [E2] slots in the chunks before this one, [E2] slots, then place_chunk's arrays
   __shared__ int32_t warp_sums[32];
-  int32_t* total = sh;
-  int32_t* prior = sh + p.E2;
+  int32_t* prior = sh;
+  int32_t* total = sh + p.E2;
   for (int e = threadIdx.x; e < 2 * p.E2; e += kPlaceThreads) sh[e] = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int pairs = p.E2 / 2;
-  const int lanes = pairs < kPlaceThreads ? pairs : kPlaceThreads;  // threads on a row of counts
-  const int split = kPlaceThreads / lanes;
-  const int grp = threadIdx.x / lanes;
+  const int pairs = p.E2 / 2;  // at most kPlaceThreads / 2
+  const int split = kPlaceThreads / pairs;
+  const int grp = threadIdx.x / pairs;
   if (grp < split) {
     const uint32_t* h = reinterpret_cast<const uint32_t*>(p.hist);
-    const int x = threadIdx.x % lanes;
+    const int x = threadIdx.x - grp * pairs;
     int a0 = 0, a1 = 0, b0 = 0, b1 = 0;
-#pragma unroll 8
-    for (int c = grp; c < p.chunks; c += split) {
-      const uint32_t v = __ldcg(h + (int64_t)c * pairs + x);
-      const int lo = v & 0xFFFF, hi = v >> 16;
-      a0 += lo, a1 += hi;
-      if (c < (int)blockIdx.x) b0 += lo, b1 += hi;
+    constexpr int kRows = 20;  // loads in flight: all of a thread's rows for 152 chunks of 256 experts
+    for (int c0 = grp; c0 < p.chunks; c0 += kRows * split) {
+      uint32_t v[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int c = c0 + i * split;
+        v[i] = c < p.chunks ? __ldcg(h + (int64_t)c * pairs + x) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int lo = v[i] & 0xFFFF, hi = v[i] >> 16;
+        a0 += lo, a1 += hi;
+        if (c0 + i * split < (int)blockIdx.x) b0 += lo, b1 += hi;
+      }
     }
     atomicAdd(total + 2 * x, a0), atomicAdd(total + 2 * x + 1, a1);
     atomicAdd(prior + 2 * x, b0), atomicAdd(prior + 2 * x + 1, b1);
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   const int64_t valid = warp_sums[31];
   __syncthreads();
   fill_order(p, valid);
-  place_chunk(p, blockIdx.x, prior, total, reinterpret_cast<uint16_t*>(sh + 2 * p.E2));
+  place_chunk(p, blockIdx.x, prior, reinterpret_cast<uint16_t*>(total), reinterpret_cast<uint16_t*>(total) + most_groups(p.E2) * p.E2);
 }
 
 // Gradient of the logits, a warp per token. With g_j = scale * dweights_j:
@@ -478,8 +501,8 @@ int64_t chunk_tokens(int64_t T) {
     else { if ((E) % 4 == 0) { CALL(32, true); } else { CALL(32, false); } }                 \
   } while (0)
 
-// Shared memory of place_chunk: first places and totals, a row of counts a warp.
-size_t place_bytes(int E2) { return (size_t)E2 * (8 + 2 * (E2 <= 512 ? 32 : 16)); }
+// Shared memory of place_chunk: first places, group totals, a row of counts a warp.
+size_t place_bytes(int E2) { return (size_t)E2 * (4 + 2 * most_groups(E2) + 2 * (E2 <= 512 ? 32 : 16)); }
 
 }  // namespace
 
