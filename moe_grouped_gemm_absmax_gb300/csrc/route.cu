@@ -128,14 +128,15 @@ struct RouteArgs {
 // before it. Where more than 32 reach it (level values, rows with most experts masked), k steps each take
 // the largest one left. All rows by such steps took 950 instructions a token of 256 experts and k = 8, with
 // each lane's best two kept 780.
-struct Cand {
+struct __align__(16) Cand {
   float sel;
   int e;
+  float logit;
 };
 template <int VPL, bool VEC>
-FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* bias, Cand* cand, int32_t* hist) {
-  float v[VPL], sel[VPL];
-  load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, -INFINITY, v);
+FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* v, const float* bias, Cand* cand,
+                          int32_t* hist) {
+  float sel[VPL];
   float best = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {  // a NaN becomes -inf; experts past E are -inf
@@ -153,21 +154,22 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* 
     const bool in = sel[i] >= bound && sel[i] > -INFINITY;
     const uint32_t m = __ballot_sync(0xffffffffu, in);
     const int at = n + __popc(m & ((1u << lane) - 1));
-    if (in && at < 32) cand[at] = {sel[i], expert_of<VEC>(lane, i)};
+    if (in && at < 32) cand[at] = {sel[i], expert_of<VEC>(lane, i), v[i]};
     n += __popc(m);
   }
   __syncwarp();
   int id = -1, rank = lane;  // this lane's expert and its place among the k
+  float l = 0.f;             // its logit
   if (n <= 32) {
     if (lane < n) {
       const Cand mine = cand[lane];
       rank = 0;
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
-        const Cand c = cand[j];
-        rank += c.sel > mine.sel || (c.sel == mine.sel && c.e < mine.e);
+        const float2 c = *reinterpret_cast<const float2*>(&cand[j]);
+        rank += c.x > mine.sel || (c.x == mine.sel && __float_as_int(c.y) < mine.e);
       }
-      if (rank < p.k) id = mine.e;
+      if (rank < p.k) id = mine.e, l = mine.logit;
     }
   } else {
     uint32_t taken = 0;
@@ -184,9 +186,9 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* 
       if (mine == e) taken |= 1u << bi;
       if (lane == j) id = (int)e;
     }
+    if (id >= 0) l = load_logit(p.logits, p.bf16, t * p.E + id);
   }
   __syncwarp();  // the candidates are read before the next token's are written
-  const float l = id >= 0 ? load_logit(p.logits, p.bf16, t * p.E + id) : 0.f;
   float w = 0.f;
   if (p.softmax) {
     if (p.renorm) {  // softmax over the experts taken
@@ -310,11 +312,11 @@ FP8_DEVI void fill_order(const RouteArgs& p, int64_t valid) {
 // The choice for a chunk of tokens, and the chunk's slots of each expert; with one chunk the table too.
 template <int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
-  extern __shared__ int32_t hist[];  // [E2]; with one chunk also place_chunk's arrays
+  extern __shared__ __align__(16) int32_t hist[];  // [E2], then the warps' candidates, or place_chunk's arrays
   __shared__ int32_t warp_sums[32];
-  __shared__ Cand cand[WARPS][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Cand* cand = reinterpret_cast<Cand*>(hist + (p.E2 + 3) / 4 * 4) + warp * 32;
   if (p.order) {
     for (int e = threadIdx.x; e < p.E2; e += blockDim.x) hist[e] = 0;
     __syncthreads();
@@ -325,7 +327,20 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
 #pragma unroll
   for (int i = 0; i < VPL; ++i) bias[i] = 0.f;
   if (p.bias) load_row<VPL, VEC>(p.bias, 0, 0, p.E, lane, 0.f, bias);
-  for (int64_t t = t0 + warp; t < t1; t += WARPS) route_token<VPL, VEC>(p, t, lane, bias, cand[warp], p.order ? hist : nullptr);
+  // a warp's next row is asked for before it works on this one, where there are registers for it
+  constexpr bool kAhead = VPL <= 8;
+  float v[VPL], next[VPL];
+  if (kAhead && t0 + warp < t1) load_row<VPL, VEC>(p.logits, p.bf16, t0 + warp, p.E, lane, -INFINITY, next);
+  for (int64_t t = t0 + warp; t < t1; t += WARPS) {
+    if (kAhead) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[i] = next[i];
+      if (t + WARPS < t1) load_row<VPL, VEC>(p.logits, p.bf16, t + WARPS, p.E, lane, -INFINITY, next);
+    } else {
+      load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, -INFINITY, v);
+    }
+    route_token<VPL, VEC>(p, t, lane, v, bias, cand, p.order ? hist : nullptr);
+  }
   if (!p.order) return;
   __syncthreads();
   if (p.chunks > 1) {
@@ -518,7 +533,9 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   RouteArgs a = {logits, bf16, bias, T,    (int)E, (int)k, softmax, renorm, scale, ids, weights,
                  order,  pos,  ends, static_cast<uint16_t*>(ws), (int)round_up64(E, 2), chunk_tokens(T), 0};
   a.chunks = (int)ceil_div64(T, a.per_chunk);
-  const size_t smem = a.chunks == 1 ? place_bytes(a.E2) : (size_t)a.E2 * 4;
+  // up to 48 KB, which needs no attribute: place_chunk's 40 to 43 KB and the candidates' 8 to 16 KB share it
+  const size_t choose = (size_t)(a.E2 + 3) / 4 * 16 + (E <= 256 ? 32 : 16) * 32 * sizeof(Cand);
+  const size_t smem = a.chunks == 1 && place_bytes(a.E2) > choose ? place_bytes(a.E2) : choose;
   // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers
 #define FP8_ROUTE(V, X) \
   route_kernel<V, X, (V <= 8 ? 32 : 16)><<<(unsigned)a.chunks, V <= 8 ? 1024 : 512, smem, c.stream>>>(a)
