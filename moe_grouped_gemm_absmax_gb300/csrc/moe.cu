@@ -9,12 +9,14 @@
 //    from HBM by TMA into a shared-memory ring and from there into the tensor cores without
 //    passing through registers. The tokens are its N.
 //  - The activations keep their precision although the MMA takes 8-bit operands: a value v, scaled
-//    by a power of two so that its row's largest lies in [128, 256), is split into e4m3 parts
+//    by a power of two so that the largest around it lies in [128, 256), is split into e4m3 parts
 //    v = p0 + p1 / 16 + p2 / 256, each part the rounding of 16 times what the ones before left. e4m3
 //    has 4 significant bits, so two parts hold a bf16 value's 8 bits exactly (to 2^-21 of the row's
 //    largest for the smallest values) and three hold the hidden layer to 2^-13 or better. The parts
 //    are neighbouring columns of N; the epilogue adds the columns up. That costs columns of N,
-//    which an MMA this narrow has to spare.
+//    which an MMA this narrow has to spare. A token is scaled as a row. The hidden layer is scaled in
+//    blocks of 32, whose scales the block-scaled MMA applies (kind::mxf8f6f4, E8M0; the weights' are one):
+//    a row's scale would need its whole row, another pass over it and another wait.
 //  - Each product is cut into units of 128 rows x 128 K bytes (16 KB), in a fixed order, and each CTA
 //    takes an equal contiguous run of them, whatever tile it ends in (the tail is at most one unit). A
 //    tile that several CTAs share leaves fp32 partial sums in the workspace; the last to arrive adds
@@ -53,7 +55,14 @@ constexpr int kRows = 128;             // weight rows of a tile (64 gate + 64 up
 constexpr int kUnitBytes = kRows * 128;
 constexpr int kMaxStages = 12;
 constexpr int kMaxEntry = 40;          // slots of an entry at most: 128 columns of N in three parts
-constexpr int kBufCols = 128;          // tensor-memory columns of an accumulator
+// Tensor-memory columns: an accumulator's (two of them), then the weights' scales (all one) and those of each
+// stage's activations, 4 columns each; a power of two in all.
+constexpr int buf_cols(int NB) { return NB <= 4 ? 32 : 128; }
+constexpr int tmem_cols(int ph, int NB) {
+  const int need = 2 * buf_cols(NB) + (ph == 2 ? 4 + 4 * 12 : 0);
+  return need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+}
+constexpr int kScaleBytes = 512;       // a stage's activation scales, in the MX scale layout's block of 128 rows
 constexpr int kSmemMax = 232448;       // 227 KB a CTA
 constexpr int kSmemPair = 115712;      // two CTAs an SM: half of 228 KB less the 1 KB reserved for each
 constexpr uint64_t kDrainNs = 2000000000ull;
@@ -70,13 +79,13 @@ struct MoeArgs {
   int cap;                // slots of an entry at most
   int stages, b_bytes;    // ring stages; bytes of a stage's activations, after its weights
   int tiles1, nk1, tiles2, nk2;
-  // workspace; the first three start at zero
+  // workspace; the first two start at zero
   uint32_t* arrived1;     // [CTA c] arrivals at the tile that c starts and does not finish
   uint32_t* arrived2;
-  uint32_t* amax;         // |hidden| maxima as bit patterns [sorted slot]
   const uint8_t* xq;      // the tokens' parts [T][2][128 nk1], zeros past H
   const float* xinv;      // [T]: their powers of two
-  float* act;             // hidden layer [sorted slot][I]
+  uint8_t* hq;            // the hidden layer's parts [sorted slot][3][128 nk2]
+  uint8_t* hs;            // and E8M0 codes of its blocks of 32 [sorted slot][4 nk2]
   float* part;            // partial sums [CTA][2][T][128]
   int32_t* status;
   uint64_t wait_ns;
@@ -95,7 +104,7 @@ struct Shared {
 
 // Shared memory after the ring: offsets in bytes (n = T k slots).
 struct Layout {
-  int acc, shared, wt, inv, mult, hist, ids, ent, slot, total;
+  int acc, shared, wt, inv, hist, ids, ent, slot, total;
 };
 __host__ __device__ inline Layout layout(int ph, int T, int k, int E) {
   const int n = T * k;
@@ -104,8 +113,7 @@ __host__ __device__ inline Layout layout(int ph, int T, int k, int E) {
   L.acc = o, o += ph == 1 ? kPerGroup1 * 64 * 4 : T * kRows * 4;  // up rows on their way to gate rows; output sums
   L.shared = o, o += (int)sizeof(Shared);
   L.wt = o, o += n * 4;    // per sorted slot: its index, then its weight
-  L.inv = o, o += n * 4;   // the activations' power of two
-  L.mult = o, o += n * 4;  // and its inverse
+  L.inv = o, o += n * 4;   // its token's power of two
   L.hist = o, o += n > 32 ? E * 4 : 0;
   L.ids = o, o += n * 4;
   L.ent = o, o += n * 4;   // per entry: expert, first slot
@@ -181,14 +189,26 @@ struct Run {
   FP8_DEVI int owner(int64_t it) const { return (int)(((it + 1) * grid - 1) / total); }
   FP8_DEVI int first(int c) const { return (int)((int64_t)c * total / grid); }
 };
-// A tile shared by CTAs costs its joining, about 3 us of stores, an atomic and loads one after the other; a unit
-// takes an SM 0.15 us. So where there are fewer tiles than CTAs and a whole tile takes no longer than that
-// above an equal share, each CTA takes one tile (one token of a 1040 x 528 layer 15.2 us, shared 16.4).
-constexpr int kJoinUnits = 20;
-FP8_DEVI Run make_run(int tiles, int per, int cta, int grid) {  // per: units of a tile
+// Shares, in the time of a unit (0.15 us an SM). CTAs that share a tile join it: about 3 us of stores, an atomic
+// and loads one after the other, and a load for each of the tile's `cols` slots from each of them (about 32 in
+// flight an SM, 0.8 us). So equal shares for all CTAs are compared with P to a tile, P by the balance of
+// those costs, and with a whole tile each. (One token of a 1040 x 528 layer 15.2 us, shared equally
+// 16.4.)
+constexpr float kJoin = 20.f, kJoinCol = 1.f / 6;
+FP8_DEVI Run make_run(int tiles, int per, int cols, int cta, int grid) {  // per: units of a tile
   Run r;
   r.total = tiles * per;
-  r.grid = tiles <= grid && per - r.total / grid <= kJoinUnits ? tiles : min(grid, r.total);
+  r.grid = min(grid, r.total);
+  if (tiles <= grid) {
+    const float all = (float)r.total / r.grid + kJoin + ((float)r.grid / tiles + 1.f) * cols * kJoinCol;
+    const int P = max(1, min((int)(sqrtf(per / (cols * kJoinCol)) + 0.5f), r.grid / tiles));
+    const float some = (float)per / P + kJoin + P * cols * kJoinCol;
+    const float best = fminf(all, some);
+    if ((float)per <= best)
+      r.grid = tiles;
+    else if (some < all)
+      r.grid = tiles * P;
+  }
   r.it0 = cta < r.grid ? r.first(cta) : 0;
   r.it1 = cta < r.grid ? r.first(cta + 1) : 0;
   return r;
@@ -292,17 +312,17 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
   constexpr int kThreads = 32 * (6 + NB);
   constexpr int kEpi0 = 2 + NB;  // first epilogue warp
   constexpr int kPer = PH == 1 ? kPerGroup1 : kPerGroup2;
+  constexpr int kBufCols = buf_cols(NB), kTmem = tmem_cols(PH, NB);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Layout L = layout(PH, p.T, p.k, p.E);
-  const int stage_bytes = kUnitBytes + p.b_bytes;
+  const int stage_bytes = kUnitBytes + p.b_bytes + (PH == 2 ? 1024 : 0);  // scales: 512 bytes, stages on 1 KB
   uint8_t* rest = smem + p.stages * stage_bytes;
   float* acc = reinterpret_cast<float*>(rest + L.acc);
   Shared& S = *reinterpret_cast<Shared*>(rest + L.shared);
   float* wt = reinterpret_cast<float*>(rest + L.wt);
   int* slot_tmp = reinterpret_cast<int*>(wt);
   float* inv = reinterpret_cast<float*>(rest + L.inv);
-  float* mult = reinterpret_cast<float*>(rest + L.mult);
   int* hist = reinterpret_cast<int*>(rest + L.hist);
   int* ids = reinterpret_cast<int*>(rest + L.ids);
   const int n = p.T * p.k;
@@ -338,9 +358,14 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     fence_mbar_init();
     tma_prefetch_desc(&tm);
   }
+  if (PH == 2) {  // the weights' scales, all one (E8M0 127), for the MMA issuer
+    uint32_t* one = reinterpret_cast<uint32_t*>(smem + kUnitBytes + p.b_bytes + kScaleBytes);
+    for (int i = tid; i < kScaleBytes / 4; i += kThreads) one[i] = 0x7F7F7F7Fu;
+    fence_proxy_async_smem();
+  }
   if (warp == 1) {
     __syncwarp();
-    tmem_alloc(&S.tmem_base, 2 * kBufCols);
+    tmem_alloc(&S.tmem_base, kTmem);
     tmem_relinquish();
   }
   if (n <= 32) {  // one warp, a slot a lane: experts in the order of their first slots
@@ -409,11 +434,12 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     if (PH == 2)
       for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
         p.out[i] = __float2bfloat16_rn(0.f);
-    if (warp == 1) tmem_dealloc(tmem_base, 2 * kBufCols);
+    if (warp == 1) tmem_dealloc(tmem_base, kTmem);
     return;
   }
   const int nk = PH == 1 ? p.nk1 : p.nk2;
-  const Run R = PH == 1 ? make_run(n_act * p.tiles1, nk, cta, grid) : make_run(p.tiles2, n_act * nk, cta, grid);
+  const Run R = PH == 1 ? make_run(n_act * p.tiles1, nk, (used + n_act - 1) / n_act, cta, grid)
+                        : make_run(p.tiles2, n_act * nk, p.T, cta, grid);
   const int units = R.it1 - R.it0;
 
   if (warp == 0) {
@@ -439,7 +465,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       // first units of its weights past its ring go to L2 meanwhile (64.7 us against 66.6 for one token
       // of the 7168 x 2048 layer; asking for them before the last loads have landed delays those).
       if (PH == 1 && !*abort_flag) {
-        const Run R2 = make_run(p.tiles2, n_act * p.nk2, cta, grid);
+        const Run R2 = make_run(p.tiles2, n_act * p.nk2, p.T, cta, grid);
         Walk<2> at2(R2.it0, p, n_act);
         for (int i = R2.it0; i < min(R2.it1, R2.it0 + kPrefetchUnits); ++i, at2.step(1))
           tma_prefetch_3d(&tm_next, at2.kk * 128, at2.tile * kRows, ent_e[at2.a]);
@@ -449,7 +475,15 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
   } else if (warp == 1) {
     // ================================== MMA issuer ==================================
     const bool leader = elect_one();
-    const uint32_t idesc0 = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kRows, 0);
+    const uint32_t idesc0 =
+        PH == 1 ? make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kRows, 0) : make_idesc_mx(kFmtE4M3, kFmtE4M3, kRows, 0);
+    // the weights' scales, all one, from a block of shared memory that the stages' own scales do not reach
+    const uint32_t sfa = tmem_base + 2 * kBufCols, sfb0 = sfa + 4;
+    const uint64_t sf_desc0 = smem_desc_plain(smem_u32(smem) + kUnitBytes + p.b_bytes, 128);
+    if (PH == 2) {
+      if (leader) tmem_cp_sf(sfa, sf_desc0 + (kScaleBytes >> 4));
+      __syncwarp();
+    }
     const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024);
     const uint32_t stage16 = (uint32_t)stage_bytes >> 4;
     bool ok = true;
@@ -481,10 +515,19 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         const uint64_t ad = desc0 + (uint64_t)((uint32_t)s * stage16);
         const uint64_t bd = ad + (kUnitBytes >> 4);
         if (leader) {
-          umma_f8f6f4(d, ad, bd, idesc, i > 0 ? 1u : 0u);
-          umma_f8f6f4(d, ad + 2, bd + 2, idesc, 1u);
-          umma_f8f6f4(d, ad + 4, bd + 4, idesc, 1u);
-          umma_f8f6f4(d, ad + 6, bd + 6, idesc, 1u);
+          if (PH == 1) {
+            umma_f8f6f4(d, ad, bd, idesc, i > 0 ? 1u : 0u);
+            umma_f8f6f4(d, ad + 2, bd + 2, idesc, 1u);
+            umma_f8f6f4(d, ad + 4, bd + 4, idesc, 1u);
+            umma_f8f6f4(d, ad + 6, bd + 6, idesc, 1u);
+          } else {
+            const uint32_t sfb = sfb0 + 4 * s;
+            tmem_cp_sf(sfb, sf_desc0 + (uint64_t)((uint32_t)s * stage16));
+            umma_mx(d, ad, bd, idesc_sf_ids(idesc, 0, 0), sfa, sfb, i > 0 ? 1u : 0u);
+            umma_mx(d, ad + 2, bd + 2, idesc_sf_ids(idesc, 1, 1), sfa, sfb, 1u);
+            umma_mx(d, ad + 4, bd + 4, idesc_sf_ids(idesc, 2, 2), sfa, sfb, 1u);
+            umma_mx(d, ad + 6, bd + 6, idesc_sf_ids(idesc, 3, 3), sfa, sfb, 1u);
+          }
           umma_commit(&S.empty[s]);
           if (i + 1 == left) umma_commit(&S.tfull[buf]);
         }
@@ -554,44 +597,59 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         leave();
       }
     } else {
-      const int col = 4 * lane;  // this lane's 4 of the unit's 128 K values
-      float4 v[kBatch];
-      auto fetch = [&](int j0) {
-        const int k0 = at.kk * 128 + col, cnt = ent_cnt[at.a], start = ent_start[at.a];
+      // the entry's 3 cnt rows of 128 codes, zeros past I (whole 16-byte chunks), and their blocks' scales
+      uint4 v[kBatch];
+      int rows = 0;
+      const int chunk = lane & 7;
+      auto fetch = [&](int r0) {
+        const uint8_t* src = p.hq + at.kk * 128 + chunk * 16;
+        const bool in = at.kk * 128 + chunk * 16 < p.I;
+        const int start = ent_start[at.a];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j0 + b < cnt && k0 < p.I)
-            v[b] = __ldcg(reinterpret_cast<const float4*>(p.act + (int64_t)(start + j0 + b) * p.I + k0));
+          const int row = r0 + 4 * b + (lane >> 3);
+          v[b] = make_uint4(0, 0, 0, 0);
+          if (row < rows && in)
+            v[b] = __ldcg(reinterpret_cast<const uint4*>(src + ((int64_t)start * 3 + row) * (p.nk2 * 128)));
         }
       };
-      if (li < units) fetch(0);
-      for (int i = tid - 64; i < used; i += 32 * NB) {
-        row_scale(__ldcg(p.amax + i), mult + i, inv + i);
-        wt[i] = __ldg(p.weights + slot_tmp[i]);
-      }
+      for (int i = tid - 64; i < used; i += 32 * NB) wt[i] = __ldg(p.weights + slot_tmp[i]);
       named_bar_sync(1, 32 * NB);
       if (lane == 0) mbar_arrive(&S.ready);
       while (li < units) {
         const int cnt = ent_cnt[at.a], start = ent_start[at.a];
+        rows = 3 * cnt;
+        fetch(0);
+        uint32_t code = 0;  // the four blocks' codes of slot `lane`, and below of slot `lane + 32`
+        auto codes = [&](int j) {
+          if (j >= cnt) return 0u;
+          const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(p.hs) + (int64_t)(start + j) * p.nk2 + at.kk);
+          const int blocks = (p.I - at.kk * 128 + 31) / 32;  // blocks with columns below I: the others have no code
+          return blocks >= 4 ? w : w & ((1u << (8 * blocks)) - 1);
+        };
+        code = codes(lane);
         if (!enter()) break;
-        for (int j0 = 0; j0 < cnt; j0 += kBatch) {
-          if (j0) fetch(j0);
+        uint8_t* scales = stage + p.b_bytes;
+        for (int j = lane; j < cnt; j += 32) {
+          if (j >= 32) code = codes(j);
+          const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {  // part q is worth 16^-q: 4 q less in the exponent
+            const uint32_t c = __vsubus4(code, 0x04040404u * q);
+            *reinterpret_cast<uint32_t*>(scales + ((row + q) & 31) * 16 + ((row + q) >> 5) * 4) = c;
+          }
+        }
+        for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
+          if (r0) fetch(r0);
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
-            const int j = j0 + b;
-            if (j >= cnt) break;
-            const float m = mult[start + j];
-            uint32_t o[3];
-            split4<3>(make_float4(v[b].x * m, v[b].y * m, v[b].z * m, v[b].w * m), o);
-            const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-              *reinterpret_cast<uint32_t*>(stage + (row + q) * 128 + (col ^ (((row + q) & 7) << 4))) = o[q];
+            const int row = r0 + 4 * b + (lane >> 3);
+            if (row >= rows) continue;
+            const int to = row / 15 * 16 + row % 15;  // 5 slots to a group of 16 columns
+            *reinterpret_cast<uint4*>(stage + to * 128 + ((chunk ^ (to & 7)) << 4)) = v[b];
           }
         }
         leave();
-        if (li < units) fetch(0);
       }
     }
   } else {
@@ -625,15 +683,22 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       named_bar_sync(2, 128);
       return S.last != 0;
     };
-    // the sum of element `at` over the partial sums of CTAs c0 .. c1, in that order. All but c0 begin
-    // inside the tile, so theirs are their first.
-    auto add_parts = [&](int c0, int c1, int first, int at) {
+    // 8 of a tile's columns (slots or tokens), from `col0` on: the sums of row r over the partial sums of CTAs
+    // c0 .. c1, in that order. All but c0 begin inside the tile, so theirs are their first.
+    auto add_parts = [&](int c0, int c1, int first, int col0, int cols, float* v) {
       const int64_t step = (int64_t)2 * p.T * kRows;
-      const float* o = p.part + c0 * step + at;
-      float v = __ldcg(R.first(c0) >= first ? o : o + p.T * kRows);
-#pragma unroll 8
-      for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(o + (c - c0) * step);
-      return v;
+      const float* o = p.part + c0 * step + (R.first(c0) >= first ? 0 : p.T * kRows) + col0 * kRows + r;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
+      o = p.part + (c0 + 1) * step + col0 * kRows + r;
+#pragma unroll 4
+      for (int c = c0 + 1; c <= c1; ++c, o += step) {
+        float u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += u[j];
+      }
     };
 
     if (PH == 1) {
@@ -648,7 +713,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         const int i = tile * 64 + (r & 63);
         const float s = i < p.I ? __ldg(p.scales + ((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i) : 0.f;
         const bool whole = len == nk;
-        // gate and up of 8 slots' row r -> the hidden layer and its maxima
+        // gate and up of 8 slots' row r -> the hidden layer, its parts and scales
         auto finish = [&](int g, const float* v) {
           if (r >= 64) {
 #pragma unroll
@@ -662,9 +727,19 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
               const int pos = start + g * kPer + j;
               const float gate = v[j] * s;
               const float h = gate / (1.0f + expf(-gate)) * acc[j * 64 + r];
-              if (i < p.I) p.act[(int64_t)pos * p.I + i] = h;
+              // this warp's 32 rows are a block of the hidden layer: its largest in [128, 256) times 2^(code - 127)
               const uint32_t m = __reduce_max_sync(0xffffffffu, i < p.I ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
-              if (lane == 0) red_max_relaxed(p.amax + pos, m);
+              const int ef = (int)(m >> 23);
+              const uint32_t code = ef == 255 ? 0xFFu : (uint32_t)max(ef - 7, 8);  // 8: the third part's is 0
+              float u = i < p.I ? h * mx_inv(code) : 0.f;
+              uint8_t* o = p.hq + (int64_t)pos * 3 * (p.nk2 * 128) + i;
+#pragma unroll
+              for (int part = 0; part < 3; ++part) {
+                const uint32_t e = cvt_fp8x2<FP8_DT_E4M3>(u, 0.f);
+                if (i < p.I) o[part * (p.nk2 * 128)] = (uint8_t)e;
+                u = (u - e4m3x2_to_f32(e).x) * 16.f;
+              }
+              if (lane == 0 && i < p.I) p.hs[(int64_t)pos * (4 * p.nk2) + i / 32] = (uint8_t)code;
             }
           }
           named_bar_sync(2, 128);
@@ -691,9 +766,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
           if (came_last(c0, c1)) {
             for (int g = 0; g * kPer < cnt; ++g) {
               float v[kPer];
-#pragma unroll
-              for (int j = 0; j < kPer; ++j)
-                v[j] = g * kPer + j < cnt ? add_parts(c0, c1, first, (g * kPer + j) * kRows + r) : 0.f;
+              add_parts(c0, c1, first, g * kPer, cnt, v);
               finish(g, v);
             }
           }
@@ -727,9 +800,8 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
             for (int j = 0; j < kPer; ++j) {
               if (g * kPer + j >= cnt) break;
               const int pos = start + g * kPer + j;
-              const float v = __uint_as_float(d[3 * j]) + __uint_as_float(d[3 * j + 1]) * 0.0625f +
-                              __uint_as_float(d[3 * j + 2]) * 0.00390625f;
-              acc[tok[pos] * kRows + r] += wt[pos] * (v * inv[pos] * s);
+              const float v = __uint_as_float(d[3 * j]) + __uint_as_float(d[3 * j + 1]) + __uint_as_float(d[3 * j + 2]);
+              acc[tok[pos] * kRows + r] += wt[pos] * (v * s);
             }
           }
           release_tile(buf);
@@ -744,9 +816,12 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         for (int t = 0; t < p.T; ++t) mine[t * kRows + r] = acc[t * kRows + r];
         const int c0 = R.owner(first), c1 = R.owner(first + per - 1);
         if (came_last(c0, c1)) {
-          for (int t = 0; t < p.T; ++t) {
-            const float v = add_parts(c0, c1, first, t * kRows + r);
-            if (nrow < p.H) p.out[(int64_t)t * p.H + nrow] = __float2bfloat16_rn(v);
+          for (int t0 = 0; t0 < p.T; t0 += 8) {
+            float v[8];
+            add_parts(c0, c1, first, t0, p.T, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (t0 + j < p.T && nrow < p.H) p.out[(int64_t)(t0 + j) * p.H + nrow] = __float2bfloat16_rn(v[j]);
           }
         }
       }
@@ -759,13 +834,13 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     if (lane == 0) mbar_wait(&S.drain, 0, nullptr, kDrainNs);  // the MMAs that write tensor memory
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, 2 * kBufCols);
+    tmem_dealloc(tmem_base, kTmem);
   }
 }
 
-// The workspace: counts and maxima (cleared by each call), the tokens' parts, hidden layer, partial sums.
+// The workspace: counts (cleared by each call), the tokens' parts, the hidden layer's, partial sums.
 struct WsLayout {
-  int64_t arrived2, amax, zeros, xq, xinv, act, part, total;
+  int64_t arrived2, zeros, xq, xinv, hq, hs, part, total;
 };
 constexpr int64_t kMaxGrid = 160;  // CTAs that the workspace holds partial sums for
 WsLayout ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
@@ -773,12 +848,12 @@ WsLayout ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   const int64_t n = T * k;
   int64_t o = kMaxGrid * 4;
   L.arrived2 = o, o += kMaxGrid * 4;
-  L.amax = o, o += n * 4;
   L.zeros = o / 4;
   o = round_up64(o, 256);
   L.xq = o, o += T * 2 * round_up64(H, 128);
   L.xinv = o, o += round_up64(T * 4, 256);
-  L.act = o, o += round_up64(n * I * 4, 256);
+  L.hq = o, o += n * 3 * round_up64(I, 128);
+  L.hs = o, o += round_up64(n * 4 * ceil_div64(I, 128), 256);
   L.part = o, o += kMaxGrid * 2 * T * kRows * 4;
   L.total = o;
   return L;
@@ -787,7 +862,7 @@ WsLayout ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
 template <int PH, int NB>
 int run_moe(const CUtensorMap& tm, const CUtensorMap& tm_next, MoeArgs a, int room, int grid, const Ctx& c) {
   const Layout L = layout(PH, a.T, a.k, a.E);
-  const int stage_bytes = kUnitBytes + a.b_bytes;
+  const int stage_bytes = kUnitBytes + a.b_bytes + (PH == 2 ? 1024 : 0);
   const int fit = (room - 1024 - L.total) / stage_bytes;  // at least 4: T, k and E are bounded
   a.stages = fit < kMaxStages ? fit : kMaxStages;
   const size_t smem = 1024 + (size_t)a.stages * stage_bytes + L.total;
@@ -837,10 +912,10 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   a.nk2 = (int)ceil_div64(I, 128);
   a.arrived1 = reinterpret_cast<uint32_t*>(base);
   a.arrived2 = reinterpret_cast<uint32_t*>(base + W.arrived2);
-  a.amax = reinterpret_cast<uint32_t*>(base + W.amax);
   a.xq = base + W.xq;
   a.xinv = reinterpret_cast<const float*>(base + W.xinv);
-  a.act = reinterpret_cast<float*>(base + W.act);
+  a.hq = base + W.hq;
+  a.hs = base + W.hs;
   a.part = reinterpret_cast<float*>(base + W.part);
   a.status = c.status;
   a.wait_ns = c.wait_ns;
