@@ -54,6 +54,7 @@ namespace {
 constexpr int kRows = 128;             // weight rows of a tile (64 gate + 64 up rows in the first product)
 constexpr int kUnitBytes = kRows * 128;
 constexpr int kMaxStages = 12;
+constexpr int kFewTokens = 8;          // two CTAs an SM up to here; an entry's slots are at most as many
 constexpr int kMaxEntry = 40;          // slots of an entry at most: 128 columns of N in three parts
 // Tensor-memory columns: an accumulator's (two of them), then the weights' scales (all one) and those of each
 // stage's activations, 4 columns each; a power of two in all.
@@ -110,7 +111,7 @@ __host__ __device__ inline Layout layout(int ph, int T, int k, int E) {
   const int n = T * k;
   Layout L;
   int o = 0;
-  L.acc = o, o += ph == 1 ? kPerGroup1 * 64 * 4 : T * kRows * 4;  // up rows on their way to gate rows; output sums
+  L.acc = o, o += ph == 1 ? 2 * kPerGroup1 * 64 * 4 : T * kRows * 4;  // gate and up on their way; output sums
   L.shared = o, o += (int)sizeof(Shared);
   L.wt = o, o += n * 4;    // per sorted slot: its index, then its weight
   L.inv = o, o += n * 4;   // its token's power of two
@@ -143,6 +144,11 @@ FP8_DEVI void tma_prefetch_3d(const CUtensorMap* m, int32_t x, int32_t y, int32_
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
                    reinterpret_cast<uint64_t>(m)),
                "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+// 16 bytes global -> shared without passing through registers; zeros where `valid` is false.
+FP8_DEVI void cp_async16(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
                : "memory");
 }
 FP8_DEVI bool elect_one() {
@@ -304,6 +310,11 @@ FP8_DEVI int valid_id(const MoeArgs& p, int s) {
   if (blockIdx.x == 0) set_status(p.status, FP8_DEV_BAD_IDS);
   return -1;
 }
+
+template <int N>
+struct Width {
+  static constexpr int value = N;
+};
 
 // PH: 1 the hidden layer, 2 the output. NB: builder warps.
 template <int PH, int NB>
@@ -564,93 +575,75 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       li += builders;
       at.step(builders);
     };
-    // Rows are loaded four at a time, a unit's first ones before the wait for its stage.
-    constexpr int kBatch = 4;
+    // 8 lanes copy a row of 128 codes. An entry of few slots (NB 4) has its rows in flight, in registers, before the
+    // wait for the unit's stage: that is worth 2 us of one token's 65. Entries of more are copied
+    // asynchronously, all rows at once, one memory latency a unit whatever its rows (through registers, 16 at a
+    // time, 32 tokens on 11 experts of 1392 x 1024 took 52 us instead of 39).
+    const int chunk = lane & 7;
+    constexpr bool kAhead = NB <= 4;
+    constexpr int kBatch = kAhead ? (PH + 1) * kFewTokens / 4 : 1;  // loads a lane for an entry's rows
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' parts / the hidden layer are there
-    if (PH == 1) {
-      // the entry's 2 cnt rows of 128 codes: 8 lanes a row, 4 rows a step
-      uint4 v[kBatch];
-      int rows = 0;
-      auto fetch = [&](int r0) {
-        const uint8_t* src = p.xq + at.kk * 128 + (lane & 7) * 16;
-        const int start = ent_start[at.a];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int row = r0 + 4 * b + (lane >> 3);
-          if (row < rows)
-            v[b] = __ldcg(reinterpret_cast<const uint4*>(
-                src + (int64_t)(2 * tok[start + (row >> 1)] + (row & 1)) * (p.nk1 * 128)));
-        }
-      };
-      while (li < units) {
-        rows = 2 * ent_cnt[at.a];
-        fetch(0);
-        if (!enter()) break;
-        for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
-          if (r0) fetch(r0);
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int row = r0 + 4 * b + (lane >> 3);
-            if (row < rows) *reinterpret_cast<uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) = v[b];
-          }
-        }
-        leave();
-      }
-    } else {
-      // the entry's 3 cnt rows of 128 codes, zeros past I (whole 16-byte chunks), and their blocks' scales
-      uint4 v[kBatch];
-      int rows = 0;
-      const int chunk = lane & 7;
-      auto fetch = [&](int r0) {
-        const uint8_t* src = p.hq + at.kk * 128 + chunk * 16;
-        const bool in = at.kk * 128 + chunk * 16 < p.I;
-        const int start = ent_start[at.a];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int row = r0 + 4 * b + (lane >> 3);
-          v[b] = make_uint4(0, 0, 0, 0);
-          if (row < rows && in)
-            v[b] = __ldcg(reinterpret_cast<const uint4*>(src + ((int64_t)start * 3 + row) * (p.nk2 * 128)));
-        }
-      };
+    if (PH == 2) {
       for (int i = tid - 64; i < used; i += 32 * NB) wt[i] = __ldg(p.weights + slot_tmp[i]);
       named_bar_sync(1, 32 * NB);
       if (lane == 0) mbar_arrive(&S.ready);
-      while (li < units) {
-        const int cnt = ent_cnt[at.a], start = ent_start[at.a];
-        rows = 3 * cnt;
-        fetch(0);
-        uint32_t code = 0;  // the four blocks' codes of slot `lane`, and below of slot `lane + 32`
-        auto codes = [&](int j) {
-          if (j >= cnt) return 0u;
-          const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(p.hs) + (int64_t)(start + j) * p.nk2 + at.kk);
-          const int blocks = (p.I - at.kk * 128 + 31) / 32;  // blocks with columns below I: the others have no code
-          return blocks >= 4 ? w : w & ((1u << (8 * blocks)) - 1);
-        };
-        code = codes(lane);
-        if (!enter()) break;
+    }
+    while (li < units) {
+      const int cnt = ent_cnt[at.a], start = ent_start[at.a];
+      const int k0 = at.kk * 128 + chunk * 16;
+      // the codes of four blocks of slot `lane`'s hidden layer; blocks past I have none
+      auto codes = [&](int j) {
+        const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(p.hs) + (int64_t)(start + j) * p.nk2 + at.kk);
+        const int blocks = (p.I - at.kk * 128 + 31) / 32;
+        return blocks >= 4 ? w : w & ((1u << (8 * blocks)) - 1);
+      };
+      uint32_t code = PH == 2 && lane < cnt ? codes(lane) : 0u;
+      // row `row` of the entry's: 2 a slot (its token's parts), or 3 a slot, 15 to a group of 16 columns, zeros past I
+      const int rows = (PH + 1) * cnt;
+      const bool in = PH == 1 || k0 < p.I;
+      auto from = [&](int row) {
+        return PH == 1 ? p.xq + (int64_t)(2 * tok[start + (row >> 1)] + (row & 1)) * (p.nk1 * 128) + k0
+                       : p.hq + ((int64_t)start * 3 + row) * (p.nk2 * 128) + k0;
+      };
+      auto to = [&](int row) {
+        const int t = PH == 1 ? row : row + row / 15;
+        return stage + t * 128 + ((chunk ^ (t & 7)) << 4);
+      };
+      uint4 v[kBatch];
+      if (kAhead) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int row = 4 * b + (lane >> 3);
+          v[b] = row < rows && in ? __ldcg(reinterpret_cast<const uint4*>(from(row))) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (!enter()) break;
+      if (kAhead) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int row = 4 * b + (lane >> 3);
+          if (row < rows) *reinterpret_cast<uint4*>(to(row)) = v[b];
+        }
+      } else {
+        for (int row = lane >> 3; row < rows; row += 4) cp_async16(to(row), from(row), in);
+      }
+      if (PH == 2) {
         uint8_t* scales = stage + p.b_bytes;
         for (int j = lane; j < cnt; j += 32) {
           if (j >= 32) code = codes(j);
-          const int row = 16 * (j / kPerGroup2) + 3 * (j % kPerGroup2);
+          const int row = 3 * j + j / kPerGroup2;
 #pragma unroll
           for (int q = 0; q < 3; ++q) {  // part q is worth 16^-q: 4 q less in the exponent
             const uint32_t c = __vsubus4(code, 0x04040404u * q);
             *reinterpret_cast<uint32_t*>(scales + ((row + q) & 31) * 16 + ((row + q) >> 5) * 4) = c;
           }
         }
-        for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
-          if (r0) fetch(r0);
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int row = r0 + 4 * b + (lane >> 3);
-            if (row >= rows) continue;
-            const int to = row / 15 * 16 + row % 15;  // 5 slots to a group of 16 columns
-            *reinterpret_cast<uint4*>(stage + to * 128 + ((chunk ^ (to & 7)) << 4)) = v[b];
-          }
-        }
-        leave();
       }
+      if (!kAhead) {
+        cp_async_commit();
+        cp_async_wait<0>();
+      }
+      leave();
     }
   } else {
     // ================================== epilogue ==================================
@@ -683,26 +676,28 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       named_bar_sync(2, 128);
       return S.last != 0;
     };
-    // 8 of a tile's columns (slots or tokens), from `col0` on: the sums of row r over the partial sums of CTAs
+    // W of a tile's columns (slots or tokens), from `col0` on: the sums of row r over the partial sums of CTAs
     // c0 .. c1, in that order. All but c0 begin inside the tile, so theirs are their first.
-    auto add_parts = [&](int c0, int c1, int first, int col0, int cols, float* v) {
+    auto add_parts = [&](auto width, int c0, int c1, int first, int col0, int cols, float* v) {
+      constexpr int W = decltype(width)::value;
       const int64_t step = (int64_t)2 * p.T * kRows;
       const float* o = p.part + c0 * step + (R.first(c0) >= first ? 0 : p.T * kRows) + col0 * kRows + r;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
+      for (int j = 0; j < W; ++j) v[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
       o = p.part + (c0 + 1) * step + col0 * kRows + r;
-#pragma unroll 4
+#pragma unroll 2
       for (int c = c0 + 1; c <= c1; ++c, o += step) {
-        float u[8];
+        float u[W];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
+        for (int j = 0; j < W; ++j) u[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += u[j];
+        for (int j = 0; j < W; ++j) v[j] += u[j];
       }
     };
 
     if (PH == 1) {
       // ---- hidden = silu(gate) * up ----
+      int xbuf = 0;
       asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int i = tid - 32 * kEpi0; i < used; i += 128) inv[i] = __ldcg(p.xinv + tok[i]);
       named_bar_sync(2, 128);
@@ -713,36 +708,53 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         const int i = tile * 64 + (r & 63);
         const float s = i < p.I ? __ldg(p.scales + ((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i) : 0.f;
         const bool whole = len == nk;
-        // gate and up of 8 slots' row r -> the hidden layer, its parts and scales
+        // Gate or up of 8 slots' row r -> the hidden layer, its parts and scales. The gate rows' threads take the
+        // first four slots, the up rows' the others; each gives the other side what it lacks.
         auto finish = [&](int g, const float* v) {
-          if (r >= 64) {
+          float* xch = acc + xbuf * (kPer * 64);
+          xbuf ^= 1;  // two buffers: one is read while the next group's is written
+          const bool gate_row = r < 64;
+          const int row = r & 63;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) acc[j * 64 + r - 64] = v[j] * s;
-          }
+          for (int j = 0; j < 4; ++j) xch[(gate_row ? j + 4 : j) * 64 + row] = (gate_row ? v[j + 4] : v[j]) * s;
           named_bar_sync(2, 128);
-          if (r < 64) {
+          const int j0 = gate_row ? 0 : 4;
+          float h[4];
+          uint32_t m[4];
+          // with few slots (NB 4) only those there are, else all four side by side
+          const int live = NB <= 4 ? cnt - g * kPer - j0 : 4;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-              if (g * kPer + j >= cnt) break;
-              const int pos = start + g * kPer + j;
-              const float gate = v[j] * s;
-              const float h = gate / (1.0f + expf(-gate)) * acc[j * 64 + r];
-              // this warp's 32 rows are a block of the hidden layer: its largest in [128, 256) times 2^(code - 127)
-              const uint32_t m = __reduce_max_sync(0xffffffffu, i < p.I ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
-              const int ef = (int)(m >> 23);
-              const uint32_t code = ef == 255 ? 0xFFu : (uint32_t)max(ef - 7, 8);  // 8: the third part's is 0
-              float u = i < p.I ? h * mx_inv(code) : 0.f;
-              uint8_t* o = p.hq + (int64_t)pos * 3 * (p.nk2 * 128) + i;
+          for (int j = 0; j < 4; ++j) {
+            if (j >= live) break;
+            const float other = xch[(j0 + j) * 64 + row];
+            const float own = (gate_row ? v[j] : v[j + 4]) * s;
+            const float gate = gate_row ? own : other, up = gate_row ? other : own;
+            h[j] = i < p.I ? gate / (1.0f + expf(-gate)) * up : 0.f;
+          }
+          // this warp's 32 rows are a block of the hidden layer: its largest in [128, 256) times 2^(code - 127)
 #pragma unroll
-              for (int part = 0; part < 3; ++part) {
-                const uint32_t e = cvt_fp8x2<FP8_DT_E4M3>(u, 0.f);
-                if (i < p.I) o[part * (p.nk2 * 128)] = (uint8_t)e;
-                u = (u - e4m3x2_to_f32(e).x) * 16.f;
-              }
-              if (lane == 0 && i < p.I) p.hs[(int64_t)pos * (4 * p.nk2) + i / 32] = (uint8_t)code;
+          for (int j = 0; j < 4; ++j) {
+            if (j >= live) break;
+            m[j] = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j >= live) break;
+            const int idx = g * kPer + j0 + j;
+            const int ef = (int)(m[j] >> 23);
+            const uint32_t code = ef == 255 ? 0xFFu : (uint32_t)max(ef - 7, 8);  // 8: the third part's is 0
+            float u = h[j] * mx_inv(code);
+            const int64_t pos = start + idx;
+            uint8_t* o = p.hq + pos * 3 * (p.nk2 * 128) + i;
+            const bool put = idx < cnt && i < p.I;
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              const uint32_t e = cvt_fp8x2<FP8_DT_E4M3>(u, 0.f);
+              if (put) o[part * (p.nk2 * 128)] = (uint8_t)e;
+              u = (u - e4m3x2_to_f32(e).x) * 16.f;
             }
+            if (lane == 0 && put) p.hs[pos * (4 * p.nk2) + i / 32] = (uint8_t)code;
           }
-          named_bar_sync(2, 128);
         };
         const int buf = seg & 1;
         if (!wait_tile(buf)) break;
@@ -766,7 +778,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
           if (came_last(c0, c1)) {
             for (int g = 0; g * kPer < cnt; ++g) {
               float v[kPer];
-              add_parts(c0, c1, first, g * kPer, cnt, v);
+              add_parts(Width<kPer>{}, c0, c1, first, g * kPer, cnt, v);
               finish(g, v);
             }
           }
@@ -816,11 +828,12 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         for (int t = 0; t < p.T; ++t) mine[t * kRows + r] = acc[t * kRows + r];
         const int c0 = R.owner(first), c1 = R.owner(first + per - 1);
         if (came_last(c0, c1)) {
-          for (int t0 = 0; t0 < p.T; t0 += 8) {
-            float v[8];
-            add_parts(c0, c1, first, t0, p.T, v);
+          constexpr int W = NB <= 4 ? kFewTokens : 16;
+          for (int t0 = 0; t0 < p.T; t0 += W) {
+            float v[W];
+            add_parts(Width<W>{}, c0, c1, first, t0, p.T, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < W; ++j)
               if (t0 + j < p.T && nrow < p.H) p.out[(int64_t)(t0 + j) * p.H + nrow] = __float2bfloat16_rn(v[j]);
           }
         }
@@ -948,7 +961,7 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   // With few tokens a stage is hardly more than its weights, and half an SM's shared memory holds
   // enough of them in flight: the two products run side by side. More tokens need longer stages and
   // more builders, and the second product then follows on each SM as the first leaves it.
-  if (T <= 8) {
+  if (T <= kFewTokens) {
     a.scales = s13;
     const int rc = run_moe<1, 4>(t13, t2, a, kSmemPair, grid, c);
     if (rc != FP8_OK) return rc;
