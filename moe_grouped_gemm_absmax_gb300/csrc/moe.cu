@@ -189,32 +189,38 @@ FP8_DEVI void split4(float4 v, uint32_t* out) {
   }
 }
 
-// One product's share of a CTA: units [it0, it1) of `total`, tile after tile of nk units each.
+// One product's share of a CTA: units [it0, it1) of `total`, tile after tile of `per` units each. Shares are
+// contiguous and equal, to a unit or (whole) to a tile.
 struct Run {
   int total, it0, it1, grid;  // grid: CTAs with a share
-  FP8_DEVI int owner(int64_t it) const { return (int)(((it + 1) * grid - 1) / total); }
-  FP8_DEVI int first(int c) const { return (int)((int64_t)c * total / grid); }
+  int quantum, quanta;        // 1, or the units of a tile; how many of them
+  FP8_DEVI int owner(int64_t it) const { return (int)(((it + 1) * grid - 1) / total); }  // for quantum 1
+  FP8_DEVI int first(int c) const { return (int)((int64_t)c * quanta / grid) * quantum; }
 };
-// Shares, in the time of a unit (0.15 us an SM). CTAs that share a tile join it: about 3 us of stores, an atomic
-// and loads one after the other, and a load for each of the tile's `cols` slots from each of them (about 32 in
-// flight an SM, 0.8 us). So equal shares for all CTAs are compared with P to a tile, P by the balance of
-// those costs, and with a whole tile each. (One token of a 1040 x 528 layer 15.2 us, shared equally
-// 16.4.)
-constexpr float kJoin = 20.f, kJoinCol = 1.f / 6;
-FP8_DEVI Run make_run(int tiles, int per, int cols, int cta, int grid) {  // per: units of a tile
+// How to share, by the time it takes. All units take kUsAll each at the memory's rate; a CTA's own take at
+// least kUsOne each, by the latency of its ring. Whole tiles may leave CTAs unequal, which costs nothing while
+// the memory is the limit. A tile that P CTAs share is joined: kUsJoin for the stores, an atomic and loads one
+// after the other, and kUsColumn for each of its `cols` slots from each of the P. (A 1040 x 528
+// layer, one token: 14.6 us with whole tiles, 16.4 shared equally; 9 tokens on 13 experts of 1024 x 256 16 and
+// 20 us.)
+constexpr float kUsAll = 0.0023f, kUsOne = 0.35f, kUsJoin = 3.f, kUsColumn = 0.025f;
+FP8_DEVI Run make_run(int tiles, int per, int cols, int cta, int grid) {
   Run r;
   r.total = tiles * per;
-  r.grid = min(grid, r.total);
+  const float all = r.total * kUsAll;
+  auto cost = [&](float most, float P) { return fmaxf(all, most * kUsOne) + kUsJoin + P * cols * kUsColumn; };
+  const int g = min(grid, r.total);
+  const float whole = fmaxf(all, (float)((tiles + grid - 1) / grid * per) * kUsOne);
+  const float equal = cost((float)r.total / g, fmaxf((float)g / tiles, 1.f) + 1.f);
+  r.grid = g;
+  r.quantum = 1, r.quanta = r.total;
+  float best = equal;
   if (tiles <= grid) {
-    const float all = (float)r.total / r.grid + kJoin + ((float)r.grid / tiles + 1.f) * cols * kJoinCol;
-    const int P = max(1, min((int)(sqrtf(per / (cols * kJoinCol)) + 0.5f), r.grid / tiles));
-    const float some = (float)per / P + kJoin + P * cols * kJoinCol;
-    const float best = fminf(all, some);
-    if ((float)per <= best)
-      r.grid = tiles;
-    else if (some < all)
-      r.grid = tiles * P;
+    const int P = max(1, min((int)(sqrtf(per * kUsOne / (cols * kUsColumn)) + 0.5f), grid / tiles));
+    const float some = cost((float)per / P, (float)P);
+    if (some < best && tiles * P <= r.total) best = some, r.grid = tiles * P;
   }
+  if (whole <= best) r.grid = min(grid, tiles), r.quantum = per, r.quanta = tiles;
   r.it0 = cta < r.grid ? r.first(cta) : 0;
   r.it1 = cta < r.grid ? r.first(cta + 1) : 0;
   return r;
@@ -472,14 +478,17 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       }
       for (int i = li > p.stages ? li - p.stages : 0; i < li; ++i)  // loads in flight land before exit
         mbar_wait(&S.full[i % p.stages], (uint32_t)((i / p.stages) & 1), nullptr, kDrainNs);
-      // While the last tiles' sums are joined and the second product starts up, memory would idle: the
-      // first units of its weights past its ring go to L2 meanwhile (64.7 us against 66.6 for one token
-      // of the 7168 x 2048 layer; asking for them before the last loads have landed delays those).
+      // While the last tiles' sums are joined and the second product starts up, memory would idle: where that
+      // product is short, the first units of its weights go to L2 meanwhile (63.9 us against 65.5 for one token
+      // of the 7168 x 2048 layer; for 32 tokens 908 against 899). Asking for them before the last loads have
+      // landed delays those.
       if (PH == 1 && !*abort_flag) {
         const Run R2 = make_run(p.tiles2, n_act * p.nk2, p.T, cta, grid);
-        Walk<2> at2(R2.it0, p, n_act);
-        for (int i = R2.it0; i < min(R2.it1, R2.it0 + kPrefetchUnits); ++i, at2.step(1))
-          tma_prefetch_3d(&tm_next, at2.kk * 128, at2.tile * kRows, ent_e[at2.a]);
+        if (R2.it1 - R2.it0 <= 16 * kPrefetchUnits) {
+          Walk<2> at2(R2.it0, p, n_act);
+          for (int i = R2.it0; i < min(R2.it1, R2.it0 + kPrefetchUnits); ++i, at2.step(1))
+            tma_prefetch_3d(&tm_next, at2.kk * 128, at2.tile * kRows, ent_e[at2.a]);
+        }
       }
     }
     __syncwarp();
