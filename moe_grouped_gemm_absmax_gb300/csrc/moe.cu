@@ -401,44 +401,57 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       }
       if (lane == 0) S.n_act = ents, S.used = slots;
     }
-  } else {  // by a count of each expert's slots
-    for (int e = tid; e < p.E; e += kThreads) hist[e] = 0;
+  } else {
+    // Each 32 slots count theirs by expert; the counts of the 32s before (in the ring, which is still empty) and
+    // of the experts before are a slot's place.
+    uint16_t* count = reinterpret_cast<uint16_t*>(smem + stage_bytes);  // [groups][E]
+    const int groups = (n + 31) / 32, chunks = (p.E + 31) / 32;
+    int* chunk_sum = reinterpret_cast<int*>(smem + stage_bytes + (groups * p.E * 2 + 15) / 16 * 16);  // [chunks][2]
+    for (int i = tid; i < groups * p.E; i += kThreads) count[i] = 0;
+    __syncthreads();
+    for (int g = warp; g < groups; g += kThreads / 32) {
+      const int s = g * 32 + lane;
+      const int id = s < n ? valid_id(p, s) : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      const int before = __popc(same & ((1u << lane) - 1));
+      if (id >= 0 && before == 0) count[g * p.E + id] = (uint16_t)__popc(same);
+      if (s < n) ids[s] = id < 0 ? -1 : id | before << 16;
+    }
+    __syncthreads();
+    for (int c = warp; c < chunks; c += kThreads / 32) {
+      const int e = c * 32 + lane;
+      int cnt = 0;
+      if (e < p.E)
+        for (int g = 0; g < groups; ++g) {
+          const int x = count[g * p.E + e];
+          count[g * p.E + e] = (uint16_t)cnt;
+          cnt += x;
+        }
+      if (e < p.E) hist[e] = cnt;
+      const int ts = __reduce_add_sync(0xffffffffu, cnt), te = __reduce_add_sync(0xffffffffu, (cnt + p.cap - 1) / p.cap);
+      if (lane == 0) chunk_sum[2 * c] = ts, chunk_sum[2 * c + 1] = te;
+    }
+    __syncthreads();
+    for (int c = warp; c < chunks; c += kThreads / 32) {
+      const int e = c * 32 + lane;
+      const int cnt = e < p.E ? hist[e] : 0;
+      int s0, a0, ts, te;
+      scan2(cnt, (cnt + p.cap - 1) / p.cap, lane, &s0, &a0, &ts, &te);
+      const int bs = __reduce_add_sync(0xffffffffu, lane < c ? chunk_sum[2 * lane] : 0);  // E <= 1024: a chunk a lane
+      const int ba = __reduce_add_sync(0xffffffffu, lane < c ? chunk_sum[2 * lane + 1] : 0);
+      if (e < p.E) hist[e] = bs + s0;
+      put_entries(p, e, cnt, bs + s0, ba + a0, ent_e, ent_start, ent_cnt);
+      if (c == chunks - 1 && lane == 0) S.n_act = ba + te, S.used = bs + ts;
+    }
     __syncthreads();
     for (int s = tid; s < n; s += kThreads) {
-      const int id = valid_id(p, s);
-      ids[s] = id;
-      if (id >= 0) atomicAdd(hist + id, 1);
+      const int v = ids[s];
+      if (v < 0) continue;
+      const int id = v & 0xFFFF, at = hist[id] + count[(s >> 5) * p.E + id] + (v >> 16);
+      slot_tmp[at] = s;
+      tok[at] = (uint16_t)(s / p.k);
     }
-    __syncthreads();
-    if (warp == 0) {
-      int slots = 0, ents = 0;
-      for (int b = 0; b < p.E; b += 32) {
-        const int e = b + lane;
-        const int cnt = e < p.E ? hist[e] : 0;
-        int s0, a0, ts, te;
-        scan2(cnt, (cnt + p.cap - 1) / p.cap, lane, &s0, &a0, &ts, &te);
-        if (e < p.E) hist[e] = slots + s0;
-        put_entries(p, e, cnt, slots + s0, ents + a0, ent_e, ent_start, ent_cnt);
-        slots += ts;
-        ents += te;
-      }
-      if (lane == 0) S.n_act = ents, S.used = slots;
-      __syncwarp();
-      for (int b = 0; b < n; b += 32) {
-        const int s = b + lane;
-        const int id = s < n ? ids[s] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, id);
-        const int before = __popc(same & ((1u << lane) - 1));
-        const int at = id >= 0 ? hist[id] + before : 0;
-        __syncwarp();
-        if (id >= 0) {
-          slot_tmp[at] = s;
-          tok[at] = (uint16_t)(s / p.k);
-          if (before == 0) hist[id] += __popc(same);
-        }
-        __syncwarp();
-      }
-    }
+    fence_proxy_async_smem();  // the ring's first loads come after these accesses
   }
   tc_fence_before();
   __syncthreads();

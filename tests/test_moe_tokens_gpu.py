@@ -207,3 +207,22 @@ def test_wait_limit_expiry_reports_timeout_and_context_survives(fp8, T, E, k, H,
         fp8.fp8_set_wait_limit_ns(old)
     assert int(st) & fp8.DEV_TIMEOUT
     _check(fp8, x, ids, wt, layer)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 1024, 16, 48, 32), (40, 1000, 16, 272, 48), (3, 1024, 16, 144, 64), (33, 2, 1, 256, 128),
+                                       (9, 300, 5, 1040, 272)])
+def test_many_experts_and_slots(fp8, T, E, k, H, I):
+    """The counting of slots by expert at its limits, and a token's unused slots in between."""
+    layer, g = _layer(E, H, I, T * E)
+    x, ids, wt = _tokens(g, T, H, E, k)
+    _check(fp8, x, ids, wt, layer)
+    ids[torch.rand(T, k, generator=g, device="cuda") < 0.3] = -1
+    _check(fp8, x, ids, wt, layer)
+
+
+def test_one_expert_takes_every_slot(fp8):
+    """64 tokens that name one expert 16 times each: 1024 slots, in entries of 40."""
+    layer, g = _layer(3, 272, 144, 9)
+    x, ids, wt = _tokens(g, 64, 272, 3, 1)
+    _check(fp8, x, torch.full((64, 16), 1, dtype=torch.int32, device="cuda"), torch.randn(64, 16, generator=g, device="cuda"),
+           layer)
