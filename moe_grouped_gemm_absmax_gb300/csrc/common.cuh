@@ -253,6 +253,14 @@ FP8_DEVI bool wait_count_geq(const uint32_t* p, uint32_t target, uint64_t limit_
 }
 
 // ------------------------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel launched by launch_dependent() may begin before the kernel before
+// it on the stream has ended, and waits here until that one has ended and its writes are visible. Nothing
+// that the kernel before may write is read, and nothing that it may read is written, ahead of the wait.
+FP8_DEVI void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Once every CTA has come here (or ended), the next kernel may begin.
+FP8_DEVI void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ------------------------------------------------------------------------------------------
 // mbarrier
 FP8_DEVI void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

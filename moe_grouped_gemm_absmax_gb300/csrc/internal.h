@@ -19,6 +19,23 @@ struct Ctx {
   int test_stall;    // failure-detection test hook (see fp8_set_test_stall)
 };
 
+// Launch that may begin before the kernel before it on the stream has ended (see pdl_wait()): its launch
+// and the kernel's start overlap that one's tail.
+template <typename... P, typename... A>
+int launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
+
 struct ScaleTab;
 // The scale table of a format (FP8_DT_E4M3 / FP8_DT_E5M2), built once on the host in fp64.
 const ScaleTab& scale_tab(int fmt);

@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kSplitThreads) moe_split_kernel(const uint16_t
                                                                   uint8_t* __restrict__ xq, float* __restrict__ xinv,
                                                                   uint32_t* __restrict__ counters, int n_counters) {
   __shared__ uint32_t red[kSplitThreads / 32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
+  pdl_trigger();  // after the wait: the next kernel reads ids ahead of its own
   const int t = blockIdx.x, tid = threadIdx.x;
   if (t == 0)
     for (int i = tid; i < n_counters; i += kSplitThreads) counters[i] = 0;
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       set_status(p.status, FP8_DEV_TIMEOUT);
     }
   };
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
 
   if (tid == 32) {
     for (int s = 0; s < p.stages; ++s) {
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
   const int n_act = S.n_act, used = S.used;
 
   if (n_act == 0) {  // nothing to read: zeros
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // not done before the kernel before it is
+    pdl_wait();  // not done before the kernel before it is
     if (PH == 2)
       for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
         p.out[i] = __float2bfloat16_rn(0.f);
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     const int chunk = lane & 7;
     constexpr bool kAhead = NB <= 4;
     constexpr int kBatch = kAhead ? (PH + 1) * kFewTokens / 4 : 1;  // loads a lane for an entry's rows
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' parts / the hidden layer are there
+    pdl_wait();  // the tokens' parts / the hidden layer are there
     if (PH == 2) {
       for (int i = tid - 64; i < used; i += 32 * NB) wt[i] = __ldg(p.weights + slot_tmp[i]);
       named_bar_sync(1, 32 * NB);
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     if (PH == 1) {
       // ---- hidden = silu(gate) * up ----
       int xbuf = 0;
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      pdl_wait();
       for (int i = tid - 32 * kEpi0; i < used; i += 128) inv[i] = __ldcg(p.xinv + tok[i]);
       named_bar_sync(2, 128);
       for (int it = R.it0; it < R.it1;) {
@@ -913,17 +914,7 @@ int run_moe(const CUtensorMap& tm, const CUtensorMap& tm_next, MoeArgs a, int ro
       return FP8_ERR_CUDA;
     done.fetch_or(bit, std::memory_order_release);
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(32 * (6 + NB));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm, tm_next, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  return launch_dependent(kern, dim3((unsigned)grid), dim3(32 * (6 + NB)), smem, c.stream, tm, tm_next, a);
 }
 
 }  // namespace
@@ -976,22 +967,22 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
     const int rc = make_tmap(&t2, w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc != FP8_OK) return rc;
   }
-  moe_split_kernel<<<(unsigned)T, kSplitThreads, 0, c.stream>>>(
-      static_cast<const uint16_t*>(x), a.H, a.nk1 * 128, base + W.xq, reinterpret_cast<float*>(base + W.xinv),
-      reinterpret_cast<uint32_t*>(base), (int)W.zeros);
-  if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
+  int rc = launch_dependent(moe_split_kernel, dim3((unsigned)T), dim3(kSplitThreads), 0, c.stream,
+                            static_cast<const uint16_t*>(x), a.H, a.nk1 * 128, base + W.xq,
+                            reinterpret_cast<float*>(base + W.xinv), reinterpret_cast<uint32_t*>(base), (int)W.zeros);
+  if (rc != FP8_OK) return rc;
   // With few tokens a stage is hardly more than its weights, and half an SM's shared memory holds
   // enough of them in flight: the two products run side by side. More tokens need longer stages and
   // more builders, and the second product then follows on each SM as the first leaves it.
   if (T <= kFewTokens) {
     a.scales = s13;
-    const int rc = run_moe<1, 4>(t13, t2, a, kSmemPair, grid, c);
+    rc = run_moe<1, 4>(t13, t2, a, kSmemPair, grid, c);
     if (rc != FP8_OK) return rc;
     a.scales = s2;
     return run_moe<2, 4>(t2, t2, a, kSmemPair, grid, c);
   }
   a.scales = s13;
-  const int rc = run_moe<1, 8>(t13, t2, a, kSmemMax, grid, c);
+  rc = run_moe<1, 8>(t13, t2, a, kSmemMax, grid, c);
   if (rc != FP8_OK) return rc;
   a.scales = s2;
   return run_moe<2, 8>(t2, t2, a, kSmemMax, grid, c);

@@ -314,13 +314,14 @@ template <int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
   extern __shared__ __align__(16) int32_t hist[];  // [E2], then the warps' candidates, or place_chunk's arrays
   __shared__ int32_t warp_sums[32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Cand* cand = reinterpret_cast<Cand*>(hist + (p.E2 + 3) / 4 * 4) + warp * 32;
   if (p.order) {
     for (int e = threadIdx.x; e < p.E2; e += blockDim.x) hist[e] = 0;
     __syncthreads();
   }
+  pdl_wait();
+  pdl_trigger();
   const int64_t t0 = blockIdx.x * p.per_chunk;
   const int64_t t1 = t0 + p.per_chunk < p.T ? t0 + p.per_chunk : p.T;
   float bias[VPL];
@@ -373,7 +374,8 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   int32_t* total = sh + p.E2;
   for (int e = threadIdx.x; e < 2 * p.E2; e += kPlaceThreads) sh[e] = 0;
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
+  pdl_trigger();
   const int pairs = p.E2 / 2;  // at most kPlaceThreads / 2
   const int split = kPlaceThreads / pairs;
   const int grp = threadIdx.x / pairs;
@@ -436,6 +438,8 @@ template <int VPL, bool VEC>
 __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBwdArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kBwdWarps + warp;
+  pdl_wait();
+  pdl_trigger();
   if (t >= p.T) return;
   int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
   float g = lane < p.k ? p.dw[t * p.k + lane] * p.scale : 0.f;
@@ -537,23 +541,14 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   const size_t choose = (size_t)(a.E2 + 3) / 4 * 16 + (E <= 256 ? 32 : 16) * 32 * sizeof(Cand);
   const size_t smem = a.chunks == 1 && place_bytes(a.E2) > choose ? place_bytes(a.E2) : choose;
   // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers
-#define FP8_ROUTE(V, X) \
-  route_kernel<V, X, (V <= 8 ? 32 : 16)><<<(unsigned)a.chunks, V <= 8 ? 1024 : 512, smem, c.stream>>>(a)
+#define FP8_ROUTE(V, X)                                                                                        \
+  rc = launch_dependent(route_kernel<V, X, (V <= 8 ? 32 : 16)>, dim3((unsigned)a.chunks), dim3(V <= 8 ? 1024 : 512), \
+                        smem, c.stream, a)
+  int rc;
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
-  if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
-  if (!order || a.chunks == 1) return FP8_OK;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)a.chunks);
-  cfg.blockDim = dim3(kPlaceThreads);
-  cfg.dynamicSmemBytes = place_bytes(a.E2);
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, route_place_kernel, a) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  if (rc != FP8_OK || !order || a.chunks == 1) return rc;
+  return launch_dependent(route_place_kernel, dim3((unsigned)a.chunks), dim3(kPlaceThreads), place_bytes(a.E2), c.stream, a);
 }
 
 int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const float* dw, int64_t T, int64_t E,
@@ -561,10 +556,11 @@ int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const flo
   if (T == 0) return FP8_OK;
   const RouteBwdArgs a = {logits, bf16, ids, dw, dlogits, T, (int)E, (int)k, softmax, renorm, scale, c.status};
   const unsigned grid = (unsigned)ceil_div64(T, kBwdWarps);
-#define FP8_ROUTE(V, X) route_bwd_kernel<V, X><<<grid, 32 * kBwdWarps, 0, c.stream>>>(a)
+#define FP8_ROUTE(V, X) rc = launch_dependent(route_bwd_kernel<V, X>, dim3(grid), dim3(32 * kBwdWarps), 0, c.stream, a)
+  int rc;
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
-  return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+  return rc;
 }
 
 }  // namespace fp8lin
