@@ -206,8 +206,9 @@ FP8_DEVI void norm_out(const NormArgs& p, int64_t row, int c, const float2* s, f
 
 // One row per team: one warp (WARP; eight rows a CTA, no barrier) or the whole CTA, VPT vectors a thread.
 // A CTA ends with its row: while some of an SM's CTAs reduce or store, others load. Persistent CTAs that
-// asked for the next row ahead had fewer warps an SM and took 43 us instead of 40 for 8192 x 4096; one that
-// took rows through shared memory 53 us.
+// asked for the next row ahead had fewer warps an SM and took 43 us instead of 40 for 8192 x 4096 at the time; one
+// that took rows through shared memory 53 us. 36.9 us now, 94% of the copy rate; without a residual and with block
+// scales the instructions bound it instead (14336 x 4096 43 us at 77% of the issue slots; the bytes are 26 us).
 template <int VPT, int GRAN, int FMT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const NormArgs p) {
   constexpr float FMAX = FmtMax<FMT>::v;
@@ -278,11 +279,17 @@ int run_norm(const NormArgs& a, int threads, const Ctx& c) {
 
 template <int GRAN, int FMT>
 int norm_dispatch(const NormArgs& a, const Ctx& c) {
-  // Two vectors a thread while a CTA of 512 threads covers the row: with few rows a row's latency counts (1021 x
-  // 5120 4.7 us, with four 5.4). Four for wider rows, and for many rows above 4096 columns, where two
-  // leave a third of an SM's threads without a CTA (8192 x 7168 with block scales 76 us, with two 82).
+  // A warp a row for the shortest rows, and with four vectors a thread up to 1024 columns where there are so many
+  // rows that the start of a CTA for each (17 us for 16384) is what a call takes: 16384 x 768 12.9 us instead of
+  // 17.0, with a residual 16.1 instead of 18.2; 16384 x 1024 15.0 instead of 17.2, 20.7 instead of 20.0.
+  // Fewer rows end sooner with a CTA each (1024 x 1024 2.6 and 2.8 us).
+  // A CTA a row else, two vectors a thread: with few rows a row's latency counts (1021 x 5120 4.8 us, with four
+  // 5.4). Four for rows above 8192 columns, which 512 threads with two do not cover, and above 5120 for many
+  // rows, where CTAs with two leave a third of an SM's threads empty (8192 x 7168 67 us, with two 74, with eight 66;
+  // but 11468 x 5120 65 us, with two 63, and without a residual 58 and 45).
   if (a.nvec <= 64) return run_norm<2, GRAN, FMT, true>(a, 256, c);
-  if (a.nvec <= 512 || (a.nvec <= 1024 && a.T < 2048))
+  if (a.nvec <= 128 && a.T >= 8192) return run_norm<4, GRAN, FMT, true>(a, 256, c);
+  if (a.nvec <= 640 || (a.nvec <= 1024 && a.T < 2048))
     return run_norm<2, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 2), 32), c);
   return run_norm<4, GRAN, FMT, false>(a, (int)round_up64(ceil_div64(a.nvec, 4), 32), c);
 }

@@ -137,6 +137,25 @@ def test_in_place_stream_and_graph(fp8):
     assert torch.equal(h, want[0]) and torch.equal(y, want[1])
 
 
+@pytest.mark.parametrize("T", [4101, 8191, 8195])
+@pytest.mark.parametrize("H", [520, 776, 1024, 1032])
+def test_many_short_rows(fp8, T, H):
+    test_row_scales(fp8, T, H, T % 2 == 0, 3)
+    test_row_scales(fp8, T, H, T % 2 == 1, 4)
+
+
+@pytest.mark.parametrize("T", [8190, 8196])
+@pytest.mark.parametrize("H", [640, 896, 1024])
+def test_many_short_rows_in_blocks(fp8, T, H):
+    test_block_scales(fp8, T, H, 3)
+    test_mx_scales(fp8, T, H, 4)
+
+
+@pytest.mark.parametrize("T,H", [(2051, 5120), (2047, 5128), (2051, 5128), (2048, 8192)])
+def test_many_wide_rows(fp8, T, H):
+    test_row_scales(fp8, T, H, True, 3)
+
+
 # ------------------------------------------------------------------------------------------ backward
 
 def _bwd_reference(dy, h, w, rstd, dh):
