@@ -7,8 +7,8 @@
 //   renormalization scale * v[e_j] / sum_i v[e_i].
 //
 // Few tokens: one CTA chooses, counts and places. More take two launches, the second started while the first
-// runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 17.9 us, of which the choice 12; the bytes
-// are 2.8 us. It is bound by the choice's ~540 instructions a token and their latency at 32 warps an SM. Candidates
+// runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 17.0 us, of which the choice 10.6; the
+// bytes are 2.8 us. It is bound by the choice's ~540 instructions a token and their latency at 32 warps an SM. Candidates
 // gathered by each lane's next one in turn, with their logits loaded again, are fewer instructions but took 19.1 us.
 #include "common.cuh"
 #include "internal.h"
@@ -45,10 +45,6 @@ FP8_DEVI float warp_max(float v) {
 template <bool VEC>
 FP8_DEVI int expert_of(int lane, int i) {
   return VEC ? (i >> 2) * 128 + lane * 4 + (i & 3) : lane + 32 * i;
-}
-template <bool VEC>
-FP8_DEVI int index_of(int e) {
-  return VEC ? (e >> 7) * 4 + (e & 3) : e >> 5;
 }
 // A row's logits (or a row of fp32 values); experts past E get `none`.
 template <int VPL, bool VEC>
@@ -255,53 +251,63 @@ FP8_DEVI int rank_groups(int E2) {
   while (g > 1 && g * (E2 / 2) > (int)blockDim.x) g >>= 1;
   return g;
 }
-FP8_DEVI void place_chunk(const RouteArgs& p, int64_t chunk, int32_t* at, uint16_t* total, uint16_t* count) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = rank_warps(p.E2), groups = rank_groups(p.E2), per = warps / groups, pairs = p.E2 / 2;
-  const int64_t n = p.T * p.k, len = p.per_chunk * p.k;
-  const int64_t s0 = chunk * len, s1 = s0 + len < n ? s0 + len : n;
+// A batch's slots in their warps' counts (which are zero before); returns the slots of the same expert before this one
+// in its warp.
+FP8_DEVI int count_slot(int id, int E2, uint16_t* count) {
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  const int before = __popc(same & ((1u << (threadIdx.x & 31)) - 1));
+  if (id >= 0 && before == 0) count[(threadIdx.x >> 5) * E2 + id] = (uint16_t)__popc(same);
+  return before;
+}
+FP8_DEVI void sum_counts(int E2, uint16_t* total, uint16_t* count) {
+  const int groups = rank_groups(E2), per = rank_warps(E2) / groups, pairs = E2 / 2;
   uint32_t* count2 = reinterpret_cast<uint32_t*>(count);
-  uint32_t* total2 = reinterpret_cast<uint32_t*>(total);
-  for (int64_t b = s0; b < s1; b += 32 * warps) {
+  for (int i = threadIdx.x; i < groups * pairs; i += blockDim.x) {
+    const int g = i / pairs, x = i - g * pairs;
+    uint32_t sum = 0;  // two 16-bit sums: at most 1024 slots in all
+#pragma unroll 4
+    for (int w = g * per; w < (g + 1) * per; ++w) {
+      const uint32_t c = count2[w * pairs + x];
+      count2[w * pairs + x] = sum;
+      sum += c;
+    }
+    reinterpret_cast<uint32_t*>(total)[g * pairs + x] = sum;
+  }
+}
+FP8_DEVI void put_slot(const RouteArgs& p, int64_t s, int id, int before, const int32_t* at, const uint16_t* total,
+                       const uint16_t* count) {
+  const int warp = threadIdx.x >> 5, per = rank_warps(p.E2) / rank_groups(p.E2);
+  int32_t place = -1;
+  if (id >= 0) {
+    place = at[id] + count[warp * p.E2 + id] + before;
+    for (int g = 0; g < warp / per; ++g) place += total[g * p.E2 + id];
+    p.order[place] = (int32_t)s;
+  }
+  p.pos[s] = place;
+}
+// The slots from b to s1; `placed`: the batch before b has been placed, its totals are not yet in `at`.
+FP8_DEVI void place_slots(const RouteArgs& p, int64_t b, int64_t s1, bool placed, int32_t* at, uint16_t* total,
+                          uint16_t* count) {
+  const int warp = threadIdx.x >> 5, warps = rank_warps(p.E2), groups = rank_groups(p.E2), pairs = p.E2 / 2;
+  for (; b < s1; b += 32 * warps, placed = true) {
     const int64_t s = b + threadIdx.x;
     const int id = warp < warps && s < s1 ? p.ids[s] : -1;
-    for (int i = threadIdx.x; i < warps * pairs; i += blockDim.x) count2[i] = 0;
+    if (placed) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        int sum = 0;
+        for (int g = 0; g < groups; ++g) sum += total[g * p.E2 + e];
+        at[e] += sum;
+      }
+    }
+    for (int i = threadIdx.x; i < warps * pairs; i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
     __syncthreads();
     int before = 0;
-    if (warp < warps) {
-      const uint32_t same = __match_any_sync(0xffffffffu, id);
-      before = __popc(same & ((1u << lane) - 1));
-      if (id >= 0 && before == 0) count[warp * p.E2 + id] = (uint16_t)__popc(same);
-    }
+    if (warp < warps) before = count_slot(id, p.E2, count);
     __syncthreads();
-    for (int i = threadIdx.x; i < groups * pairs; i += blockDim.x) {
-      const int g = i / pairs, x = i - g * pairs;
-      uint32_t sum = 0;  // two 16-bit sums: at most 1024 slots in all
-#pragma unroll 4
-      for (int w = g * per; w < (g + 1) * per; ++w) {
-        const uint32_t c = count2[w * pairs + x];
-        count2[w * pairs + x] = sum;
-        sum += c;
-      }
-      total2[g * pairs + x] = sum;
-    }
+    sum_counts(p.E2, total, count);
     __syncthreads();
-    if (warp < warps && s < s1) {
-      int32_t place = -1;
-      if (id >= 0) {
-        place = at[id] + count[warp * p.E2 + id] + before;
-        for (int g = 0; g < warp / per; ++g) place += total[g * p.E2 + id];
-        p.order[place] = (int32_t)s;
-      }
-      p.pos[s] = place;
-    }
-    if (b + 32 * warps >= s1) break;
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {  // the next batch's first places
-      int sum = 0;
-      for (int g = 0; g < groups; ++g) sum += total[g * p.E2 + e];
-      at[e] += sum;
-    }
+    if (warp < warps && s < s1) put_slot(p, s, id, before, at, total, count);
   }
 }
 // Unused slots leave the end of `order` without a slot.
@@ -314,7 +320,7 @@ FP8_DEVI void fill_order(const RouteArgs& p, int64_t valid) {
 // The choice for a chunk of tokens, and the chunk's slots of each expert; with one chunk the table too.
 template <int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
-  extern __shared__ __align__(16) int32_t hist[];  // [E2], then the warps' candidates, or place_chunk's arrays
+  extern __shared__ __align__(16) int32_t hist[];  // [E2], then the warps' candidates, or place_slots' arrays
   __shared__ int32_t warp_sums[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Cand* cand = reinterpret_cast<Cand*>(hist + (p.E2 + 3) / 4 * 4) + warp * 32;
@@ -363,23 +369,32 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
     __syncthreads();
   }
   fill_order(p, before);
-  place_chunk(p, 0, hist, reinterpret_cast<uint16_t*>(hist + p.E2), reinterpret_cast<uint16_t*>(hist + p.E2) + most_groups(p.E2) * p.E2);
+  uint16_t* sums = reinterpret_cast<uint16_t*>(hist + p.E2);
+  place_slots(p, 0, p.T * p.k, false, hist, sums, sums + most_groups(p.E2) * p.E2);
 }
 
 // The table from the chunks' counts. Each CTA sums the whole matrix of counts (16 bits each, 78 KB for 152
-// chunks and 256 experts, from L2) into its own first places, so that no launch is spent on a scan.
+// chunks and 256 experts, from L2) into its own first places, so that no launch is spent on a scan. What it takes is a
+// chain of latencies: its slots are read together with the matrix, and counted while that is summed.
 constexpr int kPlaceThreads = 1024;
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs p) {
-  extern __shared__ int32_t sh[];  // [E2] slots in the chunks before this one, [E2] slots, then place_chunk's arrays
+  extern __shared__ int32_t sh[];  // [E2] slots in the chunks before this one, [E2] slots, then place_slots' arrays
   __shared__ int32_t warp_sums[32];
   int32_t* prior = sh;
-  int32_t* total = sh + p.E2;
+  int32_t* all = sh + p.E2;
+  uint16_t* total = reinterpret_cast<uint16_t*>(sh + 2 * p.E2);
+  uint16_t* count = total + most_groups(p.E2) * p.E2;
+  const int warp = threadIdx.x >> 5, warps = rank_warps(p.E2);
+  const int pairs = p.E2 / 2;  // at most kPlaceThreads / 2
   for (int e = threadIdx.x; e < 2 * p.E2; e += kPlaceThreads) sh[e] = 0;
+  for (int i = threadIdx.x; i < warps * pairs; i += kPlaceThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int pairs = p.E2 / 2;  // at most kPlaceThreads / 2
-  const int split = kPlaceThreads / pairs;
+  const int64_t n_slots = p.T * p.k, len = p.per_chunk * p.k;
+  const int64_t s0 = blockIdx.x * len, s1 = s0 + len < n_slots ? s0 + len : n_slots, s = s0 + threadIdx.x;
+  const int id = warp < warps && s < s1 ? __ldcg(p.ids + s) : -1;
+  const int split = min(kPlaceThreads / pairs, 8);  // threads that share a pair of experts
   const int grp = threadIdx.x / pairs;
   if (grp < split) {
     const uint32_t* h = reinterpret_cast<const uint32_t*>(p.hist);
@@ -400,13 +415,16 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
         if (c0 + i * split < (int)blockIdx.x) b0 += lo, b1 += hi;
       }
     }
-    atomicAdd(total + 2 * x, a0), atomicAdd(total + 2 * x + 1, a1);
+    atomicAdd(all + 2 * x, a0), atomicAdd(all + 2 * x + 1, a1);
     atomicAdd(prior + 2 * x, b0), atomicAdd(prior + 2 * x + 1, b1);
   }
+  int before = 0;
+  if (warp < warps) before = count_slot(id, p.E2, count);
   __syncthreads();
+  sum_counts(p.E2, total, count);
   // E <= kPlaceThreads: an expert a thread
   const int e = threadIdx.x;
-  const int n = e < p.E ? total[e] : 0;
+  const int n = e < p.E ? all[e] : 0;
   const int start = block_scan(n, warp_sums);
   if (e < p.E) {
     if (blockIdx.x == 0) p.ends[e] = start + n;
@@ -415,7 +433,8 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   const int64_t valid = warp_sums[31];
   __syncthreads();
   fill_order(p, valid);
-  place_chunk(p, blockIdx.x, prior, reinterpret_cast<uint16_t*>(total), reinterpret_cast<uint16_t*>(total) + most_groups(p.E2) * p.E2);
+  if (warp < warps && s < s1) put_slot(p, s, id, before, prior, total, count);
+  place_slots(p, s0 + 32 * warps, s1, true, prior, total, count);
 }
 
 // Gradient of the logits, a warp per token. With g_j = scale * dweights_j:
@@ -504,7 +523,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
 }
 
 // Chunks of tokens: one CTA does it all for a token a warp, for two a warp where a row is one value a lane
-// (64 tokens of 8 experts 5.4 us, in chunks 5.8; of 256 experts 8.9 us, in chunks 8.0, of 512 14.3 and 8.7);
+// (64 tokens of 8 experts 5.4 us, in chunks 5.8; of 256 experts 8.9 us, in chunks 7.5, of 512 14.3 and 8.6);
 // else a chunk for each of 152 SMs, and not above what 16-bit counts hold.
 int64_t chunk_tokens(int64_t T, int64_t E) {
   if (T <= (E <= 32 ? 64 : 32)) return T < 1 ? 1 : T;
@@ -523,7 +542,7 @@ int64_t chunk_tokens(int64_t T, int64_t E) {
     else { if ((E) % 4 == 0) { CALL(32, true); } else { CALL(32, false); } }                 \
   } while (0)
 
-// Shared memory of place_chunk: first places, group totals, a row of counts a warp.
+// Shared memory of place_slots: first places, group totals, a row of counts a warp.
 size_t place_bytes(int E2) { return (size_t)E2 * (4 + 2 * most_groups(E2) + 2 * (E2 <= 512 ? 32 : 16)); }
 
 }  // namespace
@@ -540,7 +559,7 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   RouteArgs a = {logits, bf16, bias, T,    (int)E, (int)k, softmax, renorm, scale, ids, weights,
                  order,  pos,  ends, static_cast<uint16_t*>(ws), (int)round_up64(E, 2), chunk_tokens(T, E), 0};
   a.chunks = (int)ceil_div64(T, a.per_chunk);
-  // up to 48 KB, which needs no attribute: place_chunk's 40 to 43 KB and the candidates' 8 to 16 KB share it
+  // up to 48 KB, which needs no attribute: place_slots' 40 to 43 KB and the candidates' 8 to 16 KB share it
   const size_t choose = (size_t)(a.E2 + 3) / 4 * 16 + (E <= 256 ? 32 : 16) * 32 * sizeof(Cand);
   const size_t smem = a.chunks == 1 && place_bytes(a.E2) > choose ? place_bytes(a.E2) : choose;
   // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers
@@ -551,7 +570,8 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
   if (rc != FP8_OK || !order || a.chunks == 1) return rc;
-  return launch_dependent(route_place_kernel, dim3((unsigned)a.chunks), dim3(kPlaceThreads), place_bytes(a.E2), c.stream, a);
+  return launch_dependent(route_place_kernel, dim3((unsigned)a.chunks), dim3(kPlaceThreads),
+                          place_bytes(a.E2) + (size_t)a.E2 * 4, c.stream, a);
 }
 
 int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const float* dw, int64_t T, int64_t E,
