@@ -359,7 +359,8 @@ int fp8_linear_bwd(const fp8_tensor* dy, const fp8_linear_saved* saved, const fp
  *              the unrounded s.
  *  y           bf16 [T, H] or NULL: y rounded once.
  *  q           FP8 (E4M3 or E5M2) [T, H] or NULL: y quantized from its fp32 value by the recipe [Q] in
- *              fp32 (scale and inverse to 4 units in the last place); inv_scales, given with q, by granularity as for fp8_quantize ROW_MAJOR:
+ *              fp32 (scale and inverse to 4 units in the last place); inv_scales, given with q, by
+ *              granularity as for fp8_quantize ROW_MAJOR:
  *              FP8_GRAN_ROW fp32 [T]; FP8_GRAN_BLOCK_1x128 fp32 [T, H / 128] (H % 128 == 0);
  *              FP8_GRAN_MX E8M0 [fp8_mx_scale_bytes(T, H)] (H % 128 == 0). Other granularities:
  *              FP8_ERR_UNSUPPORTED. amax is that of the unrounded y, so the codes are those of y in
@@ -384,6 +385,8 @@ int fp8_add_rmsnorm(const fp8_tensor* x, const fp8_tensor* residual, const fp8_t
  *  dw          bf16 or fp32 [H] or NULL. Summed in fp32 in an order that depends on T and H only:
  *              the same bits on every run. T == 0 gives zeros.
  *  workspace   fp8_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, when dw is given.
+ * There is no status word: a wait for a load that ran out (fp8_set_wait_limit_ns) shows as NaN in its row's dx
+ * and in dw.
  */
 int fp8_add_rmsnorm_bwd(const fp8_tensor* dy, const fp8_tensor* h, const fp8_tensor* weight,
                         const fp8_tensor* rstd, const fp8_tensor* dh, fp8_tensor* dx, fp8_tensor* dw,
@@ -436,7 +439,10 @@ int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids, const fp8
  *  w2, s2      E4M3 [E, H, I] and fp32 [E, H].
  *  out         bf16 [T, H].
  *  workspace   fp8_moe_tokens_workspace_size(T, k, H, I) bytes, 16-byte aligned.
- * The activations are not rounded to 8 bits: products and sums are fp32, the result is rounded once.
+ * Sums are fp32 and the result is rounded once. The activations enter the products as sums of 8-bit parts:
+ * x exactly down to 2^-13 of its row's largest and to 2^-21 of that below, the hidden layer to 2^-13 of each
+ * value (2^-25 of the largest in its block of 32). A row with a NaN or an infinity gives NaN wherever the formula does. The same
+ * bits on every run. A wait that ran out sets FP8_DEV_TIMEOUT.
  */
 int fp8_moe_tokens(const fp8_tensor* x, const fp8_tensor* ids, const fp8_tensor* weights,
                    const fp8_tensor* w13, const fp8_tensor* s13, const fp8_tensor* w2, const fp8_tensor* s2,

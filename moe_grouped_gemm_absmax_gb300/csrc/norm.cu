@@ -209,7 +209,7 @@ FP8_DEVI void norm_out(const NormArgs& p, int64_t row, int c, const float2* s, f
 // asked for the next row ahead had fewer warps an SM and took 43 us instead of 40 for 8192 x 4096 at the time; one
 // that took rows through shared memory 53 us. 36.9 us now, 94% of the copy rate; without a residual and with block
 // scales the instructions bound it instead (14336 x 4096 43 us at 77% of the issue slots; the bytes are 26 us).
-template <int VPT, int GRAN, int FMT, bool WARP>
+template <int VPT, int GRAN, int FMT, bool WARP, bool RES>
 __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const NormArgs p) {
   constexpr float FMAX = FmtMax<FMT>::v;
   __shared__ __align__(16) float red_s[32], red_m[32];
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
   for (int i = 0; i < VPT; ++i) {
     const int c = t + i * team;
     vx[i] = c < p.nvec ? ld_stream(p.x + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
-    vr[i] = p.res && c < p.nvec ? ld_stream(p.res + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
+    vr[i] = RES && c < p.nvec ? ld_stream(p.res + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
   }
   float2 s[VPT][4];
   float2 sum2 = both(0.f);
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
 #pragma unroll
     for (int j = 0; j < 4; ++j) w8[j] = both(0.f);
     if (c < p.nvec) load_w(p.w, p.w_f32, c, w8);
-    const float m = norm_in(vx[i], vr[i], p.res != nullptr, w8, p.h && c < p.nvec ? p.h + row * p.nvec + c : nullptr,
+    const float m = norm_in(vx[i], vr[i], RES, w8, p.h && c < p.nvec ? p.h + row * p.nvec + c : nullptr,
                             s[i], &sum2);
     if (GRAN == FP8_GRAN_ROW) mx = max_nan(mx, m);
     if (GRAN == FP8_GRAN_BLOCK_1x128 || GRAN == FP8_GRAN_MX) bm[i] = block_max<GRAN>(m);
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
 
 template <int VPT, int GRAN, int FMT, bool WARP>
 int run_norm(const NormArgs& a, int threads, const Ctx& c) {
-  return launch_dependent(add_rmsnorm_kernel<VPT, GRAN, FMT, WARP>, dim3((unsigned)ceil_div64(a.T, WARP ? 8 : 1)),
-                          dim3(threads), 0, c.stream, a);
+  const auto kern = a.res ? add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, true> : add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, false>;
+  return launch_dependent(kern, dim3((unsigned)ceil_div64(a.T, WARP ? 8 : 1)), dim3(threads), 0, c.stream, a);
 }
 
 template <int GRAN, int FMT>
