@@ -207,9 +207,12 @@ FP8_DEVI void norm_out(const NormArgs& p, int64_t row, int c, const float2* s, f
 // One row per team: one warp (WARP; eight rows a CTA, no barrier) or the whole CTA, VPT vectors a thread.
 // A CTA ends with its row: while some of an SM's CTAs reduce or store, others load. Persistent CTAs that
 // asked for the next row ahead had fewer warps an SM and took 43 us instead of 40 for 8192 x 4096 at the time; one
-// that took rows through shared memory 53 us. 36.9 us now, 94% of the copy rate; without a residual and with block
-// scales the instructions bound it instead (14336 x 4096 43 us at 77% of the issue slots; the bytes are 26 us).
-template <int VPT, int GRAN, int FMT, bool WARP, bool RES>
+// that took rows through shared memory 53 us. 36 us now, 96% of the copy rate; without a residual and with block
+// scales the instructions bound it instead (14336 x 4096 39 us; the bytes are 26 us; 43 us at 77% of the issue slots
+// with one kernel for every residual and weight type). The weights' type is known at compile time except in a CTA a
+// row with four vectors a thread: there it makes the compiler load all weights ahead, in registers that cost
+// CTAs (4778 x 12288 68 us instead of 64).
+template <int VPT, int GRAN, int FMT, bool WARP, bool RES, bool WF32>
 __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const NormArgs p) {
   constexpr float FMAX = FmtMax<FMT>::v;
   __shared__ __align__(16) float red_s[32], red_m[32];
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
     float2 w8[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w8[j] = both(0.f);
-    if (c < p.nvec) load_w(p.w, p.w_f32, c, w8);
+    if (c < p.nvec) load_w(p.w, WARP || VPT == 2 ? WF32 : p.w_f32, c, w8);
     const float m = norm_in(vx[i], vr[i], RES, w8, p.h && c < p.nvec ? p.h + row * p.nvec + c : nullptr,
                             s[i], &sum2);
     if (GRAN == FP8_GRAN_ROW) mx = max_nan(mx, m);
@@ -273,20 +276,24 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
 
 template <int VPT, int GRAN, int FMT, bool WARP>
 int run_norm(const NormArgs& a, int threads, const Ctx& c) {
-  const auto kern = a.res ? add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, true> : add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, false>;
+  constexpr bool F32 = WARP || VPT == 2;
+  const auto kern = a.res ? (F32 && a.w_f32 ? add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, true, F32>
+                                            : add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, true, false>)
+                          : (F32 && a.w_f32 ? add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, false, F32>
+                                            : add_rmsnorm_kernel<VPT, GRAN, FMT, WARP, false, false>);
   return launch_dependent(kern, dim3((unsigned)ceil_div64(a.T, WARP ? 8 : 1)), dim3(threads), 0, c.stream, a);
 }
 
 template <int GRAN, int FMT>
 int norm_dispatch(const NormArgs& a, const Ctx& c) {
   // A warp a row for the shortest rows, and with four vectors a thread up to 1024 columns where there are so many
-  // rows that the start of a CTA for each (17 us for 16384) is what a call takes: 16384 x 768 12.9 us instead of
-  // 17.0, with a residual 16.1 instead of 18.2; 16384 x 1024 15.0 instead of 17.2, 20.7 instead of 20.0.
-  // Fewer rows end sooner with a CTA each (1024 x 1024 2.6 and 2.8 us).
-  // A CTA a row else, two vectors a thread: with few rows a row's latency counts (1021 x 5120 4.8 us, with four
-  // 5.4). Four for rows above 8192 columns, which 512 threads with two do not cover, and above 5120 for many
-  // rows, where CTAs with two leave a third of an SM's threads empty (8192 x 7168 67 us, with two 74, with eight 66;
-  // but 11468 x 5120 65 us, with two 63, and without a residual 58 and 45).
+  // rows that the start of a CTA for each (17 us for 16384) is what a call takes: 16384 x 768 10 us instead of
+  // 17, with a residual 15.6 instead of 17.6; 16384 x 1024 13 instead of 17, 20.9 instead of 19.1.
+  // Fewer rows end sooner with a CTA each (1024 x 1024 2.3 and 2.8 us).
+  // A CTA a row else, two vectors a thread: with few rows a row's latency counts (1024 x 5120 4.2 us, with four
+  // 5.6). Four for rows above 8192 columns, which 512 threads with two do not cover, and above 5120 for many
+  // rows, where CTAs with two leave a third of an SM's threads empty (8192 x 7168 63 us, with two 70; but 11468 x
+  // 5120 64 us, with two 61, and without a residual 50 and 40).
   if (a.nvec <= 64) return run_norm<2, GRAN, FMT, true>(a, 256, c);
   if (a.nvec <= 128 && a.T >= 8192) return run_norm<4, GRAN, FMT, true>(a, 256, c);
   if (a.nvec <= 640 || (a.nvec <= 1024 && a.T < 2048))
