@@ -7,9 +7,9 @@
 //   renormalization scale * v[e_j] / sum_i v[e_i].
 //
 // Few tokens: one CTA chooses, counts and places. More take two launches, the second started while the first
-// runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 17.0 us, of which the choice 10.6; the
+// runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 16.5 us, of which the choice 10; the
 // bytes are 2.8 us. It is bound by the choice's ~540 instructions a token and their latency at 32 warps an SM. Candidates
-// gathered by each lane's next one in turn, with their logits loaded again, are fewer instructions but took 19.1 us.
+// gathered by each lane's next one in turn, with their logits loaded again, are fewer instructions but took 1.2 us more.
 #include "common.cuh"
 #include "internal.h"
 
@@ -131,7 +131,7 @@ struct __align__(16) Cand {
   int e;
   float logit;
 };
-template <int VPL, bool VEC>
+template <int VPL, bool VEC, bool SOFTMAX>
 FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* v, const float* bias, Cand* cand,
                           int32_t* hist) {
   float sel[VPL];
@@ -188,7 +188,7 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* 
   }
   __syncwarp();  // the candidates are read before the next token's are written
   float w = 0.f;
-  if (p.softmax) {
+  if (SOFTMAX) {
     if (p.renorm) {  // softmax over the experts taken
       const float m = warp_max(id >= 0 ? l : -INFINITY);
       w = id >= 0 ? expf(l - m) : 0.f;
@@ -318,7 +318,7 @@ FP8_DEVI void fill_order(const RouteArgs& p, int64_t valid) {
 }
 
 // The choice for a chunk of tokens, and the chunk's slots of each expert; with one chunk the table too.
-template <int VPL, bool VEC, int WARPS>
+template <int VPL, bool VEC, int WARPS, bool BF16, bool SOFTMAX>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
   extern __shared__ __align__(16) int32_t hist[];  // [E2], then the warps' candidates, or place_slots' arrays
   __shared__ int32_t warp_sums[32];
@@ -339,16 +339,16 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
   // a warp's next row is asked for before it works on this one, where there are registers for it
   constexpr bool kAhead = VPL <= 8;
   float v[VPL], next[VPL];
-  if (kAhead && t0 + warp < t1) load_row<VPL, VEC>(p.logits, p.bf16, t0 + warp, p.E, lane, -INFINITY, next);
+  if (kAhead && t0 + warp < t1) load_row<VPL, VEC>(p.logits, BF16, t0 + warp, p.E, lane, -INFINITY, next);
   for (int64_t t = t0 + warp; t < t1; t += WARPS) {
     if (kAhead) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) v[i] = next[i];
-      if (t + WARPS < t1) load_row<VPL, VEC>(p.logits, p.bf16, t + WARPS, p.E, lane, -INFINITY, next);
+      if (t + WARPS < t1) load_row<VPL, VEC>(p.logits, BF16, t + WARPS, p.E, lane, -INFINITY, next);
     } else {
-      load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, -INFINITY, v);
+      load_row<VPL, VEC>(p.logits, BF16, t, p.E, lane, -INFINITY, v);
     }
-    route_token<VPL, VEC>(p, t, lane, v, bias, cand, p.order ? hist : nullptr);
+    route_token<VPL, VEC, SOFTMAX>(p, t, lane, v, bias, cand, p.order ? hist : nullptr);
   }
   if (!p.order) return;
   __syncthreads();
@@ -455,7 +455,8 @@ struct RouteBwdArgs {
   int32_t* status;
 };
 
-template <int VPL, bool VEC>
+// ALL: softmax without renormalization, which every expert's logit has a gradient of.
+template <int VPL, bool VEC, bool BF16, bool ALL>
 __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBwdArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kBwdWarps + warp;
@@ -469,13 +470,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
     id = -1;
   }
   if (id < 0) g = 0.f;
-  const float l = id >= 0 ? load_logit(p.logits, p.bf16, t * p.E + id) : 0.f;
+  const float l = id >= 0 ? load_logit(p.logits, BF16, t * p.E + id) : 0.f;
   float d = 0.f;
   float v[VPL];
   float base = 0.f, pe = 0.f;
-  if (p.softmax && !p.renorm) {
+  if (ALL) {
     float m = -INFINITY, z = 0.f;
-    load_row<VPL, VEC>(p.logits, p.bf16, t, p.E, lane, -INFINITY, v);
+    load_row<VPL, VEC>(p.logits, BF16, t, p.E, lane, -INFINITY, v);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
     m = warp_max(m);
@@ -505,11 +506,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
     }
     d = g * s * (1.0f - s);
   }
-  if (!(p.softmax && !p.renorm)) {
+  if (!ALL) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) v[i] = 0.f;
   }
-  store_row<VPL, VEC>(p.dlogits, p.bf16, t, p.E, lane, v);
+  store_row<VPL, VEC>(p.dlogits, BF16, t, p.E, lane, v);
   // an expert named twice gets the sum of its slots
   float all = 0.f;
   for (int j = 0; j < p.k; ++j) {
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
   }
   all += base * pe;
   __syncwarp();  // the row's stores above come first
-  if (id >= 0) store_logit(p.dlogits, p.bf16, t * p.E + id, all);
+  if (id >= 0) store_logit(p.dlogits, BF16, t * p.E + id, all);
 }
 
 // Chunks of tokens: one CTA does it all for a token a warp, for two a warp where a row is one value a lane
@@ -545,6 +546,24 @@ int64_t chunk_tokens(int64_t T, int64_t E) {
 // Shared memory of place_slots: first places, group totals, a row of counts a warp.
 size_t place_bytes(int E2) { return (size_t)E2 * (4 + 2 * most_groups(E2) + 2 * (E2 <= 512 ? 32 : 16)); }
 
+// 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers. Kernels by the logits' type and
+// the score: with both decided in the kernel 16384 tokens of 256 experts took 17.1 us instead of 16.5.
+template <int VPL, bool VEC>
+int run_route(const RouteArgs& a, size_t smem, const Ctx& c) {
+  constexpr int W = VPL <= 8 ? 32 : 16;
+  const auto kern = a.bf16 ? (a.softmax ? route_kernel<VPL, VEC, W, true, true> : route_kernel<VPL, VEC, W, true, false>)
+                           : (a.softmax ? route_kernel<VPL, VEC, W, false, true> : route_kernel<VPL, VEC, W, false, false>);
+  return launch_dependent(kern, dim3((unsigned)a.chunks), dim3(32 * W), smem, c.stream, a);
+}
+
+template <int VPL, bool VEC>
+int run_route_bwd(const RouteBwdArgs& a, const Ctx& c) {
+  const bool all = a.softmax && !a.renorm;
+  const auto kern = a.bf16 ? (all ? route_bwd_kernel<VPL, VEC, true, true> : route_bwd_kernel<VPL, VEC, true, false>)
+                           : (all ? route_bwd_kernel<VPL, VEC, false, true> : route_bwd_kernel<VPL, VEC, false, false>);
+  return launch_dependent(kern, dim3((unsigned)ceil_div64(a.T, kBwdWarps)), dim3(32 * kBwdWarps), 0, c.stream, a);
+}
+
 }  // namespace
 
 int64_t route_ws_bytes(int64_t T, int64_t E) { return round_up64(ceil_div64(T, chunk_tokens(T, E)) * round_up64(E, 2) * 2, 16); }
@@ -562,10 +581,7 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   // up to 48 KB, which needs no attribute: place_slots' 40 to 43 KB and the candidates' 8 to 16 KB share it
   const size_t choose = (size_t)(a.E2 + 3) / 4 * 16 + (E <= 256 ? 32 : 16) * 32 * sizeof(Cand);
   const size_t smem = a.chunks == 1 && place_bytes(a.E2) > choose ? place_bytes(a.E2) : choose;
-  // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers
-#define FP8_ROUTE(V, X)                                                                                        \
-  rc = launch_dependent(route_kernel<V, X, (V <= 8 ? 32 : 16)>, dim3((unsigned)a.chunks), dim3(V <= 8 ? 1024 : 512), \
-                        smem, c.stream, a)
+#define FP8_ROUTE(V, X) rc = run_route<V, X>(a, smem, c)
   int rc;
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
@@ -578,8 +594,7 @@ int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const flo
                      int64_t k, int softmax, int renorm, float scale, void* dlogits, const Ctx& c) {
   if (T == 0) return FP8_OK;
   const RouteBwdArgs a = {logits, bf16, ids, dw, dlogits, T, (int)E, (int)k, softmax, renorm, scale, c.status};
-  const unsigned grid = (unsigned)ceil_div64(T, kBwdWarps);
-#define FP8_ROUTE(V, X) rc = launch_dependent(route_bwd_kernel<V, X>, dim3(grid), dim3(32 * kBwdWarps), 0, c.stream, a)
+#define FP8_ROUTE(V, X) rc = run_route_bwd<V, X>(a, c)
   int rc;
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
