@@ -93,13 +93,20 @@ FP8_DEVI void team_put(float* slots, int t, int warps, float v) {
   if ((t & 31) == 0) slots[t >> 5] = v;
   if (t < 32 && t >= warps) slots[t] = 0.f;
 }
+// The same sum with two additions an instruction (PAIRS) or one: the backward kernels with several vectors a thread have
+// no registers to pair (3000 x 16384 77 us instead of 73); with one vector it is worth 1 us of 75.
+template <bool PAIRS>
 FP8_DEVI float team_sum(const float* slots, int warps) {
-  float4 a = *reinterpret_cast<const float4*>(slots);
+  const float4 v = *reinterpret_cast<const float4*>(slots);
+  float2 a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
   for (int i = 4; i < warps; i += 4) {
-    const float4 b = *reinterpret_cast<const float4*>(slots + i);
-    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    const float4 u = *reinterpret_cast<const float4*>(slots + i);
+    if (PAIRS)
+      a = fadd2_rn(a, make_float2(u.x, u.y)), b = fadd2_rn(b, make_float2(u.z, u.w));
+    else
+      a.x += u.x, a.y += u.y, b.x += u.z, b.y += u.w;
   }
-  return (a.x + a.y) + (a.z + a.w);
+  return (a.x + a.y) + (b.x + b.y);
 }
 FP8_DEVI float team_max(const float* slots, int warps) {
   float m = 0.f;
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
     team_put(red_s, t, team / 32, sum);
     if (GRAN == FP8_GRAN_ROW) team_put(red_m, t, team / 32, mx);
     __syncthreads();
-    sum = team_sum(red_s, team / 32);
+    sum = team_sum<true>(red_s, team / 32);
     if (GRAN == FP8_GRAN_ROW) mx = team_max(red_m, team / 32);
   }
   const float rstd = rsqrtf(fmaf(sum, p.inv_H, p.eps));
@@ -358,14 +365,15 @@ FP8_DEVI void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* ba
 struct RingShape {
   int vpt, team, rows, ctas, stages, tensors;
 };
-// One vector a thread up to 8192 columns (four beyond), teams for several short rows up to 512 threads a CTA,
-// as many CTAs an SM as make 1024 threads with one vector each (one CTA with four: it needs the registers),
-// and up to three groups in a CTA's ring. Measured for 8192 x 7168, 470 MB: 76 us; with the weights read from L1
-// row by row instead of kept in registers 93 us, with two vectors a thread and two CTAs an SM (spills) 91 us,
-// with a ring of five groups 78 us, without any arithmetic 75 us.
+// One vector a thread up to 8192 columns, two up to 12288 (4096 x 12288 70 us; with four, on 384 threads, 79), four
+// beyond; teams for several short rows up to 512 threads a CTA, as many CTAs an SM as make 1024 threads with one vector
+// each (one CTA with more: it needs the registers), and up to three groups in a CTA's ring. Measured for 8192 x
+// 7168, 470 MB: 74 us, 94% of the copy rate; with the weights read from L1 row by row instead of kept in registers
+// 93 us, with two vectors a thread and two CTAs an SM (spills) 91 us, with a ring of five groups 2 us more. Without
+// dh (353 MB) 66 us: there the ~250 instructions a warp and row and the barrier bound it.
 inline RingShape ring_shape(int nvec, int tensors) {
   RingShape r;
-  r.vpt = nvec <= 1024 ? 1 : 4;
+  r.vpt = nvec <= 1024 ? 1 : nvec <= 1536 ? 2 : 4;
   r.team = (int)round_up64(ceil_div64(nvec, r.vpt), 32);
   r.rows = r.team > 512 ? 1 : 512 / r.team < 8 ? 512 / r.team : 8;
   r.ctas = r.vpt == 1 && r.team * r.rows <= 512 ? 2 : 1;
@@ -440,14 +448,14 @@ struct NormBwdArgs {
   uint64_t wait_ns;
 };
 
-template <int VPT, bool WF32>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, 1) rmsnorm_bwd_kernel(const NormBwdArgs p, const Ring q) {
+template <int VPT, bool WF32, bool HAS_DH>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rmsnorm_bwd_kernel(const NormBwdArgs p, const Ring q) {
   extern __shared__ uint4 ring[];  // [stages][dy, h, dh][rows][nvec]
   __shared__ uint64_t full[kRingStages];
   __shared__ __align__(16) float red[2][8][32];
   const int nvec = q.nvec;
   const int team = threadIdx.x / q.r.team, t = threadIdx.x % q.r.team;
-  const bool has_dh = q.r.tensors == 3;
+  constexpr int kTensors = HAS_DH ? 3 : 2;
   q.start(ring, full);
   float2 dw[VPT][4];
   uint4 wv[VPT];  // bf16 weights stay in registers; fp32 ones, twice as many, come from L1
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, 1) rmsnorm_bwd_kernel(c
     rstd_next = row_rstd(g + gridDim.x);
     // a wait that ran out would show as NaN in everything that the row reaches
     if (!mbar_wait(&full[st], phase, nullptr, p.wait_ns)) rstd = __uint_as_float(0x7FC00000u);
-    const uint4* in = ring + st * q.r.tensors * q.slab + team * nvec;
+    const uint4* in = ring + st * kTensors * q.slab + team * nvec;
     uint4 vdy[VPT], vh[VPT], vdh[VPT];
     float2 sum2 = both(0.f);
 #pragma unroll
@@ -481,7 +489,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, 1) rmsnorm_bwd_kernel(c
       if (!active || c >= nvec) continue;
       vdy[i] = in[c];
       vh[i] = in[q.slab + c];
-      vdh[i] = has_dh ? in[2 * q.slab + c] : make_uint4(0, 0, 0, 0);
+      vdh[i] = HAS_DH ? in[2 * q.slab + c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 dyh = fmul2_rn(unpack2(word(vdy[i], j)), unpack2(word(vh[i], j)));
@@ -497,7 +505,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, 1) rmsnorm_bwd_kernel(c
     if (threadIdx.x == 0) q.load(ring, full, g + (int64_t)q.r.stages * gridDim.x, st);
     if (++st == q.r.stages) st = 0, phase ^= 1;
     if (!p.dx || !active) continue;
-    const float c1 = rstd * rstd * (rstd * team_sum(red[par][team], q.r.team / 32) * p.inv_H);
+    const float c1 = rstd * rstd * (rstd * team_sum<VPT == 1>(red[par][team], q.r.team / 32) * p.inv_H);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * q.r.team;
@@ -505,9 +513,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512, 1) rmsnorm_bwd_kernel(c
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 w2 = WF32 ? __ldg(static_cast<const float2*>(p.w) + 4 * c + j) : unpack2(word(wv[i], j));
         const float2 g2 = ffma2_rn(unpack2(word(vh[i], j)), both(-c1), unpack2(word(vdh[i], j)));
-        o[j] = pack_bf16(ffma2_rn(fmul2_rn(unpack2(word(vdy[i], j)), w2), both(rstd), g2));
+        o[j] = pack_bf16(ffma2_rn(fmul2_rn(unpack2(word(vdy[i], j)), WF32 ? __ldg(static_cast<const float2*>(p.w) + 4 * c + j) : unpack2(word(wv[i], j))), both(rstd), g2));
       }
       p.dx[row * nvec + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -567,12 +574,19 @@ __global__ void __launch_bounds__(512) dw_sum_kernel(const float4* part, int par
     static_cast<float4*>(dw)[c] = a;
 }
 
-template <int VPT, bool WF32>
+template <int VPT, bool WF32, bool HAS_DH>
 int run_norm_bwd(const NormBwdArgs& a, const Ring& q, int grid, const Ctx& c) {
   static std::atomic<uint64_t> done{0};
-  const int rc = allow_ring(rmsnorm_bwd_kernel<VPT, WF32>, done, c);
+  const auto kern = rmsnorm_bwd_kernel<VPT, WF32, HAS_DH>;
+  const int rc = allow_ring(kern, done, c);
   if (rc != FP8_OK) return rc;
-  return launch_dependent(rmsnorm_bwd_kernel<VPT, WF32>, dim3(grid), dim3(q.r.team * q.r.rows), ring_bytes(q), c.stream, a, q);
+  return launch_dependent(kern, dim3(grid), dim3(q.r.team * q.r.rows), ring_bytes(q), c.stream, a, q);
+}
+
+template <int VPT>
+int norm_bwd_dispatch(const NormBwdArgs& a, const Ring& q, int w_f32, int grid, const Ctx& c) {
+  if (q.r.tensors == 3) return w_f32 ? run_norm_bwd<VPT, true, true>(a, q, grid, c) : run_norm_bwd<VPT, false, true>(a, q, grid, c);
+  return w_f32 ? run_norm_bwd<VPT, true, false>(a, q, grid, c) : run_norm_bwd<VPT, false, false>(a, q, grid, c);
 }
 
 }  // namespace
@@ -591,11 +605,9 @@ int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, 
     a.part = dw ? ws : nullptr;
     a.inv_H = 1.0f / (float)H;
     a.wait_ns = c.wait_ns;
-    int rc;
-    if (q.r.vpt == 1)
-      rc = w_f32 ? run_norm_bwd<1, true>(a, q, (int)grid, c) : run_norm_bwd<1, false>(a, q, (int)grid, c);
-    else
-      rc = w_f32 ? run_norm_bwd<4, true>(a, q, (int)grid, c) : run_norm_bwd<4, false>(a, q, (int)grid, c);
+    const int rc = q.r.vpt == 1   ? norm_bwd_dispatch<1>(a, q, w_f32, (int)grid, c)
+                   : q.r.vpt == 2 ? norm_bwd_dispatch<2>(a, q, w_f32, (int)grid, c)
+                                  : norm_bwd_dispatch<4>(a, q, w_f32, (int)grid, c);
     if (rc != FP8_OK) return rc;
   }
   if (!dw) return FP8_OK;
