@@ -7,8 +7,8 @@
 //   renormalization scale * v[e_j] / sum_i v[e_i].
 //
 // Few tokens: one CTA chooses, counts and places. More take two launches, the second started while the first
-// runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 16.5 us, of which the choice 10; the
-// bytes are 2.8 us. It is bound by the choice's ~540 instructions a token and their latency at 32 warps an SM. Candidates
+// runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 16.1 us, of which the choice 10; the
+// bytes are 2.8 us. It is bound by the choice's ~500 instructions a token and their latency at 32 warps an SM. Candidates
 // gathered by each lane's next one in turn, with their logits loaded again, are fewer instructions but took 1.2 us more.
 #include "common.cuh"
 #include "internal.h"
@@ -119,6 +119,7 @@ struct RouteArgs {
   int E2;              // E rounded up to even
   int64_t per_chunk;   // tokens of a chunk (one CTA's)
   int chunks;
+  int warps, groups, per;  // place_slots: warps that take slots, groups of them, warps of a group
 };
 
 // A warp per token. The k-th largest of the lanes' maxima is a bound that at least k experts reach, and
@@ -207,8 +208,9 @@ FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* 
     if (p.renorm) w = w / (warp_sum(w) + 1e-20f);
   }
   if (id >= 0) {
-    p.ids[t * p.k + rank] = id;
-    p.weights[t * p.k + rank] = w * p.scale;
+    const int slot = (int)t * p.k + rank;  // T k < 2^31
+    p.ids[slot] = id;
+    p.weights[slot] = w * p.scale;
     if (hist) atomicAdd(hist + id, 1);
   } else if (n < p.k && lane >= n && lane < p.k) {  // fewer than k: the last slots are unused
     p.ids[t * p.k + lane] = -1;
@@ -244,11 +246,11 @@ FP8_DEVI int block_scan(int x, int32_t* warp_sums) {
 // place is its expert's, plus the slots of that expert in the warps before and in the lanes before. The
 // warps' counts (`count`, a row of E2 a warp) are summed by two experts a thread, the warps split over up to
 // 8 groups of threads whose totals (`total`, a row of E2 a group) the slots then add up.
-FP8_DEVI int rank_warps(int E2) { return min((int)blockDim.x / 32, E2 <= 512 ? 32 : 16); }
+constexpr int rank_warps(int threads, int E2) { return E2 > 512 && threads > 512 ? 16 : threads / 32; }
 __host__ __device__ constexpr int most_groups(int E2) { return E2 <= 512 ? 8 : 2; }
-FP8_DEVI int rank_groups(int E2) {
+int rank_groups(int threads, int E2) {
   int g = most_groups(E2);
-  while (g > 1 && g * (E2 / 2) > (int)blockDim.x) g >>= 1;
+  while (g > 1 && g * (E2 / 2) > threads) g >>= 1;
   return g;
 }
 // A batch's slots in their warps' counts (which are zero before); returns the slots of the same expert before this one
@@ -259,28 +261,29 @@ FP8_DEVI int count_slot(int id, int E2, uint16_t* count) {
   if (id >= 0 && before == 0) count[(threadIdx.x >> 5) * E2 + id] = (uint16_t)__popc(same);
   return before;
 }
-FP8_DEVI void sum_counts(int E2, uint16_t* total, uint16_t* count) {
-  const int groups = rank_groups(E2), per = rank_warps(E2) / groups, pairs = E2 / 2;
+FP8_DEVI void sum_counts(const RouteArgs& p, uint16_t* total, uint16_t* count) {
+  const int pairs = p.E2 / 2;
   uint32_t* count2 = reinterpret_cast<uint32_t*>(count);
-  for (int i = threadIdx.x; i < groups * pairs; i += blockDim.x) {
+  for (int i = threadIdx.x; i < p.groups * pairs; i += blockDim.x) {
     const int g = i / pairs, x = i - g * pairs;
+    uint32_t* c = count2 + g * p.per * pairs + x;
     uint32_t sum = 0;  // two 16-bit sums: at most 1024 slots in all
 #pragma unroll 4
-    for (int w = g * per; w < (g + 1) * per; ++w) {
-      const uint32_t c = count2[w * pairs + x];
-      count2[w * pairs + x] = sum;
-      sum += c;
+    for (int w = 0; w < p.per; ++w, c += pairs) {
+      const uint32_t v = *c;
+      *c = sum;
+      sum += v;
     }
-    reinterpret_cast<uint32_t*>(total)[g * pairs + x] = sum;
+    reinterpret_cast<uint32_t*>(total)[i] = sum;
   }
 }
 FP8_DEVI void put_slot(const RouteArgs& p, int64_t s, int id, int before, const int32_t* at, const uint16_t* total,
                        const uint16_t* count) {
-  const int warp = threadIdx.x >> 5, per = rank_warps(p.E2) / rank_groups(p.E2);
+  const int warp = threadIdx.x >> 5;
   int32_t place = -1;
   if (id >= 0) {
     place = at[id] + count[warp * p.E2 + id] + before;
-    for (int g = 0; g < warp / per; ++g) place += total[g * p.E2 + id];
+    for (int w = warp; w >= p.per; w -= p.per, total += p.E2) place += total[id];
     p.order[place] = (int32_t)s;
   }
   p.pos[s] = place;
@@ -288,26 +291,26 @@ FP8_DEVI void put_slot(const RouteArgs& p, int64_t s, int id, int before, const 
 // The slots from b to s1; `placed`: the batch before b has been placed, its totals are not yet in `at`.
 FP8_DEVI void place_slots(const RouteArgs& p, int64_t b, int64_t s1, bool placed, int32_t* at, uint16_t* total,
                           uint16_t* count) {
-  const int warp = threadIdx.x >> 5, warps = rank_warps(p.E2), groups = rank_groups(p.E2), pairs = p.E2 / 2;
-  for (; b < s1; b += 32 * warps, placed = true) {
+  const int warp = threadIdx.x >> 5;
+  for (; b < s1; b += 32 * p.warps, placed = true) {
     const int64_t s = b + threadIdx.x;
-    const int id = warp < warps && s < s1 ? p.ids[s] : -1;
+    const int id = warp < p.warps && s < s1 ? p.ids[s] : -1;
     if (placed) {
       __syncthreads();
       for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         int sum = 0;
-        for (int g = 0; g < groups; ++g) sum += total[g * p.E2 + e];
+        for (int g = 0; g < p.groups; ++g) sum += total[g * p.E2 + e];
         at[e] += sum;
       }
     }
-    for (int i = threadIdx.x; i < warps * pairs; i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    for (int i = threadIdx.x; i < p.warps * (p.E2 / 2); i += blockDim.x) reinterpret_cast<uint32_t*>(count)[i] = 0;
     __syncthreads();
     int before = 0;
-    if (warp < warps) before = count_slot(id, p.E2, count);
+    if (warp < p.warps) before = count_slot(id, p.E2, count);
     __syncthreads();
-    sum_counts(p.E2, total, count);
+    sum_counts(p, total, count);
     __syncthreads();
-    if (warp < warps && s < s1) put_slot(p, s, id, before, at, total, count);
+    if (warp < p.warps && s < s1) put_slot(p, s, id, before, at, total, count);
   }
 }
 // Unused slots leave the end of `order` without a slot.
@@ -377,14 +380,18 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
 // chunks and 256 experts, from L2) into its own first places, so that no launch is spent on a scan. What it takes is a
 // chain of latencies: its slots are read together with the matrix, and counted while that is summed.
 constexpr int kPlaceThreads = 1024;
-__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs p) {
+// ROWS: loads of the matrix in flight; 20 are all of a thread's for 152 chunks. REGS: with up to 40 a CTA fits an SM
+// beside one of route_kernel for few experts (24 to 46 registers and 32 warps, too), so that it has started when the
+// choice ends.
+template <int ROWS, int REGS>
+__global__ void __maxnreg__(REGS) route_place_kernel(const RouteArgs p) {
   extern __shared__ int32_t sh[];  // [E2] slots in the chunks before this one, [E2] slots, then place_slots' arrays
   __shared__ int32_t warp_sums[32];
   int32_t* prior = sh;
   int32_t* all = sh + p.E2;
   uint16_t* total = reinterpret_cast<uint16_t*>(sh + 2 * p.E2);
   uint16_t* count = total + most_groups(p.E2) * p.E2;
-  const int warp = threadIdx.x >> 5, warps = rank_warps(p.E2);
+  const int warp = threadIdx.x >> 5, warps = p.warps;
   const int pairs = p.E2 / 2;  // at most kPlaceThreads / 2
   for (int e = threadIdx.x; e < 2 * p.E2; e += kPlaceThreads) sh[e] = 0;
   for (int i = threadIdx.x; i < warps * pairs; i += kPlaceThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
@@ -400,16 +407,14 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
     const uint32_t* h = reinterpret_cast<const uint32_t*>(p.hist);
     const int x = threadIdx.x - grp * pairs;
     int a0 = 0, a1 = 0, b0 = 0, b1 = 0;
-    constexpr int kRows = 20;  // loads in flight: all of a thread's rows for 152 chunks of 256 experts
-    for (int c0 = grp; c0 < p.chunks; c0 += kRows * split) {
-      uint32_t v[kRows];
+    const int step = split * pairs;
+    for (int c0 = grp; c0 < p.chunks; c0 += ROWS * split) {
+      const uint32_t* row = h + (int64_t)c0 * pairs + x;
+      uint32_t v[ROWS];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int c = c0 + i * split;
-        v[i] = c < p.chunks ? __ldcg(h + (int64_t)c * pairs + x) : 0u;
-      }
+      for (int i = 0; i < ROWS; ++i) v[i] = c0 + i * split < p.chunks ? __ldcg(row + i * step) : 0u;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
+      for (int i = 0; i < ROWS; ++i) {  // both halves in one addition measured slower (1024 tokens 8.3 us, not 7.8)
         const int lo = v[i] & 0xFFFF, hi = v[i] >> 16;
         a0 += lo, a1 += hi;
         if (c0 + i * split < (int)blockIdx.x) b0 += lo, b1 += hi;
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   int before = 0;
   if (warp < warps) before = count_slot(id, p.E2, count);
   __syncthreads();
-  sum_counts(p.E2, total, count);
+  sum_counts(p, total, count);
   // E <= kPlaceThreads: an expert a thread
   const int e = threadIdx.x;
   const int n = e < p.E ? all[e] : 0;
@@ -523,11 +528,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps) route_bwd_kernel(const RouteBw
   if (id >= 0) store_logit(p.dlogits, BF16, t * p.E + id, all);
 }
 
-// Chunks of tokens: one CTA does it all for a token a warp, for two a warp where a row is one value a lane
-// (64 tokens of 8 experts 5.4 us, in chunks 5.8; of 256 experts 8.9 us, in chunks 7.5, of 512 14.3 and 8.6);
-// else a chunk for each of 152 SMs, and not above what 16-bit counts hold.
+// Chunks of tokens: one CTA does it all for a token a warp (32 tokens of 256 experts 5.7 us, in chunks 6.0; 64 tokens 8.9
+// and 6.1, of 512 experts 14.3 and 6.6, of 16 experts 5.4 and 4.9); else a chunk for each of 152 SMs, and not
+// above what 16-bit counts hold.
 int64_t chunk_tokens(int64_t T, int64_t E) {
-  if (T <= (E <= 32 ? 64 : 32)) return T < 1 ? 1 : T;
+  if (T <= (E <= 256 ? 32 : 16)) return T < 1 ? 1 : T;
   const int64_t n = round_up64(ceil_div64(T, 152), 8);
   return n < 65528 ? n : 65528;
 }
@@ -576,8 +581,12 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
     return FP8_OK;
   }
   RouteArgs a = {logits, bf16, bias, T,    (int)E, (int)k, softmax, renorm, scale, ids, weights,
-                 order,  pos,  ends, static_cast<uint16_t*>(ws), (int)round_up64(E, 2), chunk_tokens(T, E), 0};
+                 order,  pos,  ends, static_cast<uint16_t*>(ws), (int)round_up64(E, 2), chunk_tokens(T, E), 0, 0, 0, 0};
   a.chunks = (int)ceil_div64(T, a.per_chunk);
+  const int threads = a.chunks > 1 ? kPlaceThreads : E <= 256 ? 1024 : 512;
+  a.warps = rank_warps(threads, a.E2);
+  a.groups = rank_groups(threads, a.E2);
+  a.per = a.warps / a.groups;
   // up to 48 KB, which needs no attribute: place_slots' 40 to 43 KB and the candidates' 8 to 16 KB share it
   const size_t choose = (size_t)(a.E2 + 3) / 4 * 16 + (E <= 256 ? 32 : 16) * 32 * sizeof(Cand);
   const size_t smem = a.chunks == 1 && place_bytes(a.E2) > choose ? place_bytes(a.E2) : choose;
@@ -586,7 +595,10 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE
   if (rc != FP8_OK || !order || a.chunks == 1) return rc;
-  return launch_dependent(route_place_kernel, dim3((unsigned)a.chunks), dim3(kPlaceThreads),
+  // Up to 40 chunks a thread has at most 5 rows (100 tokens of 256 experts 6.7 us, with 20 loads 7.5); few registers for
+  // few experts (1024 tokens of 8 experts 5.3 us instead of 6.2, but of 256 8.3 instead of 7.9).
+  const auto place = a.chunks <= 40 ? route_place_kernel<5, 40> : E <= 64 ? route_place_kernel<20, 40> : route_place_kernel<20, 64>;
+  return launch_dependent(place, dim3((unsigned)a.chunks), dim3(kPlaceThreads),
                           place_bytes(a.E2) + (size_t)a.E2 * 4, c.stream, a);
 }
 

@@ -75,6 +75,15 @@ def test_choice_weights_table(fp8, T, E, k, softmax, renorm, dtype):
     assert ((w.double() - ref).abs() <= 64 * U * ref).all()
 
 
+@pytest.mark.parametrize("T,E,k", [(33, 600, 5), (60, 1024, 16), (17, 257, 4), (16, 900, 2), (320, 64, 6), (321, 65, 6), (700, 64, 8), (4000, 1000, 3), (9000, 512, 16), (499000, 4, 2), (700001, 9, 1)])
+def test_many_experts_and_long_chunks(fp8, T, E, k):
+    """Chunks of several batches of slots, and of thousands of tokens; most slots at one expert."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    logits[: T // 2, E - 1] += 8
+    _run(fp8, logits, k)
+
+
 def test_ties_take_the_lowest_index(fp8):
     g = torch.Generator(device="cuda").manual_seed(1)
     logits = torch.randint(-2, 3, (777, 200), generator=g, device="cuda").float()
