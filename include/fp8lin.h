@@ -384,7 +384,8 @@ int fp8_add_rmsnorm(const fp8_tensor* x, const fp8_tensor* residual, const fp8_t
  *              own buffer.
  *  dw          bf16 or fp32 [H] or NULL. Summed in fp32 in an order that depends on T and H only:
  *              the same bits on every run. T == 0 gives zeros.
- *  workspace   fp8_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, when dw is given.
+ *  workspace   fp8_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, when dw is given;
+ *              it serves fewer rows too.
  * There is no status word: a wait for a load that ran out (fp8_set_wait_limit_ns) shows as NaN in its row's dx
  * and in dw.
  */
@@ -409,7 +410,8 @@ size_t fp8_rmsnorm_bwd_workspace_size(int64_t T, int64_t H);
  *              expert (the offsets of fp8_grouped_mm); order int32 [T k]: the slots t * k + j sorted by
  *              expert, in slot order within an expert, -1 past ends[E - 1]; pos int32 [T, k]: each
  *              slot's place in order (the row of its product), -1 for an unused slot.
- *  workspace   fp8_moe_route_workspace_size(T, E) bytes, 16-byte aligned, with the table.
+ *  workspace   fp8_moe_route_workspace_size(T, E) bytes, 16-byte aligned, with the table; it serves
+ *              fewer tokens too.
  */
 int fp8_moe_route(const fp8_tensor* logits, const fp8_tensor* bias, int score, int renormalize, float scale,
                   fp8_tensor* ids, fp8_tensor* weights, fp8_tensor* order, fp8_tensor* pos,
@@ -438,7 +440,8 @@ int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids, const fp8
  *              (up), as fp8_quantize with FP8_GRAN_ROW writes them; E <= 1024.
  *  w2, s2      E4M3 [E, H, I] and fp32 [E, H].
  *  out         bf16 [T, H].
- *  workspace   fp8_moe_tokens_workspace_size(T, k, H, I) bytes, 16-byte aligned.
+ *  workspace   fp8_moe_tokens_workspace_size(T, k, H, I) bytes, 16-byte aligned; it serves fewer
+ *              tokens too.
  * Sums are fp32 and the result is rounded once. The activations enter the products as sums of 8-bit parts:
  * x exactly down to 2^-13 of its row's largest and to 2^-21 of that below, the hidden layer to 2^-13 of each
  * value (2^-25 of the largest in its block of 32). A row with a NaN or an infinity gives NaN wherever the formula does. The same

@@ -571,7 +571,11 @@ int run_route_bwd(const RouteBwdArgs& a, const Ctx& c) {
 
 }  // namespace
 
-int64_t route_ws_bytes(int64_t T, int64_t E) { return round_up64(ceil_div64(T, chunk_tokens(T, E)) * round_up64(E, 2) * 2, 16); }
+// A row of counts a chunk; 152 rows at least, so that a workspace for many tokens serves fewer too.
+int64_t route_ws_bytes(int64_t T, int64_t E) {
+  const int64_t chunks = ceil_div64(T, chunk_tokens(T, E));
+  return round_up64((chunks < 152 ? 152 : chunks) * round_up64(E, 2) * 2, 16);
+}
 
 int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int64_t E, int64_t k, int softmax,
                  int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,

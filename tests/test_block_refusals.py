@@ -117,6 +117,20 @@ def test_moe_tokens(fp8):
     assert fp8.fp8_moe_tokens_workspace_size(65, 2, 256, 128) == 0
 
 
+def test_workspace_for_many_serves_fewer(fp8):
+    """A workspace sized for the most tokens is large enough for any smaller number of them."""
+    counts = sorted({1, 2, 8, 16, 17, 32, 33, 63, 64, 65, 100, 1216, 1217, 1218, 2432, 2433, 5000, 16384, 10 ** 6, 10 ** 7, 10 ** 8})
+    for E in (1, 8, 32, 33, 256, 257, 1024):
+        sizes = [fp8.fp8_moe_route_workspace_size(T, E) for T in counts]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    for H in (8, 264, 2056, 4096, 7168, 8200, 12296, 16384):
+        sizes = [fp8.fp8_rmsnorm_bwd_workspace_size(T, H) for T in counts]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    for k, H, I in ((1, 512, 256), (8, 7168, 2048), (16, 1040, 528)):
+        sizes = [fp8.fp8_moe_tokens_workspace_size(T, k, H, I) for T in range(1, 65)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 def test_binding_refuses_strided_tensors(fp8):
     import torch
     x = torch.zeros(8, 512, dtype=torch.bfloat16)[:, ::2]
