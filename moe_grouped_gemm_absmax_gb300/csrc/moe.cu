@@ -895,13 +895,19 @@ WsLayout ws_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
   return L;
 }
 
+// The ring of a product in `room` bytes of shared memory; returns what its CTA takes.
+int ring(int ph, MoeArgs* a, int room) {
+  const int per = ph == 1 ? kPerGroup1 : kPerGroup2;
+  a->b_bytes = (a->cap + per - 1) / per * 16 * 128;  // columns of N for an entry
+  const int stage_bytes = kUnitBytes + a->b_bytes + (ph == 2 ? 1024 : 0);
+  const int rest = 1024 + layout(ph, a->T, a->k, a->E).total;
+  const int fit = (room - rest) / stage_bytes;  // at least 4: T, k and E are bounded
+  a->stages = fit < kMaxStages ? fit : kMaxStages;
+  return rest + a->stages * stage_bytes;
+}
 template <int PH, int NB>
 int run_moe(const CUtensorMap& tm, const CUtensorMap& tm_next, MoeArgs a, int room, int grid, const Ctx& c) {
-  const Layout L = layout(PH, a.T, a.k, a.E);
-  const int stage_bytes = kUnitBytes + a.b_bytes + (PH == 2 ? 1024 : 0);
-  const int fit = (room - 1024 - L.total) / stage_bytes;  // at least 4: T, k and E are bounded
-  a.stages = fit < kMaxStages ? fit : kMaxStages;
-  const size_t smem = 1024 + (size_t)a.stages * stage_bytes + L.total;
+  const int smem = ring(PH, &a, room);
   auto kern = moe_kernel<PH, NB>;
   // Once for each device: all of an SM's memory as shared memory, so that the two products' CTAs fit
   // together.
@@ -947,8 +953,6 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   a.wait_ns = c.wait_ns;
   a.test_stall = c.test_stall;
   a.cap = (int)(T < kMaxEntry ? T : kMaxEntry);
-  // columns of N for an entry, in the layout that needs more of them (5 slots to a group of 16)
-  a.b_bytes = (int)ceil_div64(a.cap, kPerGroup2) * 16 * 128;
   const int grid = (int)(c.sm_count < kMaxGrid ? c.sm_count : kMaxGrid);
 
   CUtensorMap t13, t2;
@@ -976,7 +980,9 @@ int launch_moe_tokens(const void* x, const int32_t* ids, const float* weights, c
   // more builders, and the second product then follows on each SM as the first leaves it.
   if (T <= kFewTokens) {
     a.scales = s13;
-    rc = run_moe<1, 4>(t13, t2, a, kSmemPair, grid, c);
+    // twice as many bytes pass through the first product: it gets what the second one's whole stages leave
+    MoeArgs second = a;
+    rc = run_moe<1, 4>(t13, t2, a, 2 * kSmemPair - ring(2, &second, kSmemPair), grid, c);
     if (rc != FP8_OK) return rc;
     a.scales = s2;
     return run_moe<2, 4>(t2, t2, a, kSmemPair, grid, c);
