@@ -257,6 +257,23 @@ FP8_DEVI bool wait_count_geq(const uint32_t* p, uint32_t target, uint64_t limit_
 // it on the stream has ended, and waits here until that one has ended and its writes are visible. Nothing
 // that the kernel before may write is read, and nothing that it may read is written, ahead of the wait.
 FP8_DEVI void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// What comes from before the wait is read with plain loads or with those below: the read-only path's (ld.global.nc, const
+// __restrict__) may be moved ahead of the wait, and so may assembly that is not volatile.
+FP8_DEVI uint32_t ld_l2(const uint32_t* p) {
+  uint32_t r;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+  return r;
+}
+FP8_DEVI int32_t ld_l2(const int32_t* p) { return (int32_t)ld_l2(reinterpret_cast<const uint32_t*>(p)); }
+FP8_DEVI float ld_l2(const float* p) { return __uint_as_float(ld_l2(reinterpret_cast<const uint32_t*>(p))); }
+FP8_DEVI uint4 ld_l2(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
 // Once every CTA has come here (or ended), the next kernel may begin.
 FP8_DEVI void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

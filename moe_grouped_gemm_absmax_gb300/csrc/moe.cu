@@ -253,9 +253,9 @@ struct Walk {
 // The tokens' parts, a CTA per token, and the counters' zeros. The first product is launched while
 // this one runs.
 constexpr int kSplitThreads = 512;
-__global__ void __launch_bounds__(kSplitThreads) moe_split_kernel(const uint16_t* __restrict__ x, int H, int Hp,
-                                                                  uint8_t* __restrict__ xq, float* __restrict__ xinv,
-                                                                  uint32_t* __restrict__ counters, int n_counters) {
+__global__ void __launch_bounds__(kSplitThreads) moe_split_kernel(const uint16_t* x, int H, int Hp,
+                                                                  uint8_t* xq, float* xinv,
+                                                                  uint32_t* counters, int n_counters) {
   __shared__ uint32_t red[kSplitThreads / 32];
   pdl_wait();
   pdl_trigger();  // after the wait: the next kernel reads ids ahead of its own
@@ -312,7 +312,7 @@ FP8_DEVI void scan2(int x, int y, int lane, int* ex, int* ey, int* tx, int* ty) 
   *ty = __shfl_sync(0xffffffffu, b, 31);
 }
 FP8_DEVI int valid_id(const MoeArgs& p, int s) {
-  const int id = p.ids[s];
+  const int id = ld_l2(p.ids + s);  // ahead of this kernel's own wait, see moe_split_kernel
   if (id >= -1 && id < p.E) return id;
   if (blockIdx.x == 0) set_status(p.status, FP8_DEV_BAD_IDS);
   return -1;
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     constexpr int kBatch = kAhead ? (PH + 1) * kFewTokens / 4 : 1;  // loads a lane for an entry's rows
     pdl_wait();  // the tokens' parts / the hidden layer are there
     if (PH == 2) {
-      for (int i = tid - 64; i < used; i += 32 * NB) wt[i] = __ldg(p.weights + slot_tmp[i]);
+      for (int i = tid - 64; i < used; i += 32 * NB) wt[i] = p.weights[slot_tmp[i]];
       named_bar_sync(1, 32 * NB);
       if (lane == 0) mbar_arrive(&S.ready);
     }
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       const int k0 = at.kk * 128 + chunk * 16;
       // the codes of four blocks of slot `lane`'s hidden layer; blocks past I have none
       auto codes = [&](int j) {
-        const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(p.hs) + (int64_t)(start + j) * p.nk2 + at.kk);
+        const uint32_t w = ld_l2(reinterpret_cast<const uint32_t*>(p.hs) + (int64_t)(start + j) * p.nk2 + at.kk);
         const int blocks = (p.I - at.kk * 128 + 31) / 32;
         return blocks >= 4 ? w : w & ((1u << (8 * blocks)) - 1);
       };
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           const int row = 4 * b + (lane >> 3);
-          v[b] = row < rows && in ? __ldcg(reinterpret_cast<const uint4*>(from(row))) : make_uint4(0, 0, 0, 0);
+          v[b] = row < rows && in ? ld_l2(reinterpret_cast<const uint4*>(from(row))) : make_uint4(0, 0, 0, 0);
         }
       }
       if (!enter()) break;
@@ -706,13 +706,13 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       const int64_t step = (int64_t)2 * p.T * kRows;
       const float* o = p.part + c0 * step + (R.first(c0) >= first ? 0 : p.T * kRows) + col0 * kRows + r;
 #pragma unroll
-      for (int j = 0; j < W; ++j) v[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
+      for (int j = 0; j < W; ++j) v[j] = col0 + j < cols ? ld_l2(o + j * kRows) : 0.f;
       o = p.part + (c0 + 1) * step + col0 * kRows + r;
 #pragma unroll 2
       for (int c = c0 + 1; c <= c1; ++c, o += step) {
         float u[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) u[j] = col0 + j < cols ? __ldcg(o + j * kRows) : 0.f;
+        for (int j = 0; j < W; ++j) u[j] = col0 + j < cols ? ld_l2(o + j * kRows) : 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) v[j] += u[j];
       }
@@ -722,14 +722,14 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
       // ---- hidden = silu(gate) * up ----
       int xbuf = 0;
       pdl_wait();
-      for (int i = tid - 32 * kEpi0; i < used; i += 128) inv[i] = __ldcg(p.xinv + tok[i]);
+      for (int i = tid - 32 * kEpi0; i < used; i += 128) inv[i] = ld_l2(p.xinv + tok[i]);
       named_bar_sync(2, 128);
       for (int it = R.it0; it < R.it1;) {
         const int X = it / nk, first = X * nk, len = min(first + nk, R.it1) - it;
         const int a = X / p.tiles1, tile = X - a * p.tiles1;
         const int cnt = ent_cnt[a], start = ent_start[a];
         const int i = tile * 64 + (r & 63);
-        const float s = i < p.I ? __ldg(p.scales + ((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i) : 0.f;
+        const float s = i < p.I ? p.scales[((int64_t)ent_e[a] * 2 + (r >> 6)) * p.I + i] : 0.f;
         const bool whole = len == nk;
         // Gate or up of 8 slots' row r -> the hidden layer, its parts and scales. The gate rows' threads take the
         // first four slots, the up rows' the others; each gives the other side what it lacks.
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         while (it < end) {
           const int X = it / nk, len = min((X + 1) * nk, end) - it;
           const int a = X - tile * n_act, cnt = ent_cnt[a], start = ent_start[a];
-          const float s = nrow < p.H ? __ldg(p.scales + (int64_t)ent_e[a] * p.H + nrow) : 0.f;
+          const float s = nrow < p.H ? p.scales[(int64_t)ent_e[a] * p.H + nrow] : 0.f;
           const int buf = seg & 1;
           if (!wait_tile(buf)) {
             ok = false;

@@ -77,14 +77,24 @@ FP8_DEVI void unpack8(uint4 v, float2* f) {
 FP8_DEVI uint4 pack8(const float2* f) {
   return make_uint4(pack_bf16(f[0]), pack_bf16(f[1]), pack_bf16(f[2]), pack_bf16(f[3]));
 }
-// 8 weights from bf16 or fp32
-FP8_DEVI void load_w(const void* w, int w_f32, int c, float2* f) {
-  if (w_f32) {
-    const float4 a = __ldg(static_cast<const float4*>(w) + 2 * c), b = __ldg(static_cast<const float4*>(w) + 2 * c + 1);
-    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+// 8 weights from bf16 (one vector) or fp32 (two)
+FP8_DEVI void unpack_w(const uint4* v, bool f32, float2* f) {
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = make_float2(__uint_as_float(i & 1 ? v[i / 2].z : v[i / 2].x), __uint_as_float(i & 1 ? v[i / 2].w : v[i / 2].y));
   } else {
-    unpack8(__ldg(static_cast<const uint4*>(w) + c), f);
+    unpack8(v[0], f);
   }
+}
+FP8_DEVI void load_w(const void* w, int f32, int c, float2* f) {
+  const uint4* v = static_cast<const uint4*>(w);
+  uint4 a[2];
+  if (f32)
+    a[0] = v[2 * c], a[1] = v[2 * c + 1];
+  else
+    a[0] = v[c];
+  unpack_w(a, f32, f);
 }
 
 // A team's values from its warps, 32 slots; the slots past its warps hold zeros. Written by the team's first warp
@@ -217,10 +227,11 @@ FP8_DEVI void norm_out(const NormArgs& p, int64_t row, int c, const float2* s, f
 // that took rows through shared memory 53 us. 36 us now, 96% of the copy rate; without a residual and with block
 // scales the instructions bound it instead (14336 x 4096 39 us; the bytes are 26 us; 43 us at 77% of the issue slots
 // with one kernel for every residual and weight type). The weights' type is known at compile time except in a CTA a
-// row with four vectors a thread: there it makes the compiler load all weights ahead, in registers that cost
-// CTAs (4778 x 12288 68 us instead of 64).
+// row with four vectors a thread: there all weights loaded ahead take registers that cost CTAs (4778 x 12288 68 us
+// instead of 64). Registers: 48 keep five CTAs of 256 threads an SM (8192 x 4096 35.8 us, with 52 37.4), 80 three
+// of 224 or 256 (8192 x 7168 with block scales and no residual 48 us, with 91 63), 64 four of eight warps.
 template <int VPT, int GRAN, int FMT, bool WARP, bool RES, bool WF32>
-__global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const NormArgs p) {
+__global__ void __maxnreg__(VPT == 2 ? 48 : WARP ? 64 : 80) add_rmsnorm_kernel(const NormArgs p) {
   constexpr float FMAX = FmtMax<FMT>::v;
   __shared__ __align__(16) float red_s[32], red_m[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -237,6 +248,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
     vx[i] = c < p.nvec ? ld_stream(p.x + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
     vr[i] = RES && c < p.nvec ? ld_stream(p.res + row * p.nvec + c) : make_uint4(0, 0, 0, 0);
   }
+  constexpr bool kTyped = WARP || VPT == 2;  // the weights' type is WF32; they are loaded ahead of h's stores
+  uint4 vw[VPT][2];
+#pragma unroll
+  for (int i = 0; kTyped && i < VPT; ++i) {
+    const int c = t + i * team;
+    const uint4* w = static_cast<const uint4*>(p.w) + (WF32 ? 2 * c : c);
+    vw[i][0] = c < p.nvec ? w[0] : make_uint4(0, 0, 0, 0);
+    vw[i][1] = WF32 && c < p.nvec ? w[1] : make_uint4(0, 0, 0, 0);
+  }
   float2 s[VPT][4];
   float2 sum2 = both(0.f);
   float mx = 0.f;
@@ -247,7 +267,10 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) add_rmsnorm_kernel(const Nor
     float2 w8[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w8[j] = both(0.f);
-    if (c < p.nvec) load_w(p.w, WARP || VPT == 2 ? WF32 : p.w_f32, c, w8);
+    if (kTyped)
+      unpack_w(vw[i], WF32, w8);
+    else if (c < p.nvec)
+      load_w(p.w, p.w_f32, c, w8);
     const float m = norm_in(vx[i], vr[i], RES, w8, p.h && c < p.nvec ? p.h + row * p.nvec + c : nullptr,
                             s[i], &sum2);
     if (GRAN == FP8_GRAN_ROW) mx = max_nan(mx, m);
@@ -295,7 +318,7 @@ template <int GRAN, int FMT>
 int norm_dispatch(const NormArgs& a, const Ctx& c) {
   // A warp a row for the shortest rows, and with four vectors a thread up to 1024 columns where there are so many
   // rows that the start of a CTA for each (17 us for 16384) is what a call takes: 16384 x 768 10 us instead of
-  // 17, with a residual 15.6 instead of 17.6; 16384 x 1024 13 instead of 17, 20.9 instead of 19.1.
+  // 17, with a residual 15.6 instead of 17.6; 16384 x 1024 11 instead of 17, 19.4 instead of 19.1.
   // Fewer rows end sooner with a CTA each (1024 x 1024 2.3 and 2.8 us).
   // A CTA a row else, two vectors a thread: with few rows a row's latency counts (1024 x 5120 4.2 us, with four
   // 5.6). Four for rows above 8192 columns, which 512 threads with two do not cover, and above 5120 for many
@@ -470,7 +493,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
   uint32_t phase = 0;
   auto row_rstd = [&](int64_t g) {
     const int64_t row = g * q.r.rows + team;
-    return row < q.T ? __ldg(p.rstd + row) : 0.f;
+    return row < q.T ? p.rstd[row] : 0.f;
   };
   float rstd_next = row_rstd(blockIdx.x);
   for (int64_t g = blockIdx.x; g < q.groups; g += gridDim.x, par ^= 1) {
@@ -494,7 +517,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
       for (int j = 0; j < 4; ++j) {
         const float2 dyh = fmul2_rn(unpack2(word(vdy[i], j)), unpack2(word(vh[i], j)));
         dw[i][j] = ffma2_rn(dyh, both(rstd), dw[i][j]);
-        sum2 = ffma2_rn(dyh, WF32 ? __ldg(static_cast<const float2*>(p.w) + 4 * c + j) : unpack2(word(wv[i], j)), sum2);
+        sum2 = ffma2_rn(dyh, WF32 ? static_cast<const float2*>(p.w)[4 * c + j] : unpack2(word(wv[i], j)), sum2);
       }
     }
     float sum = sum2.x + sum2.y;  // of dy * w * h: rstd comes in below
@@ -514,7 +537,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 g2 = ffma2_rn(unpack2(word(vh[i], j)), both(-c1), unpack2(word(vdh[i], j)));
-        o[j] = pack_bf16(ffma2_rn(fmul2_rn(unpack2(word(vdy[i], j)), WF32 ? __ldg(static_cast<const float2*>(p.w) + 4 * c + j) : unpack2(word(wv[i], j))), both(rstd), g2));
+        o[j] = pack_bf16(ffma2_rn(fmul2_rn(unpack2(word(vdy[i], j)), WF32 ? static_cast<const float2*>(p.w)[4 * c + j] : unpack2(word(wv[i], j))), both(rstd), g2));
       }
       p.dx[row * nvec + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -557,7 +580,7 @@ __global__ void __launch_bounds__(512) dw_sum_kernel(const float4* part, int par
   if (c < n4) {
 #pragma unroll 8
     for (int r = threadIdx.y; r < parts; r += 16) {
-      const float4 v = __ldcg(part + (int64_t)r * n4 + c);
+      const float4 v = part[(int64_t)r * n4 + c];
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
   }

@@ -20,8 +20,8 @@ namespace {
 constexpr int kBwdWarps = 8;
 
 FP8_DEVI float load_logit(const void* p, int bf16, int64_t i) {
-  return bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16)
-              : __ldg(static_cast<const float*>(p) + i);
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16)
+              : static_cast<const float*>(p)[i];
 }
 FP8_DEVI void store_logit(void* p, int bf16, int64_t i, float v) {
   if (bf16)
@@ -56,11 +56,11 @@ FP8_DEVI void load_row(const void* p, int bf16, int64_t row, int E, int lane, fl
       float4 q = make_float4(none, none, none, none);
       if (e < E) {
         if (bf16) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + row * E + e));
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + row * E + e);
           q = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
                           __uint_as_float(w.y & 0xFFFF0000u));
         } else {
-          q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + row * E + e));
+          q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + row * E + e);
         }
       }
       v[i] = q.x;
@@ -400,7 +400,7 @@ __global__ void __maxnreg__(REGS) route_place_kernel(const RouteArgs p) {
   pdl_trigger();
   const int64_t n_slots = p.T * p.k, len = p.per_chunk * p.k;
   const int64_t s0 = blockIdx.x * len, s1 = s0 + len < n_slots ? s0 + len : n_slots, s = s0 + threadIdx.x;
-  const int id = warp < warps && s < s1 ? __ldcg(p.ids + s) : -1;
+  const int id = warp < warps && s < s1 ? p.ids[s] : -1;
   const int split = min(kPlaceThreads / pairs, 8);  // threads that share a pair of experts
   const int grp = threadIdx.x / pairs;
   if (grp < split) {
@@ -412,7 +412,7 @@ __global__ void __maxnreg__(REGS) route_place_kernel(const RouteArgs p) {
       const uint32_t* row = h + (int64_t)c0 * pairs + x;
       uint32_t v[ROWS];
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) v[i] = c0 + i * split < p.chunks ? __ldcg(row + i * step) : 0u;
+      for (int i = 0; i < ROWS; ++i) v[i] = c0 + i * split < p.chunks ? row[i * step] : 0u;
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {  // both halves in one addition measured slower (1024 tokens 8.3 us, not 7.8)
         const int lo = v[i] & 0xFFFF, hi = v[i] >> 16;
