@@ -30,7 +30,8 @@ class Fp8MoEBlock:
 
     def __call__(self, x, residual=None, status=None):
         """x (and residual) bf16 [T, H] -> (the experts' weighted sum bf16 [T, H], the new residual stream bf16 [T, H]).
-        More than MOE_MAX_TOKENS tokens need top_k experts that can be chosen for each (see fp8_moe_route)."""
+        A token with fewer than top_k experts that can be chosen (see fp8_moe_route) gets the sum over those there are,
+        one with none zeros."""
         T, H = x.shape
         few = T <= MOE_MAX_TOKENS
         h, y, q, inv, _ = add_rmsnorm_alloc(x, self.norm_weight, self.eps, residual, None if few else GRAN_ROW, want_y=True)
@@ -41,18 +42,24 @@ class Fp8MoEBlock:
                                                          self.scale, table=not few, status=status)
         if few:
             return moe_tokens_alloc(y, ids, weights, self.w13, self.s13, self.w2, self.s2, status=status), h
-        # rows by expert: codes and scales of the slots' tokens
-        token = order.div(self.top_k, rounding_mode="floor").long()
+        # rows by expert: codes and scales of the slots' tokens. Unused slots leave rows at the end; they go to the last
+        # expert with any token's codes (the offsets cover all rows, without a look at the device's counts), and
+        # `pos` -1 takes the last row, of zeros, behind the product's.
+        ends[-1:].fill_(T * self.top_k)
+        token = order.div(self.top_k, rounding_mode="floor").clamp_(min=0).long()
         a = q.view(torch.uint8)[token].view(q.dtype)
         gate_up = self._grouped(a, inv[token], self.w13, self.s13, ends, status).float()
         gate, up = gate_up.chunk(2, 1)
         act = (torch.nn.functional.silu(gate) * up).to(torch.bfloat16)
         aq, _, ainv = quantize_alloc(act, GRAN_ROW, DT_E4M3)
-        out = self._grouped(aq, ainv, self.w2, self.s2, ends, status)[pos.view(-1).long()].float()
+        out = self._grouped(aq, ainv, self.w2, self.s2, ends, status, spare=1)
+        out[-1:].zero_()
+        out = out[pos.view(-1).long()].float()
         return (out.view(T, self.top_k, H) * weights[..., None]).sum(1).to(torch.bfloat16), h
 
     @staticmethod
-    def _grouped(a, inv, w, s, ends, status):
-        out = torch.empty((a.shape[0], w.shape[1]), dtype=torch.bfloat16, device=a.device)
-        fp8_grouped_mm(a, w, ends, inv, s, out, GROUPED_JAGGED_M, status=status)
+    def _grouped(a, inv, w, s, ends, status, spare=0):
+        """The product's rows, and `spare` more that it does not write."""
+        out = torch.empty((a.shape[0] + spare, w.shape[1]), dtype=torch.bfloat16, device=a.device)
+        fp8_grouped_mm(a, w, ends, inv, s, out[:a.shape[0]], GROUPED_JAGGED_M, status=status)
         return out
