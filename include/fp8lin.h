@@ -434,8 +434,8 @@ int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids, const fp8
  * with W[e, n, k] = code * scale of its row. Only the experts named are read, each once.
  *  x           bf16 [T, H], T <= FP8_MOE_MAX_TOKENS; H and I multiples of 16, <= 65536.
  *  ids         int32 [T, k], k <= 16: -1 marks an unused slot (its weight is not read); a token
- *              without any used slot gives zeros. Other ids outside 0 .. E - 1 set FP8_DEV_BAD_IDS and
- *              count as unused. weights fp32 [T, k].
+ *              without any used slot gives zeros (NaN if its x holds a NaN or an infinity). Other ids
+ *              outside 0 .. E - 1 set FP8_DEV_BAD_IDS and count as unused. weights fp32 [T, k].
  *  w13, s13    E4M3 [E, 2 I, H] and fp32 [E, 2 I]: rows 0 .. I - 1 are W1 (gate), rows I .. 2 I - 1 W3
  *              (up), as fp8_quantize with FP8_GRAN_ROW writes them; E <= 1024.
  *  w2, s2      E4M3 [E, H, I] and fp32 [E, H].

@@ -114,7 +114,7 @@ __host__ __device__ inline Layout layout(int ph, int T, int k, int E) {
   L.acc = o, o += ph == 1 ? 2 * kPerGroup1 * 64 * 4 : T * kRows * 4;  // gate and up on their way; output sums
   L.shared = o, o += (int)sizeof(Shared);
   L.wt = o, o += n * 4;    // per sorted slot: its index, then its weight
-  L.inv = o, o += n * 4;   // its token's power of two
+  L.inv = o, o += n * 4;   // its token's power of two; in the second product, per token, what its sum starts from
   L.hist = o, o += n > 32 ? E * 4 : 0;
   L.ids = o, o += n * 4;
   L.ent = o, o += n * 4;   // per entry: expert, first slot
@@ -167,12 +167,13 @@ FP8_DEVI uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
 }
 
 // The power of two that brings a row's largest magnitude (bit pattern of an fp32) into [128, 256), and
-// its inverse. A row with an infinity or a NaN gets NaN, which makes all of its values NaN.
+// its inverse. A row with an infinity or a NaN gets NaN for both, which makes all of its values NaN, and its
+// output even where no expert takes it.
 FP8_DEVI void row_scale(uint32_t amax_bits, float* mult, float* inv) {
   const int ef = (int)(amax_bits >> 23);
   const int s = min(134 - ef, 126);
   *mult = ef == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 + s) << 23);
-  *inv = ef == 255 ? 1.0f : __uint_as_float((uint32_t)(127 - s) << 23);
+  *inv = ef == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - s) << 23);
 }
 
 // Four values, already scaled, into PARTS words of e4m3 codes.
@@ -460,11 +461,11 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
   const uint32_t tmem_base = S.tmem_base;
   const int n_act = S.n_act, used = S.used;
 
-  if (n_act == 0) {  // nothing to read: zeros
+  if (n_act == 0) {  // nothing to read: zeros, NaN for a token that holds one
     pdl_wait();  // not done before the kernel before it is
     if (PH == 2)
       for (int64_t i = (int64_t)cta * kThreads + tid; i < (int64_t)p.T * p.H; i += (int64_t)grid * kThreads)
-        p.out[i] = __float2bfloat16_rn(0.f);
+        p.out[i] = __float2bfloat16_rn(0.f * ld_l2(p.xinv + i / p.H));
     if (warp == 1) tmem_dealloc(tmem_base, kTmem);
     return;
   }
@@ -608,6 +609,8 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
     pdl_wait();  // the tokens' parts / the hidden layer are there
     if (PH == 2) {
       for (int i = tid - 64; i < used; i += 32 * NB) wt[i] = p.weights[slot_tmp[i]];
+      if (used < n)  // a token without experts: its sum starts from 0, or from NaN
+        for (int i = tid - 64; i < p.T; i += 32 * NB) inv[i] = 0.f * ld_l2(p.xinv + i);
       named_bar_sync(1, 32 * NB);
       if (lane == 0) mbar_arrive(&S.ready);
     }
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(32 * (6 + NB), NB <= 4 ? 2 : 1)
         const int nrow = tile * kRows + r;
         const bool whole = it == first && end == first + per;
         float* mine = my_part + (it == R.it0 ? 0 : p.T * kRows);
-        for (int t = 0; t < p.T; ++t) acc[t * kRows + r] = 0.f;
+        for (int t = 0; t < p.T; ++t) acc[t * kRows + r] = used < n ? inv[t] : 0.f;
         while (it < end) {
           const int X = it / nk, len = min((X + 1) * nk, end) - it;
           const int a = X - tile * n_act, cnt = ent_cnt[a], start = ent_start[a];

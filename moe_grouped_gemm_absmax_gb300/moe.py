@@ -31,7 +31,7 @@ class Fp8MoEBlock:
     def __call__(self, x, residual=None, status=None):
         """x (and residual) bf16 [T, H] -> (the experts' weighted sum bf16 [T, H], the new residual stream bf16 [T, H]).
         A token with fewer than top_k experts that can be chosen (see fp8_moe_route) gets the sum over those there are,
-        one with none zeros."""
+        one with none zeros. A NaN or an infinity in a token gives NaN in its row of both."""
         T, H = x.shape
         few = T <= MOE_MAX_TOKENS
         h, y, q, inv, _ = add_rmsnorm_alloc(x, self.norm_weight, self.eps, residual, None if few else GRAN_ROW, want_y=True)
@@ -55,6 +55,9 @@ class Fp8MoEBlock:
         out = self._grouped(aq, ainv, self.w2, self.s2, ends, status, spare=1)
         out[-1:].zero_()
         out = out[pos.view(-1).long()].float()
+        # A NaN or an infinity makes all logits of its token NaN: no expert takes it, and none would show it. The row's
+        # scale is NaN too.
+        weights = weights + inv[:, None] * 0
         return (out.view(T, self.top_k, H) * weights[..., None]).sum(1).to(torch.bfloat16), h
 
     @staticmethod
