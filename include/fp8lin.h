@@ -386,8 +386,8 @@ int fp8_add_rmsnorm(const fp8_tensor* x, const fp8_tensor* residual, const fp8_t
  *              the same bits on every run. T == 0 gives zeros.
  *  workspace   fp8_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, when dw is given;
  *              it serves fewer rows too.
- * There is no status word: a wait for a load that ran out (fp8_set_wait_limit_ns) shows as NaN in its row's dx
- * and in dw.
+ * There is no status word: a wait for a load that ran out (fp8_set_wait_limit_ns) shows as NaN in dx of all rows
+ * of its CTA and in all of dw.
  */
 int fp8_add_rmsnorm_bwd(const fp8_tensor* dy, const fp8_tensor* h, const fp8_tensor* weight,
                         const fp8_tensor* rstd, const fp8_tensor* dh, fp8_tensor* dx, fp8_tensor* dw,
@@ -455,10 +455,11 @@ size_t fp8_moe_tokens_workspace_size(int64_t T, int64_t top_k, int64_t H, int64_
 
 /* Test hook for failure detection: while enabled, every GEMM launch (and fp8_moe_tokens) first waits
  * on a barrier that nothing signals, the grid barrier of the tensorwise quantize waits for one arrival more
- * than there are CTAs, the column-wise quantize sees no tile maxima as written, and the MX
- * quantize with a column-major output of a dense tensor loads no tile into its ring; the wait
- * runs out after the wait limit (fp8_set_wait_limit_ns), the kernel reports FP8_DEV_TIMEOUT,
- * drains and returns. Off by default. Returns the previous setting. */
+ * than there are CTAs, the column-wise quantize sees no tile maxima as written, the MX
+ * quantize with a column-major output of a dense tensor loads no tile into its ring, and
+ * fp8_add_rmsnorm_bwd does not load each CTA's first rows; the wait runs out after the wait limit
+ * (fp8_set_wait_limit_ns), the kernel reports FP8_DEV_TIMEOUT (fp8_add_rmsnorm_bwd: NaN), drains
+ * and returns. Off by default. Returns the previous setting. */
 int fp8_set_test_stall(int enable);
 
 /* Test hook for the cast step ([Q] section 2: round to nearest even, saturating; [F] formats):

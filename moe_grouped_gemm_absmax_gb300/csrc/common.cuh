@@ -306,6 +306,11 @@ FP8_DEVI bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Waits for work already in flight (TMA loads, MMAs) before tensor memory is freed or the CTA
+// leaves use this fixed bound, not the adjustable one, so a short limit never frees resources
+// under running hardware.
+constexpr uint64_t kDrainNs = 2000000000ull;
+
 // Bounded wait for the phase of `parity` to complete. Returns false when `limit_ns` elapsed or
 // when another role raised `*abort` (abort may be null).
 FP8_DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {

@@ -45,11 +45,6 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxExperts = 2048;
 constexpr int64_t kGroupBytes = 32ll << 20;  // rasterization: the A panels of a group of M-blocks, in L2
 constexpr int kStageOut = 4096;  // per epilogue warp: output staging for TMA stores (pairs)
-// Waits for work already in flight (TMA loads, MMAs) before tensor memory is freed or the CTA
-// leaves use this fixed bound, not the adjustable one, so a short limit never frees resources
-// under running hardware.
-constexpr uint64_t kDrainNs = 2000000000ull;
-
 // kDenseAmax: the dense schedule whose epilogue also folds max |out| into the side outputs;
 // kDenseQuant: the dense schedule whose epilogue writes the next quantization of the (bf16) result:
 // FP8 codes and 1 x 128 or MX scales along the rows

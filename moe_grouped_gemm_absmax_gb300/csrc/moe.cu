@@ -66,7 +66,6 @@ constexpr int tmem_cols(int ph, int NB) {
 constexpr int kScaleBytes = 512;       // a stage's activation scales, in the MX scale layout's block of 128 rows
 constexpr int kSmemMax = 232448;       // 227 KB a CTA
 constexpr int kSmemPair = 115712;      // two CTAs an SM: half of 228 KB less the 1 KB reserved for each
-constexpr uint64_t kDrainNs = 2000000000ull;
 // columns of N: groups of 16 hold 8 slots in two parts (columns 2 j, 2 j + 1), or 5 in three
 constexpr int kPerGroup1 = 8, kPerGroup2 = 5;
 constexpr int kPrefetchUnits = 8;      // units a CTA brings into L2 for the second product

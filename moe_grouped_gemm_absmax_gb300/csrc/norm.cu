@@ -416,6 +416,7 @@ struct Ring {
   const uint4* src[3];
   int64_t T, groups;
   int nvec, slab;  // vectors of a row, of a tensor's part of a stage
+  int test_stall;  // each CTA's first group is never loaded
   RingShape r;
   FP8_DEVI void load(uint4* ring, uint64_t* full, int64_t g, int s) const {
     if (g >= groups) return;
@@ -431,13 +432,19 @@ struct Ring {
       for (int s = 0; s < r.stages; ++s) mbar_init(&full[s], 1);
       fence_mbar_init();
       pdl_wait();
-      for (int s = 0; s < r.stages; ++s) load(ring, full, blockIdx.x + (int64_t)s * gridDim.x, s);
+      for (int s = test_stall ? 1 : 0; s < r.stages; ++s) load(ring, full, blockIdx.x + (int64_t)s * gridDim.x, s);
     }
     pdl_wait();
     __syncthreads();
   }
+  // The loads in flight land, where group stages - 1 behind g is the last that was asked for.
+  FP8_DEVI void drain(uint64_t* full, int64_t g) const {
+    int64_t use = (g - blockIdx.x) / gridDim.x;
+    for (int i = 0; i < r.stages && g < groups; ++i, ++use, g += gridDim.x)
+      if (use > 0 || !test_stall) mbar_wait(&full[use % r.stages], (uint32_t)(use / r.stages) & 1, nullptr, kDrainNs);
+  }
 };
-inline Ring make_ring(const void* a, const void* b, const void* c, int64_t T, int64_t H) {
+inline Ring make_ring(const void* a, const void* b, const void* c, int64_t T, int64_t H, int test_stall) {
   Ring q = {};
   int n = 0;
   for (const void* t : {a, b, c})
@@ -447,6 +454,7 @@ inline Ring make_ring(const void* a, const void* b, const void* c, int64_t T, in
   q.T = T;
   q.groups = ceil_div64(T, q.r.rows);
   q.slab = q.r.rows * q.nvec;
+  q.test_stall = test_stall;
   return q;
 }
 inline size_t ring_bytes(const Ring& q) { return (size_t)q.r.stages * q.r.tensors * q.slab * 16; }
@@ -479,6 +487,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
   const int nvec = q.nvec;
   const int team = threadIdx.x / q.r.team, t = threadIdx.x % q.r.team;
   constexpr int kTensors = HAS_DH ? 3 : 2;
+  __shared__ volatile int lost;       // a wait ran out
+  __shared__ volatile int64_t lost_g;  // the group behind which there were no more loads
+  if (threadIdx.x == 0) lost = 0, lost_g = -1;
   q.start(ring, full);
   float2 dw[VPT][4];
   uint4 wv[VPT];  // bf16 weights stay in registers; fp32 ones, twice as many, come from L1
@@ -499,10 +510,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
   for (int64_t g = blockIdx.x; g < q.groups; g += gridDim.x, par ^= 1) {
     const int64_t row = g * q.r.rows + team;
     const bool active = row < q.T;
-    float rstd = rstd_next;
+    const float rstd = rstd_next;
     rstd_next = row_rstd(g + gridDim.x);
-    // a wait that ran out would show as NaN in everything that the row reaches
-    if (!mbar_wait(&full[st], phase, nullptr, p.wait_ns)) rstd = __uint_as_float(0x7FC00000u);
+    if (!mbar_wait(&full[st], phase, &lost, p.wait_ns)) lost = 1;
     const uint4* in = ring + st * kTensors * q.slab + team * nvec;
     uint4 vdy[VPT], vh[VPT], vdh[VPT];
     float2 sum2 = both(0.f);
@@ -525,7 +535,12 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     team_put(red[par][team], t, q.r.team / 32, sum);  // two buffers: a group's are read while the next one's are written
     __syncthreads();
-    if (threadIdx.x == 0) q.load(ring, full, g + (int64_t)q.r.stages * gridDim.x, st);
+    if (threadIdx.x == 0) {
+      if (!lost)
+        q.load(ring, full, g + (int64_t)q.r.stages * gridDim.x, st);
+      else if (lost_g < 0)
+        lost_g = g;
+    }
     if (++st == q.r.stages) st = 0, phase ^= 1;
     if (!p.dx || !active) continue;
     const float c1 = rstd * rstd * (rstd * team_sum<VPT == 1>(red[par][team], q.r.team / 32) * p.inv_H);
@@ -541,6 +556,18 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
       }
       p.dx[row * nvec + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
+  }
+  // A wait that ran out ended all other waits and the loads; what was computed from there on means nothing. NaN in all
+  // of the CTA's rows and of dw. (That within the loop, from the group on, cost 4% without dh.)
+  if (lost) {
+    if (threadIdx.x == 0) q.drain(full, lost_g);
+    __syncthreads();
+    for (int64_t row = (int64_t)blockIdx.x * q.r.rows + team; p.dx && row < q.T; row += (int64_t)gridDim.x * q.r.rows)
+      for (int c = t; c < nvec; c += q.r.team) p.dx[row * nvec + c] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dw[i][j] = both(__uint_as_float(0x7FC00000u));
   }
   if (p.part) {
     float4* mine = reinterpret_cast<float4*>(p.part) + (int64_t)blockIdx.x * nvec * 2;
@@ -618,7 +645,7 @@ int64_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t H) { return ring_grid(T, H) * H 
 
 int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, const float* rstd, const void* dh,
                        int64_t T, int64_t H, void* dx, void* dw, int dw_bf16, float* ws, const Ctx& c) {
-  const Ring q = make_ring(dy, h, dh, T, H);
+  const Ring q = make_ring(dy, h, dh, T, H, c.test_stall);
   const int64_t grid = ring_grid(T, H);
   if (grid > 0) {
     NormBwdArgs a;
