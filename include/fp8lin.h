@@ -385,7 +385,7 @@ int fp8_add_rmsnorm(const fp8_tensor* x, const fp8_tensor* residual, const fp8_t
  *  dw          bf16 or fp32 [H] or NULL. Summed in fp32 in an order that depends on T and H only:
  *              the same bits on every run. T == 0 gives zeros.
  *  workspace   fp8_rmsnorm_bwd_workspace_size(T, H) bytes, 16-byte aligned, when dw is given;
- *              it serves fewer rows too.
+ *              it serves fewer rows too. (The size is 0 for T or H that the call does not take.)
  * There is no status word: a wait for a load that ran out (fp8_set_wait_limit_ns) shows as NaN in dx of all rows
  * of its CTA and in all of dw.
  */

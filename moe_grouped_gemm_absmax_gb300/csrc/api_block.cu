@@ -27,12 +27,14 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;
 // ------------------------------------------------------------------------------------------
 // norm
 
+static bool norm_width(int64_t H) { return H > 0 && H <= 16384 && H % 8 == 0; }
+
 static int check_norm_input(const fp8_tensor* x, const fp8_tensor* weight) {
   FP8_CHECK(valid_desc(x) && x->dtype == FP8_DT_BF16 && x->ndim == 2, FP8_ERR_INVALID_ARG);
   FP8_CHECK(shape_max(x, kMaxDim - 1), FP8_ERR_UNSUPPORTED);
   const int64_t H = x->shape[1];
   FP8_CHECK(H % 8 == 0, FP8_ERR_ALIGNMENT);
-  FP8_CHECK(H > 0 && H <= 16384, FP8_ERR_UNSUPPORTED);
+  FP8_CHECK(norm_width(H), FP8_ERR_UNSUPPORTED);
   FP8_CHECK(aligned16(x->ptr), FP8_ERR_ALIGNMENT);
   FP8_CHECK(valid_desc(weight) && is_out(weight->dtype) && shape_is(weight, 1, H), FP8_ERR_INVALID_ARG);
   FP8_CHECK(aligned16(weight->ptr), FP8_ERR_ALIGNMENT);
@@ -82,7 +84,8 @@ extern "C" int fp8_add_rmsnorm(const fp8_tensor* x, const fp8_tensor* residual, 
 }
 
 extern "C" size_t fp8_rmsnorm_bwd_workspace_size(int64_t T, int64_t H) {
-  return T > 0 && H > 0 && T < kMaxDim && H < kMaxDim ? (size_t)rmsnorm_bwd_ws_bytes(T, H) : 0;
+  // the widths that the call takes: the shape of its ring is defined for those only
+  return T > 0 && T < kMaxDim && norm_width(H) ? (size_t)rmsnorm_bwd_ws_bytes(T, H) : 0;
 }
 
 extern "C" int fp8_add_rmsnorm_bwd(const fp8_tensor* dy, const fp8_tensor* h, const fp8_tensor* weight,
