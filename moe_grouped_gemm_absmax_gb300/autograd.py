@@ -122,21 +122,22 @@ class AddRmsNormFunction(torch.autograd.Function):
         h, y, _, _, rstd = add_rmsnorm_alloc(x2, w, eps, r2, want_rstd=True)
         ctx.save_for_backward(h, w, rstd)
         ctx.shape, ctx.has_residual = x.shape, residual is not None
+        ctx.set_materialize_grads(False)  # an output that nothing uses costs no gradient of zeros
         return y.reshape(x.shape), (h.reshape(x.shape) if residual is not None else x.view_as(x))
 
     @staticmethod
     def backward(ctx, dy, dh):
         h, w, rstd = ctx.saved_tensors
         T, H = h.shape
-        dy2 = dy.reshape(T, H).to(torch.bfloat16).contiguous()
         dh2 = dh.reshape(T, H).to(torch.bfloat16).contiguous() if dh is not None else None
         need_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[1]
-        dx = torch.empty_like(h) if need_x else None
-        dw = torch.empty_like(w) if ctx.needs_input_grad[2] else None
-        if need_x or dw is not None:
-            fp8_add_rmsnorm_bwd(dy2, h, w, rstd, dx, dw, dh2,
+        dw = (torch.zeros_like if dy is None else torch.empty_like)(w) if ctx.needs_input_grad[2] else None
+        dx = dh2  # where only h is used, its gradient passes through
+        if dy is not None and (need_x or dw is not None):
+            dx = torch.empty_like(h) if need_x else None
+            fp8_add_rmsnorm_bwd(dy.reshape(T, H).to(torch.bfloat16).contiguous(), h, w, rstd, dx, dw, dh2,
                                 rmsnorm_bwd_workspace(T, H, h.device) if dw is not None else None)
-        g = dx.reshape(ctx.shape) if need_x else None
+        g = dx.reshape(ctx.shape) if dx is not None else None
         return (g if ctx.needs_input_grad[0] else None,
                 g if ctx.has_residual and ctx.needs_input_grad[1] else None, dw, None)
 
