@@ -107,6 +107,24 @@ def swap_linears(module, granularity=GRAN_ROW, wgrad_mode=WGRAD_BF16, module_fil
     return swapped
 
 
+class _OnceFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the gradients of the fp8lin functions are not differentiable")
+
+
+def _once(*grads):
+    """Gradients whose own derivative is refused, not taken for zero. (once_differentiable refuses it only where the
+    incoming gradient requires one; these depend on the saved inputs too.)"""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(g if g is None else _OnceFunction.apply(g.detach().requires_grad_(True)) for g in grads)
+
+
 class AddRmsNormFunction(torch.autograd.Function):
     """(y, h) = norm(x + residual) * weight and the new residual stream; x, residual [..., H] bf16, weight [H] bf16 or
     fp32. Without a residual (None), h is x. Gradients of x, residual and weight."""
@@ -138,8 +156,8 @@ class AddRmsNormFunction(torch.autograd.Function):
             fp8_add_rmsnorm_bwd(dy.reshape(T, H).to(torch.bfloat16).contiguous(), h, w, rstd, dx, dw, dh2,
                                 rmsnorm_bwd_workspace(T, H, h.device) if dw is not None else None)
         g = dx.reshape(ctx.shape) if dx is not None else None
-        return (g if ctx.needs_input_grad[0] else None,
-                g if ctx.has_residual and ctx.needs_input_grad[1] else None, dw, None)
+        return _once(g if ctx.needs_input_grad[0] else None,
+                     g if ctx.has_residual and ctx.needs_input_grad[1] else None, dw, None)
 
 
 class MoERouteFunction(torch.autograd.Function):
@@ -160,4 +178,4 @@ class MoERouteFunction(torch.autograd.Function):
         logits, ids = ctx.saved_tensors
         dlogits = torch.empty_like(logits)
         fp8_moe_route_bwd(logits, ids, dweights.float().contiguous(), dlogits, *ctx.args)
-        return dlogits, None, None, None, None, None
+        return _once(dlogits, None, None, None, None, None)

@@ -1,4 +1,5 @@
-"""The training functions of the norm and the router where a gradient is absent."""
+"""The training functions of the norm and the router where a gradient is absent, and where a second derivative is asked
+for."""
 import pytest
 import torch
 
@@ -51,3 +52,17 @@ def test_only_the_stream_has_a_gradient(ag, residual):
     if residual:
         assert torch.equal(res.grad, c.bfloat16())
     assert w.grad is not None and not w.grad.any()
+
+
+def test_a_second_derivative_is_refused(ag):
+    """A gradient penalty would lose its terms through these functions without a word; it raises instead."""
+    x, res, w, c, r = _inputs()
+    y, _ = ag.AddRmsNormFunction.apply(x, res, w)
+    gx, = torch.autograd.grad((y.float() * c).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (gx.float().sum() + x.float().sum()).backward()
+    logits = r(12, 16).requires_grad_(True)
+    weights, _ = ag.MoERouteFunction.apply(logits, 3)
+    gl, = torch.autograd.grad((weights * r(12, 3)).sum(), logits, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (gl.sum() + logits.sum()).backward()
