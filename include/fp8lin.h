@@ -117,6 +117,8 @@ enum { FP8_WGRAD_FP8 = 0, FP8_WGRAD_BF16 = 1 };
 
 /* score function of the router (fp8_moe_route) */
 enum { FP8_SCORE_SOFTMAX = 0, FP8_SCORE_SIGMOID = 1 };
+/* OR-ed into the score function: the router's bias is added to the score instead of to the logit */
+enum { FP8_SCORE_BIASED = 1 << 4 };
 
 /* most tokens of one fp8_moe_tokens call */
 #define FP8_MOE_MAX_TOKENS 64
@@ -398,11 +400,16 @@ size_t fp8_rmsnorm_bwd_workspace_size(int64_t T, int64_t H);
  * fp8_moe_route — the router of a mixture-of-experts layer: the top k experts of each token, their
  * weights, and the table that fp8_grouped_mm's offsets need.
  *  logits      bf16 or fp32 [T, E], E <= 1024. k = ids->shape[1], 1 <= k <= 16, k <= E.
- *  bias        fp32 [E] or NULL: added to the logits (in fp32) for the choice only, not for the weights.
- *  The k experts with the largest logit + bias are taken, in falling order, ties by the lowest
- *  index. One whose sum is -inf or NaN is never taken: where fewer than k are left, the slot's id
- *  is -1 and its weight 0.
  *  score       FP8_SCORE_SOFTMAX: v = softmax(logits) over all E; FP8_SCORE_SIGMOID: v = sigmoid(logit).
+ *  bias        fp32 [E] or NULL: added (in fp32) for the choice only, not for the weights: to the logit, or
+ *              with FP8_SCORE_BIASED OR-ed into score to the score v (to 4 units in the last place).
+ *              The correction bias of auxiliary-loss-free load balancing, as published and as models
+ *              are trained with it, belongs to the score: it needs FP8_SCORE_BIASED. Added to the
+ *              logit it would choose other experts, since v is not linear in the logit. Without a
+ *              bias the flag changes nothing.
+ *  The k experts with the largest sum are taken, in falling order, ties by the lowest
+ *  index. One whose logit or sum is -inf or NaN is never taken: where fewer than k are left, the slot's
+ *  id is -1 and its weight 0.
  *  renormalize 0: weight = scale * v. Else over the experts taken: softmax: weight = scale * softmax of
  *              their logits; sigmoid: weight = scale * v / (sum of their v + 1e-20).
  *  ids         int32 [T, k]; weights fp32 [T, k].

@@ -31,7 +31,7 @@ OK = 0
 DEV_BAD_OFFSETS = 1 << 8
 DEV_TIMEOUT = 1 << 9
 DEV_BAD_IDS = 1 << 10
-SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_BIASED = 0, 1, 16
 MOE_MAX_TOKENS = 64
 
 _TORCH_DT = {
@@ -313,7 +313,8 @@ def fp8_add_rmsnorm_bwd(dy, h, weight, rstd, dx=None, dw=None, dh=None, workspac
 def fp8_moe_route(logits, ids, weights, order=None, pos=None, ends=None, bias=None, score=SCORE_SOFTMAX,
                   renormalize=True, scale=1.0, workspace=None, status=None, stream=None):
     """Top-k experts (k = ids.shape[1]) and their weights for each row of logits; with order, pos and ends also the
-    slots sorted by expert (needs a workspace, route_workspace)."""
+    slots sorted by expert (needs a workspace, route_workspace). bias is added to the logits for the choice, or with
+    score | SCORE_BIASED to the scores, as the correction bias of auxiliary-loss-free balancing is."""
     _check(lib.fp8_moe_route(_pack(logits), _pack(bias), score, bool(renormalize), scale, _pack(ids), _pack(weights),
                              _pack(order), _pack(pos), _pack(ends), *_ws(workspace), _ptr(status), _stream(stream)),
            "fp8_moe_route")

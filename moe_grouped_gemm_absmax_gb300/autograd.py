@@ -10,7 +10,7 @@ non-FP8 step."""
 import torch
 
 from . import (GRAN_BLOCK_1x128, GRAN_MX, GRAN_ROW, GRAN_TENSOR, MM_FAST_ACCUM, OP_LINEAR_BWD, OP_LINEAR_FWD,
-               SCORE_SOFTMAX, WGRAD_BF16, WGRAD_FP8, add_rmsnorm_alloc, fp8_add_rmsnorm_bwd, fp8_linear_bwd,
+               SCORE_BIASED, SCORE_SOFTMAX, WGRAD_BF16, WGRAD_FP8, add_rmsnorm_alloc, fp8_add_rmsnorm_bwd, fp8_linear_bwd,
                fp8_linear_fwd, fp8_moe_route_bwd, fp8_workspace_size, linear_saved_alloc, make_saved, moe_route_alloc,
                rmsnorm_bwd_workspace)
 
@@ -161,13 +161,13 @@ class AddRmsNormFunction(torch.autograd.Function):
 
 
 class MoERouteFunction(torch.autograd.Function):
-    """(weights fp32 [T, k], ids int32 [T, k]) of fp8_moe_route; the gradient of the weights reaches the logits, the
-    choice and its bias get none."""
+    """(weights fp32 [T, k], ids int32 [T, k]) of fp8_moe_route, with bias the balancing bias, added to the scores for the
+    choice; the gradient of the weights reaches the logits, the choice and its bias get none."""
 
     @staticmethod
     def forward(ctx, logits, top_k, bias=None, score=SCORE_SOFTMAX, renormalize=True, scale=1.0):
         logits = logits.contiguous()
-        ids, weights, _, _, _ = moe_route_alloc(logits, top_k, bias, score, renormalize, scale, table=False)
+        ids, weights, _, _, _ = moe_route_alloc(logits, top_k, bias, score | SCORE_BIASED, renormalize, scale, table=False)
         ctx.save_for_backward(logits, ids)
         ctx.args = (score, renormalize, scale)
         ctx.mark_non_differentiable(ids)

@@ -113,10 +113,12 @@ extern "C" int fp8_add_rmsnorm_bwd(const fp8_tensor* dy, const fp8_tensor* h, co
 // ------------------------------------------------------------------------------------------
 // router
 
+static int score_kind(int score) { return score & ~FP8_SCORE_BIASED; }
+
 static int check_route(const fp8_tensor* logits, const fp8_tensor* ids, int score) {
   FP8_CHECK(valid_desc(logits) && is_out(logits->dtype) && logits->ndim == 2, FP8_ERR_INVALID_ARG);
   FP8_CHECK(valid_desc(ids) && ids->dtype == FP8_DT_I32 && ids->ndim == 2, FP8_ERR_INVALID_ARG);
-  FP8_CHECK(score == FP8_SCORE_SOFTMAX || score == FP8_SCORE_SIGMOID, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(score_kind(score) == FP8_SCORE_SOFTMAX || score_kind(score) == FP8_SCORE_SIGMOID, FP8_ERR_INVALID_ARG);
   const int64_t T = logits->shape[0], E = logits->shape[1], k = ids->shape[1];
   FP8_CHECK(ids->shape[0] == T && k >= 1 && k <= E, FP8_ERR_INVALID_ARG);
   FP8_CHECK(E <= 1024 && k <= 16 && T < kMaxDim && T * k < kMaxDim, FP8_ERR_UNSUPPORTED);
@@ -146,8 +148,8 @@ extern "C" int fp8_moe_route(const fp8_tensor* logits, const fp8_tensor* bias, i
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   return launch_route(logits->ptr, logits->dtype == FP8_DT_BF16, bias ? static_cast<const float*>(bias->ptr) : nullptr,
-                      T, E, k, score == FP8_SCORE_SOFTMAX, renormalize != 0, scale, static_cast<int32_t*>(ids->ptr),
-                      static_cast<float*>(weights->ptr), ends ? static_cast<int32_t*>(order->ptr) : nullptr,
+                      T, E, k, score_kind(score) == FP8_SCORE_SOFTMAX, (score & FP8_SCORE_BIASED) != 0, renormalize != 0,
+                      scale, static_cast<int32_t*>(ids->ptr), static_cast<float*>(weights->ptr), ends ? static_cast<int32_t*>(order->ptr) : nullptr,
                       ends ? static_cast<int32_t*>(pos->ptr) : nullptr,
                       ends ? static_cast<int32_t*>(ends->ptr) : nullptr, workspace, c);
 }
@@ -162,7 +164,7 @@ extern "C" int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   return launch_route_bwd(logits->ptr, logits->dtype == FP8_DT_BF16, static_cast<const int32_t*>(ids->ptr),
-                          static_cast<const float*>(dweights->ptr), T, E, k, score == FP8_SCORE_SOFTMAX,
+                          static_cast<const float*>(dweights->ptr), T, E, k, score_kind(score) == FP8_SCORE_SOFTMAX,
                           renormalize != 0, scale, dlogits->ptr, c);
 }
 

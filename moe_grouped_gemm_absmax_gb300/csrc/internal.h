@@ -105,10 +105,11 @@ int launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, int w_f32, 
                        int64_t T, int64_t H, void* dx, void* dw, int dw_bf16, float* ws, const Ctx& c);
 
 // --- router (route.cu) ---
-// logits [T, E] bf16 or fp32; order, pos and ends all given or all null. E <= 1024, k <= 16.
+// logits [T, E] bf16 or fp32; order, pos and ends all given or all null. E <= 1024, k <= 16. biased: bias is added to
+// the score, else to the logit.
 int64_t route_ws_bytes(int64_t T, int64_t E);
 int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int64_t E, int64_t k, int softmax,
-                 int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,
+                 int biased, int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,
                  void* ws, const Ctx& c);
 int launch_route_bwd(const void* logits, int bf16, const int32_t* ids, const float* dw, int64_t T, int64_t E,
                      int64_t k, int softmax, int renorm, float scale, void* dlogits, const Ctx& c);

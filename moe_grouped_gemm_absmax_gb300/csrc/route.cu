@@ -2,9 +2,9 @@
 // the table of the (token, expert) slots sorted by expert that the grouped GEMM's offsets need,
 // and the gradient of the logits.
 //
-//   sel[e] = logit[e] + bias[e] decides the k experts (ties: the lowest index; -inf and NaN are
-//   never taken); v[e] = softmax(logits)[e] or sigmoid(logit[e]); w_j = scale * v[e_j], or with
-//   renormalization scale * v[e_j] / sum_i v[e_i].
+//   v[e] = softmax(logits)[e] or sigmoid(logit[e]); sel[e] = logit[e] + bias[e] or (BIASED) v[e] + bias[e]
+//   decides the k experts (ties: the lowest index; a logit or sum of -inf or NaN is never taken);
+//   w_j = scale * v[e_j], or with renormalization scale * v[e_j] / sum_i v[e_i].
 //
 // Few tokens: one CTA chooses, counts and places. More take two launches, the second started while the first
 // runs (programmatic dependent launch). 16384 tokens of 256 experts, k = 8: 16.1 us, of which the choice 10; the
@@ -132,16 +132,34 @@ struct __align__(16) Cand {
   int e;
   float logit;
 };
-template <int VPL, bool VEC, bool SOFTMAX>
+template <int VPL, bool VEC, bool SOFTMAX, bool BIASED>
 FP8_DEVI void route_token(const RouteArgs& p, int64_t t, int lane, const float* v, const float* bias, Cand* cand,
                           int32_t* hist) {
   float sel[VPL];
   float best = -INFINITY;
+  if (BIASED) {  // the score to 4 units in the last place
+    float m = 0.f, z = 0.f;
+    if (SOFTMAX) {
+      m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {  // a NaN becomes -inf; experts past E are -inf
-    sel[i] = fmaxf(v[i] + bias[i], -INFINITY);
-    best = fmaxf(best, sel[i]);
+      for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
+      m = warp_max(m);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      sel[i] = SOFTMAX ? expf(v[i] - m) : __fdividef(1.0f, 1.0f + expf(-v[i]));
+      z += fmaxf(sel[i], 0.f);  // without NaN
+    }
+    if (SOFTMAX) z = 1.0f / warp_sum(z);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      sel[i] = v[i] > -INFINITY ? fmaxf((SOFTMAX ? sel[i] * z : sel[i]) + bias[i], -INFINITY) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sel[i] = fmaxf(v[i] + bias[i], -INFINITY);  // a NaN becomes -inf; experts past E are -inf
   }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) best = fmaxf(best, sel[i]);
   float bound = -INFINITY;
   for (int j = 0; j < p.k; ++j) {
     bound = redux_max(best);
@@ -321,7 +339,7 @@ FP8_DEVI void fill_order(const RouteArgs& p, int64_t valid) {
 }
 
 // The choice for a chunk of tokens, and the chunk's slots of each expert; with one chunk the table too.
-template <int VPL, bool VEC, int WARPS, bool BF16, bool SOFTMAX>
+template <int VPL, bool VEC, int WARPS, bool BF16, bool SOFTMAX, bool BIASED>
 __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
   extern __shared__ __align__(16) int32_t hist[];  // [E2], then the warps' candidates, or place_slots' arrays
   __shared__ int32_t warp_sums[32];
@@ -351,7 +369,7 @@ __global__ void __launch_bounds__(32 * WARPS) route_kernel(const RouteArgs p) {
     } else {
       load_row<VPL, VEC>(p.logits, BF16, t, p.E, lane, -INFINITY, v);
     }
-    route_token<VPL, VEC, SOFTMAX>(p, t, lane, v, bias, cand, p.order ? hist : nullptr);
+    route_token<VPL, VEC, SOFTMAX, BIASED>(p, t, lane, v, bias, cand, p.order ? hist : nullptr);
   }
   if (!p.order) return;
   __syncthreads();
@@ -552,13 +570,19 @@ int64_t chunk_tokens(int64_t T, int64_t E) {
 size_t place_bytes(int E2) { return (size_t)E2 * (4 + 2 * most_groups(E2) + 2 * (E2 <= 512 ? 32 : 16)); }
 
 // 32 warps a CTA where a lane holds up to 8 experts, 16 where it needs more registers. Kernels by the logits' type and
-// the score: with both decided in the kernel 16384 tokens of 256 experts took 17.1 us instead of 16.5.
-template <int VPL, bool VEC>
-int run_route(const RouteArgs& a, size_t smem, const Ctx& c) {
+// the score: with both decided in the kernel 16384 tokens of 256 experts took 17.1 us instead of 16.5. And by where the
+// bias goes: on the score, 256 sigmoids or exponentials a token more, they take 17.6.
+template <int VPL, bool VEC, bool BIASED>
+int run_route_on(const RouteArgs& a, size_t smem, const Ctx& c) {
   constexpr int W = VPL <= 8 ? 32 : 16;
-  const auto kern = a.bf16 ? (a.softmax ? route_kernel<VPL, VEC, W, true, true> : route_kernel<VPL, VEC, W, true, false>)
-                           : (a.softmax ? route_kernel<VPL, VEC, W, false, true> : route_kernel<VPL, VEC, W, false, false>);
+  const auto kern = a.bf16 ? (a.softmax ? route_kernel<VPL, VEC, W, true, true, BIASED> : route_kernel<VPL, VEC, W, true, false, BIASED>)
+                           : (a.softmax ? route_kernel<VPL, VEC, W, false, true, BIASED> : route_kernel<VPL, VEC, W, false, false, BIASED>);
   return launch_dependent(kern, dim3((unsigned)a.chunks), dim3(32 * W), smem, c.stream, a);
+}
+
+template <int VPL, bool VEC>
+int run_route(const RouteArgs& a, bool biased, size_t smem, const Ctx& c) {
+  return biased ? run_route_on<VPL, VEC, true>(a, smem, c) : run_route_on<VPL, VEC, false>(a, smem, c);
 }
 
 template <int VPL, bool VEC>
@@ -578,7 +602,7 @@ int64_t route_ws_bytes(int64_t T, int64_t E) {
 }
 
 int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int64_t E, int64_t k, int softmax,
-                 int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,
+                 int biased, int renorm, float scale, int32_t* ids, float* weights, int32_t* order, int32_t* pos, int32_t* ends,
                  void* ws, const Ctx& c) {
   if (T == 0) {
     if (ends && cudaMemsetAsync(ends, 0, (size_t)E * 4, c.stream) != cudaSuccess) return FP8_ERR_CUDA;
@@ -594,7 +618,7 @@ int launch_route(const void* logits, int bf16, const float* bias, int64_t T, int
   // up to 48 KB, which needs no attribute: place_slots' 40 to 43 KB and the candidates' 8 to 16 KB share it
   const size_t choose = (size_t)(a.E2 + 3) / 4 * 16 + (E <= 256 ? 32 : 16) * 32 * sizeof(Cand);
   const size_t smem = a.chunks == 1 && place_bytes(a.E2) > choose ? place_bytes(a.E2) : choose;
-#define FP8_ROUTE(V, X) rc = run_route<V, X>(a, smem, c)
+#define FP8_ROUTE(V, X) rc = run_route<V, X>(a, biased && bias, smem, c)
   int rc;
   FP8_BY_EXPERTS(E, FP8_ROUTE);
 #undef FP8_ROUTE

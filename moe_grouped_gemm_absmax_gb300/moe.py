@@ -5,20 +5,20 @@ Up to MOE_MAX_TOKENS tokens (decode) take fp8_moe_tokens, which reads the named 
 take the grouped GEMM on rows sorted by expert, with the norm's 8-bit output as its operand."""
 import torch
 
-from . import (DT_E4M3, GRAN_ROW, GROUPED_JAGGED_M, MOE_MAX_TOKENS, SCORE_SOFTMAX, add_rmsnorm_alloc,
+from . import (DT_E4M3, GRAN_ROW, GROUPED_JAGGED_M, MOE_MAX_TOKENS, SCORE_BIASED, SCORE_SOFTMAX, add_rmsnorm_alloc,
                fp8_grouped_mm, fp8_scaled_mm, moe_route_alloc, moe_tokens_alloc, quantize_alloc)
 
 
 class Fp8MoEBlock:
     """norm_weight [H]; router_weight bf16 [E, H]; w1 (gate), w3 (up) bf16 [E, I, H]; w2 bf16 [E, H, I]; bias fp32
-    [E] or None, added to the router's logits for the choice. The experts' weights are quantized once, e4m3 with a
+    [E] or None, the balancing bias: added to the router's scores for the choice. The experts' weights are quantized once, e4m3 with a
     scale per row."""
 
     def __init__(self, norm_weight, router_weight, w1, w3, w2, top_k, eps=1e-6, bias=None, score=SCORE_SOFTMAX,
                  renormalize=True, scale=1.0):
         E, I, H = w1.shape
         self.norm_weight, self.router_weight, self.bias = norm_weight.contiguous(), router_weight.contiguous(), bias
-        self.top_k, self.eps, self.score, self.renormalize, self.scale = top_k, eps, score, renormalize, scale
+        self.top_k, self.eps, self.score, self.renormalize, self.scale = top_k, eps, score | SCORE_BIASED, renormalize, scale
 
         def rows(w):
             n = w.shape[1]
