@@ -146,6 +146,9 @@ extern "C" const char* fp8_status_string(int code) {
     case FP8_DEV_TIMEOUT: return "device: a bounded wait ran out";
     case FP8_DEV_BAD_IDS: return "device: expert ids outside -1 .. E - 1";
     case FP8_DEV_BAD_IDS | FP8_DEV_TIMEOUT: return "device: bad expert ids and a wait ran out";
+    case FP8_DEV_BAD_IDS | FP8_DEV_BAD_OFFSETS: return "device: bad expert ids and bad offsets";
+    case FP8_DEV_BAD_IDS | FP8_DEV_BAD_OFFSETS | FP8_DEV_TIMEOUT:
+      return "device: bad expert ids, bad offsets and a wait ran out";
     case FP8_DEV_BAD_OFFSETS | FP8_DEV_TIMEOUT: return "device: bad offsets and a wait ran out";
     default: return "unknown status";
   }
