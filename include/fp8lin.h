@@ -438,7 +438,8 @@ int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids, const fp8
 /*
  * fp8_moe_tokens — the experts of a few tokens (decode), from the hidden state to the weighted sum:
  *   out[t] = sum_j weights[t, j] * W2[e] (silu(W1[e] x[t]) * (W3[e] x[t])),   e = ids[t, j],
- * with W[e, n, k] = code * scale of its row. Only the experts named are read, each once.
+ * with W[e, n, k] = code * scale of its row. Only the experts named are read, each once for 40 slots
+ * that name it (so once for up to 40 tokens whose experts are distinct).
  *  x           bf16 [T, H], T <= FP8_MOE_MAX_TOKENS; H and I multiples of 16, <= 65536.
  *  ids         int32 [T, k], k <= 16: -1 marks an unused slot (its weight is not read); a token
  *              without any used slot gives zeros (NaN if its x holds a NaN or an infinity). Other ids
@@ -451,8 +452,8 @@ int fp8_moe_route_bwd(const fp8_tensor* logits, const fp8_tensor* ids, const fp8
  *              tokens too.
  * Sums are fp32 and the result is rounded once. The activations enter the products as sums of 8-bit parts:
  * x exactly down to 2^-13 of its row's largest and to 2^-21 of that below, the hidden layer to 2^-13 of each
- * value (2^-25 of the largest in its block of 32). A row with a NaN or an infinity gives NaN wherever the formula does. The same
- * bits on every run. A wait that ran out sets FP8_DEV_TIMEOUT.
+ * value (2^-25 of the largest in its block of 32). A row with a NaN or an infinity gives NaN in its
+ * whole output row. The same bits on every run. A wait that ran out sets FP8_DEV_TIMEOUT.
  */
 int fp8_moe_tokens(const fp8_tensor* x, const fp8_tensor* ids, const fp8_tensor* weights,
                    const fp8_tensor* w13, const fp8_tensor* s13, const fp8_tensor* w2, const fp8_tensor* s2,

@@ -3,8 +3,8 @@
 // on FP8 weights with one inverse scale per row: w13 [E, 2 I, H] holds W1 (gate) and below it W3
 // (up), w2 [E, H, I].
 //
-// With a few tokens the work is reading the named experts' weights once; everything here serves to
-// keep that stream going. Persistent CTAs, one for each SM:
+// With a few tokens the work is reading the named experts' weights once (once for each 40 slots of an expert,
+// kMaxEntry); everything here serves to keep that stream going. Persistent CTAs, one for each SM:
 //  - The weights are the MMA's A operand (tcgen05.mma kind::f8f6f4, M = 128 weight rows), so they go
 //    from HBM by TMA into a shared-memory ring and from there into the tensor cores without
 //    passing through registers. The tokens are its N.

@@ -225,7 +225,7 @@ FP8_DEVI void norm_out(const NormArgs& p, int64_t row, int c, const float2* s, f
 // A CTA ends with its row: while some of an SM's CTAs reduce or store, others load. Persistent CTAs that
 // asked for the next row ahead had fewer warps an SM and took 43 us instead of 40 for 8192 x 4096 at the time; one
 // that took rows through shared memory 53 us. 36 us now, 96% of the copy rate; without a residual and with block
-// scales the instructions bound it instead (14336 x 4096 39 us; the bytes are 26 us; 43 us at 77% of the issue slots
+// scales the instructions bound it instead (14336 x 4096 37 us; the bytes are 26 us; 43 us at 77% of the issue slots
 // with one kernel for every residual and weight type). The weights' type is known at compile time except in a CTA a
 // row with four vectors a thread: there all weights loaded ahead take registers that cost CTAs (4778 x 12288 68 us
 // instead of 64). Registers: 48 keep five CTAs of 256 threads an SM (8192 x 4096 35.8 us, with 52 37.4), 80 three
@@ -393,7 +393,7 @@ struct RingShape {
 // each (one CTA with more: it needs the registers), and up to three groups in a CTA's ring. Measured for 8192 x
 // 7168, 470 MB: 74 us, 94% of the copy rate; with the weights read from L1 row by row instead of kept in registers
 // 93 us, with two vectors a thread and two CTAs an SM (spills) 91 us, with a ring of five groups 2 us more. Without
-// dh (353 MB) 66 us: there the ~250 instructions a warp and row and the barrier bound it.
+// dh (353 MB) 68 us: there the ~250 instructions a warp and row and the barrier bound it.
 inline RingShape ring_shape(int nvec, int tensors) {
   RingShape r;
   r.vpt = nvec <= 1024 ? 1 : nvec <= 1536 ? 2 : 4;
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 768 : 512, 1) rms
     }
   }
   // A wait that ran out ended all other waits and the loads; what was computed from there on means nothing. NaN in all
-  // of the CTA's rows and of dw. (That within the loop, from the group on, cost 4% without dh.)
+  // of the CTA's rows and of dw. (Ending the loop there instead took 69.3 us without dh, not 67.9.)
   if (lost) {
     if (threadIdx.x == 0) q.drain(full, lost_g);
     __syncthreads();

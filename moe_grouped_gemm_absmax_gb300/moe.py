@@ -1,8 +1,10 @@
 """The mixture-of-experts block of a transformer on FP8 weights, for serving: the norm with the residual, the
 router and the experts, through the library's entry points.
 
-Up to MOE_MAX_TOKENS tokens (decode) take fp8_moe_tokens, which reads the named experts' weights once; more
-take the grouped GEMM on rows sorted by expert, with the norm's 8-bit output as its operand."""
+Up to MOE_MAX_TOKENS tokens (decode) take fp8_moe_tokens, which reads the named experts' weights once (for each 40
+slots of an expert) and holds the activations to bf16's precision; more take the grouped GEMM on rows sorted by
+expert, with the norm's 8-bit output as its operand and the hidden layer in 8 bits too (a scale per row): the results
+of the two differ by the rounding to e4m3."""
 import torch
 
 from . import (DT_E4M3, GRAN_ROW, GROUPED_JAGGED_M, MOE_MAX_TOKENS, SCORE_BIASED, SCORE_SOFTMAX, add_rmsnorm_alloc,
@@ -11,8 +13,8 @@ from . import (DT_E4M3, GRAN_ROW, GROUPED_JAGGED_M, MOE_MAX_TOKENS, SCORE_BIASED
 
 class Fp8MoEBlock:
     """norm_weight [H]; router_weight bf16 [E, H]; w1 (gate), w3 (up) bf16 [E, I, H]; w2 bf16 [E, H, I]; bias fp32
-    [E] or None, the balancing bias: added to the router's scores for the choice. The experts' weights are quantized once, e4m3 with a
-    scale per row."""
+    [E] or None, the balancing bias: added to the router's scores for the choice. The experts' weights are quantized
+    once, e4m3 with a scale per row."""
 
     def __init__(self, norm_weight, router_weight, w1, w3, w2, top_k, eps=1e-6, bias=None, score=SCORE_SOFTMAX,
                  renormalize=True, scale=1.0):
