@@ -106,7 +106,8 @@ enum {
   FP8_MM_A_MN_MAJOR = 2, /* BF16 only: A is given as [K, M] (M contiguous) */
   FP8_MM_B_MN_MAJOR = 4, /* BF16 only: B is given as [K, N] (N contiguous) */
   FP8_MM_BLOCKWISE = 8   /* FP8 only: sA [M, K/128] (1 x 128 tiles of A) and sB [ceil(N/128), K/128]
-                            (128 x 128 tiles of B) inverse scales, K % 128 == 0 ([B]) */
+                            (128 x 128 tiles of B; for each expert in grouped calls) inverse scales,
+                            K % 128 == 0 ([B]) */
 };
 
 /* grouped GEMM modes */
@@ -119,6 +120,10 @@ enum { FP8_WGRAD_FP8 = 0, FP8_WGRAD_BF16 = 1 };
 enum { FP8_SCORE_SOFTMAX = 0, FP8_SCORE_SIGMOID = 1 };
 /* OR-ed into the score function: the router's bias is added to the score instead of to the logit */
 enum { FP8_SCORE_BIASED = 1 << 4 };
+
+/* activation of the gated feed-forward (fp8_gated_mm): x / (1 + exp(-x)); GELU in its tanh form,
+ * x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+enum { FP8_ACT_SILU = 0, FP8_ACT_GELU = 1 };
 
 /* most tokens of one fp8_moe_tokens call */
 #define FP8_MOE_MAX_TOKENS 64
@@ -250,6 +255,9 @@ int fp8_scaled_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* sA
  *   A = G^T and B = X^T in the segment-padded column-major layout written by fp8_quantize
  *   (COL granularity with offsets): A FP8 [N, P], B FP8 [K, P]; sA fp32 [E, N]; sB fp32 [E, K];
  *   out bf16/fp32 [E, N, K]. An empty segment gives out[e] = 0.
+ * Blockwise ([B]; FP8_MM_BLOCKWISE, JAGGED_M only, K % 128 == 0): sA fp32 [M, K / 128], sB fp32 [E,
+ *   ceil(N / 128), K / 128]:  out[r, n] = sum_kb sA[r, kb] * sB[e, n / 128, kb] * sum_{k in kb} A[r, k] * B[e, n, k],
+ *   each K block's product accumulated by itself, then added up in fp32 in the blocks' order.
  * MX ([MX]; sA, sB of dtype FP8_DT_E8M0, K % 128 == 0, scales in the MX scale layout):
  *   JAGGED_M: sA = the segment-padded row-major scales of A (fp8_quantize MX ROW_MAJOR with
  *   offsets; P = 32 * bytes / K rows, P % 128 == 0, P >= M + 127 E); sB = E * fp8_mx_scale_bytes(N,
@@ -460,6 +468,46 @@ int fp8_moe_tokens(const fp8_tensor* x, const fp8_tensor* ids, const fp8_tensor*
                    fp8_tensor* out, void* workspace, size_t workspace_bytes, int32_t* d_status,
                    void* stream);
 size_t fp8_moe_tokens_workspace_size(int64_t T, int64_t top_k, int64_t H, int64_t I);
+
+/*
+ * fp8_gated_mm — the gated feed-forward's hidden layer: both projections, the activation and the product in
+ * one kernel,
+ *   g = A W1^T,  u = A W3^T,  h = act(g) * u        (g and u scaled as the GEMM's results, all in fp32)
+ *  A           FP8 or bf16 [M, K].
+ *  B           A's kind, K-major [2 I, K]: rows 0 .. I - 1 are W1 (gate), rows I .. 2 I - 1 W3 (up). With
+ *              offsets [E, 2 I, K] (FP8 only), an expert's weights each, and A's rows routed as for
+ *              fp8_grouped_mm JAGGED_M (E <= 2048; a bad vector sets FP8_DEV_BAD_OFFSETS). Not e5m2 x e5m2.
+ *              K > 0; K % 16 == 0 for FP8, K % 8 for bf16; I % 8 == 0.
+ *  sA, sB      FP8: inverse scales fp32, sA [M] or [1], sB [2 I] or [1]; with offsets sA [M], sB [E, 2 I].
+ *              With FP8_MM_BLOCKWISE ([B]; K and I multiples of 128) sA [M, K / 128], sB [2 I / 128, K / 128],
+ *              [E, 2 I / 128, K / 128] with offsets. MX scales: FP8_ERR_UNSUPPORTED. NULL for bf16.
+ *  act         FP8_ACT_SILU or FP8_ACT_GELU. flags: FP8_MM_BLOCKWISE (FP8_MM_FAST_ACCUM changes nothing).
+ *  h           bf16 [M, I] or NULL: h rounded once.
+ *  gu          bf16 [M, 2 I] or NULL: g, and beside it u, rounded once (for the backward pass).
+ *  q           FP8 (E4M3 or E5M2) [M, I] or NULL, with inv_scales fp32 [M, I / 128] (I % 128 == 0): the unrounded
+ *              h in 1 x 128 blocks by the recipe [Q] in fp32 (scale and inverse to 2 units in the last
+ *              place), the operand of a blockwise product with W2.
+ * At least one output is given. A row with a NaN or an infinity gives what the formulas give. No workspace.
+ */
+int fp8_gated_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets, const fp8_tensor* sA,
+                 const fp8_tensor* sB, int act, int flags, fp8_tensor* h, fp8_tensor* gu, fp8_tensor* q,
+                 fp8_tensor* inv_scales, int32_t* d_status, void* stream);
+
+/*
+ * fp8_gated_mm_bwd — gradients of the gated feed-forward's projections from that of its output, y = h W2^T:
+ *   dh = dY W2,  dgu = [dh * u * act'(g), dh * act(g)],  and h again (act(g) * u), for W2's gradient
+ *  dy          FP8 or bf16 [M, K], K the width of y.
+ *  B           W2^T: A's kind, [I, K], with offsets [E, I, K]; or bf16 [K, I] (W2 itself) with
+ *              FP8_MM_B_MN_MAJOR.
+ *  offsets, sdy, sB, act, flags    as in fp8_gated_mm, with I rows of B where it has 2 I (blockwise: K % 128 == 0
+ *              only, sB [ceil(I / 128), K / 128]).
+ *  gu          bf16 [M, 2 I] from fp8_gated_mm: the derivative is taken at these rounded values.
+ *  dgu         bf16 [M, 2 I]; may be gu's own buffer. x's gradient is dgu [W1; W3], theirs dgu^T x.
+ *  h           bf16 [M, I] or NULL.
+ */
+int fp8_gated_mm_bwd(const fp8_tensor* dy, const fp8_tensor* B, const fp8_tensor* offsets, const fp8_tensor* sdy,
+                     const fp8_tensor* sB, int act, int flags, const fp8_tensor* gu, fp8_tensor* dgu, fp8_tensor* h,
+                     int32_t* d_status, void* stream);
 
 /* Test hook for failure detection: while enabled, every GEMM launch (and fp8_moe_tokens) first waits
  * on a barrier that nothing signals, the grid barrier of the tensorwise quantize waits for one arrival more

@@ -32,6 +32,7 @@ DEV_BAD_OFFSETS = 1 << 8
 DEV_TIMEOUT = 1 << 9
 DEV_BAD_IDS = 1 << 10
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_BIASED = 0, 1, 16
+ACT_SILU, ACT_GELU = 0, 1
 MOE_MAX_TOKENS = 64
 
 _TORCH_DT = {
@@ -98,6 +99,8 @@ def _load():
     L.fp8_moe_route.argtypes = [P, P, I, I, F, P, P, P, P, P, P, Z, P, P]
     L.fp8_moe_route_bwd.argtypes = [P, P, P, I, I, F, P, P, P]
     L.fp8_moe_tokens.argtypes = [P, P, P, P, P, P, P, P, P, Z, P, P]
+    L.fp8_gated_mm.argtypes = [P, P, P, P, P, I, I, P, P, P, P, P, P]
+    L.fp8_gated_mm_bwd.argtypes = [P, P, P, P, P, I, I, P, P, P, P, P]
     for name, n in (("rmsnorm_bwd", 2), ("moe_route", 2), ("moe_tokens", 4)):
         f = getattr(L, f"fp8_{name}_workspace_size")
         f.argtypes, f.restype = [L64] * n, Z
@@ -112,7 +115,8 @@ EXPORTS = ("fp8_quantize", "fp8_scaled_mm", "fp8_grouped_mm", "fp8_linear_fwd", 
            "fp8_quantize_tensor_noalloc", "fp8_set_test_stall", "fp8_mx_scale_bytes", "fp8_scaled_mm_amax",
            "fp8_quantize_from_amax", "fp8_test_cast_bits", "fp8_scaled_mm_quant", "fp8_add_rmsnorm",
            "fp8_add_rmsnorm_bwd", "fp8_rmsnorm_bwd_workspace_size", "fp8_moe_route", "fp8_moe_route_bwd",
-           "fp8_moe_route_workspace_size", "fp8_moe_tokens", "fp8_moe_tokens_workspace_size")
+           "fp8_moe_route_workspace_size", "fp8_moe_tokens", "fp8_moe_tokens_workspace_size",
+           "fp8_gated_mm", "fp8_gated_mm_bwd")
 
 
 def status_string(code: int) -> str:
@@ -334,6 +338,21 @@ def fp8_moe_tokens(x, ids, weights, w13, s13, w2, s2, out, workspace=None, statu
                               _pack(out), *_ws(workspace), _ptr(status), _stream(stream)), "fp8_moe_tokens")
 
 
+def fp8_gated_mm(A, B, sA=None, sB=None, h=None, gu=None, q=None, inv_scales=None, offsets=None, act=ACT_SILU, flags=0,
+                 status=None, stream=None):
+    """h = act(A W1^T) * (A W3^T), B = [W1; W3] (one for each expert with offsets); gu: both projections, for the
+    backward pass; q / inv_scales: h in 8 bits with 1 x 128 scales. Any of the outputs may be None."""
+    _check(lib.fp8_gated_mm(_pack(A), _pack(B), _pack(offsets), _pack(sA), _pack(sB), act, flags, _pack(h), _pack(gu),
+                            _pack(q), _pack(inv_scales), _ptr(status), _stream(stream)), "fp8_gated_mm")
+
+
+def fp8_gated_mm_bwd(dy, B, sdy, sB, gu, dgu, h=None, offsets=None, act=ACT_SILU, flags=0, status=None, stream=None):
+    """dgu: the gradients of fp8_gated_mm's projections gu (its own buffer too) from the gradient dy of y = h W2^T, with
+    B = W2^T (or W2 itself, bf16, with MM_B_MN_MAJOR); h: the hidden layer again."""
+    _check(lib.fp8_gated_mm_bwd(_pack(dy), _pack(B), _pack(offsets), _pack(sdy), _pack(sB), act, flags, _pack(gu),
+                                _pack(dgu), _pack(h), _ptr(status), _stream(stream)), "fp8_gated_mm_bwd")
+
+
 def fp8_rmsnorm_bwd_workspace_size(T, H) -> int:
     return int(lib.fp8_rmsnorm_bwd_workspace_size(T, H))
 
@@ -429,6 +448,19 @@ def moe_tokens_alloc(x, ids, weights, w13, s13, w2, s2, status=None, stream=None
     ws = moe_tokens_workspace(x.shape[0], ids.shape[1], x.shape[1], w13.shape[1] // 2, x.device)
     fp8_moe_tokens(x, ids, weights, w13, s13, w2, s2, out, ws, status, stream)
     return out
+
+
+def gated_mm_alloc(A, B, sA=None, sB=None, offsets=None, act=ACT_SILU, flags=0, want_h=True, want_gu=False, q_dtype=None,
+                   status=None, stream=None):
+    """Returns (h, gu, q, inv_scales), None for what was not asked: q and inv_scales with a q_dtype (DT_E4M3, DT_E5M2)."""
+    M, I = A.shape[0], B.shape[-2] // 2
+    empty = lambda n, dt: torch.empty((M, n), dtype=dt, device=A.device)  # noqa: E731
+    h = empty(I, torch.bfloat16) if want_h else None
+    gu = empty(2 * I, torch.bfloat16) if want_gu else None
+    q = empty(I, FP8_TORCH[q_dtype]) if q_dtype is not None else None
+    inv = empty(I // 128, torch.float32) if q_dtype is not None else None
+    fp8_gated_mm(A, B, sA, sB, h, gu, q, inv, offsets, act, flags, status, stream)
+    return h, gu, q, inv
 
 
 def quantize_alloc(x, granularity, out_dtype, layout=None, offsets=None, padded_rows=None, status=None,

@@ -545,7 +545,6 @@ extern "C" int fp8_quantize_from_amax(const fp8_tensor* x, int granularity, int 
 extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets,
                               const fp8_tensor* sA, const fp8_tensor* sB, fp8_tensor* out, int mode, int flags,
                               int32_t* d_status, void* stream) {
-  (void)flags;
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   FP8_CHECK(valid_desc(A) && valid_desc(B) && valid_desc(out) && valid_desc(offsets) && valid_desc(sA) &&
@@ -596,9 +595,15 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
       if (M == 0 || N == 0) return FP8_OK;
       return launch_gemm(g, c);
     }
-    FP8_CHECK(numel(sA) == M && numel(sB) == E * N, FP8_ERR_INVALID_ARG);
     FP8_CHECK(K % 16 == 0, FP8_ERR_ALIGNMENT);
     FP8_CHECK(M < (int64_t(1) << 31) && E * N < (int64_t(1) << 31), FP8_ERR_UNSUPPORTED);
+    if (flags & FP8_MM_BLOCKWISE) {  // [B]: sA [M, K/128], sB [E, ceil(N/128), K/128]
+      FP8_CHECK(K % 128 == 0 && K < (int64_t(1) << 31), FP8_ERR_UNSUPPORTED);
+      FP8_CHECK(numel(sA) == M * (K / 128) && numel(sB) == E * ((N + 127) / 128) * (K / 128), FP8_ERR_INVALID_ARG);
+      g.blockwise = 1;
+    } else {
+      FP8_CHECK(numel(sA) == M && numel(sB) == E * N, FP8_ERR_INVALID_ARG);
+    }
     g.M = M;
     g.N = N;
     g.K = K;
@@ -623,6 +628,7 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
       if (N == 0 || Kd == 0) return FP8_OK;
       return launch_gemm(g, c);
     }
+    FP8_CHECK((flags & FP8_MM_BLOCKWISE) == 0, FP8_ERR_UNSUPPORTED);  // blocks of 128 along the rows: not implemented
     FP8_CHECK(numel(sA) == E * N && numel(sB) == E * Kd, FP8_ERR_INVALID_ARG);
     FP8_CHECK(P % 16 == 0, FP8_ERR_ALIGNMENT);
     g.M = N;

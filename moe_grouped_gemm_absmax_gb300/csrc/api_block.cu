@@ -203,3 +203,121 @@ extern "C" int fp8_moe_tokens(const fp8_tensor* x, const fp8_tensor* ids, const 
                            w13->ptr, static_cast<const float*>(s13->ptr), w2->ptr, static_cast<const float*>(s2->ptr),
                            T, k, E, H, I, out->ptr, workspace, c);
 }
+
+// ------------------------------------------------------------------------------------------
+// gated feed-forward
+
+// The operands of fp8_gated_mm (per = 2: B has the gate's rows and the up projection's) and of its backward pass (1).
+static int check_gated(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets, const fp8_tensor* sA,
+                       const fp8_tensor* sB, int act, int flags, int per, GatedArgs* g) {
+  FP8_CHECK(valid_desc(A) && A->ndim == 2 && valid_desc(B), FP8_ERR_INVALID_ARG);
+  FP8_CHECK(act == FP8_ACT_SILU || act == FP8_ACT_GELU, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(shape_max(A, kMaxDim - 1) && shape_max(B, kMaxDim - 1), FP8_ERR_UNSUPPORTED);
+  const bool fp8 = is_fp8(A->dtype);
+  FP8_CHECK(fp8 ? is_fp8(B->dtype) : A->dtype == FP8_DT_BF16 && B->dtype == FP8_DT_BF16, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(!(A->dtype == FP8_DT_E5M2 && B->dtype == FP8_DT_E5M2), FP8_ERR_UNSUPPORTED);
+  const int known = FP8_MM_FAST_ACCUM | (fp8 ? FP8_MM_BLOCKWISE : per == 1 ? FP8_MM_B_MN_MAJOR : 0);
+  FP8_CHECK((flags & ~known) == 0, FP8_ERR_UNSUPPORTED);
+  int64_t E = 0;
+  if (offsets) {
+    FP8_CHECK(valid_desc(offsets) && offsets->dtype == FP8_DT_I32 && offsets->ndim == 1 && offsets->shape[0] >= 1,
+              FP8_ERR_INVALID_ARG);
+    E = offsets->shape[0];
+    FP8_CHECK(fp8 && E <= 2048, FP8_ERR_UNSUPPORTED);
+    FP8_CHECK(B->ndim == 3 && B->shape[0] == E, FP8_ERR_INVALID_ARG);
+    FP8_CHECK((reinterpret_cast<uintptr_t>(offsets->ptr) & 3u) == 0, FP8_ERR_ALIGNMENT);
+  } else {
+    FP8_CHECK(B->ndim == 2, FP8_ERR_INVALID_ARG);
+  }
+  const int b_mn = (flags & FP8_MM_B_MN_MAJOR) ? 1 : 0;
+  const int64_t M = A->shape[0], K = A->shape[1];
+  const int64_t rows = B->shape[b_mn ? 1 : B->ndim - 2], kb = B->shape[b_mn ? 0 : B->ndim - 1], I = rows / per;
+  FP8_CHECK(kb == K && rows % per == 0, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(K % (fp8 ? 16 : 8) == 0 && I % 8 == 0, FP8_ERR_ALIGNMENT);
+  FP8_CHECK(K > 0, FP8_ERR_UNSUPPORTED);  // an empty contraction: not implemented here
+  FP8_CHECK(aligned16(A->ptr) && aligned16(B->ptr), FP8_ERR_ALIGNMENT);
+  const bool block = (flags & FP8_MM_BLOCKWISE) != 0;
+  if (fp8) {
+    FP8_CHECK(valid_desc(sA) && valid_desc(sB), FP8_ERR_INVALID_ARG);
+    FP8_CHECK(sA->dtype != FP8_DT_E8M0 && sB->dtype != FP8_DT_E8M0, FP8_ERR_UNSUPPORTED);  // MX block scales
+    FP8_CHECK(sA->dtype == FP8_DT_F32 && sB->dtype == FP8_DT_F32, FP8_ERR_INVALID_ARG);
+    FP8_CHECK(shape_max(sA, kMaxDim - 1) && shape_max(sB, kMaxDim - 1), FP8_ERR_UNSUPPORTED);
+    const int64_t la = numel(sA), lb = numel(sB), n = E ? E : 1;
+    if (block) {
+      FP8_CHECK(K % 128 == 0 && (per == 1 || I % 128 == 0), FP8_ERR_UNSUPPORTED);
+      FP8_CHECK(la == M * (K / 128) && lb == n * ((rows + 127) / 128) * (K / 128), FP8_ERR_INVALID_ARG);
+    } else {
+      g->sa_scalar = !E && la == 1;
+      g->sb_scalar = !E && lb == 1;
+      FP8_CHECK((la == M || g->sa_scalar) && (lb == n * rows || g->sb_scalar), FP8_ERR_INVALID_ARG);
+    }
+    FP8_CHECK(aligned16(sA->ptr) && aligned16(sB->ptr), FP8_ERR_ALIGNMENT);
+    g->sA = static_cast<const float*>(sA->ptr);
+    g->sB = static_cast<const float*>(sB->ptr);
+  } else {
+    FP8_CHECK(sA == nullptr && sB == nullptr, FP8_ERR_INVALID_ARG);
+  }
+  g->A = A->ptr;
+  g->B = B->ptr;
+  g->a_dtype = A->dtype;
+  g->b_dtype = B->dtype;
+  g->b_mn = b_mn;
+  g->blockwise = block;
+  g->M = M;
+  g->I = I;
+  g->K = K;
+  g->ends = offsets ? static_cast<const int32_t*>(offsets->ptr) : nullptr;
+  g->E = E;
+  g->act = act;
+  return FP8_OK;
+}
+
+extern "C" int fp8_gated_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets, const fp8_tensor* sA,
+                            const fp8_tensor* sB, int act, int flags, fp8_tensor* h, fp8_tensor* gu, fp8_tensor* q,
+                            fp8_tensor* inv_scales, int32_t* d_status, void* stream) {
+  GatedArgs g = {};
+  FP8_TRY(check_gated(A, B, offsets, sA, sB, act, flags, 2, &g));
+  FP8_CHECK((q != nullptr) == (inv_scales != nullptr), FP8_ERR_INVALID_ARG);
+  FP8_CHECK(h || gu || q, FP8_ERR_INVALID_ARG);
+  if (h) {
+    FP8_TRY(check_tensor(h, FP8_DT_BF16, 2, g.M, g.I));
+    g.h = h->ptr;
+  }
+  if (gu) {
+    FP8_TRY(check_tensor(gu, FP8_DT_BF16, 2, g.M, 2 * g.I));
+    g.gu = gu->ptr;
+  }
+  if (q) {
+    FP8_CHECK(valid_desc(q) && is_fp8(q->dtype), FP8_ERR_INVALID_ARG);
+    FP8_CHECK(g.I % 128 == 0, FP8_ERR_UNSUPPORTED);
+    FP8_TRY(check_tensor(q, q->dtype, 2, g.M, g.I));
+    FP8_TRY(check_tensor(inv_scales, FP8_DT_F32, 2, g.M, g.I / 128));
+    g.q = q->ptr;
+    g.inv = static_cast<float*>(inv_scales->ptr);
+    g.q_fmt = q->dtype;
+  }
+  Ctx c;
+  FP8_TRY(make_ctx(&c, stream, d_status));
+  if (g.M == 0 || g.I == 0) return FP8_OK;
+  return launch_gated(g, c);
+}
+
+extern "C" int fp8_gated_mm_bwd(const fp8_tensor* dy, const fp8_tensor* B, const fp8_tensor* offsets,
+                                const fp8_tensor* sdy, const fp8_tensor* sB, int act, int flags, const fp8_tensor* gu,
+                                fp8_tensor* dgu, fp8_tensor* h, int32_t* d_status, void* stream) {
+  GatedArgs g = {};
+  FP8_TRY(check_gated(dy, B, offsets, sdy, sB, act, flags, 1, &g));
+  FP8_TRY(check_tensor(gu, FP8_DT_BF16, 2, g.M, 2 * g.I));
+  FP8_TRY(check_tensor(dgu, FP8_DT_BF16, 2, g.M, 2 * g.I));
+  if (h) {
+    FP8_TRY(check_tensor(h, FP8_DT_BF16, 2, g.M, g.I));
+    g.h = h->ptr;
+  }
+  g.backward = 1;
+  g.gu_in = gu->ptr;
+  g.gu = dgu->ptr;
+  Ctx c;
+  FP8_TRY(make_ctx(&c, stream, d_status));
+  if (g.M == 0 || g.I == 0) return FP8_OK;
+  return launch_gated(g, c);
+}

@@ -1,0 +1,111 @@
+// The gated feed-forward's GEMMs (sm_103a): both projections of a row with the activation and the product, and its
+// backward pass, as epilogues of the scaled GEMM (gemm_kernel.cuh; formulas: gate.cuh).
+//
+//   h = act(x W1^T) * (x W3^T)          a tile of 128 columns of h takes the MMA's 256 columns: 128 rows of W1 and the
+//                                       same 128 of W3, so both values of an element meet in one thread
+//   dh = dY W2, du = dh act(g), dg = dh u act'(g)     dh stays in the accumulator
+#include "args.h"
+#include "gemm_kernel.cuh"
+
+namespace fp8lin {
+
+namespace {
+
+template <int KIND, int B_MN, int EPI>
+int run_dense(bool pair, const CUtensorMap& ta, const CUtensorMap& tb, const GemmParams& p, const Ctx& c) {
+  CUtensorMap none;
+  memset(&none, 0, sizeof(none));
+  const int64_t tiles = p.num_m * p.num_n;
+  if constexpr (KIND != kBLK)
+    if (pair) return run<KIND, kDense, 0, B_MN, 2, EPI>(ta, tb, none, none, none, p, tiles, c);
+  return run<KIND, kDense, 0, B_MN, 1, EPI>(ta, tb, none, none, none, p, tiles, c);
+}
+
+template <int KIND, int EPI>
+int run_experts(bool pair, const CUtensorMap& ta, const CUtensorMap& tb, const GemmParams& p, const Ctx& c) {
+  CUtensorMap none;
+  memset(&none, 0, sizeof(none));
+  if constexpr (KIND != kBLK)
+    if (pair) return run<KIND, kJagM, 0, 0, 2, EPI>(ta, tb, none, none, none, p, 0, c);
+  return run<KIND, kJagM, 0, 0, 1, EPI>(ta, tb, none, none, none, p, 0, c);
+}
+
+template <int EPI>
+int launch(const GatedArgs& g, const Ctx& c) {
+  constexpr bool kForward = EPI == kGate;
+  const bool fp8 = g.a_dtype != FP8_DT_BF16, grouped = g.ends != nullptr;
+  const int esz = fp8 ? 1 : 2;
+  GemmParams p = {};
+  p.M = g.M;
+  p.N = g.I;
+  p.K = g.K;
+  p.sA = g.sA;
+  p.sB = g.sB;
+  p.sa_scalar = g.sa_scalar;
+  p.sb_scalar = g.sb_scalar;
+  p.ends = g.ends;
+  p.E = (int)g.E;
+  p.total_rows = g.M;
+  p.status = c.status;
+  p.wait_ns = c.wait_ns;
+  p.test_stall = c.test_stall;
+  p.gate.act = g.act;
+  p.gate.gu_in = static_cast<const __nv_bfloat16*>(g.gu_in);
+  p.gate.gu = static_cast<__nv_bfloat16*>(g.gu);
+  p.gate.h = static_cast<__nv_bfloat16*>(g.h);
+  p.gate.q = static_cast<uint8_t*>(g.q);
+  p.gate.inv = g.inv;
+  p.gate.q_fmt = g.q_fmt;
+  if (grouped && (g.E < 1 || g.E > kMaxExperts)) return FP8_ERR_UNSUPPORTED;
+  const int tn = kForward ? BN / 2 : BN;
+  p.num_n = (g.I + tn - 1) / tn;
+  p.nkb = (g.K * esz + BKB - 1) / BKB;
+  // CTA pairs and single CTAs by the plain GEMMs' rule (launch_gemm)
+  const bool pair = !g.blockwise && (grouped ? g.M >= 2048 : ((g.M + 255) / 256) * p.num_n * 2 >= c.sm_count);
+  const int tile_m = pair ? 2 * BM : BM;
+  p.num_m = (g.M + tile_m - 1) / tile_m;
+  set_walk(p, (int64_t)tile_m * g.K * esz, (int64_t)BN * g.K * esz);
+  if ((p.num_m + (grouped ? g.E : 0)) * p.num_n >= (int64_t)1 << 31) return FP8_ERR_UNSUPPORTED;
+
+  // operand maps: 128-byte rows of K. The forward's B boxes have 128 rows (one projection's), the backward's those of
+  // a CTA.
+  const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint32_t kbox = (uint32_t)(BKB / esz), b_rows = kForward || pair ? BN / 2 : BN;
+  const uint64_t rows = (uint64_t)(kForward ? 2 * g.I : g.I);
+  CUtensorMap ta, tb;
+  {
+    const uint64_t d[2] = {(uint64_t)g.K, (uint64_t)g.M}, st[1] = {(uint64_t)(g.K * esz)};
+    const uint32_t box[2] = {kbox, BM};
+    FP8_TRY(make_tmap(&ta, g.A, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  }
+  if (grouped) {
+    const uint64_t d[3] = {(uint64_t)g.K, rows, (uint64_t)g.E}, st[2] = {(uint64_t)g.K, rows * (uint64_t)g.K};
+    const uint32_t box[3] = {kbox, b_rows, 1};
+    FP8_TRY(make_tmap(&tb, g.B, dt, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  } else if (g.b_mn) {
+    const uint64_t d[2] = {rows, (uint64_t)g.K}, st[1] = {rows * 2};
+    const uint32_t box[2] = {64, 64};
+    FP8_TRY(make_tmap(&tb, g.B, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  } else {
+    const uint64_t d[2] = {(uint64_t)g.K, rows}, st[1] = {(uint64_t)(g.K * esz)};
+    const uint32_t box[2] = {kbox, b_rows};
+    FP8_TRY(make_tmap(&tb, g.B, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  }
+  if (!fp8) {
+    p.idesc = make_idesc(kFmtBF16, kFmtBF16, 0, (uint32_t)g.b_mn, tile_m, BN);
+    if constexpr (!kForward)
+      if (g.b_mn) return run_dense<kBF16, 1, EPI>(pair, ta, tb, p, c);
+    return run_dense<kBF16, 0, EPI>(pair, ta, tb, p, c);
+  }
+  p.idesc = make_idesc(g.a_dtype == FP8_DT_E4M3 ? kFmtE4M3 : kFmtE5M2, g.b_dtype == FP8_DT_E4M3 ? kFmtE4M3 : kFmtE5M2,
+                       0, 0, tile_m, BN);
+  if (grouped)
+    return g.blockwise ? run_experts<kBLK, EPI>(false, ta, tb, p, c) : run_experts<kFP8, EPI>(pair, ta, tb, p, c);
+  return g.blockwise ? run_dense<kBLK, 0, EPI>(false, ta, tb, p, c) : run_dense<kFP8, 0, EPI>(pair, ta, tb, p, c);
+}
+
+}  // namespace
+
+int launch_gated(const GatedArgs& g, const Ctx& c) { return g.backward ? launch<kGateBwd>(g, c) : launch<kGate>(g, c); }
+
+}  // namespace fp8lin

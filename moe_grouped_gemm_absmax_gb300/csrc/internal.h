@@ -148,7 +148,7 @@ struct GemmArgs {
   uint32_t* col_amax;
   int amax_whole;         // col_amax is one word: the maximum over the whole output
   int blockwise;          // FP8 operands with blockwise inverse scales: sA [M, K/128] (1 x 128 tiles),
-                          // sB [ceil(N/128), K/128] (128 x 128 tiles); dense only
+                          // sB [ceil(N/128), K/128] (128 x 128 tiles), per expert for jagged M
   // quantized output (dense FP8, N % 128 == 0): codes [M, N] in q_fmt and scales of the result's
   // bf16 rounding, 1 x 128 blocks (q_mx 0: fp32 inverse scales [M, N/128]) or MX blocks of 32
   // (q_mx 1: E8M0 bytes in the MX scale layout for rows M, contraction N); out is then unused
@@ -158,6 +158,30 @@ struct GemmArgs {
   int q_fmt;
 };
 int launch_gemm(const GemmArgs& g, const Ctx& c);
+
+// --- the gated feed-forward's GEMMs (gated.cu) ---
+struct GatedArgs {
+  const void* A;          // [M, K] FP8 or bf16: the rows (forward), the output's gradient (backward)
+  const void* B;          // forward [2 I, K] ([E, 2 I, K]), the gate's rows before the up projection's; backward [I, K]
+  int a_dtype, b_dtype;   // ([E, I, K]), or with b_mn [K, I] (bf16 only)
+  int b_mn;
+  const float* sA;        // [1], [M], or [M, K / 128] (blockwise); null for bf16
+  const float* sB;        // [1], one for each of B's rows, or for each 128 x 128 block
+  int sa_scalar, sb_scalar;
+  int blockwise;
+  int64_t M, I, K;
+  const int32_t* ends;    // null: dense
+  int64_t E;
+  int backward;
+  int act;
+  const void* gu_in;      // backward: the projections [M, 2 I] bf16
+  void* gu;               // the projections (forward, may be null) or their gradients (backward) [M, 2 I] bf16
+  void* h;                // bf16 [M, I] or null
+  void* q;                // forward: FP8 [M, I] with inv fp32 [M, I / 128], or null
+  float* inv;
+  int q_fmt;
+};
+int launch_gated(const GatedArgs& g, const Ctx& c);
 
 }  // namespace fp8lin
 
