@@ -277,6 +277,17 @@ FP8_DEVI uint4 ld_l2(const uint4* p) {
 // Once every CTA has come here (or ended), the next kernel may begin.
 FP8_DEVI void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// One lane of a converged warp, the same one every time.
+FP8_DEVI bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ------------------------------------------------------------------------------------------
 // mbarrier
 FP8_DEVI void mbar_init(uint64_t* bar, uint32_t count) {

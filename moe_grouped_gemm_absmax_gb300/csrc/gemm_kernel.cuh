@@ -558,15 +558,20 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ================================ MMA issuer ================================
-    if (lane == 0 && issuer) {
+    // The loop runs warp-uniform: elect.sync picks the lane that issues, all lanes wait. Descriptors are offsets of
+    // per-kernel bases (address field in 16-byte units). Control flow of one lane alone, and descriptors built for
+    // every MMA, cost the blockwise loop a third of its time.
+    if (issuer) {
+      const bool leader = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int buf = 0;
       uint32_t aphase = 0;
       bool ok = true;
-      // MX: stage 0's A descriptor and the four scale-factor ids
-      const uint64_t mx_a_desc0 = smem_desc(smem_u32(smem), 16, 1024);
-      uint32_t mx_id[4];
+      const uint64_t a_desc0 = smem_desc(smem_u32(smem), A_MN ? 8192 : 16, 1024);
+      const uint64_t b_desc0 = smem_desc(smem_u32(smem) + C::A_BYTES, B_MN ? 8192 : 16, 1024);
+      constexpr uint64_t kStepA = (A_MN ? 2048 : 32) >> 4, kStepB = (B_MN ? 2048 : 32) >> 4;
+      uint32_t mx_id[4];  // MX: the four scale-factor ids
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mx_id[kk] = idesc_sf_ids(p.idesc, (uint32_t)kk, (uint32_t)kk);
       if (p.test_stall && !mbar_wait(&S.never, 0, abort_flag, p.wait_ns)) {
@@ -574,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         ok = false;
       }
       for (int64_t t = unit; t < total && ok; t += n_units) {
-        const int64_t nkb = tile_nkb<SCHED>(p, t, aux);
+        const int nkb = (int)tile_nkb<SCHED>(p, t, aux);
         if (nkb == 0) continue;
         uint32_t idesc = p.idesc;
         if (kTail && p.tail_t) {  // transposed tail tile: swapped formats, N = N'
@@ -588,16 +593,13 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
           }
           tc_fence_after();
         }
-        uint32_t d_tmem = tmem_base + (uint32_t)(buf * TBN);
-        for (int64_t kb = 0; kb < nkb; ++kb) {
+        for (int kb = 0; kb < nkb; ++kb) {
           if (KIND == kBLK) {  // each K block into the next free partial buffer
             if (!mbar_wait(&S.tempty[buf], aphase ^ 1, abort_flag, p.wait_ns)) {
               if (!*abort_flag) fail();
               ok = false;
               break;
             }
-            tc_fence_after();
-            d_tmem = tmem_base + (uint32_t)(buf * TBN);
           }
           // MX: the scale warp's commit on sff[stage] follows the stage's full barrier
           if (!mbar_wait(KIND == kMX ? &S.sff[stage] : &S.full[stage], phase, abort_flag, p.wait_ns)) {
@@ -606,82 +608,67 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES);
-          const uint32_t sb = sa + C::A_BYTES;
-          if (KIND == kMX) {
-            // the stage's scales are in its tensor-memory slot (copied by the scale warp).
-            // Descriptors are offsets of per-kernel bases (address field in 16-byte units), so
-            // the single issuing thread spends few instructions per stage.
+          if (leader) {
+            const uint32_t d_tmem = tmem_base + (uint32_t)(buf * TBN);
+            const uint64_t soff = (uint64_t)((uint32_t)(stage * C::STAGE_BYTES) >> 4);
+            const uint64_t ad0 = a_desc0 + soff, bd0 = b_desc0 + soff;
+            // MX: the stage's scales are in its tensor-memory slot (copied by the scale warp)
             const uint32_t sf_t = tmem_base + (uint32_t)(C::SF_COL0 + 16 * stage);
-            const uint64_t soff = (uint64_t)((stage * C::STAGE_BYTES) >> 4);
-            const uint64_t ad0 = mx_a_desc0 + soff;
             const uint32_t sfb_t = sf_t + 4;  // 256-column tiles start on a 128-row scale block
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ad = ad0 + 2 * kk;
-              const uint64_t bd = ad + (C::A_BYTES >> 4);
-              const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
+              const uint64_t ad = ad0 + kk * kStepA, bd = bd0 + kk * kStepB;
+              const uint32_t acc = ((KIND != kBLK && kb > 0) || kk > 0) ? 1u : 0u;
+              if (KIND == kMX) {
+                if (CG == 2)
+                  umma_mx_pair(d_tmem, ad, bd, mx_id[kk], sf_t, sfb_t, acc);
+                else
+                  umma_mx(d_tmem, ad, bd, mx_id[kk], sf_t, sfb_t, acc);
+              } else if (KIND == kBF16) {
+                if (CG == 2)
+                  umma_f16_pair(d_tmem, ad, bd, p.idesc, acc);
+                else
+                  umma_f16(d_tmem, ad, bd, p.idesc, acc);
+              } else {
+                if (CG == 2)
+                  umma_f8f6f4_pair(d_tmem, ad, bd, idesc, acc);
+                else
+                  umma_f8f6f4(d_tmem, ad, bd, p.idesc, acc);
+              }
+            }
+            // frees the stage (in both CTAs of a pair) once these MMAs have read it; with the tile's last K block
+            // (kBLK: with every one) the accumulator is ready for the epilogue(s)
+            if (CG == 2)
+              umma_commit_pair(&S.empty[stage], 0x3);
+            else
+              umma_commit(&S.empty[stage]);
+            if (KIND == kBLK || kb + 1 == nkb) {
               if (CG == 2)
-                umma_mx_pair(d_tmem, ad, bd, mx_id[kk], sf_t, sfb_t, acc);
+                umma_commit_pair(&S.tfull[buf], 0x3);
               else
-                umma_mx(d_tmem, ad, bd, mx_id[kk], sf_t, sfb_t, acc);
-            }
-          } else {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = A_MN ? smem_desc(sa + kk * 2048, 8192, 1024) : smem_desc(sa + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc(sb + kk * 2048, 8192, 1024) : smem_desc(sb + kk * 32, 16, 1024);
-            const uint32_t acc = ((KIND != kBLK && kb > 0) || kk > 0) ? 1u : 0u;
-            if (CG == 2) {
-              if (KIND == kFP8 || KIND == kBLK)
-                umma_f8f6f4_pair(d_tmem, ad, bd, idesc, acc);
-              else
-                umma_f16_pair(d_tmem, ad, bd, p.idesc, acc);
-            } else {
-              if (KIND == kFP8 || KIND == kBLK)
-                umma_f8f6f4(d_tmem, ad, bd, p.idesc, acc);
-              else
-                umma_f16(d_tmem, ad, bd, p.idesc, acc);
+                umma_commit(&S.tfull[buf]);
             }
           }
-          }
-          // frees the stage (in both CTAs of a pair) once these MMAs have read it
-          if (CG == 2)
-            umma_commit_pair(&S.empty[stage], 0x3);
-          else
-            umma_commit(&S.empty[stage]);
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
-          if (KIND == kBLK) {  // this K block's partial is ready for promotion
-            if (CG == 2)
-              umma_commit_pair(&S.tfull[buf], 0x3);
-            else
-              umma_commit(&S.tfull[buf]);
+          if (KIND == kBLK || kb + 1 == nkb) {
             if (++buf == C::NBUF) {
               buf = 0;
               aphase ^= 1;
             }
           }
         }
-        if (!ok) break;
-        if (KIND == kBLK) continue;
-        // accumulator ready for the epilogue(s)
-        if (CG == 2)
-          umma_commit_pair(&S.tfull[buf], 0x3);
-        else
-          umma_commit(&S.tfull[buf]);
-        if (++buf == C::NBUF) {
-          buf = 0;
-          aphase ^= 1;
-        }
       }
-      // Drain every MMA this thread issued before the tensor memory is released.
-      if (CG == 2)
-        umma_commit_pair(&S.drain, 0x3);
-      else
-        umma_commit(&S.drain);
+      // Drain every MMA issued before the tensor memory is released.
+      if (leader) {
+        if (CG == 2)
+          umma_commit_pair(&S.drain, 0x3);
+        else
+          umma_commit(&S.drain);
+      }
     }
     __syncwarp();
   } else if (KIND == kBLK && warp == C::SF_WARP) {
