@@ -38,15 +38,6 @@ FP8_DEVI uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-FP8_DEVI uint4 pack_bf16x8(const float* f) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-}
-FP8_DEVI void unpack_bf16x8(uint4 v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-}
-
 // max(a, b) that keeps a NaN, for a block's largest magnitude
 FP8_DEVI float max_nan(float a, float b) {
   float r;
@@ -54,27 +45,63 @@ FP8_DEVI float max_nan(float a, float b) {
   return r;
 }
 
-// N values of a row in bf16 at o, those in front of column `left` (a multiple of 8, as is every row's width: a group of
-// 8 is written whole or not at all)
-template <int N>
-FP8_DEVI void store_row(__nv_bfloat16* o, const float* f, int64_t left) {
+// 32 values of a row, packed in 16 words, at o, or from there: those in front of column `left`, a multiple of 8 as is
+// every row's width, so that a group of 8 is written whole or not at all. wide: rows are 32-byte aligned.
+FP8_DEVI void store_row32(__nv_bfloat16* o, const uint32_t* w, int64_t left, int wide) {
+  if (wide && left >= 32) {
+    st_v8(o, w);
+    st_v8(o + 16, w + 8);
+    return;
+  }
 #pragma unroll
-  for (int j = 0; j < N; j += 8)
-    if (j < left) *reinterpret_cast<uint4*>(o + j) = pack_bf16x8(f + j);
+  for (int j = 0; j < 4; ++j)
+    if (8 * j < left) *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+FP8_DEVI void load_row32(const __nv_bfloat16* o, uint32_t* w, int64_t left, int wide) {
+  if (wide && left >= 32) {
+    ld_v8(o, w);
+    ld_v8(o + 16, w + 8);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (8 * j < left) v = *reinterpret_cast<const uint4*>(o + 8 * j);
+    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+  }
+}
+FP8_DEVI void pack_row32(const float* f, uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+}
+// N fp32 values of a row
+template <int N>
+FP8_DEVI void store_row(__nv_bfloat16* o, const float* f, int64_t left, int wide) {
+#pragma unroll
+  for (int j = 0; j < N; j += 32) {
+    uint32_t w[16];
+    pack_row32(f + j, w);
+    store_row32(o + j, w, left - j, wide);
+  }
 }
 
-// Codes of N values of a row, 16 bytes at a time.
+// Codes of N values of a row.
 template <int FMT, int N>
-FP8_DEVI void store_codes(uint8_t* o, const float* f, float scale) {
+FP8_DEVI void store_codes(uint8_t* o, const float* f, float scale, int wide) {
+  uint32_t w[N / 4];
 #pragma unroll
-  for (int j = 0; j < N; j += 16) {
-    uint32_t w[4];
+  for (int i = 0; i < N / 4; ++i) {
+    const float* v = f + 4 * i;
+    w[i] = cvt_fp8x2<FMT>(v[0] * scale, v[1] * scale) | (cvt_fp8x2<FMT>(v[2] * scale, v[3] * scale) << 16);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* v = f + j + 4 * i;
-      w[i] = cvt_fp8x2<FMT>(v[0] * scale, v[1] * scale) | (cvt_fp8x2<FMT>(v[2] * scale, v[3] * scale) << 16);
+  for (int j = 0; j < N / 4; j += 8) {
+    if (wide) {
+      st_v8(o + 4 * j, w + j);
+    } else {
+      *reinterpret_cast<uint4*>(o + 4 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+      *reinterpret_cast<uint4*>(o + 4 * j + 16) = make_uint4(w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
     }
-    *reinterpret_cast<uint4*>(o + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -86,32 +113,38 @@ struct GateArgs {
   uint8_t* q;                  // h in 8 bits [M, I] with inverse scales [M, I / 128] of its 1 x 128 blocks, may be null
   float* inv;
   int q_fmt;
+  int wide;                    // every row of gu_in, gu, h and q in use starts on 32 bytes
 };
 
-// Backward, N columns from n of row m: dh (fp32) with the projections' values to their gradients, and h again. gu may be
-// gu_in's own buffer: every value is read by the thread that writes its place, before it does.
-template <int N>
-FP8_DEVI void gate_bwd_row(const GateArgs& p, const float* dh, int64_t m, int64_t n, int64_t I) {
+// Backward, 32 columns from n of row m: their projections, loaded ahead, and with dh (fp32) the projections' gradients and
+// h again. gu may be gu_in's own buffer: every value is read by the thread that writes its place, before it does. (The
+// compiler cannot know that they never overlap otherwise, so that the loads are where they are written: all of a chunk's
+// ahead of its stores, and ahead of the wait for its accumulator.)
+struct GuChunk {
+  uint32_t g[16], u[16];
+};
+FP8_DEVI void gate_load(const GateArgs& p, GuChunk& c, int64_t m, int64_t n, int64_t I) {
   const __nv_bfloat16* gi = p.gu_in + m * 2 * I + n;
-  __nv_bfloat16* go = p.gu + m * 2 * I + n;
+  load_row32(gi, c.g, I - n, p.wide);
+  load_row32(gi + I, c.u, I - n, p.wide);
+}
+FP8_DEVI void gate_bwd(const GateArgs& p, const GuChunk& c, const float* dh, int64_t m, int64_t n, int64_t I) {
+  uint32_t dg[16], du[16], h[16];
 #pragma unroll
-  for (int j = 0; j < N; j += 8) {
-    if (n + j >= I) break;
-    float g[8], u[8], h[8];
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(gi + j), g);
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(gi + I + j), u);
+  for (int i = 0; i < 16; ++i) {
+    float a[2], d[2];
+    const float g[2] = {__uint_as_float(c.g[i] << 16), __uint_as_float(c.g[i] & 0xFFFF0000u)};
+    const float u[2] = {__uint_as_float(c.u[i] << 16), __uint_as_float(c.u[i] & 0xFFFF0000u)};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float d;
-      const float a = act_bwd(g[i], p.act, &d);
-      h[i] = a * u[i];
-      g[i] = dh[j + i] * u[i] * d;
-      u[i] = dh[j + i] * a;
-    }
-    *reinterpret_cast<uint4*>(go + j) = pack_bf16x8(g);
-    *reinterpret_cast<uint4*>(go + I + j) = pack_bf16x8(u);
-    if (p.h) *reinterpret_cast<uint4*>(p.h + m * I + n + j) = pack_bf16x8(h);
+    for (int k = 0; k < 2; ++k) a[k] = act_bwd(g[k], p.act, &d[k]);
+    dg[i] = pack_bf16(dh[2 * i] * u[0] * d[0], dh[2 * i + 1] * u[1] * d[1]);
+    du[i] = pack_bf16(dh[2 * i] * a[0], dh[2 * i + 1] * a[1]);
+    h[i] = pack_bf16(a[0] * u[0], a[1] * u[1]);
   }
+  __nv_bfloat16* go = p.gu + m * 2 * I + n;
+  store_row32(go, dg, I - n, p.wide);
+  store_row32(go + I, du, I - n, p.wide);
+  if (p.h) store_row32(p.h + m * I + n, h, I - n, p.wide);
 }
 
 }  // namespace fp8lin

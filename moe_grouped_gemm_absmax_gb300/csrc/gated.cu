@@ -56,6 +56,8 @@ int launch(const GatedArgs& g, const Ctx& c) {
   p.gate.q = static_cast<uint8_t*>(g.q);
   p.gate.inv = g.inv;
   p.gate.q_fmt = g.q_fmt;
+  p.gate.wide = ((reinterpret_cast<uintptr_t>(g.gu_in) | reinterpret_cast<uintptr_t>(g.gu) | reinterpret_cast<uintptr_t>(g.h) |
+                  reinterpret_cast<uintptr_t>(g.q)) & 31) == 0 && g.I % 16 == 0;
   if (grouped && (g.E < 1 || g.E > kMaxExperts)) return FP8_ERR_UNSUPPORTED;
   const int tn = kForward ? BN / 2 : BN;
   p.num_n = (g.I + tn - 1) / tn;
@@ -67,10 +69,9 @@ int launch(const GatedArgs& g, const Ctx& c) {
   set_walk(p, (int64_t)tile_m * g.K * esz, (int64_t)BN * g.K * esz);
   if ((p.num_m + (grouped ? g.E : 0)) * p.num_n >= (int64_t)1 << 31) return FP8_ERR_UNSUPPORTED;
 
-  // operand maps: 128-byte rows of K. The forward's B boxes have 128 rows (one projection's), the backward's those of
-  // a CTA.
+  // operand maps: 128-byte rows of K. The forward's B boxes have rows of one projection, the backward's all of a CTA's.
   const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint32_t kbox = (uint32_t)(BKB / esz), b_rows = kForward || pair ? BN / 2 : BN;
+  const uint32_t kbox = (uint32_t)(BKB / esz),  b_rows = kForward ? (g.blockwise ? 64 : 128) : pair ? 128 : 256;
   const uint64_t rows = (uint64_t)(kForward ? 2 * g.I : g.I);
   CUtensorMap ta, tb;
   {
@@ -100,8 +101,8 @@ int launch(const GatedArgs& g, const Ctx& c) {
   p.idesc = make_idesc(g.a_dtype == FP8_DT_E4M3 ? kFmtE4M3 : kFmtE5M2, g.b_dtype == FP8_DT_E4M3 ? kFmtE4M3 : kFmtE5M2,
                        0, 0, tile_m, BN);
   if (grouped)
-    return g.blockwise ? run_experts<kBLK, EPI>(false, ta, tb, p, c) : run_experts<kFP8, EPI>(pair, ta, tb, p, c);
-  return g.blockwise ? run_dense<kBLK, 0, EPI>(false, ta, tb, p, c) : run_dense<kFP8, 0, EPI>(pair, ta, tb, p, c);
+    return g.blockwise ? run_experts<kBLK, EPI>(pair, ta, tb, p, c) : run_experts<kFP8, EPI>(pair, ta, tb, p, c);
+  return g.blockwise ? run_dense<kBLK, 0, EPI>(pair, ta, tb, p, c) : run_dense<kFP8, 0, EPI>(pair, ta, tb, p, c);
 }
 
 }  // namespace

@@ -93,17 +93,17 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
   p.ends = g.ends;
   p.E = (int)g.E;
   const bool mx = g.mx != 0;
-  const int tbn = mx ? Cfg<kMX, 1>::TBN : (g.blockwise ? Cfg<kBLK, 1>::TBN : BN);
+  const int tbn = mx ? Cfg<kMX, 1>::TBN : BN;
   p.num_n = (g.N + tbn - 1) / tbn;
   const int esz = fp8 ? 1 : 2;
   p.nkb = (g.K * esz + BKB - 1) / BKB;
   p.ldo = g.N;
   p.vec_ok = p.out_f32 ? (p.ldo % 4 == 0) : (p.ldo % 8 == 0);
+  p.wide = ((reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(p.ldo * (p.out_f32 ? 4 : 2))) & 31) == 0;
   if (g.mode != -1 && (g.E < 1 || g.E > kMaxExperts)) return FP8_ERR_UNSUPPORTED;
-  // pair tiles when there are at least ~one per SM pair. Blockwise scaling runs on single CTAs:
-  // its per-K-block commit / promotion / release cycle ran at half the speed across a CTA pair
-  // (1050 vs 560 us on 8192 x 14336 x 4096; 600 us for the pair even with the promotion's waits
-  // removed, so the pair's per-block commits, not the promotion, set that pace).
+  // pair tiles when there are at least ~one per SM pair. Blockwise scaling runs on single CTAs: each K block's
+  // partial goes from the MMAs to the promoting warps and back, and across a pair that takes longer than
+  // the pair saves in operand traffic (8192 x 14336 x 4096: 523 us against 452).
   const int64_t pair_tiles = ((g.M + 255) / 256) * p.num_n * (g.mode == FP8_GROUPED_JAGGED_K ? g.E : 1);
   const bool pair = !g.blockwise && (g.mode == FP8_GROUPED_JAGGED_M ? g.M >= 2048 : pair_tiles * 2 >= c.sm_count);
   const int tile_m = pair ? 256 : 128;
@@ -164,15 +164,9 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
       if (rc) return rc;
       if (g.mode == -1) {
         const int64_t tiles = p.num_m * p.num_n;
-        if (g.blockwise) {  // sA [M, K/128], sB [ceil(N/128), K/128]; 128-column tiles
+        if (g.blockwise) {  // sA [M, K/128], sB [ceil(N/128), K/128]
           if (g.K % 128 || p.row_amax || p.col_amax) return FP8_ERR_UNSUPPORTED;
-          constexpr int TB = Cfg<kBLK, 1>::TBN;
-          p.idesc = make_idesc(af, bf, 0, 0, tile_m, TB);
-          const uint32_t boxB2[2] = {BKB, pair ? TB / 2 : TB};
-          CUtensorMap tbb;
-          rc = make_tmap(&tbb, g.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dB, strideK, boxB2, CU_TENSOR_MAP_SWIZZLE_128B);
-          if (rc) return rc;
-          return run<kBLK, kDense, 0, 0, 1>(ta, tbb, to, none, none, p, tiles, c);
+          return run<kBLK, kDense, 0, 0, 1>(ta, tb, to, none, none, p, tiles, c);
         }
         if (p.row_amax || p.col_amax)
           return pair ? run<kFP8, kDenseAmax, 0, 0, 2>(ta, tb, to, none, none, p, tiles, c)

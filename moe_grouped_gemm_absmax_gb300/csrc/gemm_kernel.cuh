@@ -73,17 +73,14 @@ enum { kStore = 0, kGate = 1, kGateBwd = 2 };
 // release it at once, so the next tile's MMAs wait only for those loads, not for the stores.
 template <int KIND, int CG, int SCHED = 0>
 struct Cfg {
-  // kBLK: single-CTA 128 x 256 tiles and two K-block partials (the MMAs run one K block ahead
-  // of the promotion). 128-column tiles with four partials were slower: the MMA's cost is per
-  // instruction, so halving N halves the tensor-core rate.
+  // kBLK: two K-block partials, so the MMAs run one K block ahead of the promotion.
   static constexpr int TBN = BN;                          // tile columns
-  static constexpr int NBUF = KIND == kMX ? 1 : 2;        // accumulators / K-block partials
-  static constexpr int EPI_WARPS = (KIND == kMX || KIND == kBLK) ? 16 : 8;
+    static constexpr int NBUF = KIND == kMX ? 1 : 2;        // accumulators / K-block partials
+  static constexpr int EPI_WARPS = KIND == kMX ? 16 : 8;
   static constexpr int EPI_THREADS = 32 * EPI_WARPS;
-  // MX: the warp that copies scales to tensor memory; kBLK: the warp that stages each K block's
-  // tile scales in shared memory ahead of the promotion
-  static constexpr int SF_WARP = 2 + EPI_WARPS;
-  static constexpr int THREADS = 64 + EPI_THREADS + ((KIND == kMX || KIND == kBLK) ? 32 : 0);
+  static constexpr int EPI0 = KIND == kBLK ? 4 : 2;      // first epilogue warp (kBLK: warpgroups share registers)
+  static constexpr int SF_WARP = 2 + EPI_WARPS;          // MX: the warp that copies scales to tensor memory
+  static constexpr int THREADS = 32 * EPI0 + EPI_THREADS + (KIND == kMX ? 32 : 0);
   static constexpr int WCOLS = TBN * 4 / EPI_WARPS;      // columns per epilogue warp: 128 or 64
   static constexpr int A_BYTES = BM * BKB;               // this CTA's 128 rows of A
   static constexpr int B_ROWS = TBN / CG;                // this CTA's rows of B
@@ -116,6 +113,7 @@ struct GemmParams {
   void* out;
   int out_f32;
   int vec_ok;          // 16-byte aligned output rows
+  int wide;            // 32-byte aligned output rows (kBLK)
   int64_t ldo;         // output row stride (elements)
   const int32_t* ends;
   int E;
@@ -143,13 +141,13 @@ struct GemmParams {
 };
 
 struct Tile {
-  int64_t m0, n0;   // first row / column of the (pair's) tile of D
-  int64_t pm0;      // m0 in the segment-padded row space of the MX A scales (jagged M), else m0
-  int64_t row_end;  // rows >= row_end are masked (segment end, or M)
-  int64_t k0;       // first contraction coordinate
-  int64_t nkb;      // K blocks
+  int32_t m0, n0;   // first row / column of the (pair's) tile of D
+  int32_t row_end;  // rows >= row_end are masked (segment end, or M)
+  int32_t k0;       // first contraction coordinate
+  int32_t nkb;      // K blocks
   int e;            // expert (jagged)
   int tt;           // jagged M, transposed tail tile: its rows (1..255); 0 for an ordinary tile
+  int64_t pm0;      // m0 in the segment-padded row space of the MX A scales (jagged M), else m0
 };
 
 constexpr int kMaxStages = 5;  // ring stages the barrier arrays below hold
@@ -167,22 +165,16 @@ struct Shared {
   int abort;
 };
 constexpr int kSharedBytes = 2304;
-// kBLK: a ring of K-block tile scales in shared memory, filled by the scale warp ahead of the
-// promotion: per slot this CTA's 128 row scales and the tile's two 128-column block scales
-constexpr int kScGroup = 8;   // K blocks whose scales the scale warp loads in one burst
-constexpr int kScSlots = 16;  // two bursts: one being consumed while the next is loaded
-struct ScaleRing {
-  float a[kScSlots][128];
-  float b[kScSlots][4];
-  uint64_t full[kScSlots];   // 32 arrivals: every lane of the scale warp after its stores
-  uint64_t empty[kScSlots];  // one arrival per promoter warp after its reads
-};
-constexpr int kScaleRingBytes = (int)((sizeof(ScaleRing) + 127) / 128 * 128);
+// kBLK: K blocks whose scales a promoting lane loads together, one group ahead
+constexpr int kScGroup = 4;
+// kBLK: registers a thread of the four warps that issue and of the eight that promote: 128 x 40 + 256 x 232 = 384 x 168,
+// what the block is launched with
+constexpr int kIssueRegs = 40, kPromoteRegs = 232;
 static_assert(sizeof(Shared) <= kSharedBytes, "shared block");
 // kGate with codes: the largest magnitudes of a row's columns that the warps of a lane quarter hold, alternating between
 // consecutive tiles
 struct AmaxShare {
-  float a[2][4][128];
+  float a[2][2][128];
 };
 
 FP8_DEVI int find_expert(const int32_t* tpre, int E, int64_t t) {
@@ -224,35 +216,35 @@ FP8_DEVI Tile get_tile(const GemmParams& p, int64_t t64, const int32_t* tpre, co
       mb = r / gsz;
       nb = first_n + (r - mb * gsz);
     }
-    T.m0 = (int64_t)mb * TILE_M;
+    T.m0 = (int32_t)(mb * TILE_M);
     T.pm0 = T.m0;
-    T.n0 = (int64_t)nb * TBN;
-    T.row_end = p.M;
+    T.n0 = (int32_t)(nb * TBN);
+    T.row_end = (int32_t)p.M;
     T.k0 = 0;
-    T.nkb = p.nkb;
+    T.nkb = (int32_t)p.nkb;
     T.e = 0;
     T.tt = 0;
   } else if (SCHED == kJagM) {
     const int e = find_expert(tpre, p.E, t64);
     const uint32_t local = t - (uint32_t)tpre[e];
     const uint32_t mb = local / num_n, nb = local - mb * num_n;
-    T.m0 = aux[e] + (int64_t)mb * TILE_M;  // aux[e] = segment start row
+    T.m0 = aux[e] + (int32_t)(mb * TILE_M);  // aux[e] = segment start row
     T.pm0 = pst ? pst[e] + (int64_t)mb * TILE_M : T.m0;
-    T.n0 = (int64_t)nb * TBN;
+    T.n0 = (int32_t)(nb * TBN);
     T.row_end = aux[e + 1];
     T.k0 = 0;
-    T.nkb = p.nkb;
+    T.nkb = (int32_t)p.nkb;
     T.e = e;
-    T.tt = (p.tail_t && T.row_end - T.m0 < TILE_M) ? (int)(T.row_end - T.m0) : 0;
+    T.tt = (p.tail_t && T.row_end - T.m0 < TILE_M) ? T.row_end - T.m0 : 0;
   } else {
     const uint32_t per = (uint32_t)p.num_m * num_n;
     const uint32_t e = t / per;
     const uint32_t local = t - e * per;
     const uint32_t mb = local / num_n, nb = local - mb * num_n;
-    T.m0 = (int64_t)mb * TILE_M;
+    T.m0 = (int32_t)(mb * TILE_M);
     T.pm0 = T.m0;
-    T.n0 = (int64_t)nb * TBN;
-    T.row_end = p.M;
+    T.n0 = (int32_t)(nb * TBN);
+    T.row_end = (int32_t)p.M;
     T.k0 = aux[e];                             // aux[e] = padded start of segment e
     T.nkb = (aux[e + 1] - aux[e]) / BKB;       // padded length / 128
     T.e = (int)e;
@@ -275,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmSA,
                 const __grid_constant__ CUtensorMap tmSB, const GemmParams p) {
   using C = Cfg<KIND, CG, SCHED>;
+  static_assert(KIND != kBLK || CG == 1, "blockwise scaling runs on single CTAs");
   static_assert(C::STAGES <= kMaxStages && C::NBUF <= 4, "ring and accumulator barriers fit the shared block");
   constexpr int STAGES = C::STAGES;
   constexpr int kThreads = C::THREADS;
@@ -290,8 +283,6 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
   uint8_t* out_stage = smem + C::RING_BYTES;  // [8 warps][kStageOut], pairs only
   Shared& S = *reinterpret_cast<Shared*>(smem + C::RING_BYTES + C::OUT_BYTES);
   uint8_t* rest = smem + C::RING_BYTES + C::OUT_BYTES + kSharedBytes;
-  ScaleRing& SR = *reinterpret_cast<ScaleRing*>(rest);  // kBLK
-  if (KIND == kBLK) rest += kScaleRingBytes;
   AmaxShare& AS = *reinterpret_cast<AmaxShare*>(rest);  // kGate
   if (EPI == kGate) rest += sizeof(AmaxShare);
   int32_t* tpre = reinterpret_cast<int32_t*>(rest);
@@ -378,12 +369,6 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
     mbar_init(&S.drain, 1);
     for (int s2 = 0; s2 < STAGES; ++s2) mbar_init(&S.sff[s2], 1);
     mbar_init(&S.sf_drain, 1);
-    if (KIND == kBLK) {
-      for (int i = 0; i < kScSlots; ++i) {
-        mbar_init(&SR.full[i], 32);
-        mbar_init(&SR.empty[i], C::EPI_WARPS);
-      }
-    }
     mbar_init(&S.never, 1);
     S.abort = 0;
     fence_mbar_init();
@@ -415,6 +400,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
     set_status(p.status, FP8_DEV_TIMEOUT);
   };
 
+  if (KIND == kBLK) {
+    if (warp < C::EPI0)
+      setmaxnreg_dec<kIssueRegs>();
+    else
+      setmaxnreg_inc<kPromoteRegs>();
+  }
   if (warp == 0) {
     // ================================ TMA producer ================================
     if (lane == 0) {
@@ -424,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
       bool ok = true;
       for (int64_t t = unit; t < total && ok; t += n_units) {
         const Tile T = get_tile<SCHED, C::TILE_M, TN>(p, t, tpre, aux, pst);
-        const int32_t am = (int32_t)(T.m0 + (int64_t)rank * BM);        // this CTA's A rows
+        const int32_t am = T.m0 + (int32_t)rank * BM;        // this CTA's A rows
         // this CTA's B rows; kGate on a pair: the gate's 128 in the even CTA, the up projection's in the other
         const int32_t bn = (int32_t)(T.n0 + (int64_t)rank * (EPI == kGate ? p.N : C::B_ROWS));
         // MX scale blocks: this CTA's 128 A rows; the two 128-row B blocks holding the tile's
@@ -439,7 +430,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
           tail_box = tail_half <= 32 ? 32 : (tail_half <= 64 ? 64 : 128);
         }
         const uint32_t tx = tail_box ? (uint32_t)(C::A_BYTES + tail_box * BKB) : (uint32_t)C::TX_BYTES;
-        for (int64_t kb = 0; kb < T.nkb; ++kb) {
+        for (int32_t kb = 0; kb < T.nkb; ++kb) {
           if (!mbar_wait(&S.empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
             if (!*abort_flag) fail();
             ok = false;
@@ -465,15 +456,15 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             } else if (KIND == kFP8 || KIND == kBLK) {
               const int32_t kx = (int32_t)(T.k0 + kb * BKB);
               tma_load_2d(sa, &tmA, fb, kx, am);
-              if (SCHED == kJagM)
-                tma_load_3d(sb, &tmB, fb, kx, bn, T.e);
-              else
-                tma_load_2d(sb, &tmB, fb, kx, bn);
-              if (EPI == kGate) {  // boxes of 128 rows: the up projection's follow the gate's
+              // kGate: boxes of 128 rows, the up projection's after the gate's (kBLK: of 64, one after the other)
+              constexpr int kBoxes = EPI == kGate ? (KIND == kBLK ? 4 : 2) : 1;
+#pragma unroll
+              for (int h = 0; h < kBoxes; ++h) {
+                const int32_t r = bn + (h & 1) * (int32_t)p.N + h / 2 * 64;
                 if (SCHED == kJagM)
-                  tma_load_3d(sb + C::B_BYTES / 2, &tmB, fb, kx, bn + (int32_t)p.N, T.e);
+                  tma_load_3d(sb + h * (C::B_BYTES / kBoxes), &tmB, fb, kx, r, T.e);
                 else
-                  tma_load_2d(sb + C::B_BYTES / 2, &tmB, fb, kx, bn + (int32_t)p.N);
+                  tma_load_2d(sb + h * (C::B_BYTES / kBoxes), &tmB, fb, kx, r);
               }
             } else {
               const int32_t kx = (int32_t)(kb * (BKB / 2));  // 64 bf16 per block
@@ -506,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
                 tma_load_3d_pair(ssf + 512, &tmSB, fb, 0, kx / 128, sfb_rb);
               }
               tma_load_3d_pair(ssf, &tmSA, fb, 0, kx / 128, sfa_rb);
-            } else if (KIND == kFP8 || KIND == kBLK) {
+            } else if (KIND == kFP8) {
               const int32_t kx = (int32_t)(T.k0 + kb * BKB);
               if (kTail && tail_box) {
                 tma_load_3d_pair(sa, &tmB, fb, kx, bn, T.e);  // this CTA's 128 weight rows
@@ -594,12 +585,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
           tc_fence_after();
         }
         for (int kb = 0; kb < nkb; ++kb) {
-          if (KIND == kBLK) {  // each K block into the next free partial buffer
-            if (!mbar_wait(&S.tempty[buf], aphase ^ 1, abort_flag, p.wait_ns)) {
-              if (!*abort_flag) fail();
-              ok = false;
-              break;
-            }
+          // kBLK: each K block into the next free partial
+          if (KIND == kBLK && !mbar_wait(&S.tempty[buf], aphase ^ 1, abort_flag, p.wait_ns)) {
+            if (!*abort_flag) fail();
+            ok = false;
+            break;
           }
           // MX: the scale warp's commit on sff[stage] follows the stage's full barrier
           if (!mbar_wait(KIND == kMX ? &S.sff[stage] : &S.full[stage], phase, abort_flag, p.wait_ns)) {
@@ -608,6 +598,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             break;
           }
           tc_fence_after();
+          const bool done = KIND == kBLK || kb + 1 == nkb;  // the accumulator is complete with these MMAs
           if (leader) {
             const uint32_t d_tmem = tmem_base + (uint32_t)(buf * TBN);
             const uint64_t soff = (uint64_t)((uint32_t)(stage * C::STAGE_BYTES) >> 4);
@@ -636,13 +627,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
                   umma_f8f6f4(d_tmem, ad, bd, p.idesc, acc);
               }
             }
-            // frees the stage (in both CTAs of a pair) once these MMAs have read it; with the tile's last K block
-            // (kBLK: with every one) the accumulator is ready for the epilogue(s)
+            // frees the stage (in both CTAs of a pair) once these MMAs have read it
             if (CG == 2)
               umma_commit_pair(&S.empty[stage], 0x3);
             else
               umma_commit(&S.empty[stage]);
-            if (KIND == kBLK || kb + 1 == nkb) {
+            if (done) {
               if (CG == 2)
                 umma_commit_pair(&S.tfull[buf], 0x3);
               else
@@ -654,11 +644,9 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             stage = 0;
             phase ^= 1;
           }
-          if (KIND == kBLK || kb + 1 == nkb) {
-            if (++buf == C::NBUF) {
-              buf = 0;
-              aphase ^= 1;
-            }
+          if (done && ++buf == C::NBUF) {
+            buf = 0;
+            aphase ^= 1;
           }
         }
       }
@@ -671,56 +659,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (KIND == kBLK && warp == C::SF_WARP) {
-    // ======================= blockwise: tile scales, K block by K block =======================
-    // For every K block of every tile this CTA computes: this CTA's 128 row scales
-    // sA[m, kb] (lane l holds rows l, l + 32, l + 64, l + 96) and the two 128-column block
-    // scales sB[n / 128, kb], into the next ring slot. The loads for kScGroup K blocks go out
-    // together (one memory latency per burst, not per block), and the ring holds two bursts.
-    int slot = 0;
-    uint32_t ph = 0;
-    const int64_t KB = p.nkb;
-    bool ok = true;
-    for (int64_t t = unit; t < total && ok; t += n_units) {
-      const Tile T = get_tile<SCHED, C::TILE_M, TN>(p, t, tpre, aux, pst);
-      const int64_t r0 = T.m0 + (int64_t)rank * BM;
-      // the scales of the tile's two 128-column blocks (kGate: of the gate's and of the up projection's)
-      const int64_t blocks = (EPI == kGate ? 2 * p.N : p.N + 127) / 128;
-      const int64_t nb = T.n0 / 128 + (lane & 1) * (EPI == kGate ? p.N / 128 : 1);
-      const bool b_live = lane < 2 && nb < blocks;
-      const float* sB = p.sB + (int64_t)T.e * blocks * KB;
-      for (int64_t kb0 = 0; kb0 < T.nkb && ok; kb0 += kScGroup) {
-        float va[4][kScGroup], vb[kScGroup];
-#pragma unroll
-        for (int j = 0; j < kScGroup; ++j) {
-          const bool k_live = kb0 + j < T.nkb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + lane + 32 * i;
-            va[i][j] = (k_live && r < p.M) ? __ldg(p.sA + r * KB + kb0 + j) : 0.0f;
-          }
-          vb[j] = (k_live && b_live) ? __ldg(sB + nb * KB + kb0 + j) : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kScGroup; ++j) {
-          if (kb0 + j >= T.nkb) break;
-          if (!mbar_wait(&SR.empty[slot], ph ^ 1, abort_flag, p.wait_ns)) {
-            if (!*abort_flag) fail();
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) SR.a[slot][lane + 32 * i] = va[i][j];
-          if (lane < 2) SR.b[slot][lane] = vb[j];
-          mbar_arrive(&SR.full[slot]);  // release: this lane's stores before the arrival
-          if (++slot == kScSlots) {
-            slot = 0;
-            ph ^= 1;
-          }
-        }
-      }
-    }
-    __syncwarp();
+  } else if (KIND == kBLK && warp < C::EPI0) {
+    // no role: these warps complete the warpgroup
   } else if (KIND == kMX && warp == C::SF_WARP) {
     // ============================ MX scale copies ============================
     // For every stage the MMA thread will consume: wait for its loads, copy its three scale
@@ -770,13 +710,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
   } else {
     // ================================ epilogue ================================
     const int q = warp & 3;              // TMEM lane quarter this warp may access
-    const int c0 = ((warp - 2) >> 2) * C::WCOLS;  // first tile column of this warp's share
-    const int etid = tid - 64;           // 0..255 across the epilogue warps
+    const int c0 = ((warp - C::EPI0) >> 2) * C::WCOLS;  // first tile column of this warp's share
+    const int etid = tid - 32 * C::EPI0;  // 0..255 across the epilogue warps
     const int row = (int)rank * BM + q * 32 + lane;  // row within the pair's tile
     const bool stage_sb = KIND == kFP8 && !p.sb_scalar;
     int buf = 0, sbi = 0;
-    int sc_slot = 0;       // kBLK: scale-ring slot and phase
-    uint32_t sc_ph = 0;
     uint32_t oseq = 0;  // TMA stores issued by this warp
     uint32_t aphase = 0;
     // The next tile and the scales it needs (this thread's row scale; its column scale, or the
@@ -792,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         sb_nx = etid < Tn.tt ? (p.sa_scalar ? __ldg(p.sA) : __ldg(p.sA + Tn.m0 + etid)) : 0.0f;
         return;
       }
-      const int64_t m = Tn.m0 + row;
+      const int64_t m = (int64_t)Tn.m0 + row;
       const float* sbp = p.sB;
       if (!is_dense(SCHED)) sbp += (int64_t)Tn.e * (EPI == kGate ? 2 * p.N : p.N);
       sa_nx = 1.0f;
@@ -810,16 +748,16 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
       }
     };
     // kGate: the hidden layer's columns n .. n + W - 1 of row m, from fp32. A row's 128-column block lies in the warps of
-    // one lane quarter (four of 32 columns, or two of 64): they share its largest magnitude through shared memory.
+    // one lane quarter, 64 columns each: they share its largest magnitude through shared memory.
     int amax_buf = 0;
     auto gate_out = [&](const float* hv, auto width, int64_t m, int64_t n, bool row_ok) {
       constexpr int W = decltype(width)::value;
-      if (p.gate.h && row_ok) store_row<W>(p.gate.h + m * p.N + n, hv, p.N - n);
+      if (p.gate.h && row_ok) store_row<W>(p.gate.h + m * p.N + n, hv, p.N - n, p.gate.wide);
       if (!p.gate.q) return;
       float a = 0.0f;
 #pragma unroll
       for (int j = 0; j < W; ++j) a = max_nan(a, fabsf(hv[j]));
-      const int at = q * 32 + lane, part = (warp - 2) >> 2;
+      const int at = q * 32 + lane, part = (warp - C::EPI0) >> 2;
       AS.a[amax_buf][part][at] = a;
       named_bar_sync(3 + q, 128 / W * 32);
 #pragma unroll
@@ -831,16 +769,35 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
       if (part == 0) p.gate.inv[m * (p.N / 128) + n / 128] = a * (e4 ? 1.0f / kE4M3Max : 1.0f / kE5M2Max);
       uint8_t* o = p.gate.q + m * p.N + n;
       if (e4)
-        store_codes<FP8_DT_E4M3, W>(o, hv, __fdiv_rn(kE4M3Max, a));
+        store_codes<FP8_DT_E4M3, W>(o, hv, __fdiv_rn(kE4M3Max, a), p.gate.wide);
       else
-        store_codes<FP8_DT_E5M2, W>(o, hv, __fdiv_rn(kE5M2Max, a));
+        store_codes<FP8_DT_E5M2, W>(o, hv, __fdiv_rn(kE5M2Max, a), p.gate.wide);
+    };
+    // kBLK: the scales of kScGroup K blocks from kb0 on: this lane's row of A, and the 128-column block of B that the
+    // warp's columns lie in (kGate: the gate's and the up projection's). Loaded a group ahead, so that no promotion
+    // waits for memory.
+    float ra[kScGroup], rb[kScGroup], rc[kScGroup];
+    auto load_scales = [&](const Tile& T, int32_t kb0) {
+      const int64_t KB = p.nkb, r = (int64_t)T.m0 + row;
+      const int64_t blocks = (EPI == kGate ? 2 * p.N : p.N + 127) / 128;
+      const int64_t nb = T.n0 / 128 + (EPI == kGate ? 0 : c0 / 128);
+      const float* a = p.sA + r * KB;
+      const float* b = p.sB + ((int64_t)T.e * blocks + nb) * KB;
+#pragma unroll
+      for (int j = 0; j < kScGroup; ++j) {
+        const bool live = kb0 + j < KB;
+        ra[j] = live && r < p.M ? __ldg(a + kb0 + j) : 0.0f;
+        rb[j] = live && nb < blocks ? __ldg(b + kb0 + j) : 0.0f;
+        if (EPI == kGate) rc[j] = live ? __ldg(b + (p.N / 128) * KB + kb0 + j) : 0.0f;
+      }
     };
     if (unit < total) fetch(unit);
+    if (KIND == kBLK && unit < total) load_scales(Tn, 0);
     for (int64_t t = unit; t < total; t += n_units) {
       const Tile T = Tn;
       const float sa = sa_nx, sb_mine = sb_nx;
-      if (t + n_units < total) fetch(t + n_units);
-      const int64_t m = T.m0 + row;
+      if (KIND != kBLK && t + n_units < total) fetch(t + n_units);
+      const int64_t m = (int64_t)T.m0 + row;
       const bool row_ok = m < T.row_end;
       const int64_t orow = SCHED == kJagK ? (int64_t)T.e * p.M + m : m;
       if (stage_sb || (kTail && T.tt)) {  // one column scale per epilogue thread; reused by all 128 rows
@@ -860,72 +817,68 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         }
         continue;
       }
-      if (KIND == kBLK) {
-        // promotion: for every K block, this warp's columns of the partial into registers, the
-        // partial back to the MMAs, then acc += partial * sA[m, kb] * sB[n / 128, kb] (the
-        // warp's columns lie in one 128-column scale block). Stores after the last block.
-        constexpr int WC = C::WCOLS, NL = WC / 16;
-        const int bsel = c0 / 128;  // which of the tile's two 128-column scale blocks
-        // first tile column of the warp's 16-column chunk h (kGate: half its chunks from the gate, half from the up
-        // projection, the same columns of the hidden layer)
-        auto chunk_col = [&](int h) {
-          if (EPI != kGate) return c0 + 16 * h;
-          return h < NL / 2 ? c0 / 2 + 16 * h : 128 + c0 / 2 + 16 * (h - NL / 2);
-        };
+      if constexpr (KIND == kBLK) {
+        // promotion: for every K block, this warp's half of the partial into registers, the partial back to the MMAs,
+        // acc += partial * sA[m, kb] * sB[n / 128, kb]. The next 16 columns are on their way while these are added.
+        constexpr int WC = C::WCOLS;
+        static_assert(WC == 128, "a warp promotes 128 columns");
         float acc[WC];
 #pragma unroll
         for (int j = 0; j < WC; ++j) acc[j] = 0.0f;
-        const uint32_t tq = (uint32_t)(q * 32) << 16;
+        auto add16 = [](float* a, const uint32_t* v, float sc) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) a[j] = fmaf(__uint_as_float(v[j]), sc, a[j]);
+        };
         bool live = true;
-        for (int64_t kb = 0; kb < T.nkb; ++kb) {
-          // this K block's scales from the ring (staged ahead by the scale warp)
-          if (!mbar_wait(&SR.full[sc_slot], sc_ph, abort_flag, p.wait_ns)) {
-            if (!*abort_flag) fail();
-            live = false;
-            break;
-          }
-          const float sk = SR.a[sc_slot][q * 32 + lane] * SR.b[sc_slot][EPI == kGate ? 0 : bsel];
-          const float sk_up = EPI == kGate ? SR.a[sc_slot][q * 32 + lane] * SR.b[sc_slot][1] : sk;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&SR.empty[sc_slot]);
-          if (++sc_slot == kScSlots) {
-            sc_slot = 0;
-            sc_ph ^= 1;
-          }
-          if (!mbar_wait(&S.tfull[buf], aphase, abort_flag, p.wait_ns)) {
-            if (!*abort_flag) fail();
-            live = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t taddr = tmem_base + (uint32_t)(buf * TBN) + tq;
-          // 16 columns at a time (the accumulators already hold WC registers); overlapping the
-          // loads with the adds through a second staging set measured no faster
-          uint32_t v[16];
+        for (int32_t kb0 = 0; kb0 < T.nkb && live; kb0 += kScGroup) {
+          float sk[kScGroup], su[kScGroup];
 #pragma unroll
-          for (int h = 0; h + 1 < NL; ++h) {
-            tmem_ld16(taddr + chunk_col(h), v);
-            tmem_ld_wait_regs16(v);
-            const float s = h < NL / 2 ? sk : sk_up;
+          for (int j = 0; j < kScGroup; ++j) {
+            sk[j] = ra[j] * rb[j];
+            su[j] = EPI == kGate ? ra[j] * rc[j] : sk[j];
+          }
+          load_scales(T, kb0 + kScGroup);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[16 * h + j] = fmaf(__uint_as_float(v[j]), s, acc[16 * h + j]);
-          }
-          tmem_ld16(taddr + chunk_col(NL - 1), v);
-          tmem_ld_wait_regs16(v);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2)
-              mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&S.tempty[buf]), 0));
-            else
-              mbar_arrive_relaxed(&S.tempty[buf]);
-          }
-          if (++buf == C::NBUF) {
-            buf = 0;
-            aphase ^= 1;
-          }
+          for (int j = 0; j < kScGroup; ++j) {
+            if (kb0 + j >= T.nkb) break;
+            if (!mbar_wait(&S.tfull[buf], aphase, abort_flag, p.wait_ns)) {
+              if (!*abort_flag) fail();
+              live = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (uint32_t)(buf * TBN + c0) + ((uint32_t)(q * 32) << 16);
+            uint32_t va[16], vb[16];
+            tmem_ld16(taddr, va);
+            tmem_ld_wait_regs16(va);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[16 * (NL - 1) + j] = fmaf(__uint_as_float(v[j]), sk_up, acc[16 * (NL - 1) + j]);
+            for (int c = 0; c < WC; c += 32) {
+              tmem_ld16(taddr + c + 16, vb);
+              add16(acc + c, va, c < WC / 2 ? sk[j] : su[j]);
+              tmem_ld_wait_regs16(vb);
+              if (c + 32 == WC) break;
+              tmem_ld16(taddr + c + 32, va);
+              add16(acc + c + 16, vb, c < WC / 2 ? sk[j] : su[j]);
+              tmem_ld_wait_regs16(va);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 2)
+                mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&S.tempty[buf]), 0));
+              else
+                mbar_arrive_relaxed(&S.tempty[buf]);
+            }
+            add16(acc + WC - 16, vb, su[j]);
+            if (++buf == 2) {
+              buf = 0;
+              aphase ^= 1;
+            }
+          }
+        }
+        if (t + n_units < total) {  // the next tile, not held in registers before
+          fetch(t + n_units);
+          load_scales(Tn, 0);
         }
         // the decision is uniform where warps meet at a barrier below
         if (EPI == kGate && p.gate.q) live = named_bar_and(2, kEpiThreads, live);
@@ -933,8 +886,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         if constexpr (EPI == kGate) {
           const int64_t n = T.n0 + c0 / 2;
           if (p.gate.gu && row_ok) {
-            store_row<WC / 2>(p.gate.gu + m * 2 * p.N + n, acc, p.N - n);
-            store_row<WC / 2>(p.gate.gu + m * 2 * p.N + p.N + n, acc + WC / 2, p.N - n);
+            store_row<WC / 2>(p.gate.gu + m * 2 * p.N + n, acc, p.N - n, p.gate.wide);
+            store_row<WC / 2>(p.gate.gu + m * 2 * p.N + p.N + n, acc + WC / 2, p.N - n, p.gate.wide);
           }
 #pragma unroll
           for (int j = 0; j < WC / 2; ++j) acc[j] = act_fwd(acc[j], p.gate.act) * acc[j + WC / 2];
@@ -942,7 +895,16 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
           continue;
         }
         if constexpr (EPI == kGateBwd) {
-          if (row_ok) gate_bwd_row<WC>(p.gate, acc, m, T.n0 + c0, p.N);
+          if (row_ok) {
+            const int64_t n = T.n0 + c0;
+            GuChunk cu[2];
+            gate_load(p.gate, cu[0], m, n, p.N);
+#pragma unroll
+            for (int ch = 0; ch < WC / 32; ++ch) {
+              if (ch + 1 < WC / 32) gate_load(p.gate, cu[(ch + 1) & 1], m, n + 32 * ch + 32, p.N);
+              gate_bwd(p.gate, cu[ch & 1], acc + 32 * ch, m, n + 32 * ch, p.N);
+            }
+          }
           continue;
         }
         if (row_ok) {
@@ -954,32 +916,32 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             const bool full = p.vec_ok && n + 32 <= p.N;
             if (p.out_f32) {
               float* o = static_cast<float*>(p.out) + orow * p.ldo + n;
-              if (full) {
+              if (full && p.wide) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) st_v8(o + j, reinterpret_cast<const uint32_t*>(a + j));
+              } else if (full) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
               } else {
                 for (int j = 0; j < 32 && n + j < p.N; ++j) o[j] = a[j];
               }
             } else {
-              uint16_t* o = static_cast<uint16_t*>(p.out) + orow * p.ldo + n;
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + orow * p.ldo + n;
               uint32_t wd[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const __nv_bfloat162 hb = __floats2bfloat162_rn(a[2 * j], a[2 * j + 1]);
-                wd[j] = *reinterpret_cast<const uint32_t*>(&hb);
-              }
-              if (full) {
-#pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                  *reinterpret_cast<uint4*>(o + 2 * j) = make_uint4(wd[j], wd[j + 1], wd[j + 2], wd[j + 3]);
+              pack_row32(a, wd);
+              if (p.vec_ok) {
+                store_row32(o, wd, p.N - n, p.wide);
               } else {
-                for (int j = 0; j < 32 && n + j < p.N; ++j) o[j] = (uint16_t)(wd[j >> 1] >> (16 * (j & 1)));
+                for (int j = 0; j < 32 && n + j < p.N; ++j)
+                  reinterpret_cast<uint16_t*>(o)[j] = (uint16_t)(wd[j >> 1] >> (16 * (j & 1)));
               }
             }
           }
         }
         continue;
       }
+      GuChunk cu[2];
+      if (EPI == kGateBwd && row_ok) gate_load(p.gate, cu[0], m, T.n0 + c0, p.N);
       const bool got = mbar_wait(&S.tfull[buf], aphase, abort_flag, p.wait_ns);
       if (!named_bar_and(2, kEpiThreads, got)) {  // uniform decision across the epilogue warps
         if (!got && !*abort_flag) fail();
@@ -1155,8 +1117,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             if (ch == 1) release();
             if (p.gate.gu && row_ok) {
               const int64_t nc = n + 32 * ch;
-              store_row<32>(p.gate.gu + m * 2 * p.N + nc, hv + 32 * ch, p.N - nc);
-              store_row<32>(p.gate.gu + m * 2 * p.N + p.N + nc, u, p.N - nc);
+              store_row<32>(p.gate.gu + m * 2 * p.N + nc, hv + 32 * ch, p.N - nc, p.gate.wide);
+              store_row<32>(p.gate.gu + m * 2 * p.N + p.N + nc, u, p.N - nc, p.gate.wide);
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) hv[32 * ch + j] = act_fwd(hv[32 * ch + j], p.gate.act) * u[j];
@@ -1167,9 +1129,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
           for (int ch = 0; ch < 4; ++ch) {
             float dh[32];
             load32(c0 + 32 * ch, dh);
-            if (row_ok) gate_bwd_row<32>(p.gate, dh, m, T.n0 + c0 + 32 * ch, p.N);
+            if (ch == 3) release();
+            const int64_t n = T.n0 + c0 + 32 * ch;
+            if (row_ok && ch < 3) gate_load(p.gate, cu[(ch + 1) & 1], m, n + 32, p.N);
+            if (row_ok) gate_bwd(p.gate, cu[ch & 1], dh, m, n, p.N);
           }
-          release();
         }
         continue;
       }
@@ -1470,7 +1434,7 @@ int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const 
   constexpr int kThreads = C::THREADS;
   const int n_arrays = is_dense(SCHED) ? 0 : (KIND == kMX && SCHED == kJagM) ? 3 : 2;
   const size_t smem = 1024 + C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +
-                     (KIND == kBLK ? kScaleRingBytes : 0) + (EPI == kGate ? sizeof(AmaxShare) : 0);
+                     (EPI == kGate ? sizeof(AmaxShare) : 0);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return FP8_ERR_CUDA;
   int64_t units = c.sm_count / CG;
