@@ -107,6 +107,10 @@ int launch(const GatedArgs& g, const Ctx& c) {
 
 }  // namespace
 
-int launch_gated(const GatedArgs& g, const Ctx& c) { return g.backward ? launch<kGateBwd>(g, c) : launch<kGate>(g, c); }
+int launch_gated(const GatedArgs& g, const Ctx& c) {
+  if (g.backward) return launch<kGateBwd>(g, c);
+  if (g.a_dtype != FP8_DT_BF16 && g.M <= kFewRows) return launch_few_gated(g, c);
+  return launch<kGate>(g, c);
+}
 
 }  // namespace fp8lin

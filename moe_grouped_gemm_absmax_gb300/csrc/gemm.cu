@@ -196,6 +196,7 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
       const uint32_t boxB[3] = {BKB, b_rows, 1};
       rc = make_tmap(&tb, g.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dB, sB_, boxB, CU_TENSOR_MAP_SWIZZLE_128B);
       if (rc) return rc;
+      if (g.blockwise && g.M <= kFewRows) return launch_few_blockwise(g, c);
       if (g.blockwise) return run<kBLK, kJagM, 0, 0, 1>(ta, tb, to, none, none, p, 0, c);
       if (!pair) return run<kFP8, kJagM, 0, 0, 1>(ta, tb, to, none, none, p, 0, c);
       // An expert's last tile with fewer than 256 rows runs transposed: the expert's 256 weight

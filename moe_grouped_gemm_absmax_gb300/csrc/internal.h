@@ -183,6 +183,11 @@ struct GatedArgs {
 };
 int launch_gated(const GatedArgs& g, const Ctx& c);
 
+// --- FP8 products of a few rows (few.cu) ---
+constexpr int64_t kFewRows = 64;  // most rows of a call that takes it
+int launch_few_gated(const GatedArgs& g, const Ctx& c);          // forward, FP8
+int launch_few_blockwise(const GemmArgs& g, const Ctx& c);       // jagged M, block scales
+
 }  // namespace fp8lin
 
 namespace fp8lin {

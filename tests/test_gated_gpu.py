@@ -275,3 +275,18 @@ def test_gradient_against_differences(fp8):
             # half a step of bf16, fp32 sums, and differences' own error (third derivatives below 2, rounding)
             bound = HALF_BF16 * num.abs() + 1e-4 * (d.abs() @ w.abs().T) * (1 + x[:, I:].abs())
             assert ((got - num).abs() <= bound).all()
+
+
+# the few rows' kernel: rows of a tile (16, 32, 64), one or several CTAs a tile, ragged and empty experts
+FEW = [(1, 128, 128, None), (1, 7168, 256, None), (16, 2048, 136, None), (17, 1024, 384, None), (32, 4096, 128, None),
+       (33, 512, 640, None), (64, 1536, 264, None), (64, 256, 13000, None), (8, 1024, 256, [0, 3, 0, 4, 1]),
+       (64, 512, 200, [1, 0, 40, 23]), (40, 2048, 128, [40]), (64, 384, 384, [1] * 64 + [0] * 200), (5, 640, 2048, [0] * 1999 + [5])]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("kind", ["row", "block"])
+@pytest.mark.parametrize("M,K,I,counts", FEW)
+def test_few_rows(fp8, M, K, I, counts, kind, act):
+    if kind == "block":
+        K, I = -(-K // 128) * 128, -(-I // 128) * 128
+    _run(fp8, M, K, I, counts, kind, act)
