@@ -435,74 +435,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_all(mbar_wait_cluster(&S.part_full, part_phase, abort_flag, p.wait_ns))) break;
         const uint32_t mine = smem_u32(part) + 4 * r;
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-          const int row = first + j * step;
-          if (row >= T.cnt) break;
+        for (int j0 = 0; j0 < NT / 2; j0 += 8) {
+          if (first + j0 * step >= T.cnt) break;
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            float sum = 0.f;
-            for (int c = 0; c < p.split; ++c) sum += ld_cluster(mapa_shared(mine + (g * NT + row) * (kRows * 4), (uint32_t)c));
-            v[g][j] = sum;
+          for (int j = j0; j < j0 + 8; ++j)
+#pragma unroll
+            for (int g = 0; g < G; ++g) v[g][j] = 0.f;
+          for (int c = 0; c < p.split; ++c) {
+            const uint32_t from = mapa_shared(mine, (uint32_t)c);
+#pragma unroll
+            for (int j = j0; j < j0 + 8; ++j)
+              if (first + j * step < T.cnt)
+#pragma unroll
+                for (int g = 0; g < G; ++g) v[g][j] += ld_cluster(from + (uint32_t)((g * NT + first + j * step) * (kRows * 4)));
           }
         }
         __syncwarp();
         if (lane < p.split) mbar_arrive_cluster(mapa_shared(smem_u32(&S.part_empty), (uint32_t)lane));
         part_phase ^= 1;
       }
-      if (!BLOCK) {  // (acc * sA[row]) * sB[column], as the tile kernel rounds
+      // eight rows at a time, without a branch between them, so that their latencies overlap
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (first + j * step >= T.cnt) break;
-          const float s = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
+      for (int j0 = 0; j0 < NT; j0 += 8) {
+        if (first + j0 * step >= T.cnt) break;
+        if (!BLOCK) {  // (acc * sA[row]) * sB[column], as the tile kernel rounds
 #pragma unroll
-          for (int g = 0; g < G; ++g) v[g][j] = v[g][j] * s * sb[g];
-        }
-      }
-      if constexpr (!GATED) {
+          for (int j = j0; j < j0 + 8; ++j) {
+            const float s = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int row = first + j * step;
-          if (row >= T.cnt) break;
-          const int64_t at = (int64_t)(T.row0 + row) * p.N + n;
-          if (n_ok && p.out_f32)
-            static_cast<float*>(p.out)[at] = v[0][j];
-          else if (n_ok)
-            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v[0][j]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; GATED && j < NT; ++j) {
-        const int row = first + j * step;
-        if (row >= T.cnt) break;
-        const int64_t m = T.row0 + row;
-        const float g = v[0][j], u = v[G - 1][j], h = act_fwd(g, p.gate.act) * u;
-        if (n_ok) {
-          if (p.gate.gu) {
-            p.gate.gu[m * 2 * p.N + n] = __float2bfloat16_rn(g);
-            p.gate.gu[m * 2 * p.N + p.N + n] = __float2bfloat16_rn(u);
+            for (int g = 0; g < G; ++g) v[g][j] = v[g][j] * s * sb[g];
           }
-          if (p.gate.h) p.gate.h[m * p.N + n] = __float2bfloat16_rn(h);
         }
-        v[0][j] = h;
-        if (p.gate.q) {  // bit patterns of magnitudes order as the magnitudes, a NaN's above all
-          const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
-          if (lane == 0) S.amax[q][j] = am;
+        if constexpr (!GATED) {
+#pragma unroll
+          for (int j = j0; j < j0 + 8; ++j) {
+            const int row = first + j * step;
+            const int64_t at = (int64_t)(T.row0 + row) * p.N + n;
+            const bool put = n_ok && row < T.cnt;
+            if (put && p.out_f32)
+              static_cast<float*>(p.out)[at] = v[0][j];
+            else if (put)
+              static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v[0][j]);
+          }
+        } else {
+          if (p.gate.gu) {
+#pragma unroll
+            for (int j = j0; j < j0 + 8; ++j) {
+              const int row = first + j * step;
+              __nv_bfloat16* o = p.gate.gu + (int64_t)(T.row0 + row) * 2 * p.N + n;
+              if (n_ok && row < T.cnt) {
+                o[0] = __float2bfloat16_rn(v[0][j]);
+                o[p.N] = __float2bfloat16_rn(v[G - 1][j]);
+              }
+            }
+          }
+#pragma unroll
+          for (int j = j0; j < j0 + 8; ++j) v[0][j] = act_fwd(v[0][j], p.gate.act) * v[G - 1][j];
+          if (p.gate.h) {
+#pragma unroll
+            for (int j = j0; j < j0 + 8; ++j) {
+              const int row = first + j * step;
+              if (n_ok && row < T.cnt) p.gate.h[(int64_t)(T.row0 + row) * p.N + n] = __float2bfloat16_rn(v[0][j]);
+            }
+          }
+          if (p.gate.q) {  // bit patterns of magnitudes order as the magnitudes, a NaN's above all
+#pragma unroll
+            for (int j = j0; j < j0 + 8; ++j) {
+              const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(v[0][j]) & 0x7FFFFFFFu);
+              if (lane == 0) S.amax[q][j] = am;
+            }
+          }
         }
       }
       if (GATED && p.gate.q) {  // N % 128 == 0: the tile's columns are one whole block
         named_bar_sync(1, 128);
         const bool e4 = p.gate.q_fmt == FP8_DT_E4M3;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int row = first + j * step;
-          if (row >= T.cnt) break;
-          const int64_t m = T.row0 + row;
-          const float a = max_nan(__uint_as_float(max(max(S.amax[0][j], S.amax[1][j]), max(S.amax[2][j], S.amax[3][j]))),
-                                  (float)kEps);
-          if (etid == 0) p.gate.inv[m * (p.N / kRows) + T.n0 / kRows] = a * (e4 ? 1.0f / kE4M3Max : 1.0f / kE5M2Max);
-          const float x = v[0][j] * __fdiv_rn(e4 ? kE4M3Max : kE5M2Max, a);
-          p.gate.q[m * p.N + n] =
-              (uint8_t)(e4 ? cvt_fp8x2<FP8_DT_E4M3>(x, 0.f) : cvt_fp8x2<FP8_DT_E5M2>(x, 0.f));
+        for (int j0 = 0; j0 < NT; j0 += 8) {
+          if (first + j0 * step >= T.cnt) break;
+#pragma unroll
+          for (int j = j0; j < j0 + 8; ++j) {
+            const int row = first + j * step;
+            const int64_t m = T.row0 + row;
+            const float a = max_nan(__uint_as_float(max(max(S.amax[0][j], S.amax[1][j]), max(S.amax[2][j], S.amax[3][j]))),
+                                    (float)kEps);
+            const float x = v[0][j] * __fdiv_rn(e4 ? kE4M3Max : kE5M2Max, a);
+            const uint8_t code = (uint8_t)(e4 ? cvt_fp8x2<FP8_DT_E4M3>(x, 0.f) : cvt_fp8x2<FP8_DT_E5M2>(x, 0.f));
+            if (row < T.cnt) {
+              p.gate.q[m * p.N + n] = code;
+              if (etid == 0) p.gate.inv[m * (p.N / kRows) + T.n0 / kRows] = a * (e4 ? 1.0f / kE4M3Max : 1.0f / kE5M2Max);
+            }
+          }
         }
         named_bar_sync(1, 128);  // read before the next tile's are written
       }
