@@ -476,7 +476,7 @@ size_t fp8_moe_tokens_workspace_size(int64_t T, int64_t top_k, int64_t H, int64_
  *  A           FP8 or bf16 [M, K].
  *  B           A's kind, K-major [2 I, K]: rows 0 .. I - 1 are W1 (gate), rows I .. 2 I - 1 W3 (up). With
  *              offsets [E, 2 I, K] (FP8 only), an expert's weights each, and A's rows routed as for
- *              fp8_grouped_mm JAGGED_M (E <= 2048; a bad vector sets FP8_DEV_BAD_OFFSETS). Not e5m2 x e5m2.
+ *              fp8_grouped_mm JAGGED_M (E <= 1024; a bad vector sets FP8_DEV_BAD_OFFSETS). Not e5m2 x e5m2.
  *              K > 0; K % 16 == 0 for FP8, K % 8 for bf16; I % 8 == 0.
  *  sA, sB      FP8: inverse scales fp32, sA [M] or [1], sB [2 I] or [1]; with offsets sA [M], sB [E, 2 I].
  *              With FP8_MM_BLOCKWISE ([B]; K and I multiples of 128) sA [M, K / 128], sB [2 I / 128, K / 128],

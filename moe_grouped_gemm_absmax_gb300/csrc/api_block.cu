@@ -223,7 +223,7 @@ static int check_gated(const fp8_tensor* A, const fp8_tensor* B, const fp8_tenso
     FP8_CHECK(valid_desc(offsets) && offsets->dtype == FP8_DT_I32 && offsets->ndim == 1 && offsets->shape[0] >= 1,
               FP8_ERR_INVALID_ARG);
     E = offsets->shape[0];
-    FP8_CHECK(fp8 && E <= 2048, FP8_ERR_UNSUPPORTED);
+    FP8_CHECK(fp8 && E <= kMaxGatedExperts, FP8_ERR_UNSUPPORTED);
     FP8_CHECK(B->ndim == 3 && B->shape[0] == E, FP8_ERR_INVALID_ARG);
     FP8_CHECK((reinterpret_cast<uintptr_t>(offsets->ptr) & 3u) == 0, FP8_ERR_ALIGNMENT);
   } else {

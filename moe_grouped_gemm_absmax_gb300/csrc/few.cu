@@ -7,7 +7,7 @@
 //  - The weights are the MMA's M side (128 rows a tile; gated: 128 of the gate and the same 128 of the up projection, each
 //    with an accumulator of its own, so that both values of an element meet in one thread), the rows its N: 16, 32 or
 //    64 of them. Experts with more take several tiles.
-//  - Where there are fewer tiles than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's contraction: each leaves its
+//  - Where there are fewer tiles than SMs, a cluster of 2 or 4 CTAs shares a tile's contraction: each leaves its
 //    fp32 sums in shared memory and takes a share of the tile's rows to add them up, in the CTAs' order, so that the
 //    result is the same on every run.
 //  - One K block of 128 a ring stage: the weights' 16 or 32 KB by TMA, past L2's other lines, and the rows' codes.
@@ -30,8 +30,9 @@ namespace {
 constexpr int kRows = 128;  // weight rows of an MMA, output columns of a tile
 constexpr int kBox = kRows * 128;
 constexpr int kThreads = 192, kEpi0 = 2;
-constexpr int kMaxStages = 12, kMaxSplit = 8;
+constexpr int kMaxStages = 12, kMaxSplit = 4;
 constexpr int kSmemMax = 232448;  // 227 KB a CTA
+constexpr int kSmemPair = 115712;  // two CTAs an SM: half of 228 KB less the 1 KB reserved for each
 constexpr int kGroup = 8;         // K blocks whose scales are staged together
 
 struct FewParams {
@@ -489,8 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-#pragma unroll
-          for (int j = j0; j < j0 + 8; ++j) v[0][j] = act_fwd(v[0][j], p.gate.act) * v[G - 1][j];
+          gate_fwd<8>(p.gate.act, v[0] + j0, v[G - 1] + j0, v[0] + j0);
           if (p.gate.h) {
 #pragma unroll
             for (int j = j0; j < j0 + 8; ++j) {
@@ -554,13 +554,19 @@ int run_few(const CUtensorMap& tw, const CUtensorMap& ta, FewParams p, int64_t t
       return FP8_ERR_CUDA;
     done.fetch_or(bit, std::memory_order_release);
   }
-  // fewer tiles than fill the GPU: 2, 4 or 8 CTAs share one's contraction (see the file's comment)
+  // Fewer tiles than SMs: 2 or 4 CTAs share one's contraction, as long as all clusters run at once (one token of 7168 x
+  // 2048, 16 tiles: 21 us alone, 14 in twos, 11 in fours, 18 in eights, of which few fit the GPU at a time; 4096 x
+  // 14336, 112 tiles: 22 and 23, 34 in fours).
   p.split = 1;
-  while (p.split < kMaxSplit && tiles * p.split < 96 && p.nkb >= 4 * p.split) p.split *= 2;
+  while (p.split < kMaxSplit && 2 * tiles * p.split * 16 <= (int64_t)c.sm_count * 15 && p.nkb >= 4 * p.split) p.split *= 2;
   p.stage_bytes = G * kBox + NT * 128;
   const int rest = 1024 + (p.split > 1 ? G * NT * kRows * 4 : 0) + (BLOCK ? 2 * kGroup * G * NT * 4 : 0) +
                    (int)sizeof(Shared) + 8 * (p.E + 1);
-  const int fit = (kSmemMax - rest) / p.stage_bytes;
+  // Where half an SM's shared memory holds four stages or more, the ring takes no more, and the next call's CTAs start
+  // up beside this one's (8 experts of 2048 x 7168, one row each: 25.1 to 23.9 us; three stages of the gated
+  // product in it, 22.6 us for 4096 x 14336, against six alone, 22.0).
+  const int pair = (kSmemPair - rest) / p.stage_bytes;
+  const int fit = pair >= 4 ? pair : (kSmemMax - rest) / p.stage_bytes;
   p.stages = fit < kMaxStages ? fit : kMaxStages;
   const int64_t units = c.sm_count / p.split;
   const int64_t grid = (tiles < units ? tiles : units) * p.split;

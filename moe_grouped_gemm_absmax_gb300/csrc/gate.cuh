@@ -4,34 +4,52 @@
 //   a = 0.044715, because (1 + tanh z) / 2 = s(2 z), which keeps its relative precision where 1 + tanh z cancels.
 //   act'(g) = s + g s (1 - s) w'.
 //   h = act(g) u;  given dh:  dg = dh u act'(g),  du = dh act(g).
-// All in fp32 from the fp32 accumulators, each output rounded once. The exponential and the quotient are the fast
-// ones (2 units in the last place each, and |w| 2^-24 from the argument's rounding): 2^-17 of a value at |w| = 80,
-// below which s underflows; a bf16 result's half step is 2^-9.
+// All in fp32 from the fp32 accumulators, each output rounded once. The exponential and the reciprocal are the approximate
+// instructions (2 units in the last place, and |w| 2^-24 from the argument's rounding): 2^-17 of a value at |w| = 80,
+// below which s underflows to 0; a bf16 result's half step is 2^-9 of it.
 #pragma once
 
 #include "common.cuh"
 
 namespace fp8lin {
 
-FP8_DEVI float logistic(float w) { return __fdividef(1.0f, 1.0f + __expf(-w)); }
+FP8_DEVI float logistic(float w) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(w * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return s;
+}
 
 constexpr float kGelu2C = 1.5957691216057308f, kGeluA = 0.044715f;  // 2 sqrt(2 / pi), a
 
-FP8_DEVI float act_fwd(float g, int act) {
-  const float w = act == FP8_ACT_GELU ? kGelu2C * fmaf(kGeluA * g * g, g, g) : g;
+template <int ACT>
+FP8_DEVI float act_fwd(float g) {
+  const float w = ACT == FP8_ACT_GELU ? kGelu2C * fmaf(kGeluA * g * g, g, g) : g;
   return g * logistic(w);
 }
 // act(g), and its derivative in *d
-FP8_DEVI float act_bwd(float g, int act, float* d) {
+template <int ACT>
+FP8_DEVI float act_bwd(float g, float* d) {
   float w = g, dw = 1.0f;
-  if (act == FP8_ACT_GELU) {
+  if (ACT == FP8_ACT_GELU) {
     const float g2 = kGeluA * g * g;
     w = kGelu2C * fmaf(g2, g, g);
     dw = fmaf(3.0f * kGelu2C, g2, kGelu2C);
   }
   const float s = logistic(w), a = g * s;
-  *d = fmaf(a * (1.0f - s), dw, s);
+  *d = ACT == FP8_ACT_GELU ? fmaf(a * (1.0f - s), dw, s) : fmaf(a, 1.0f - s, s);
   return a;
+}
+// h[0 .. N - 1] = act(g) * u: one branch on the activation for all of them, which leaves their latencies free to overlap
+template <int N>
+FP8_DEVI void gate_fwd(int act, const float* g, const float* u, float* h) {
+  if (act == FP8_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[j] = act_fwd<FP8_ACT_GELU>(g[j]) * u[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) h[j] = act_fwd<FP8_ACT_SILU>(g[j]) * u[j];
+  }
 }
 
 FP8_DEVI uint32_t pack_bf16(float lo, float hi) {
@@ -45,7 +63,7 @@ FP8_DEVI float max_nan(float a, float b) {
   return r;
 }
 
-// 32 values of a row, packed in 16 words, at o, or from there: those in front of column `left`, a multiple of 8 as is
+// 32 values of a row, packed in 16 words, at o: those in front of column `left`, a multiple of 8 as is
 // every row's width, so that a group of 8 is written whole or not at all. wide: rows are 32-byte aligned.
 FP8_DEVI void store_row32(__nv_bfloat16* o, const uint32_t* w, int64_t left, int wide) {
   if (wide && left >= 32) {
@@ -57,34 +75,10 @@ FP8_DEVI void store_row32(__nv_bfloat16* o, const uint32_t* w, int64_t left, int
   for (int j = 0; j < 4; ++j)
     if (8 * j < left) *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
-FP8_DEVI void load_row32(const __nv_bfloat16* o, uint32_t* w, int64_t left, int wide) {
-  if (wide && left >= 32) {
-    ld_v8(o, w);
-    ld_v8(o + 16, w + 8);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (8 * j < left) v = *reinterpret_cast<const uint4*>(o + 8 * j);
-    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-  }
-}
 FP8_DEVI void pack_row32(const float* f, uint32_t* w) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) w[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
 }
-// N fp32 values of a row
-template <int N>
-FP8_DEVI void store_row(__nv_bfloat16* o, const float* f, int64_t left, int wide) {
-#pragma unroll
-  for (int j = 0; j < N; j += 32) {
-    uint32_t w[16];
-    pack_row32(f + j, w);
-    store_row32(o + j, w, left - j, wide);
-  }
-}
-
 // Codes of N values of a row.
 template <int FMT, int N>
 FP8_DEVI void store_codes(uint8_t* o, const float* f, float scale, int wide) {
@@ -107,44 +101,32 @@ FP8_DEVI void store_codes(uint8_t* o, const float* f, float scale, int wide) {
 
 struct GateArgs {
   int act;
-  const __nv_bfloat16* gu_in;  // backward: the projections [M, 2 I]
-  __nv_bfloat16* gu;           // their values [M, 2 I] (forward, may be null), or their gradients (backward)
+  __nv_bfloat16* gu;           // the projections [M, 2 I] (forward, may be null), or their gradients (backward)
   __nv_bfloat16* h;            // [M, I], may be null
   uint8_t* q;                  // h in 8 bits [M, I] with inverse scales [M, I / 128] of its 1 x 128 blocks, may be null
   float* inv;
   int q_fmt;
-  int wide;                    // every row of gu_in, gu, h and q in use starts on 32 bytes
+  int wide;                    // every row of gu, h and q in use starts on 32 bytes
 };
 
-// Backward, 32 columns from n of row m: their projections, loaded ahead, and with dh (fp32) the projections' gradients and
-// h again. gu may be gu_in's own buffer: every value is read by the thread that writes its place, before it does. (The
-// compiler cannot know that they never overlap otherwise, so that the loads are where they are written: all of a chunk's
-// ahead of its stores, and ahead of the wait for its accumulator.)
+// Backward, 32 columns of a row: in c their projections, replaced by the projections' gradients from dh (fp32); h: the
+// hidden layer again.
 struct GuChunk {
   uint32_t g[16], u[16];
 };
-FP8_DEVI void gate_load(const GateArgs& p, GuChunk& c, int64_t m, int64_t n, int64_t I) {
-  const __nv_bfloat16* gi = p.gu_in + m * 2 * I + n;
-  load_row32(gi, c.g, I - n, p.wide);
-  load_row32(gi + I, c.u, I - n, p.wide);
-}
-FP8_DEVI void gate_bwd(const GateArgs& p, const GuChunk& c, const float* dh, int64_t m, int64_t n, int64_t I) {
-  uint32_t dg[16], du[16], h[16];
+template <int ACT>
+FP8_DEVI void gate_bwd(GuChunk& c, const float* dh, uint32_t* h) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float a[2], d[2];
     const float g[2] = {__uint_as_float(c.g[i] << 16), __uint_as_float(c.g[i] & 0xFFFF0000u)};
     const float u[2] = {__uint_as_float(c.u[i] << 16), __uint_as_float(c.u[i] & 0xFFFF0000u)};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) a[k] = act_bwd(g[k], p.act, &d[k]);
-    dg[i] = pack_bf16(dh[2 * i] * u[0] * d[0], dh[2 * i + 1] * u[1] * d[1]);
-    du[i] = pack_bf16(dh[2 * i] * a[0], dh[2 * i + 1] * a[1]);
+    for (int k = 0; k < 2; ++k) a[k] = act_bwd<ACT>(g[k], &d[k]);
+    c.g[i] = pack_bf16(dh[2 * i] * u[0] * d[0], dh[2 * i + 1] * u[1] * d[1]);
+    c.u[i] = pack_bf16(dh[2 * i] * a[0], dh[2 * i + 1] * a[1]);
     h[i] = pack_bf16(a[0] * u[0], a[1] * u[1]);
   }
-  __nv_bfloat16* go = p.gu + m * 2 * I + n;
-  store_row32(go, dg, I - n, p.wide);
-  store_row32(go + I, du, I - n, p.wide);
-  if (p.h) store_row32(p.h + m * I + n, h, I - n, p.wide);
 }
 
 }  // namespace fp8lin

@@ -11,23 +11,24 @@ namespace fp8lin {
 
 namespace {
 
+// Operands; out: the hidden layer (forward) or the projections' gradients; gu: the projections
+struct Maps {
+  CUtensorMap a, b, out, gu;
+};
+
 template <int KIND, int B_MN, int EPI>
-int run_dense(bool pair, const CUtensorMap& ta, const CUtensorMap& tb, const GemmParams& p, const Ctx& c) {
-  CUtensorMap none;
-  memset(&none, 0, sizeof(none));
+int run_dense(bool pair, const Maps& m, const GemmParams& p, const Ctx& c) {
   const int64_t tiles = p.num_m * p.num_n;
   if constexpr (KIND != kBLK)
-    if (pair) return run<KIND, kDense, 0, B_MN, 2, EPI>(ta, tb, none, none, none, p, tiles, c);
-  return run<KIND, kDense, 0, B_MN, 1, EPI>(ta, tb, none, none, none, p, tiles, c);
+    if (pair) return run<KIND, kDense, 0, B_MN, 2, EPI>(m.a, m.b, m.out, m.gu, m.gu, p, tiles, c);
+  return run<KIND, kDense, 0, B_MN, 1, EPI>(m.a, m.b, m.out, m.gu, m.gu, p, tiles, c);
 }
 
 template <int KIND, int EPI>
-int run_experts(bool pair, const CUtensorMap& ta, const CUtensorMap& tb, const GemmParams& p, const Ctx& c) {
-  CUtensorMap none;
-  memset(&none, 0, sizeof(none));
+int run_experts(bool pair, const Maps& m, const GemmParams& p, const Ctx& c) {
   if constexpr (KIND != kBLK)
-    if (pair) return run<KIND, kJagM, 0, 0, 2, EPI>(ta, tb, none, none, none, p, 0, c);
-  return run<KIND, kJagM, 0, 0, 1, EPI>(ta, tb, none, none, none, p, 0, c);
+    if (pair) return run<KIND, kJagM, 0, 0, 2, EPI>(m.a, m.b, m.out, m.gu, m.gu, p, 0, c);
+  return run<KIND, kJagM, 0, 0, 1, EPI>(m.a, m.b, m.out, m.gu, m.gu, p, 0, c);
 }
 
 template <int EPI>
@@ -50,15 +51,14 @@ int launch(const GatedArgs& g, const Ctx& c) {
   p.wait_ns = c.wait_ns;
   p.test_stall = c.test_stall;
   p.gate.act = g.act;
-  p.gate.gu_in = static_cast<const __nv_bfloat16*>(g.gu_in);
   p.gate.gu = static_cast<__nv_bfloat16*>(g.gu);
   p.gate.h = static_cast<__nv_bfloat16*>(g.h);
   p.gate.q = static_cast<uint8_t*>(g.q);
   p.gate.inv = g.inv;
   p.gate.q_fmt = g.q_fmt;
-  p.gate.wide = ((reinterpret_cast<uintptr_t>(g.gu_in) | reinterpret_cast<uintptr_t>(g.gu) | reinterpret_cast<uintptr_t>(g.h) |
+  p.gate.wide = ((reinterpret_cast<uintptr_t>(g.gu) | reinterpret_cast<uintptr_t>(g.h) |
                   reinterpret_cast<uintptr_t>(g.q)) & 31) == 0 && g.I % 16 == 0;
-  if (grouped && (g.E < 1 || g.E > kMaxExperts)) return FP8_ERR_UNSUPPORTED;
+  if (grouped && (g.E < 1 || g.E > kMaxGatedExperts)) return FP8_ERR_UNSUPPORTED;
   const int tn = kForward ? BN / 2 : BN;
   p.num_n = (g.I + tn - 1) / tn;
   p.nkb = (g.K * esz + BKB - 1) / BKB;
@@ -73,36 +73,56 @@ int launch(const GatedArgs& g, const Ctx& c) {
   const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint32_t kbox = (uint32_t)(BKB / esz),  b_rows = kForward ? (g.blockwise ? 64 : 128) : pair ? 128 : 256;
   const uint64_t rows = (uint64_t)(kForward ? 2 * g.I : g.I);
-  CUtensorMap ta, tb;
+  Maps m;
+  memset(&m, 0, sizeof(m));
   {
     const uint64_t d[2] = {(uint64_t)g.K, (uint64_t)g.M}, st[1] = {(uint64_t)(g.K * esz)};
     const uint32_t box[2] = {kbox, BM};
-    FP8_TRY(make_tmap(&ta, g.A, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+    FP8_TRY(make_tmap(&m.a, g.A, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
   }
   if (grouped) {
     const uint64_t d[3] = {(uint64_t)g.K, rows, (uint64_t)g.E}, st[2] = {(uint64_t)g.K, rows * (uint64_t)g.K};
     const uint32_t box[3] = {kbox, b_rows, 1};
-    FP8_TRY(make_tmap(&tb, g.B, dt, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+    FP8_TRY(make_tmap(&m.b, g.B, dt, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
   } else if (g.b_mn) {
     const uint64_t d[2] = {rows, (uint64_t)g.K}, st[1] = {rows * 2};
     const uint32_t box[2] = {64, 64};
-    FP8_TRY(make_tmap(&tb, g.B, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+    FP8_TRY(make_tmap(&m.b, g.B, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
   } else {
     const uint64_t d[2] = {(uint64_t)g.K, rows}, st[1] = {(uint64_t)(g.K * esz)};
     const uint32_t box[2] = {kbox, b_rows};
-    FP8_TRY(make_tmap(&tb, g.B, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+    FP8_TRY(make_tmap(&m.b, g.B, dt, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  }
+  m.out = m.gu = m.a;  // maps without a use are valid ones all the same
+  // boxes of 32 rows x 32 columns of the hidden layer [M, I] and of the projections [M][2][I]
+  const uint64_t I = (uint64_t)g.I;
+  auto gu_map = [&](CUtensorMap* t, const void* base) {
+    const uint64_t d[3] = {I, 2, (uint64_t)g.M}, st[2] = {2 * I, 4 * I};
+    const uint32_t box[3] = {32, 1, 32};
+    return make_tmap(t, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, d, st, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  };
+  if (!kForward) {
+    FP8_TRY(gu_map(&m.gu, g.gu_in));
+    FP8_TRY(gu_map(&m.out, g.gu));
+  } else {
+    if (g.gu) FP8_TRY(gu_map(&m.gu, g.gu));
+    if (g.h) {
+      const uint64_t d[2] = {I, (uint64_t)g.M}, st[1] = {2 * I};
+      const uint32_t box[2] = {32, 32};
+      FP8_TRY(make_tmap(&m.out, g.h, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, st, box, CU_TENSOR_MAP_SWIZZLE_64B));
+    }
   }
   if (!fp8) {
     p.idesc = make_idesc(kFmtBF16, kFmtBF16, 0, (uint32_t)g.b_mn, tile_m, BN);
     if constexpr (!kForward)
-      if (g.b_mn) return run_dense<kBF16, 1, EPI>(pair, ta, tb, p, c);
-    return run_dense<kBF16, 0, EPI>(pair, ta, tb, p, c);
+      if (g.b_mn) return run_dense<kBF16, 1, EPI>(pair, m, p, c);
+    return run_dense<kBF16, 0, EPI>(pair, m, p, c);
   }
   p.idesc = make_idesc(g.a_dtype == FP8_DT_E4M3 ? kFmtE4M3 : kFmtE5M2, g.b_dtype == FP8_DT_E4M3 ? kFmtE4M3 : kFmtE5M2,
                        0, 0, tile_m, BN);
   if (grouped)
-    return g.blockwise ? run_experts<kBLK, EPI>(pair, ta, tb, p, c) : run_experts<kFP8, EPI>(pair, ta, tb, p, c);
-  return g.blockwise ? run_dense<kBLK, 0, EPI>(pair, ta, tb, p, c) : run_dense<kFP8, 0, EPI>(pair, ta, tb, p, c);
+    return g.blockwise ? run_experts<kBLK, EPI>(pair, m, p, c) : run_experts<kFP8, EPI>(pair, m, p, c);
+  return g.blockwise ? run_dense<kBLK, 0, EPI>(pair, m, p, c) : run_dense<kFP8, 0, EPI>(pair, m, p, c);
 }
 
 }  // namespace

@@ -50,6 +50,7 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxExperts = 2048;
 constexpr int64_t kGroupBytes = 32ll << 20;  // rasterization: the A panels of a group of M-blocks, in L2
 constexpr int kStageOut = 4096;  // per epilogue warp: output staging for TMA stores (pairs)
+constexpr int kGateBox = 2048;   // a box of 32 rows x 32 bf16 columns
 // kDenseAmax: the dense schedule whose epilogue also folds max |out| into the side outputs;
 // kDenseQuant: the dense schedule whose epilogue writes the next quantization of the (bf16) result:
 // FP8 codes and 1 x 128 or MX scales along the rows
@@ -71,7 +72,7 @@ enum { kStore = 0, kGate = 1, kGateBwd = 2 };
 // fit in the 512 columns, two accumulators would not. Sixteen epilogue warps (four per lane
 // quarter, 64 columns each) move the accumulator into registers right after the tile's MMAs and
 // release it at once, so the next tile's MMAs wait only for those loads, not for the stores.
-template <int KIND, int CG, int SCHED = 0>
+template <int KIND, int CG, int SCHED = 0, int EPI = kStore>
 struct Cfg {
   // kBLK: two K-block partials, so the MMAs run one K block ahead of the promotion.
   static constexpr int TBN = BN;                          // tile columns
@@ -92,9 +93,13 @@ struct Cfg {
   // so those tiles store through shared memory with TMA (64 KB of staging for 16 warps), which
   // leaves room for 4 stages; the other MX schedules store from registers and keep 5
   static constexpr bool MX_TMA_OUT = KIND == kMX && CG == 2 && SCHED == 2;
-  static constexpr int STAGES = (CG == 2 && !MX_TMA_OUT) ? 5 : 4;
+  // The gated epilogues' stores, and the backward's loads of the projections, pass through shared memory too: boxes of
+  // 32 rows x 32 columns, two a warp, or two of either projection's.
+  static constexpr bool GATE_BOXES = EPI == kGateBwd || (EPI == kGate && KIND != kBLK);
+  static constexpr int STAGES = (CG == 2 && !MX_TMA_OUT ? 5 : 4) - (EPI == kGateBwd || (GATE_BOXES && CG == 1) ? 1 : 0);
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-  static constexpr int OUT_BYTES = (CG == 2 && ((KIND != kMX && KIND != kBLK) || MX_TMA_OUT)) ? EPI_WARPS * kStageOut : 0;
+  static constexpr int OUT_BYTES = GATE_BOXES ? EPI_WARPS * (EPI == kGate ? 2 : 4) * kGateBox
+                                   : (CG == 2 && ((KIND != kMX && KIND != kBLK) || MX_TMA_OUT)) ? EPI_WARPS * kStageOut : 0;
   static constexpr int TILE_M = BM * CG;
   static constexpr int SF_COL0 = NBUF * TBN;             // first scale-factor slot (16 columns each)
 };
@@ -175,6 +180,10 @@ static_assert(sizeof(Shared) <= kSharedBytes, "shared block");
 // consecutive tiles
 struct AmaxShare {
   float a[2][2][128];
+};
+// kGateBwd: a warp's boxes of the projections have landed
+struct BoxBars {
+  uint64_t full[8][2];
 };
 
 FP8_DEVI int find_expert(const int32_t* tpre, int E, int64_t t) {
@@ -262,11 +271,11 @@ FP8_DEVI int64_t tile_nkb(const GemmParams& p, int64_t t, const int32_t* aux) {
 }
 
 template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI>
-__global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmSA,
                 const __grid_constant__ CUtensorMap tmSB, const GemmParams p) {
-  using C = Cfg<KIND, CG, SCHED>;
+  using C = Cfg<KIND, CG, SCHED, EPI>;
   static_assert(KIND != kBLK || CG == 1, "blockwise scaling runs on single CTAs");
   static_assert(C::STAGES <= kMaxStages && C::NBUF <= 4, "ring and accumulator barriers fit the shared block");
   constexpr int STAGES = C::STAGES;
@@ -285,6 +294,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
   uint8_t* rest = smem + C::RING_BYTES + C::OUT_BYTES + kSharedBytes;
   AmaxShare& AS = *reinterpret_cast<AmaxShare*>(rest);  // kGate
   if (EPI == kGate) rest += sizeof(AmaxShare);
+  BoxBars& BB = *reinterpret_cast<BoxBars*>(rest);  // kGateBwd
+  if (EPI == kGateBwd) rest += sizeof(BoxBars);
   int32_t* tpre = reinterpret_cast<int32_t*>(rest);
   int32_t* aux = tpre + (p.E + 1);
   int32_t* pst = kPadRows ? aux + (p.E + 1) : nullptr;  // padded segment starts
@@ -370,11 +381,13 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
     for (int s2 = 0; s2 < STAGES; ++s2) mbar_init(&S.sff[s2], 1);
     mbar_init(&S.sf_drain, 1);
     mbar_init(&S.never, 1);
+    if (EPI == kGateBwd)
+      for (int i = 0; i < 16; ++i) mbar_init(&BB.full[i >> 1][i & 1], 1);
     S.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    if (CG == 2 && EPI == kStore) tma_prefetch_desc(&tmO);
+    if (EPI != kStore || CG == 2) tma_prefetch_desc(&tmO);
     if (KIND == kMX || (kTail && p.tail_t)) {
       tma_prefetch_desc(&tmSA);
       tma_prefetch_desc(&tmSB);
@@ -747,12 +760,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         sb_nx = __ldg(sbp);
       }
     };
-    // kGate: the hidden layer's columns n .. n + W - 1 of row m, from fp32. A row's 128-column block lies in the warps of
+    // kGate: the codes of the hidden layer's columns n .. n + W - 1 of row m. A row's 128-column block lies in the warps of
     // one lane quarter, 64 columns each: they share its largest magnitude through shared memory.
     int amax_buf = 0;
-    auto gate_out = [&](const float* hv, auto width, int64_t m, int64_t n, bool row_ok) {
+    auto gate_codes = [&](const float* hv, auto width, int64_t m, int64_t n, bool row_ok) {
       constexpr int W = decltype(width)::value;
-      if (p.gate.h && row_ok) store_row<W>(p.gate.h + m * p.N + n, hv, p.N - n, p.gate.wide);
       if (!p.gate.q) return;
       float a = 0.0f;
 #pragma unroll
@@ -773,6 +785,132 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
       else
         store_codes<FP8_DT_E5M2, W>(o, hv, __fdiv_rn(kE5M2Max, a), p.gate.wide);
     };
+    // Boxes of 32 rows x 32 columns in shared memory, 64 bytes a row, swizzled (16-byte chunk ^ row / 2 % 4): lane `lane`
+    // reads and writes its own row.
+    uint8_t* box0 = out_stage + (warp - C::EPI0) * ((EPI == kGate ? 2 : 4) * kGateBox);
+    auto box_at = [&](uint8_t* box, int c) {
+      return reinterpret_cast<uint4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+    };
+    auto box_put = [&](uint8_t* box, const uint32_t* w) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) *box_at(box, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    };
+    auto box_get = [&](uint8_t* box, uint32_t* w) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = *box_at(box, c);
+        w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+      }
+    };
+    // kGate: 32 columns from n of the warp's rows: the hidden layer (half < 0) or a projection. Past a segment's end rows
+    // belong to others: such a warp's rows are stored by the lanes that hold them.
+    uint32_t box_seq = 0;
+    auto put32 = [&](const float* f, int half, int64_t m, int64_t n, const Tile& T, bool row_ok) {
+      uint32_t w[16];
+      pack_row32(f, w);
+      const int64_t wrow0 = m - lane;
+      if (C::GATE_BOXES && (SCHED != kJagM || wrow0 + 32 <= T.row_end)) {
+        if (n >= p.N) return;
+        uint8_t* box = box0 + (box_seq++ & 1) * kGateBox;
+        if (lane == 0) bulk_wait_read_1();  // the store before the last one has read this box
+        __syncwarp();
+        box_put(box, w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (half < 0)
+            tma_store_2d(&tmO, box, (int32_t)n, (int32_t)wrow0);
+          else
+            tma_store_3d(&tmSA, box, (int32_t)n, half, (int32_t)wrow0);
+          bulk_commit();
+        }
+      } else if (row_ok) {
+        store_row32(half < 0 ? p.gate.h + m * p.N + n : p.gate.gu + m * 2 * p.N + half * p.N + n, w, p.N - n, p.gate.wide);
+      }
+    };
+    // kGateBwd: the warp's chunks (32 rows x 32 columns of a tile that hold any element of D) in the order of its tiles; the
+    // projections' boxes of two of them are in shared memory or on their way. `ahead` is the next one to ask for.
+    struct Ahead {
+      int64_t t;
+      int32_t m0, n0, row_end;
+      int ch;
+    } ahead = {unit, 0, 0, 0, 0};
+    uint32_t asked = 0, done = 0;
+    bool dead = false;  // a wait ran out: the warp goes on to the next vote
+    auto chunk_live = [&](int32_t m0, int32_t n0, int32_t row_end, int ch) {
+      return m0 + (int32_t)rank * BM + q * 32 < row_end && n0 + c0 + 32 * ch < p.N;
+    };
+    auto seek = [&]() {  // to the next live chunk, from ahead.ch of tile ahead.t on
+      while (ahead.t < total) {
+        if (ahead.ch == 0) {
+          const Tile A = get_tile<SCHED, C::TILE_M, TN>(p, ahead.t, tpre, aux, pst);
+          ahead.m0 = A.m0, ahead.n0 = A.n0, ahead.row_end = A.row_end;
+        }
+        if (ahead.ch < C::WCOLS / 32 && chunk_live(ahead.m0, ahead.n0, ahead.row_end, ahead.ch)) return;
+        ahead.t += n_units, ahead.ch = 0;  // the chunks behind a dead one are dead
+      }
+    };
+    auto ask = [&]() {  // loads of the next chunk into the boxes that chunk asked - 2 had
+      if (ahead.t >= total) return;
+      if (lane == 0) {
+        uint8_t* box = box0 + (asked & 1) * (2 * kGateBox);
+        uint64_t* bar = &BB.full[warp - C::EPI0][asked & 1];
+        mbar_arrive_expect_tx(bar, 2 * kGateBox);
+        const int32_t x = ahead.n0 + c0 + 32 * ahead.ch, y = ahead.m0 + (int32_t)rank * BM + q * 32;
+        tma_load_3d(box, &tmSA, bar, x, 0, y);
+        tma_load_3d(box + kGateBox, &tmSA, bar, x, 1, y);
+      }
+      ++asked;
+      ++ahead.ch;
+      seek();
+    };
+    auto bwd_chunk = [&](const float* dh, const Tile& T, int ch, int64_t m, bool row_ok) {
+      if (!chunk_live(T.m0, T.n0, T.row_end, ch)) return;
+      if (done > 0) {  // the chunk before this one: its boxes have been read by its stores
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        ask();
+      }
+      uint8_t* box = box0 + (done & 1) * (2 * kGateBox);
+      if (!mbar_wait(&BB.full[warp - C::EPI0][done & 1], (done >> 1) & 1, abort_flag, p.wait_ns)) {
+        if (!*abort_flag) fail();
+        dead = true;
+        mbar_wait(&BB.full[warp - C::EPI0][done & 1], (done >> 1) & 1, nullptr, kDrainNs);  // it may still land
+      }
+      ++done;
+      GuChunk c;
+      box_get(box, c.g);
+      box_get(box + kGateBox, c.u);
+      const int64_t n = T.n0 + c0 + 32 * ch, wrow0 = m - lane;
+      const bool boxes = SCHED != kJagM || wrow0 + 32 <= T.row_end;
+      uint32_t h[16];
+      if (p.gate.act == FP8_ACT_GELU)
+        gate_bwd<FP8_ACT_GELU>(c, dh, h);
+      else
+        gate_bwd<FP8_ACT_SILU>(c, dh, h);
+      if (boxes) {
+        box_put(box, c.g);
+        box_put(box + kGateBox, c.u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmO, box, (int32_t)n, 0, (int32_t)wrow0);
+          tma_store_3d(&tmO, box + kGateBox, (int32_t)n, 1, (int32_t)wrow0);
+          bulk_commit();
+        }
+      } else if (row_ok) {
+        __nv_bfloat16* go = p.gate.gu + m * 2 * p.N + n;
+        store_row32(go, c.g, p.N - n, p.gate.wide);
+        store_row32(go + p.N, c.u, p.N - n, p.gate.wide);
+      }
+      if (p.gate.h && row_ok) store_row32(p.gate.h + m * p.N + n, h, p.N - n, p.gate.wide);
+      __syncwarp();
+    };
+    if (EPI == kGateBwd) {
+      seek();
+      ask();
+      ask();
+    }
     // kBLK: the scales of kScGroup K blocks from kb0 on: this lane's row of A, and the 128-column block of B that the
     // warp's columns lie in (kGate: the gate's and the up projection's). Loaded a group ahead, so that no promotion
     // waits for memory.
@@ -885,26 +1023,22 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         if (!live) break;
         if constexpr (EPI == kGate) {
           const int64_t n = T.n0 + c0 / 2;
-          if (p.gate.gu && row_ok) {
-            store_row<WC / 2>(p.gate.gu + m * 2 * p.N + n, acc, p.N - n, p.gate.wide);
-            store_row<WC / 2>(p.gate.gu + m * 2 * p.N + p.N + n, acc + WC / 2, p.N - n, p.gate.wide);
-          }
 #pragma unroll
-          for (int j = 0; j < WC / 2; ++j) acc[j] = act_fwd(acc[j], p.gate.act) * acc[j + WC / 2];
-          gate_out(acc, std::integral_constant<int, WC / 2>(), m, n, row_ok);
+          for (int j = 0; j < WC / 2; j += 32) {
+            if (p.gate.gu) {
+              put32(acc + j, 0, m, n + j, T, row_ok);
+              put32(acc + WC / 2 + j, 1, m, n + j, T, row_ok);
+            }
+            gate_fwd<32>(p.gate.act, acc + j, acc + WC / 2 + j, acc + j);
+            if (p.gate.h) put32(acc + j, -1, m, n + j, T, row_ok);
+          }
+          gate_codes(acc, std::integral_constant<int, WC / 2>(), m, n, row_ok);
           continue;
         }
         if constexpr (EPI == kGateBwd) {
-          if (row_ok) {
-            const int64_t n = T.n0 + c0;
-            GuChunk cu[2];
-            gate_load(p.gate, cu[0], m, n, p.N);
 #pragma unroll
-            for (int ch = 0; ch < WC / 32; ++ch) {
-              if (ch + 1 < WC / 32) gate_load(p.gate, cu[(ch + 1) & 1], m, n + 32 * ch + 32, p.N);
-              gate_bwd(p.gate, cu[ch & 1], acc + 32 * ch, m, n + 32 * ch, p.N);
-            }
-          }
+          for (int ch = 0; ch < WC / 32; ++ch) bwd_chunk(acc + 32 * ch, T, ch, m, row_ok);
+          if (dead) break;
           continue;
         }
         if (row_ok) {
@@ -940,9 +1074,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         }
         continue;
       }
-      GuChunk cu[2];
-      if (EPI == kGateBwd && row_ok) gate_load(p.gate, cu[0], m, T.n0 + c0, p.N);
-      const bool got = mbar_wait(&S.tfull[buf], aphase, abort_flag, p.wait_ns);
+      const bool got = !dead && mbar_wait(&S.tfull[buf], aphase, abort_flag, p.wait_ns);
       if (!named_bar_and(2, kEpiThreads, got)) {  // uniform decision across the epilogue warps
         if (!got && !*abort_flag) fail();
         break;
@@ -1115,24 +1247,21 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
             load32(hc + 32 * ch, hv + 32 * ch);
             load32(128 + hc + 32 * ch, u);
             if (ch == 1) release();
-            if (p.gate.gu && row_ok) {
-              const int64_t nc = n + 32 * ch;
-              store_row<32>(p.gate.gu + m * 2 * p.N + nc, hv + 32 * ch, p.N - nc, p.gate.wide);
-              store_row<32>(p.gate.gu + m * 2 * p.N + p.N + nc, u, p.N - nc, p.gate.wide);
+            if (p.gate.gu) {
+              put32(hv + 32 * ch, 0, m, n + 32 * ch, T, row_ok);
+              put32(u, 1, m, n + 32 * ch, T, row_ok);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) hv[32 * ch + j] = act_fwd(hv[32 * ch + j], p.gate.act) * u[j];
+            gate_fwd<32>(p.gate.act, hv + 32 * ch, u, hv + 32 * ch);
+            if (p.gate.h) put32(hv + 32 * ch, -1, m, n + 32 * ch, T, row_ok);
           }
-          gate_out(hv, std::integral_constant<int, 64>(), m, n, row_ok);
+          gate_codes(hv, std::integral_constant<int, 64>(), m, n, row_ok);
         } else {
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
             float dh[32];
             load32(c0 + 32 * ch, dh);
             if (ch == 3) release();
-            const int64_t n = T.n0 + c0 + 32 * ch;
-            if (row_ok && ch < 3) gate_load(p.gate, cu[(ch + 1) & 1], m, n + 32, p.N);
-            if (row_ok) gate_bwd(p.gate, cu[ch & 1], dh, m, n, p.N);
+            bwd_chunk(dh, T, ch, m, row_ok);
           }
         }
         continue;
@@ -1386,9 +1515,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED>::THREADS, 1)
         aphase ^= 1;
       }
     }
+    if (EPI == kGateBwd)  // loads asked for and not used land before the CTA may exit
+      for (; done < asked; ++done) mbar_wait(&BB.full[warp - C::EPI0][done & 1], (done >> 1) & 1, nullptr, kDrainNs);
   }
 
-  if (CG == 2 && warp >= 2 && warp < 2 + C::EPI_WARPS && lane == 0) bulk_wait_all();  // this warp's stores are done
+  if ((CG == 2 || C::GATE_BOXES) && warp >= C::EPI0 && warp < C::EPI0 + C::EPI_WARPS && lane == 0)
+    bulk_wait_all();  // this warp's stores are done
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_barrier();  // no remote arrive or load into a CTA that has left
@@ -1430,11 +1562,11 @@ template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI = kStore>
 int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const CUtensorMap& sfa,
         const CUtensorMap& sfb, const GemmParams& p, int64_t total_tiles_hint, const Ctx& c) {
   auto kern = gemm_kernel<KIND, SCHED, A_MN, B_MN, CG, EPI>;
-  using C = Cfg<KIND, CG, SCHED>;
+  using C = Cfg<KIND, CG, SCHED, EPI>;
   constexpr int kThreads = C::THREADS;
   const int n_arrays = is_dense(SCHED) ? 0 : (KIND == kMX && SCHED == kJagM) ? 3 : 2;
   const size_t smem = 1024 + C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +
-                     (EPI == kGate ? sizeof(AmaxShare) : 0);
+                     (EPI == kGate ? sizeof(AmaxShare) : EPI == kGateBwd ? sizeof(BoxBars) : 0);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return FP8_ERR_CUDA;
   int64_t units = c.sm_count / CG;

@@ -160,6 +160,7 @@ struct GemmArgs {
 int launch_gemm(const GemmArgs& g, const Ctx& c);
 
 // --- the gated feed-forward's GEMMs (gated.cu) ---
+constexpr int64_t kMaxGatedExperts = 1024;  // offsets, loads and stores share an SM's memory with the ring
 struct GatedArgs {
   const void* A;          // [M, K] FP8 or bf16: the rows (forward), the output's gradient (backward)
   const void* B;          // forward [2 I, K] ([E, 2 I, K]), the gate's rows before the up projection's; backward [I, K]

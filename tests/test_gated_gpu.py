@@ -30,7 +30,7 @@ def _operands(seed, M, K, rows, counts, kind, a_dt=E4, b_dt=E4, a_size=1.0):
 DENSE = [(1, 16, 8), (1, 4096, 1024), (3, 128, 136), (17, 400, 1000), (128, 128, 128), (130, 1040, 264), (300, 2064, 72),
          (2500, 256, 1288), (2048, 512, 1280)]
 EXPERTS = [(1, 128, 128, [0, 1, 0]), (9, 256, 200, [9]), (77, 144, 264, [0, 30, 0, 46, 1]), (300, 512, 512, [129, 0, 171]),
-           (2304, 256, 640, [256, 0, 1, 700, 1300, 47, 0]), (4000, 384, 384, [3999, 1])]
+           (2304, 256, 640, [256, 0, 1, 700, 1300, 47, 0]), (4000, 384, 384, [3999, 1]), (2100, 128, 264, [0] * 1000 + [2000, 77, 23] + [0] * 21)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -280,7 +280,7 @@ def test_gradient_against_differences(fp8):
 # the few rows' kernel: rows of a tile (16, 32, 64), one or several CTAs a tile, ragged and empty experts
 FEW = [(1, 128, 128, None), (1, 7168, 256, None), (16, 2048, 136, None), (17, 1024, 384, None), (32, 4096, 128, None),
        (33, 512, 640, None), (64, 1536, 264, None), (64, 256, 13000, None), (8, 1024, 256, [0, 3, 0, 4, 1]),
-       (64, 512, 200, [1, 0, 40, 23]), (40, 2048, 128, [40]), (64, 384, 384, [1] * 64 + [0] * 200), (5, 640, 2048, [0] * 1999 + [5])]
+       (64, 512, 200, [1, 0, 40, 23]), (40, 2048, 128, [40]), (64, 384, 384, [1] * 64 + [0] * 200), (5, 640, 2048, [0] * 1023 + [5])]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])

@@ -75,7 +75,7 @@ def test_operands(fp8, call):
     assert call(fp8, E=3, off=d(I32, 2)) == INVALID and call(fp8, E=3, off=d(F32, 3)) == INVALID
     assert call(fp8, E=3, B=d(E4M3, rows, 256)) == INVALID and call(fp8, E=3, sA=d(F32, 1)) == INVALID
     assert call(fp8, E=3, sB=d(F32, 1)) == INVALID and call(fp8, E=3, sB=d(F32, 3, rows + 1)) == INVALID
-    assert call(fp8, E=2049) == UNSUPPORTED and call(fp8, E=3, off=d(I32, 0)) == INVALID
+    assert call(fp8, E=1025) == UNSUPPORTED and call(fp8, E=3, off=d(I32, 0)) == INVALID
     assert call(fp8, E=3, off=d(I32, 3, ptr=4098)) == ALIGNMENT
     # blockwise
     assert call(fp8, flags=BLOCK, K=272) == UNSUPPORTED
