@@ -94,9 +94,11 @@ struct Cfg {
   // leaves room for 4 stages; the other MX schedules store from registers and keep 5
   static constexpr bool MX_TMA_OUT = KIND == kMX && CG == 2 && SCHED == 2;
   // The gated epilogues' stores, and the backward's loads of the projections, pass through shared memory too: boxes of
-  // 32 rows x 32 columns, two a warp, or two of either projection's.
+  // 32 rows x 32 columns, two a warp, or two of either projection's. A stage less where they do not fit beside the ring
+  // (the dense backward on pairs with 4 stages: 437 us at 8192 x 14336 x 4096, with 5 400).
   static constexpr bool GATE_BOXES = EPI == kGateBwd || (EPI == kGate && KIND != kBLK);
-  static constexpr int STAGES = (CG == 2 && !MX_TMA_OUT ? 5 : 4) - (EPI == kGateBwd || (GATE_BOXES && CG == 1) ? 1 : 0);
+  static constexpr int STAGES = (CG == 2 && !MX_TMA_OUT ? 5 : 4) -
+                                (GATE_BOXES && (CG == 1 || (EPI == kGateBwd && !is_dense(SCHED))) ? 1 : 0);
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr int OUT_BYTES = GATE_BOXES ? EPI_WARPS * (EPI == kGate ? 2 : 4) * kGateBox
                                    : (CG == 2 && ((KIND != kMX && KIND != kBLK) || MX_TMA_OUT)) ? EPI_WARPS * kStageOut : 0;
@@ -287,8 +289,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
   // FP8 jagged M on pairs: transposed tail tiles, whose row boxes of 32 and 64 rows come in the
   // tmSA and tmSB slots (unused by FP8 operands); 128-row boxes are tmA's own
   constexpr bool kTail = KIND == kFP8 && SCHED == kJagM && CG == 2 && EPI == kStore;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* out_stage = smem + C::RING_BYTES;  // [8 warps][kStageOut], pairs only
   Shared& S = *reinterpret_cast<Shared*>(smem + C::RING_BYTES + C::OUT_BYTES);
   uint8_t* rest = smem + C::RING_BYTES + C::OUT_BYTES + kSharedBytes;
@@ -881,6 +882,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
       GuChunk c;
       box_get(box, c.g);
       box_get(box + kGateBox, c.u);
+      fence_proxy_async_smem();  // these reads come before the next loads' writes to the boxes, which are another proxy's
       const int64_t n = T.n0 + c0 + 32 * ch, wrow0 = m - lane;
       const bool boxes = SCHED != kJagM || wrow0 + 32 <= T.row_end;
       uint32_t h[16];
@@ -1565,7 +1567,7 @@ int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const 
   using C = Cfg<KIND, CG, SCHED, EPI>;
   constexpr int kThreads = C::THREADS;
   const int n_arrays = is_dense(SCHED) ? 0 : (KIND == kMX && SCHED == kJagM) ? 3 : 2;
-  const size_t smem = 1024 + C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +
+  const size_t smem = C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +
                      (EPI == kGate ? sizeof(AmaxShare) : EPI == kGateBwd ? sizeof(BoxBars) : 0);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return FP8_ERR_CUDA;
