@@ -93,8 +93,13 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
   p.ends = g.ends;
   p.E = (int)g.E;
   const bool mx = g.mx != 0;
-  const int tbn = mx ? Cfg<kMX, 1>::TBN : BN;
-  p.num_n = (g.N + tbn - 1) / tbn;
+  int blk_cols = BN;
+  if (g.blockwise && g.mode == FP8_GROUPED_JAGGED_M) {
+    if (g.M <= kFewRows) return launch_few_blockwise(g, c);
+    const int64_t mb = (g.M + BM - 1) / BM + (g.E < g.M ? g.E : g.M) / 2;  // half of the last tiles' rows are empty
+    blk_cols = tile_width(128, c.sm_count, [&](int w) { return mb * ((g.N + w - 1) / w); });
+  }
+  p.num_n = (g.N + blk_cols - 1) / blk_cols;
   const int esz = fp8 ? 1 : 2;
   p.nkb = (g.K * esz + BKB - 1) / BKB;
   p.ldo = g.N;
@@ -108,7 +113,7 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
   const bool pair = !g.blockwise && (g.mode == FP8_GROUPED_JAGGED_M ? g.M >= 2048 : pair_tiles * 2 >= c.sm_count);
   const int tile_m = pair ? 256 : 128;
   p.num_m = (g.M + tile_m - 1) / tile_m;
-  set_walk(p, (int64_t)tile_m * g.K * esz, (int64_t)tbn * g.K * esz);
+  set_walk(p, (int64_t)tile_m * g.K * esz, (int64_t)BN * g.K * esz);
   // the kernels index tiles with 32-bit arithmetic
   const int64_t max_tiles = g.mode == FP8_GROUPED_JAGGED_K ? g.E * p.num_m * p.num_n
                             : g.mode == FP8_GROUPED_JAGGED_M ? (p.num_m + g.E) * p.num_n
@@ -193,11 +198,14 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
       p.total_rows = g.M;
       const uint64_t dB[3] = {(uint64_t)g.K, (uint64_t)g.N, (uint64_t)g.E};
       const uint64_t sB_[2] = {(uint64_t)g.K, (uint64_t)(g.N * g.K)};
-      const uint32_t boxB[3] = {BKB, b_rows, 1};
+      const uint32_t boxB[3] = {BKB, g.blockwise ? (uint32_t)blk_cols : b_rows, 1};
       rc = make_tmap(&tb, g.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dB, sB_, boxB, CU_TENSOR_MAP_SWIZZLE_128B);
       if (rc) return rc;
-      if (g.blockwise && g.M <= kFewRows) return launch_few_blockwise(g, c);
-      if (g.blockwise) return run<kBLK, kJagM, 0, 0, 1>(ta, tb, to, none, none, p, 0, c);
+      if (g.blockwise) {
+        p.idesc = make_idesc(af, bf, 0, 0, tile_m, blk_cols);
+        return blk_cols == 256 ? run<kBLK, kJagM, 0, 0, 1>(ta, tb, to, none, none, p, 0, c)
+                               : run<kBLK, kJagM, 0, 0, 1, kStore, 128>(ta, tb, to, none, none, p, 0, c);
+      }
       if (!pair) return run<kFP8, kJagM, 0, 0, 1>(ta, tb, to, none, none, p, 0, c);
       // An expert's last tile with fewer than 256 rows runs transposed: the expert's 256 weight
       // rows as the MMA's M, the tile's rows rounded up to 16 as its N, and only the row boxes

@@ -50,6 +50,9 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxExperts = 2048;
 constexpr int64_t kGroupBytes = 32ll << 20;  // rasterization: the A panels of a group of M-blocks, in L2
 constexpr int kStageOut = 4096;  // per epilogue warp: output staging for TMA stores (pairs)
+constexpr int kMaxStages = 6;    // ring stages the barrier arrays hold
+constexpr int kSharedBytes = 2304;
+constexpr int kSmemMax = 232448;  // 227 KB a CTA
 constexpr int kGateBox = 2048;   // a box of 32 rows x 32 bf16 columns
 // kDenseAmax: the dense schedule whose epilogue also folds max |out| into the side outputs;
 // kDenseQuant: the dense schedule whose epilogue writes the next quantization of the (bf16) result:
@@ -72,10 +75,10 @@ enum { kStore = 0, kGate = 1, kGateBwd = 2 };
 // fit in the 512 columns, two accumulators would not. Sixteen epilogue warps (four per lane
 // quarter, 64 columns each) move the accumulator into registers right after the tile's MMAs and
 // release it at once, so the next tile's MMAs wait only for those loads, not for the stores.
-template <int KIND, int CG, int SCHED = 0, int EPI = kStore>
+template <int KIND, int CG, int SCHED = 0, int EPI = kStore, int NT = BN>
 struct Cfg {
   // kBLK: two K-block partials, so the MMAs run one K block ahead of the promotion.
-  static constexpr int TBN = BN;                          // tile columns
+  static constexpr int TBN = NT;                          // tile columns (less than 256 on single CTAs: tile_width)
     static constexpr int NBUF = KIND == kMX ? 1 : 2;        // accumulators / K-block partials
   static constexpr int EPI_WARPS = KIND == kMX ? 16 : 8;
   static constexpr int EPI_THREADS = 32 * EPI_WARPS;
@@ -94,14 +97,18 @@ struct Cfg {
   // leaves room for 4 stages; the other MX schedules store from registers and keep 5
   static constexpr bool MX_TMA_OUT = KIND == kMX && CG == 2 && SCHED == 2;
   // The gated epilogues' stores, and the backward's loads of the projections, pass through shared memory too: boxes of
-  // 32 rows x 32 columns, two a warp, or two of either projection's. A stage less where they do not fit beside the ring
-  // (the dense backward on pairs with 4 stages: 437 us at 8192 x 14336 x 4096, with 5 400).
+  // 32 rows x 32 columns, two a warp, or two of either projection's.
   static constexpr bool GATE_BOXES = EPI == kGateBwd || (EPI == kGate && KIND != kBLK);
-  static constexpr int STAGES = (CG == 2 && !MX_TMA_OUT ? 5 : 4) -
-                                (GATE_BOXES && (CG == 1 || (EPI == kGateBwd && !is_dense(SCHED))) ? 1 : 0);
-  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr int OUT_BYTES = GATE_BOXES ? EPI_WARPS * (EPI == kGate ? 2 : 4) * kGateBox
                                    : (CG == 2 && ((KIND != kMX && KIND != kBLK) || MX_TMA_OUT)) ? EPI_WARPS * kStageOut : 0;
+  // Gated and blockwise: as many stages as fit beside that, the barriers and the experts' offsets (the dense backward on
+  // pairs with 4 stages: 437 us at 8192 x 14336 x 4096, with 5 400)
+  static constexpr int FIT = (kSmemMax - kSharedBytes - OUT_BYTES - (EPI == kGate ? 2048 : EPI == kGateBwd ? 128 : 0) -
+                              (SCHED == 0 ? 0 : EPI == kStore ? 8 * (kMaxExperts + 1) : 8 * ((int)kMaxGatedExperts + 1))) /
+                             STAGE_BYTES;
+  static constexpr int STAGES = EPI != kStore || KIND == kBLK ? (FIT < kMaxStages ? FIT : kMaxStages)
+                                : (CG == 2 && !MX_TMA_OUT ? 5 : 4);
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr int TILE_M = BM * CG;
   static constexpr int SF_COL0 = NBUF * TBN;             // first scale-factor slot (16 columns each)
 };
@@ -157,7 +164,6 @@ struct Tile {
   int64_t pm0;      // m0 in the segment-padded row space of the MX A scales (jagged M), else m0
 };
 
-constexpr int kMaxStages = 5;  // ring stages the barrier arrays below hold
 struct Shared {
   float sb[2][BN];  // per-tile column scales, alternating between consecutive tiles
   uint64_t full[kMaxStages];
@@ -171,7 +177,6 @@ struct Shared {
   uint32_t tmem_base;
   int abort;
 };
-constexpr int kSharedBytes = 2304;
 // kBLK: K blocks whose scales a promoting lane loads together, one group ahead
 constexpr int kScGroup = 4;
 // kBLK: registers a thread of the four warps that issue and of the eight that promote: 128 x 40 + 256 x 232 = 384 x 168,
@@ -272,12 +277,12 @@ FP8_DEVI int64_t tile_nkb(const GemmParams& p, int64_t t, const int32_t* aux) {
   return (aux[e + 1] - aux[e]) / BKB;
 }
 
-template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI>
-__global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
+template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI, int NT>
+__global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmSA,
                 const __grid_constant__ CUtensorMap tmSB, const GemmParams p) {
-  using C = Cfg<KIND, CG, SCHED, EPI>;
+  using C = Cfg<KIND, CG, SCHED, EPI, NT>;
   static_assert(KIND != kBLK || CG == 1, "blockwise scaling runs on single CTAs");
   static_assert(C::STAGES <= kMaxStages && C::NBUF <= 4, "ring and accumulator barriers fit the shared block");
   constexpr int STAGES = C::STAGES;
@@ -470,11 +475,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
             } else if (KIND == kFP8 || KIND == kBLK) {
               const int32_t kx = (int32_t)(T.k0 + kb * BKB);
               tma_load_2d(sa, &tmA, fb, kx, am);
-              // kGate: boxes of 128 rows, the up projection's after the gate's (kBLK: of 64, one after the other)
+              // kGate: the up projection's rows after the gate's (kBLK: either half of them)
               constexpr int kBoxes = EPI == kGate ? (KIND == kBLK ? 4 : 2) : 1;
 #pragma unroll
               for (int h = 0; h < kBoxes; ++h) {
-                const int32_t r = bn + (h & 1) * (int32_t)p.N + h / 2 * 64;
+                const int32_t r = bn + (h & 1) * (int32_t)p.N + h / 2 * (TBN / 4);
                 if (SCHED == kJagM)
                   tma_load_3d(sb + h * (C::B_BYTES / kBoxes), &tmB, fb, kx, r, T.e);
                 else
@@ -755,8 +760,9 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
           sa_nx = p.sa_scalar ? __ldg(p.sA) : __ldg(p.sA + m);
       }
       if (stage_sb) {
-        const int64_t n = Tn.n0 + (EPI == kGate ? etid & 127 : etid);
-        sb_nx = n < p.N ? __ldg(sbp + n + (EPI == kGate && etid >= 128 ? p.N : 0)) : 0.0f;
+        const int part = EPI == kGate ? etid / TN : 0;  // kGate: the gate's columns, then the up projection's
+        const int64_t n = Tn.n0 + etid - part * TN;
+        sb_nx = n < p.N && part < 2 ? __ldg(sbp + n + part * p.N) : 0.0f;
       } else {
         sb_nx = __ldg(sbp);
       }
@@ -766,7 +772,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
     int amax_buf = 0;
     auto gate_codes = [&](const float* hv, auto width, int64_t m, int64_t n, bool row_ok) {
       constexpr int W = decltype(width)::value;
-      if (!p.gate.q) return;
+      if (W < 64 || !p.gate.q) return;  // codes: tiles of whole blocks
       float a = 0.0f;
 #pragma unroll
       for (int j = 0; j < W; ++j) a = max_nan(a, fabsf(hv[j]));
@@ -920,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
     auto load_scales = [&](const Tile& T, int32_t kb0) {
       const int64_t KB = p.nkb, r = (int64_t)T.m0 + row;
       const int64_t blocks = (EPI == kGate ? 2 * p.N : p.N + 127) / 128;
-      const int64_t nb = T.n0 / 128 + (EPI == kGate ? 0 : c0 / 128);
+      const int64_t nb = (T.n0 + (EPI == kGate ? 0 : c0)) / 128;
       const float* a = p.sA + r * KB;
       const float* b = p.sB + ((int64_t)T.e * blocks + nb) * KB;
 #pragma unroll
@@ -961,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
         // promotion: for every K block, this warp's half of the partial into registers, the partial back to the MMAs,
         // acc += partial * sA[m, kb] * sB[n / 128, kb]. The next 16 columns are on their way while these are added.
         constexpr int WC = C::WCOLS;
-        static_assert(WC == 128, "a warp promotes 128 columns");
+        static_assert(WC % 32 == 0 && WC <= 128, "a warp's columns, in one block of B's scales");
         float acc[WC];
 #pragma unroll
         for (int j = 0; j < WC; ++j) acc[j] = 0.0f;
@@ -1208,7 +1214,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
         continue;
       }
       if constexpr (EPI != kStore) {
-        // kGate: 64 columns of the hidden layer, in two chunks of 32 from either half of the accumulator. kGateBwd: 128
+        // kGate: the warp's columns of the hidden layer, 32 at a time, from either half of the accumulator. kGateBwd: its
         // columns of the hidden layer's gradient.
         const float2 sa2 = make_float2(sa, sa);
         auto load32 = [&](int col, float* f) {  // 32 tile columns, scaled
@@ -1240,15 +1246,16 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
           }
         };
         if constexpr (EPI == kGate) {
-          const int hc = c0 / 2;  // the warp's first column of the tile's 128
+          const int hc = c0 / 2;  // the warp's first column of the hidden layer's
           const int64_t n = T.n0 + hc;
-          float hv[64];
+          constexpr int W = C::WCOLS / 2;
+          float hv[W];
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
+          for (int ch = 0; ch < W / 32; ++ch) {
             float u[32];
             load32(hc + 32 * ch, hv + 32 * ch);
-            load32(128 + hc + 32 * ch, u);
-            if (ch == 1) release();
+            load32(TN + hc + 32 * ch, u);
+            if (ch + 1 == W / 32) release();
             if (p.gate.gu) {
               put32(hv + 32 * ch, 0, m, n + 32 * ch, T, row_ok);
               put32(u, 1, m, n + 32 * ch, T, row_ok);
@@ -1256,13 +1263,13 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI>::THREADS, 1)
             gate_fwd<32>(p.gate.act, hv + 32 * ch, u, hv + 32 * ch);
             if (p.gate.h) put32(hv + 32 * ch, -1, m, n + 32 * ch, T, row_ok);
           }
-          gate_codes(hv, std::integral_constant<int, 64>(), m, n, row_ok);
+          gate_codes(hv, std::integral_constant<int, W>(), m, n, row_ok);
         } else {
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
+          for (int ch = 0; ch < C::WCOLS / 32; ++ch) {
             float dh[32];
             load32(c0 + 32 * ch, dh);
-            if (ch == 3) release();
+            if (ch + 1 == C::WCOLS / 32) release();
             bwd_chunk(dh, T, ch, m, row_ok);
           }
         }
@@ -1560,11 +1567,28 @@ void set_walk(GemmParams& p, int64_t pa, int64_t pb) {
   p.group_n = by_n < by_m ? gn : 0;
 }
 
-template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI = kStore>
+// Columns of a tile on single CTAs: 256, or 128 or 64 (least) of them where that takes fewer or shorter rounds of CTAs.
+// A narrower tile's K blocks and its epilogue take less time, not in proportion: kCost (100 rows, K 4096, 2048 columns of
+// the hidden layer in bf16: the backward in 28.7, 22.6 and 19.5 us at 256, 128 and 64 columns, the forward in 24.4 and
+// 20.6; but where 256 take one round and 128 two, 37.9 and 53.4). tiles(width): their number.
+template <typename F>
+int tile_width(int least, int sm_count, F tiles) {
+  constexpr int kWidth[3] = {256, 128, 64};
+  constexpr float kCost[3] = {1.0f, 0.78f, 0.62f};
+  int best = 256;
+  float cost = 0.0f;
+  for (int i = 0; i < 3 && kWidth[i] >= least; ++i) {
+    const float c = (float)((tiles(kWidth[i]) + sm_count - 1) / sm_count) * kCost[i];
+    if (i == 0 || c < cost) best = kWidth[i], cost = c;
+  }
+  return best;
+}
+
+template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI = kStore, int NT = BN>
 int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const CUtensorMap& sfa,
         const CUtensorMap& sfb, const GemmParams& p, int64_t total_tiles_hint, const Ctx& c) {
-  auto kern = gemm_kernel<KIND, SCHED, A_MN, B_MN, CG, EPI>;
-  using C = Cfg<KIND, CG, SCHED, EPI>;
+  auto kern = gemm_kernel<KIND, SCHED, A_MN, B_MN, CG, EPI, NT>;
+  using C = Cfg<KIND, CG, SCHED, EPI, NT>;
   constexpr int kThreads = C::THREADS;
   const int n_arrays = is_dense(SCHED) ? 0 : (KIND == kMX && SCHED == kJagM) ? 3 : 2;
   const size_t smem = C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +

@@ -28,8 +28,9 @@ def _operands(seed, M, K, rows, counts, kind, a_dt=E4, b_dt=E4, a_size=1.0):
 
 # (M, K, I, counts by expert or None)
 DENSE = [(1, 16, 8), (1, 4096, 1024), (3, 128, 136), (17, 400, 1000), (128, 128, 128), (130, 1040, 264), (300, 2064, 72),
-         (2500, 256, 1288), (2048, 512, 1280)]
-EXPERTS = [(1, 128, 128, [0, 1, 0]), (9, 256, 200, [9]), (77, 144, 264, [0, 30, 0, 46, 1]), (300, 512, 512, [129, 0, 171]),
+         (2500, 256, 1288), (2048, 512, 1280),
+         (1200, 256, 1920), (1200, 128, 3840), (250, 64, 9600), (250, 64, 19200), (200, 512, 2048)]
+EXPERTS = [(1500, 256, 1408, [700, 0, 800]), (1500, 128, 2816, [1, 1400, 99]), (1, 128, 128, [0, 1, 0]), (9, 256, 200, [9]), (77, 144, 264, [0, 30, 0, 46, 1]), (300, 512, 512, [129, 0, 171]),
            (2304, 256, 640, [256, 0, 1, 700, 1300, 47, 0]), (4000, 384, 384, [3999, 1]), (2100, 128, 264, [0] * 1000 + [2000, 77, 23] + [0] * 21)]
 
 

@@ -16,7 +16,7 @@ def fp8():
 
 FEW = [([0, 0, 1], 7168, 128), ([16], 2048, 520), ([1] * 17, 1024, 128), ([33], 4096, 264), ([0, 40, 0, 24], 512, 1000),
        ([64], 384, 7168), ([2, 0] * 16, 1152, 384), ([0] * 2000 + [3], 640, 136)]
-CASES = FEW + [([1], 128, 8), ([0, 1, 0], 256, 128), ([8] * 1, 2048, 7168), ([3, 0, 0, 5], 384, 200), ([1] * 9, 1024, 520),
+CASES = FEW + [([1900], 256, 2560), ([100] * 9, 512, 1300), ([1], 128, 8), ([0, 1, 0], 256, 128), ([8] * 1, 2048, 7168), ([3, 0, 0, 5], 384, 200), ([1] * 9, 1024, 520),
          ([17, 33, 0, 64, 65], 512, 264), ([129, 0, 171], 640, 1000), ([0, 0, 0, 700], 256, 129 * 8),
          ([256, 0, 1, 700, 1300, 47, 0], 256, 640), ([1, 2, 4000], 384, 384), ([2] * 300, 128, 136), ([64, 64], 7168, 24)]
 
