@@ -480,7 +480,8 @@ size_t fp8_moe_tokens_workspace_size(int64_t T, int64_t top_k, int64_t H, int64_
  *              K > 0; K % 16 == 0 for FP8, K % 8 for bf16; I % 8 == 0.
  *  sA, sB      FP8: inverse scales fp32, sA [M] or [1], sB [2 I] or [1]; with offsets sA [M], sB [E, 2 I].
  *              With FP8_MM_BLOCKWISE ([B]; K and I multiples of 128) sA [M, K / 128], sB [2 I / 128, K / 128],
- *              [E, 2 I / 128, K / 128] with offsets. MX scales: FP8_ERR_UNSUPPORTED. NULL for bf16.
+ *              [E, 2 I / 128, K / 128] with offsets. 4-byte aligned. MX scales: FP8_ERR_UNSUPPORTED. NULL for
+ *              bf16.
  *  act         FP8_ACT_SILU or FP8_ACT_GELU. flags: FP8_MM_BLOCKWISE (FP8_MM_FAST_ACCUM changes nothing).
  *  h           bf16 [M, I] or NULL: h rounded once.
  *  gu          bf16 [M, 2 I] or NULL: g, and beside it u, rounded once (for the backward pass).

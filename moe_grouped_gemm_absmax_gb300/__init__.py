@@ -463,6 +463,14 @@ def gated_mm_alloc(A, B, sA=None, sB=None, offsets=None, act=ACT_SILU, flags=0, 
     return h, gu, q, inv
 
 
+def gated_mm_bwd_alloc(dy, B, sdy, sB, gu, offsets=None, act=ACT_SILU, flags=0, want_h=False, status=None, stream=None):
+    """Returns (dgu, h), h None unless asked for."""
+    dgu = torch.empty_like(gu)
+    h = torch.empty((gu.shape[0], gu.shape[1] // 2), dtype=gu.dtype, device=gu.device) if want_h else None
+    fp8_gated_mm_bwd(dy, B, sdy, sB, gu, dgu, h, offsets, act, flags, status, stream)
+    return dgu, h
+
+
 def quantize_alloc(x, granularity, out_dtype, layout=None, offsets=None, padded_rows=None, status=None,
                    stream=None):
     """Returns (out or None, out_t or None, inv_scales). Shapes follow include/fp8lin.h."""

@@ -9,10 +9,11 @@ them into autograd. No bias: the pages' hot path is the bias-free matmul, and a 
 non-FP8 step."""
 import torch
 
-from . import (GRAN_BLOCK_1x128, GRAN_MX, GRAN_ROW, GRAN_TENSOR, MM_FAST_ACCUM, OP_LINEAR_BWD, OP_LINEAR_FWD,
-               SCORE_BIASED, SCORE_SOFTMAX, WGRAD_BF16, WGRAD_FP8, add_rmsnorm_alloc, fp8_add_rmsnorm_bwd, fp8_linear_bwd,
-               fp8_linear_fwd, fp8_moe_route_bwd, fp8_workspace_size, linear_saved_alloc, make_saved, moe_route_alloc,
-               rmsnorm_bwd_workspace)
+from . import (ACT_SILU, DT_E4M3, DT_E5M2, GRAN_BLOCK_1x128, GRAN_COL, GRAN_MX, GRAN_ROW, GRAN_TENSOR, LAYOUT_COL_MAJOR,
+               MM_A_MN_MAJOR, MM_B_MN_MAJOR, MM_BLOCKWISE, MM_FAST_ACCUM, OP_LINEAR_BWD, OP_LINEAR_FWD, SCORE_BIASED,
+               SCORE_SOFTMAX, WGRAD_BF16, WGRAD_FP8, add_rmsnorm_alloc, blk_quantize_alloc, fp8_add_rmsnorm_bwd,
+               fp8_linear_bwd, fp8_linear_fwd, fp8_moe_route_bwd, fp8_scaled_mm, fp8_workspace_size, gated_mm_alloc,
+               gated_mm_bwd_alloc, linear_saved_alloc, make_saved, moe_route_alloc, quantize_alloc, rmsnorm_bwd_workspace)
 
 
 def _workspace(nbytes, device):
@@ -179,3 +180,104 @@ class MoERouteFunction(torch.autograd.Function):
         dlogits = torch.empty_like(logits)
         fp8_moe_route_bwd(logits, ids, dweights.float().contiguous(), dlogits, *ctx.args)
         return _once(dlogits, None, None, None, None, None)
+
+
+def _mm(a, b, sa=None, sb=None, flags=0):
+    """a b^T in bf16; with flags' MN-major layouts a [K, M], b [K, N]."""
+    M = a.shape[1] if flags & MM_A_MN_MAJOR else a.shape[0]
+    N = b.shape[1] if flags & MM_B_MN_MAJOR else b.shape[0]
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    fp8_scaled_mm(a, b, sa, sb, out, flags)
+    return out
+
+
+class GatedMLPFunction(torch.autograd.Function):
+    """y = W2 (act(W1 x) * (W3 x)) in FP8: x [..., H] bf16, w13 bf16 [2 I, H] (W1 above W3), w2 bf16 [H, I] -> y [..., H]
+    bf16. Scales per row, or with GRAN_BLOCK_1x128 per 1 x 128 of the activations and 128 x 128 of the weights (H and I
+    multiples of 128). The forward keeps x and both projections in bf16; the backward makes the hidden layer again, takes
+    dY and the projections' gradients in e5m2, and the weight gradients in bf16."""
+
+    @staticmethod
+    def forward(ctx, x, w13, w2, granularity=GRAN_ROW, act=ACT_SILU):
+        if any(t.dtype != torch.bfloat16 for t in (x, w13, w2)):
+            raise TypeError("GatedMLPFunction takes bf16 x, w13 and w2")
+        if granularity not in (GRAN_ROW, GRAN_BLOCK_1x128):
+            raise ValueError("GatedMLPFunction takes GRAN_ROW or GRAN_BLOCK_1x128")
+        x2, w13, w2 = x.reshape(-1, x.shape[-1]).contiguous(), w13.contiguous(), w2.contiguous()
+        if granularity == GRAN_ROW:
+            xq, _, xi = quantize_alloc(x2, GRAN_ROW, DT_E4M3)
+            wq, _, wi = quantize_alloc(w13, GRAN_ROW, DT_E4M3)
+            h, gu, _, _ = gated_mm_alloc(xq, wq, xi, wi, act=act, want_gu=True)
+            hq, _, hi = quantize_alloc(h, GRAN_ROW, DT_E4M3)
+            wq, _, wi = quantize_alloc(w2, GRAN_ROW, DT_E4M3)
+            y = _mm(hq, wq, hi, wi)
+        else:
+            xq, _, xi, _ = blk_quantize_alloc(x2, DT_E4M3)
+            wq, _, wi, _ = blk_quantize_alloc(w13, DT_E4M3, tile128=True)
+            _, gu, hq, hi = gated_mm_alloc(xq, wq, xi, wi, act=act, flags=MM_BLOCKWISE, want_h=False, want_gu=True,
+                                           q_dtype=DT_E4M3)
+            wq, _, wi, _ = blk_quantize_alloc(w2, DT_E4M3, tile128=True)
+            y = _mm(hq, wq, hi, wi, MM_BLOCKWISE)
+        ctx.save_for_backward(x2, w13, w2, gu)
+        ctx.granularity, ctx.act, ctx.x_shape = granularity, act, x.shape
+        return y.reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, w13, w2, gu = ctx.saved_tensors
+        need_x, need_13, need_2 = ctx.needs_input_grad[:3]
+        dy2 = dy.reshape(x2.shape).to(torch.bfloat16).contiguous()
+        row = ctx.granularity == GRAN_ROW
+
+        def left(t):  # gradients, the GEMM's left operand
+            if row:
+                q, _, inv = quantize_alloc(t, GRAN_ROW, DT_E5M2)
+                return q, inv
+            q, _, inv, _ = blk_quantize_alloc(t, DT_E5M2)
+            return q, inv
+
+        def transposed(w):  # a weight, its transpose the right operand
+            if row:
+                _, q, inv = quantize_alloc(w, GRAN_COL, DT_E4M3)
+                return q, inv
+            _, q, _, inv = blk_quantize_alloc(w, DT_E4M3, tile128=True, layout=LAYOUT_COL_MAJOR)
+            return q, inv
+
+        flags = 0 if row else MM_BLOCKWISE
+        dx = dw13 = None
+        outer = MM_A_MN_MAJOR | MM_B_MN_MAJOR  # sums over the rows
+        dyq, sdy = left(dy2)
+        wq, wi = transposed(w2)
+        dgu, h = gated_mm_bwd_alloc(dyq, wq, sdy, wi, gu, act=ctx.act, flags=flags, want_h=need_2)
+        dw2 = _mm(dy2, h, flags=outer) if need_2 else None
+        if need_13:
+            dw13 = _mm(dgu, x2, flags=outer)
+        if need_x:
+            dq, sd = left(dgu)
+            wq, wi = transposed(w13)
+            dx = _mm(dq, wq, sd, wi, flags).reshape(ctx.x_shape)
+        return _once(dx, dw13, dw2, None, None)
+
+
+class Fp8GatedMLP(torch.nn.Module):
+    """The gated feed-forward of a transformer layer, y = W2 (act(W1 x) * (W3 x)), with bf16 weights w13 [2 I, H] and w2
+    [H, I] and its products in FP8 (GatedMLPFunction)."""
+
+    def __init__(self, hidden, inner, granularity=GRAN_ROW, act=ACT_SILU, device=None):
+        super().__init__()
+        if hidden % 16 or inner % 16:
+            raise ValueError("FP8 GEMM operands need hidden and inner divisible by 16")
+        if granularity == GRAN_BLOCK_1x128 and (hidden % 128 or inner % 128):
+            raise ValueError("block scales need hidden and inner divisible by 128")
+        self.granularity, self.act = granularity, act
+        self.w13 = torch.nn.Parameter(torch.empty((2 * inner, hidden), dtype=torch.bfloat16, device=device))
+        self.w2 = torch.nn.Parameter(torch.empty((hidden, inner), dtype=torch.bfloat16, device=device))
+        for w in (self.w13, self.w2):
+            torch.nn.init.kaiming_uniform_(w, a=5 ** 0.5)
+
+    def forward(self, x):
+        return GatedMLPFunction.apply(x.to(torch.bfloat16), self.w13, self.w2, self.granularity, self.act)
+
+    def extra_repr(self):
+        g = {GRAN_ROW: "row", GRAN_BLOCK_1x128: "blockwise"}[self.granularity]
+        return f"hidden={self.w13.shape[1]}, inner={self.w2.shape[1]}, scaling={g}, act={'silu' if self.act == ACT_SILU else 'gelu'}"

@@ -62,7 +62,7 @@ def test_operands(fp8, call):
     assert call(fp8, B=d(E4M3, 1 << 40, 256)) == UNSUPPORTED
     assert call(fp8, sA=None) == INVALID and call(fp8, sB=None) == INVALID
     assert call(fp8, sA=d(F32, 5)) == INVALID and call(fp8, sB=d(F32, rows + 1)) == INVALID
-    assert call(fp8, sA=d(F32, 4, ptr=4100)) == ALIGNMENT and call(fp8, sB=d(F32, rows, ptr=4100)) == ALIGNMENT
+    assert call(fp8, sA=d(F32, 4, ptr=4098)) == ALIGNMENT and call(fp8, sB=d(F32, rows, ptr=4098)) == ALIGNMENT
     assert call(fp8, sA=d(E8M0, 1024), sB=d(E8M0, 1024)) == UNSUPPORTED  # MX scales
     assert call(fp8, sA=d(BF16, 4)) == INVALID
     # bf16
