@@ -195,7 +195,8 @@ class GatedMLPFunction(torch.autograd.Function):
     """y = W2 (act(W1 x) * (W3 x)) in FP8: x [..., H] bf16, w13 bf16 [2 I, H] (W1 above W3), w2 bf16 [H, I] -> y [..., H]
     bf16. Scales per row, or with GRAN_BLOCK_1x128 per 1 x 128 of the activations and 128 x 128 of the weights (H and I
     multiples of 128). The forward keeps x and both projections in bf16; the backward makes the hidden layer again, takes
-    dY and the projections' gradients in e5m2, and the weight gradients in bf16."""
+    dY and the projections' gradients in e5m2, and the weight gradients in bf16. (A backward pass is captured into a CUDA
+    graph only while no eager graph of the same weights lives: torch's own rule.)"""
 
     @staticmethod
     def forward(ctx, x, w13, w2, granularity=GRAN_ROW, act=ACT_SILU):
@@ -204,6 +205,10 @@ class GatedMLPFunction(torch.autograd.Function):
         if granularity not in (GRAN_ROW, GRAN_BLOCK_1x128):
             raise ValueError("GatedMLPFunction takes GRAN_ROW or GRAN_BLOCK_1x128")
         x2, w13, w2 = x.reshape(-1, x.shape[-1]).contiguous(), w13.contiguous(), w2.contiguous()
+        ctx.granularity, ctx.act, ctx.x_shape = granularity, act, x.shape
+        if x2.shape[0] == 0:  # nothing to quantize
+            ctx.save_for_backward(x2, w13, w2, x2)
+            return torch.empty_like(x)
         if granularity == GRAN_ROW:
             xq, _, xi = quantize_alloc(x2, GRAN_ROW, DT_E4M3)
             wq, _, wi = quantize_alloc(w13, GRAN_ROW, DT_E4M3)
@@ -219,13 +224,15 @@ class GatedMLPFunction(torch.autograd.Function):
             wq, _, wi, _ = blk_quantize_alloc(w2, DT_E4M3, tile128=True)
             y = _mm(hq, wq, hi, wi, MM_BLOCKWISE)
         ctx.save_for_backward(x2, w13, w2, gu)
-        ctx.granularity, ctx.act, ctx.x_shape = granularity, act, x.shape
         return y.reshape(x.shape)
 
     @staticmethod
     def backward(ctx, dy):
         x2, w13, w2, gu = ctx.saved_tensors
         need_x, need_13, need_2 = ctx.needs_input_grad[:3]
+        if x2.shape[0] == 0:
+            return _once(torch.empty_like(dy) if need_x else None, torch.zeros_like(w13) if need_13 else None,
+                         torch.zeros_like(w2) if need_2 else None, None, None)
         dy2 = dy.reshape(x2.shape).to(torch.bfloat16).contiguous()
         row = ctx.granularity == GRAN_ROW
 

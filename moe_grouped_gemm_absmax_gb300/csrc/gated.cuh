@@ -63,10 +63,12 @@ int launch_gated_epi(const GatedArgs& g, const Ctx& c) {
                   reinterpret_cast<uintptr_t>(g.q)) & 31) == 0 && g.I % 16 == 0;
   if (grouped && (g.E < 1 || g.E > kMaxGatedExperts)) return FP8_ERR_UNSUPPORTED;
   p.nkb = (g.K * esz + BKB - 1) / BKB;
-  // CTA pairs and single CTAs by the plain GEMMs' rule (launch_gemm)
+  // CTA pairs, whose tiles have 256 rows, where they fill the GPU; by experts, where these have rows for such tiles (no
+  // transposed tails here; 4096 x 2048, forward: 16 experts of 256 rows 67 us on pairs, 81 on single CTAs; 32 of 128 rows
+  // 109 and 101; 64 of 64 rows 197 and 181).
   const int64_t per = kForward ? 2 : 1;  // tile columns for each column of the hidden layer
   auto num_n = [&](int w) { return (g.I * per + w - 1) / w; };
-  const bool pair = !g.blockwise && (grouped ? g.M >= 2048 : ((g.M + 255) / 256) * num_n(BN) * 2 >= c.sm_count);
+  const bool pair = !g.blockwise && (grouped ? g.M >= 2048 && g.M >= 192 * g.E : ((g.M + 255) / 256) * num_n(BN) * 2 >= c.sm_count);
   const int tile_m = pair ? 2 * BM : BM;
   p.num_m = (g.M + tile_m - 1) / tile_m;
   int width = BN;
@@ -80,7 +82,7 @@ int launch_gated_epi(const GatedArgs& g, const Ctx& c) {
 
   // operand maps: 128-byte rows of K. The forward's B boxes have rows of one projection, the backward's all of a CTA's.
   const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint32_t kbox = (uint32_t)(BKB / esz),  
+  const uint32_t kbox = (uint32_t)(BKB / esz),
                  b_rows = (uint32_t)width / (kForward ? (g.blockwise ? 4 : 2) : pair ? 2 : 1);
   const uint64_t rows = (uint64_t)(kForward ? 2 * g.I : g.I);
   Maps m;

@@ -93,7 +93,8 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
   p.ends = g.ends;
   p.E = (int)g.E;
   const bool mx = g.mx != 0;
-  int blk_cols = BN;
+  if (g.mode != -1 && (g.E < 1 || g.E > kMaxExperts)) return FP8_ERR_UNSUPPORTED;
+  int blk_cols = BN;  // jagged M with block scales: columns of a tile
   if (g.blockwise && g.mode == FP8_GROUPED_JAGGED_M) {
     if (g.M <= kFewRows) return launch_few_blockwise(g, c);
     const int64_t mb = (g.M + BM - 1) / BM + (g.E < g.M ? g.E : g.M) / 2;  // half of the last tiles' rows are empty
@@ -105,7 +106,6 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
   p.ldo = g.N;
   p.vec_ok = p.out_f32 ? (p.ldo % 4 == 0) : (p.ldo % 8 == 0);
   p.wide = ((reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(p.ldo * (p.out_f32 ? 4 : 2))) & 31) == 0;
-  if (g.mode != -1 && (g.E < 1 || g.E > kMaxExperts)) return FP8_ERR_UNSUPPORTED;
   // pair tiles when there are at least ~one per SM pair. Blockwise scaling runs on single CTAs: each K block's
   // partial goes from the MMAs to the promoting warps and back, and across a pair that takes longer than
   // the pair saves in operand traffic (8192 x 14336 x 4096: 523 us against 452).

@@ -107,8 +107,16 @@ def test_module_and_gradients_that_are_not_asked_for(fp8, ag):
     xr = x.clone().requires_grad_(True)
     mlp(xr).float().square().sum().backward()
     assert xr.grad.isfinite().all() and xr.grad.any()
-    y = mlp(x[:0])
-    assert y.shape == (0, 256)
+    mlp.zero_grad()
+    mlp.w13.requires_grad_(True)
+    mlp.w2.requires_grad_(True)
+    for gran in (fp8.GRAN_ROW, fp8.GRAN_BLOCK_1x128):  # no rows: zeros
+        mlp.granularity = gran
+        xr = x[:0].clone().requires_grad_(True)
+        y = mlp(xr)
+        assert y.shape == (0, 256)
+        y.float().sum().backward()
+        assert xr.grad.shape == (0, 256) and not mlp.w13.grad.any() and not mlp.w2.grad.any()
 
 
 def test_refusals(fp8, ag):

@@ -126,4 +126,5 @@ def test_grouped_product(fp8):
     assert call(K=272, sA=d(F32, 4, 2), sB=d(F32, 3, 1, 2)) == UNSUPPORTED
     assert call(sA=d(F32, 4)) == INVALID and call(sB=d(F32, 3, 128)) == INVALID and call(sB=d(F32, 1, 2)) == INVALID
     assert call(flags=0) == INVALID  # block scales where row scales belong
+    assert call(M=8, E=2049) == UNSUPPORTED and call(M=300, E=2049) == UNSUPPORTED
     assert call(mode=1, A=d(E4M3, 128, 256), B=d(E4M3, 128, 256), out=d(BF16, 3, 128, 128)) == UNSUPPORTED
