@@ -243,7 +243,12 @@ FP8_DEVI Tile get_tile(const GemmParams& p, int64_t t64, const int32_t* tpre, co
   } else if (SCHED == kJagM) {
     const int e = find_expert(tpre, p.E, t64);
     const uint32_t local = t - (uint32_t)tpre[e];
-    const uint32_t mb = local / num_n, nb = local - mb * num_n;
+    // as dense tiles: a group of the expert's M-blocks per N-block, so that its weights pass once for each group
+    const uint32_t gm = (uint32_t)p.group_m, per_group = gm * num_n;
+    const uint32_t first_m = local / per_group * gm, r = local - first_m * num_n;
+    const uint32_t left = ((uint32_t)tpre[e + 1] - (uint32_t)tpre[e]) / num_n - first_m;
+    const uint32_t gsz = left < gm ? left : gm;
+    const uint32_t nb = r / gsz, mb = first_m + (r - nb * gsz);
     T.m0 = aux[e] + (int32_t)(mb * TILE_M);  // aux[e] = segment start row
     T.pm0 = pst ? pst[e] + (int64_t)mb * TILE_M : T.m0;
     T.n0 = (int32_t)(nb * TBN);
