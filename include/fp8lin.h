@@ -257,7 +257,8 @@ int fp8_scaled_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* sA
  *   out bf16/fp32 [E, N, K]. An empty segment gives out[e] = 0.
  * Blockwise ([B]; FP8_MM_BLOCKWISE, JAGGED_M only, K % 128 == 0): sA fp32 [M, K / 128], sB fp32 [E,
  *   ceil(N / 128), K / 128]:  out[r, n] = sum_kb sA[r, kb] * sB[e, n / 128, kb] * sum_{k in kb} A[r, k] * B[e, n, k],
- *   each K block's product accumulated by itself, then added up in fp32 in the blocks' order.
+ *   each K block's product accumulated by itself, then added up in fp32 in an order set by the sizes alone: the
+ *   blocks', or up to 64 rows up to 4 runs of blocks, each in the blocks' order, and then the runs.
  * MX ([MX]; sA, sB of dtype FP8_DT_E8M0, K % 128 == 0, scales in the MX scale layout):
  *   JAGGED_M: sA = the segment-padded row-major scales of A (fp8_quantize MX ROW_MAJOR with
  *   offsets; P = 32 * bytes / K rows, P % 128 == 0, P >= M + 127 E); sB = E * fp8_mx_scale_bytes(N,

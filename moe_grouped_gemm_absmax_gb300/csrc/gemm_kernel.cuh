@@ -6,18 +6,20 @@
 //   grouped: per-row sA, per-expert-column sB, rows routed by cumulative offsets ("FP8 training
 //   on AMD GPUs with TorchTitan and TorchAO", "Scaling FP8 to MoE Architectures", Figure 3).
 //
-// Design (persistent; 320 threads per CTA; CG = 1 or 2 CTAs per MMA):
-//   CG = 1: one CTA per SM computes 128 x 256 tiles;
+// Design (persistent; 320 threads per CTA, 384 with block scales, 608 with MX; CG = 1 or 2 CTAs per MMA):
+//   CG = 1: one CTA per SM computes 128 x 256 tiles (block scales by expert and the gated kernels: or 128 or 64
+//           columns, NT, where that takes shorter rounds);
 //   CG = 2: a cluster of two CTAs (a CTA pair on two SMs) computes 256 x 256 tiles with
 //           tcgen05.mma.cta_group::2: each CTA stages its own 128 rows of A and 128 of the 256
 //           rows of B, the even CTA issues the MMAs for both, and each CTA's tensor memory
 //           holds the accumulator of its own 128 rows. Per CTA a stage is 32 KB instead of
-//           48 KB, so the ring is 6 stages deep and B is read from L2 once per pair.
+//           48 KB, so the ring is deeper (5 or 6 stages, not 4) and B is read from L2 once per pair.
 //   warp 0      TMA producer (128-byte swizzle; K blocks of 128 bytes) into the stage ring,
 //               guarded by full/empty mbarriers (the pair's full barrier lives in the even CTA
 //               and counts both CTAs' bytes);
-//   warp 1      allocates 512 TMEM columns; lane 0 of the issuing CTA issues the MMAs (M=128
-//               or 256, N=256; K=32 for FP8, K=16 for BF16) into one of two fp32
+//   warp 1      allocates 512 TMEM columns; in the issuing CTA its loop runs warp-uniform (waits and descriptors
+//               in all lanes, an elected lane's MMAs: 8192 x 14336 x 4096 took 270 us with lane 0
+//               in the loop alone, 259 so). MMAs (M=128 or 256, N=256; K=32 for FP8, K=16 for BF16) go into one of two fp32
 //               accumulators and commits each stage back to the producers and each finished
 //               tile to the epilogues (multicast to both CTAs of a pair);
 //   warps 2..9  epilogue: each warp owns 32 TMEM lanes (tile rows) and one half (128 columns)
@@ -29,6 +31,8 @@
 // 256 rows, is computed transposed: its 256 weight rows are the MMA's M and its rows, rounded up
 // to 16, the MMA's N, loaded with a row box of 32, 64 or 128 per CTA. These GEMMs are bound by
 // operand traffic from L2, so a short tail costs the bytes and MMAs of its own rows.
+// Block scales (kBLK; single CTAs): below, at the promotion.
+// The gated feed-forward (EPI kGate, kGateBwd; formulas: gate.cuh) has the same main loop and epilogues of its own.
 // Every wait is bounded; on a timeout the kernel raises FP8_DEV_TIMEOUT, drains in-flight TMA
 // and MMA work, frees its tensor memory and returns.
 #pragma once
@@ -971,6 +975,10 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
       if constexpr (KIND == kBLK) {
         // promotion: for every K block, this warp's half of the partial into registers, the partial back to the MMAs,
         // acc += partial * sA[m, kb] * sB[n / 128, kb]. The next 16 columns are on their way while these are added.
+        // What bounds it: two partials fill tensor memory, and a K block of 512 cycles of MMAs comes back after its commit
+        // (~310 cycles), two hand-overs between warps (257) and the promotion (342 to 390 alone); ~980 cycles in all. Eight
+        // warps with 128 accumulators a thread, instead of sixteen with 64: 529 to 411 us at 8192 x 14336 x 4096 (2354
+        // TFLOP/s); CTA pairs 523, with the partial in halves or not.
         constexpr int WC = C::WCOLS;
         static_assert(WC % 32 == 0 && WC <= 128, "a warp's columns, in one block of B's scales");
         float acc[WC];
