@@ -36,8 +36,9 @@ FP8_DEVI float act_bwd(float g, float* d) {
     w = kGelu2C * fmaf(g2, g, g);
     dw = fmaf(3.0f * kGelu2C, g2, kGelu2C);
   }
-  const float s = logistic(w), a = g * s;
-  *d = ACT == FP8_ACT_GELU ? fmaf(a * (1.0f - s), dw, s) : fmaf(a, 1.0f - s, s);
+  const float s = logistic(w), a = g * s, t = a * (1.0f - s);
+  // a saturated gate's derivative is s alone: GELU's w' overflows from |g| = 4e19 on, where t is 0
+  *d = ACT == FP8_ACT_GELU ? (t == 0.0f ? s : fmaf(t, dw, s)) : fmaf(a, 1.0f - s, s);
   return a;
 }
 // h[0 .. N - 1] = act(g) * u: one branch on the activation for all of them, which leaves their latencies free to overlap
@@ -123,7 +124,7 @@ FP8_DEVI void gate_bwd(GuChunk& c, const float* dh, uint32_t* h) {
     const float u[2] = {__uint_as_float(c.u[i] << 16), __uint_as_float(c.u[i] & 0xFFFF0000u)};
 #pragma unroll
     for (int k = 0; k < 2; ++k) a[k] = act_bwd<ACT>(g[k], &d[k]);
-    c.g[i] = pack_bf16(dh[2 * i] * u[0] * d[0], dh[2 * i + 1] * u[1] * d[1]);
+    c.g[i] = pack_bf16(dh[2 * i] * (u[0] * d[0]), dh[2 * i + 1] * (u[1] * d[1]));  // (act' is at most 1.13)
     c.u[i] = pack_bf16(dh[2 * i] * a[0], dh[2 * i + 1] * a[1]);
     h[i] = pack_bf16(a[0] * u[0], a[1] * u[1]);
   }
