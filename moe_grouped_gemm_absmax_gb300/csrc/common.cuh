@@ -344,6 +344,22 @@ FP8_DEVI bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abor
   }
 }
 
+// The same for two barriers, whose tests overlap: one costs the waiting warp about 100 cycles, ready or not.
+FP8_DEVI bool mbar_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, const volatile int* abort,
+                             uint64_t limit_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+      : "memory");
+  return ok || (mbar_wait(a, pa, abort, limit_ns) && mbar_wait(b, pb, abort, limit_ns));
+}
+
 // Registers a thread of the executing warpgroup (all its warps execute it): some given back, or taken from what the
 // block was launched with and others gave back.
 template <int N>

@@ -83,7 +83,7 @@ template <int KIND, int CG, int SCHED = 0, int EPI = kStore, int NT = BN>
 struct Cfg {
   // kBLK: two K-block partials, so the MMAs run one K block ahead of the promotion.
   static constexpr int TBN = NT;                          // tile columns (less than 256 on single CTAs: tile_width)
-    static constexpr int NBUF = KIND == kMX ? 1 : 2;        // accumulators / K-block partials
+  static constexpr int NBUF = KIND == kMX ? 1 : 2;        // accumulators / K-block partials
   static constexpr int EPI_WARPS = KIND == kMX ? 16 : 8;
   static constexpr int EPI_THREADS = 32 * EPI_WARPS;
   static constexpr int EPI0 = KIND == kBLK ? 4 : 2;      // first epilogue warp (kBLK: warpgroups share registers)
@@ -128,6 +128,7 @@ struct GemmParams {
   const float* sA;
   const float* sB;
   int sa_scalar, sb_scalar;
+  int sc_vec;          // kBLK: four K blocks' scales start on 16 bytes (nkb % 4 == 0)
   void* out;
   int out_f32;
   int vec_ok;          // 16-byte aligned output rows
@@ -613,14 +614,10 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
           tc_fence_after();
         }
         for (int kb = 0; kb < nkb; ++kb) {
-          // kBLK: each K block into the next free partial
-          if (KIND == kBLK && !mbar_wait(&S.tempty[buf], aphase ^ 1, abort_flag, p.wait_ns)) {
-            if (!*abort_flag) fail();
-            ok = false;
-            break;
-          }
-          // MX: the scale warp's commit on sff[stage] follows the stage's full barrier
-          if (!mbar_wait(KIND == kMX ? &S.sff[stage] : &S.full[stage], phase, abort_flag, p.wait_ns)) {
+          // kBLK: each K block into the next free partial. MX: the scale warp's commit on sff[stage] follows the
+          // stage's full barrier
+          if (!(KIND == kBLK ? mbar_wait_both(&S.tempty[buf], aphase ^ 1, &S.full[stage], phase, abort_flag, p.wait_ns)
+                             : mbar_wait(KIND == kMX ? &S.sff[stage] : &S.full[stage], phase, abort_flag, p.wait_ns))) {
             if (!*abort_flag) fail();
             ok = false;
             break;
@@ -932,12 +929,26 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
     // warp's columns lie in (kGate: the gate's and the up projection's). Loaded a group ahead, so that no promotion
     // waits for memory.
     float ra[kScGroup], rb[kScGroup], rc[kScGroup];
+    const float *pa = p.sA, *pb = p.sB, *pc = p.sB;  // sc_vec: the tile's (rows and columns past the end: any scales)
     auto load_scales = [&](const Tile& T, int32_t kb0) {
       const int64_t KB = p.nkb, r = (int64_t)T.m0 + row;
       const int64_t blocks = (EPI == kGate ? 2 * p.N : p.N + 127) / 128;
       const int64_t nb = (T.n0 + (EPI == kGate ? 0 : c0)) / 128;
       const float* a = p.sA + r * KB;
       const float* b = p.sB + ((int64_t)T.e * blocks + nb) * KB;
+      if (p.sc_vec) {  // one load for a group: its 32 rows' lines pass the L1 once, not four times
+        if (kb0 == 0) pa = r < p.M ? a : p.sA, pb = nb < blocks ? b : p.sB, pc = b + (p.N / 128) * KB;
+        if (kb0 >= KB) return;
+        const float4 va = __ldg(reinterpret_cast<const float4*>(pa + kb0));
+        const float4 vb = __ldg(reinterpret_cast<const float4*>(pb + kb0));
+        ra[0] = va.x, ra[1] = va.y, ra[2] = va.z, ra[3] = va.w;
+        rb[0] = vb.x, rb[1] = vb.y, rb[2] = vb.z, rb[3] = vb.w;
+        if (EPI == kGate) {
+          const float4 vc = __ldg(reinterpret_cast<const float4*>(pc + kb0));
+          rc[0] = vc.x, rc[1] = vc.y, rc[2] = vc.z, rc[3] = vc.w;
+        }
+        return;
+      }
 #pragma unroll
       for (int j = 0; j < kScGroup; ++j) {
         const bool live = kb0 + j < KB;
@@ -1028,11 +1039,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
               else
                 mbar_arrive_relaxed(&S.tempty[buf]);
             }
-            add16(acc + WC - 16, vb, su[j]);
             if (++buf == 2) {
               buf = 0;
               aphase ^= 1;
             }
+            add16(acc + WC - 16, vb, su[j]);
           }
         }
         if (t + n_units < total) {  // the next tile, not held in registers before
@@ -1599,7 +1610,7 @@ int tile_width(int least, int sm_count, F tiles) {
 
 template <int KIND, int SCHED, int A_MN, int B_MN, int CG, int EPI = kStore, int NT = BN>
 int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const CUtensorMap& sfa,
-        const CUtensorMap& sfb, const GemmParams& p, int64_t total_tiles_hint, const Ctx& c) {
+        const CUtensorMap& sfb, GemmParams p, int64_t total_tiles_hint, const Ctx& c) {
   auto kern = gemm_kernel<KIND, SCHED, A_MN, B_MN, CG, EPI, NT>;
   using C = Cfg<KIND, CG, SCHED, EPI, NT>;
   constexpr int kThreads = C::THREADS;
@@ -1608,6 +1619,8 @@ int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const 
                      (EPI == kGate ? sizeof(AmaxShare) : EPI == kGateBwd ? sizeof(BoxBars) : 0);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return FP8_ERR_CUDA;
+  if (KIND == kBLK)
+    p.sc_vec = p.nkb % kScGroup == 0 && ((reinterpret_cast<uintptr_t>(p.sA) | reinterpret_cast<uintptr_t>(p.sB)) & 15) == 0;
   int64_t units = c.sm_count / CG;
   if (total_tiles_hint > 0 && total_tiles_hint < units) units = total_tiles_hint;
   if (units < 1) units = 1;
