@@ -580,7 +580,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
     // ================================ MMA issuer ================================
     // The loop runs warp-uniform: elect.sync picks the lane that issues, all lanes wait. Descriptors are offsets of
     // per-kernel bases (address field in 16-byte units). Control flow of one lane alone, and descriptors built for
-    // every MMA, cost the blockwise loop a third of its time.
+    // every MMA, cost the blockwise loop a third of its time. A K block costs the warp 98 cycles a wait, 200 for the MMAs,
+    // 160 for the first commit and 100 for the second, ready or not.
     if (issuer) {
       const bool leader = elect_one();
       int stage = 0;
@@ -986,10 +987,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
       if constexpr (KIND == kBLK) {
         // promotion: for every K block, this warp's half of the partial into registers, the partial back to the MMAs,
         // acc += partial * sA[m, kb] * sB[n / 128, kb]. The next 16 columns are on their way while these are added.
-        // What bounds it: two partials fill tensor memory, and a K block of 512 cycles of MMAs comes back after its commit
-        // (~310 cycles), two hand-overs between warps (257) and the promotion (342 to 390 alone); ~980 cycles in all. Eight
-        // warps with 128 accumulators a thread, instead of sixteen with 64: 529 to 411 us at 8192 x 14336 x 4096 (2354
-        // TFLOP/s); CTA pairs 523, with the partial in halves or not.
+        // What bounds it: the chain of each promoting warp. Two warps a scheduler read 16 columns, 50 cycles after they
+        // asked, and add them: 400 cycles to the partial's release, 620 to the last addition, 200 to the next partial (a test
+        // of a barrier alone takes 98), and the first K block of a group of scales 350 more. 870 cycles a K block, 512 of
+        // them MMAs: 355 us at 8192 x 14336 x 4096 (2710 TFLOP/s). Sixteen warps with 64 accumulators a thread 394, loads of
+        // 32 columns 406, the row's scales by TMA 381, a second warp issuing every other K block 3345; CTA pairs, before
+        // these steps, 523 for 452.
         constexpr int WC = C::WCOLS;
         static_assert(WC % 32 == 0 && WC <= 128, "a warp's columns, in one block of B's scales");
         float acc[WC];
@@ -1008,9 +1011,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
             su[j] = EPI == kGate ? ra[j] * rc[j] : sk[j];
           }
           load_scales(T, kb0 + kScGroup);
+#pragma unroll 1  // (unrolled, the same time and four times the code)
+          for (int j = 0; j < kScGroup && kb0 + j < T.nkb; ++j) {
+            const float skj = sk[0], suj = su[0];
 #pragma unroll
-          for (int j = 0; j < kScGroup; ++j) {
-            if (kb0 + j >= T.nkb) break;
+            for (int i = 0; i + 1 < kScGroup; ++i) sk[i] = sk[i + 1], su[i] = su[i + 1];
             if (!mbar_wait(&S.tfull[buf], aphase, abort_flag, p.wait_ns)) {
               if (!*abort_flag) fail();
               live = false;
@@ -1024,11 +1029,11 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < WC; c += 32) {
               tmem_ld16(taddr + c + 16, vb);
-              add16(acc + c, va, c < WC / 2 ? sk[j] : su[j]);
+              add16(acc + c, va, c < WC / 2 ? skj : suj);
               tmem_ld_wait_regs16(vb);
               if (c + 32 == WC) break;
               tmem_ld16(taddr + c + 32, va);
-              add16(acc + c + 16, vb, c < WC / 2 ? sk[j] : su[j]);
+              add16(acc + c + 16, vb, c < WC / 2 ? skj : suj);
               tmem_ld_wait_regs16(va);
             }
             tc_fence_before();
@@ -1043,7 +1048,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, SCHED, EPI, NT>::THREADS, 1)
               buf = 0;
               aphase ^= 1;
             }
-            add16(acc + WC - 16, vb, su[j]);
+            add16(acc + WC - 16, vb, suj);
           }
         }
         if (t + n_units < total) {  // the next tile, not held in registers before
