@@ -90,6 +90,38 @@ def test_outputs_between_sectors(fp8, kind, M, counts):
     assert (qb[:16].float() == 7).all() and (qb[-16:].float() == 7).all() and (ib[:4] == 7).all() and (ib[-4:] == 7).all()
 
 
+@pytest.mark.parametrize("M,counts", [(9, None), (130, None), (9, [4, 0, 5]), (300, [120, 180])])
+def test_scales_at_any_word(fp8, M, counts):
+    """Block scales that start on 4 bytes and not on 16 give the bits of those that do."""
+    K, I = 1024, 256
+    g = gen(M + 1)
+    lead = (len(counts),) if counts else ()
+    off = ends(counts) if counts else None
+
+    def word(t):
+        x = torch.zeros(t.numel() + 1, device="cuda")
+        x[1:] = t.flatten()
+        return x[1:].view(t.shape)
+
+    A, sA, _ = operand(g, (M, K), "block")
+    B, sB, _ = operand(g, lead + (2 * I, K), "block", rows=128, size=0.1)
+    D, sD, _ = operand(g, (M, K), "block", E5)
+    W, sW, _ = operand(g, lead + (I, K), "block", rows=128, size=0.1)
+    gu = randn(g, M, 2 * I).to(torch.bfloat16)
+    got = []
+    for f in (lambda t: t, word):
+        h, _, q, inv = fp8.gated_mm_alloc(A, B, f(sA), f(sB), off, flags=fp8.MM_BLOCKWISE, q_dtype=fp8.DT_E4M3)
+        dgu, h2 = fp8.gated_mm_bwd_alloc(D, W, f(sD), f(sW), gu, off, flags=fp8.MM_BLOCKWISE, want_h=True)
+        out = torch.empty(M, I, device="cuda")
+        if counts:
+            fp8.fp8_grouped_mm(A, W, off, f(sA), f(sW), out, fp8.GROUPED_JAGGED_M, fp8.MM_BLOCKWISE)
+        else:
+            fp8.fp8_scaled_mm(A, W, f(sA), f(sW), out, fp8.MM_BLOCKWISE)
+        got.append([h, q, inv, dgu, h2, out])
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 @pytest.mark.parametrize("kind", ["row", "block"])
 @pytest.mark.parametrize("counts", [None, [69981, 0, 50]])
 def test_more_than_2_31_elements(fp8, kind, counts):
