@@ -39,6 +39,7 @@
 
 #include <string.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1622,8 +1623,15 @@ int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const 
   const int n_arrays = is_dense(SCHED) ? 0 : (KIND == kMX && SCHED == kJagM) ? 3 : 2;
   const size_t smem = C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +
                      (EPI == kGate ? sizeof(AmaxShare) : EPI == kGateBwd ? sizeof(BoxBars) : 0);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return FP8_ERR_CUDA;
+  // Once for each device, and all that a CTA may have: the limit is the process's, and the experts' offsets make `smem`
+  // another for each E, so a limit set by one thread's call could be below what another's is about to launch with.
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+      return FP8_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_release);
+  }
   if (KIND == kBLK)
     p.sc_vec = p.nkb % kScGroup == 0 && ((reinterpret_cast<uintptr_t>(p.sA) | reinterpret_cast<uintptr_t>(p.sB)) & 15) == 0;
   int64_t units = c.sm_count / CG;
