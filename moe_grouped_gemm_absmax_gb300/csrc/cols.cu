@@ -29,6 +29,8 @@
 // its two reads in L2 whatever the tensor's size, and cannot deadlock: a chunk's pass 1 waits only
 // for the pass 2 of earlier chunks, whose pass 1 is complete.
 // With the maxima given (fp8_quantize_from_amax) the launch runs pass 2 alone.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -675,8 +677,20 @@ int launch_quant_cols(const void* x, int64_t rows_total, int64_t C, int64_t n_gr
   const int64_t grid = units > 0 ? (units < c.sm_count ? units : c.sm_count) : 1;
   const ScaleTab& tab = scale_tab(fmt);
   auto kern = fmt == FP8_DT_E4M3 ? colpipe_kernel<FP8_DT_E4M3> : colpipe_kernel<FP8_DT_E5M2>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return FP8_ERR_CUDA;
+  // Once for each device, and all that a CTA may have beside its static memory: the segment tables make
+  // `smem` another for each number of segments, and a limit set by one thread's call could be below
+  // what another's is about to launch with.
+  static std::atomic<uint64_t> done[2];
+  std::atomic<uint64_t>& set = done[fmt == FP8_DT_E4M3];
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(set.load(std::memory_order_acquire) & bit)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCqSmemMax - (int)fa.sharedSizeBytes) !=
+            cudaSuccess)
+      return FP8_ERR_CUDA;
+    set.fetch_or(bit, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs resident: they wait on one another's maxima
