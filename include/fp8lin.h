@@ -264,6 +264,7 @@ int fp8_scaled_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* sA
  *   offsets; P = 32 * bytes / K rows, P % 128 == 0, P >= M + 127 E); sB = E * fp8_mx_scale_bytes(N,
  *   K) bytes. JAGGED_K: A = G^T [N, P] and B = X^T [K, P] from fp8_quantize MX COL_MAJOR with
  *   offsets; sA = fp8_mx_scale_bytes(N, P), sB = fp8_mx_scale_bytes(K, P) bytes.
+ * flags: FP8_MM_FAST_ACCUM, and with fp32 scales FP8_MM_BLOCKWISE; any other: FP8_ERR_UNSUPPORTED.
  */
 int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets,
                    const fp8_tensor* sA, const fp8_tensor* sB, fp8_tensor* out, int mode,

@@ -552,11 +552,9 @@ extern "C" int fp8_quantize_from_amax(const fp8_tensor* x, int granularity, int 
 // ------------------------------------------------------------------------------------------
 // fp8_grouped_mm
 
-extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets,
-                              const fp8_tensor* sA, const fp8_tensor* sB, fp8_tensor* out, int mode, int flags,
-                              int32_t* d_status, void* stream) {
-  Ctx c;
-  FP8_TRY(make_ctx(&c, stream, d_status));
+// Every check of the call, ahead of any device work; *ga: the launch's arguments.
+static int check_grouped(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets, const fp8_tensor* sA,
+                         const fp8_tensor* sB, const fp8_tensor* out, int mode, int flags, GemmArgs* ga) {
   FP8_CHECK(valid_desc(A) && valid_desc(B) && valid_desc(out) && valid_desc(offsets) && valid_desc(sA) &&
                 valid_desc(sB),
             FP8_ERR_INVALID_ARG);
@@ -564,11 +562,13 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
   FP8_CHECK(!(A->dtype == FP8_DT_E5M2 && B->dtype == FP8_DT_E5M2), FP8_ERR_UNSUPPORTED);
   FP8_CHECK(offsets->dtype == FP8_DT_I32 && offsets->ndim == 1 && offsets->shape[0] >= 1, FP8_ERR_INVALID_ARG);
   const bool mx = sA->dtype == FP8_DT_E8M0;
+  // a flag that changes nothing here would leave the caller with another product than was asked for
+  FP8_CHECK((flags & ~(FP8_MM_FAST_ACCUM | (mx ? 0 : FP8_MM_BLOCKWISE))) == 0, FP8_ERR_UNSUPPORTED);
   FP8_CHECK(mx ? sB->dtype == FP8_DT_E8M0 : (sA->dtype == FP8_DT_F32 && sB->dtype == FP8_DT_F32), FP8_ERR_INVALID_ARG);
   FP8_CHECK(aligned16(A->ptr) && aligned16(B->ptr) && aligned16(out->ptr), FP8_ERR_ALIGNMENT);
   if (mx) FP8_CHECK(aligned16(sA->ptr) && aligned16(sB->ptr), FP8_ERR_ALIGNMENT);
   const int64_t E = offsets->shape[0];
-  GemmArgs g = {};
+  GemmArgs& g = *ga;
   g.A = A->ptr;
   g.B = B->ptr;
   g.a_dtype = A->dtype;
@@ -602,8 +602,7 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
       g.N = N;
       g.K = K;
       g.sfa_rows = P;
-      if (M == 0 || N == 0) return FP8_OK;
-      return launch_gemm(g, c);
+      return FP8_OK;
     }
     FP8_CHECK(K % 16 == 0, FP8_ERR_ALIGNMENT);
     FP8_CHECK(M < (int64_t(1) << 31) && E * N < (int64_t(1) << 31), FP8_ERR_UNSUPPORTED);
@@ -619,8 +618,7 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
     g.K = K;
     g.sA_len = M;
     g.sB_len = E * N;
-    if (M == 0 || N == 0) return FP8_OK;
-    return launch_gemm(g, c);
+    return FP8_OK;
   }
   if (mode == FP8_GROUPED_JAGGED_K) {
     FP8_CHECK(A->ndim == 2 && B->ndim == 2 && A->shape[1] == B->shape[1], FP8_ERR_INVALID_ARG);
@@ -635,8 +633,7 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
       g.K = P;
       g.k_dim = Kd;
       g.sfa_rows = N;
-      if (N == 0 || Kd == 0) return FP8_OK;
-      return launch_gemm(g, c);
+      return FP8_OK;
     }
     FP8_CHECK((flags & FP8_MM_BLOCKWISE) == 0, FP8_ERR_UNSUPPORTED);  // blocks of 128 along the rows: not implemented
     FP8_CHECK(numel(sA) == E * N && numel(sB) == E * Kd, FP8_ERR_INVALID_ARG);
@@ -647,10 +644,20 @@ extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp
     g.k_dim = Kd;
     g.sA_len = E * N;
     g.sB_len = E * Kd;
-    if (N == 0 || Kd == 0) return FP8_OK;
-    return launch_gemm(g, c);
+    return FP8_OK;
   }
   return FP8_ERR_INVALID_ARG;
+}
+
+extern "C" int fp8_grouped_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* offsets,
+                              const fp8_tensor* sA, const fp8_tensor* sB, fp8_tensor* out, int mode, int flags,
+                              int32_t* d_status, void* stream) {
+  GemmArgs g = {};
+  FP8_TRY(check_grouped(A, B, offsets, sA, sB, out, mode, flags, &g));
+  Ctx c;
+  FP8_TRY(make_ctx(&c, stream, d_status));
+  if (g.M == 0 || g.N == 0) return FP8_OK;
+  return launch_gemm(g, c);
 }
 
 // ------------------------------------------------------------------------------------------
