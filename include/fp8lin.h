@@ -37,7 +37,9 @@
  *       with saturation. The GEMM computes sum_k X_A[m, k/32] X_B[n, k/32] A[m, k] B[n, k].
  *
  * Conventions for every entry point:
- *  - Tensors are described by fp8_tensor: a DEVICE pointer (global memory, 16-byte aligned),
+ *  - Tensors are described by fp8_tensor: a DEVICE pointer (global memory, 16-byte aligned;
+ *    fp32 scales and maxima and int32 offsets of the quantizations and GEMMs may start at any
+ *    word, anything else is FP8_ERR_ALIGNMENT),
  *    a dtype, and a logical shape, always dense and row-major (last index contiguous). A
  *    "column-major [R, C]" operand is passed as the row-major tensor of shape [C, R].
  *  - Ownership: the caller allocates and frees every buffer, including the workspace. The

@@ -298,6 +298,7 @@ static int quantize_impl(const fp8_tensor* x, int gran, int out_dtype, int layou
 extern "C" int fp8_quantize(const fp8_tensor* x, int granularity, int out_dtype, int layout, fp8_tensor* out,
                             fp8_tensor* out_t, fp8_tensor* inv_scales, const fp8_tensor* offsets, void* workspace,
                             size_t workspace_bytes, int32_t* d_status, void* stream) {
+  FP8_CHECK(word_aligned({inv_scales, offsets}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   return quantize_impl(x, granularity, out_dtype, layout, out, out_t, inv_scales, offsets, workspace,
@@ -428,6 +429,7 @@ static int scaled_mm_impl(const fp8_tensor* A, const fp8_tensor* B, const fp8_te
 
 extern "C" int fp8_scaled_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* sA, const fp8_tensor* sB,
                              fp8_tensor* out, int flags, int32_t* d_status, void* stream) {
+  FP8_CHECK(word_aligned({sA, sB}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   return scaled_mm_impl(A, B, sA, sB, out, flags, c);
@@ -436,6 +438,7 @@ extern "C" int fp8_scaled_mm(const fp8_tensor* A, const fp8_tensor* B, const fp8
 extern "C" int fp8_scaled_mm_amax(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* sA,
                                   const fp8_tensor* sB, fp8_tensor* out, int flags, fp8_tensor* row_amax,
                                   fp8_tensor* col_amax, int32_t* d_status, void* stream) {
+  FP8_CHECK(word_aligned({sA, sB, row_amax, col_amax}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   FP8_CHECK(valid_desc(out) && out->ndim == 2 && out->dtype == FP8_DT_BF16, FP8_ERR_UNSUPPORTED);
@@ -463,6 +466,7 @@ extern "C" int fp8_scaled_mm_amax(const fp8_tensor* A, const fp8_tensor* B, cons
 extern "C" int fp8_scaled_mm_quant(const fp8_tensor* A, const fp8_tensor* B, const fp8_tensor* sA,
                                    const fp8_tensor* sB, int flags, int out_granularity, fp8_tensor* out_q,
                                    fp8_tensor* out_scales, int32_t* d_status, void* stream) {
+  FP8_CHECK(word_aligned({sA, sB, out_scales}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   FP8_CHECK(valid_desc(A) && valid_desc(B) && valid_desc(sA) && valid_desc(sB) && valid_desc(out_q) &&
@@ -516,6 +520,7 @@ extern "C" int fp8_scaled_mm_quant(const fp8_tensor* A, const fp8_tensor* B, con
 extern "C" int fp8_quantize_from_amax(const fp8_tensor* x, int granularity, int out_dtype, int layout,
                                       fp8_tensor* out, fp8_tensor* out_t, fp8_tensor* inv_scales,
                                       const fp8_tensor* amax, int32_t* d_status, void* stream) {
+  FP8_CHECK(word_aligned({inv_scales, amax}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   FP8_CHECK(valid_desc(x) && x->dtype == FP8_DT_BF16 && x->ndim == 2, FP8_ERR_INVALID_ARG);
@@ -566,7 +571,8 @@ static int check_grouped(const fp8_tensor* A, const fp8_tensor* B, const fp8_ten
   FP8_CHECK((flags & ~(FP8_MM_FAST_ACCUM | (mx ? 0 : FP8_MM_BLOCKWISE))) == 0, FP8_ERR_UNSUPPORTED);
   FP8_CHECK(mx ? sB->dtype == FP8_DT_E8M0 : (sA->dtype == FP8_DT_F32 && sB->dtype == FP8_DT_F32), FP8_ERR_INVALID_ARG);
   FP8_CHECK(aligned16(A->ptr) && aligned16(B->ptr) && aligned16(out->ptr), FP8_ERR_ALIGNMENT);
-  if (mx) FP8_CHECK(aligned16(sA->ptr) && aligned16(sB->ptr), FP8_ERR_ALIGNMENT);
+  FP8_CHECK(mx ? aligned16(sA->ptr) && aligned16(sB->ptr) : word_aligned({sA, sB}), FP8_ERR_ALIGNMENT);
+  FP8_CHECK(word_aligned({offsets}), FP8_ERR_ALIGNMENT);
   const int64_t E = offsets->shape[0];
   GemmArgs& g = *ga;
   g.A = A->ptr;
@@ -769,9 +775,11 @@ extern "C" size_t fp8_workspace_size(int op, int64_t d0, int64_t d1, int64_t d2,
 extern "C" int fp8_linear_fwd(const fp8_tensor* x, const fp8_tensor* w, int granularity, int flags, fp8_tensor* y,
                               fp8_linear_saved* saved, void* workspace, size_t workspace_bytes, int32_t* d_status,
                               void* stream) {
+  FP8_CHECK(saved, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(word_aligned({&saved->x_inv, &saved->w_inv, &saved->xt_inv, &saved->wt_inv}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
-  FP8_CHECK(valid_desc(x) && valid_desc(w) && valid_desc(y) && saved, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(valid_desc(x) && valid_desc(w) && valid_desc(y), FP8_ERR_INVALID_ARG);
   FP8_CHECK(x->ndim == 2 && w->ndim == 2 && x->dtype == FP8_DT_BF16 && w->dtype == FP8_DT_BF16, FP8_ERR_INVALID_ARG);
   const int64_t M = x->shape[0], K = x->shape[1], N = w->shape[0];
   FP8_CHECK(w->shape[1] == K, FP8_ERR_INVALID_ARG);
@@ -823,9 +831,11 @@ extern "C" int fp8_linear_fwd(const fp8_tensor* x, const fp8_tensor* w, int gran
 extern "C" int fp8_linear_bwd(const fp8_tensor* dy, const fp8_linear_saved* saved, const fp8_tensor* x,
                               const fp8_tensor* w, int granularity, int wgrad_mode, fp8_tensor* dx, fp8_tensor* dw,
                               void* workspace, size_t workspace_bytes, int32_t* d_status, void* stream) {
+  FP8_CHECK(saved, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(word_aligned({&saved->x_inv, &saved->w_inv, &saved->xt_inv, &saved->wt_inv}), FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
-  FP8_CHECK(valid_desc(dy) && saved && dy->ndim == 2 && dy->dtype == FP8_DT_BF16, FP8_ERR_INVALID_ARG);
+  FP8_CHECK(valid_desc(dy) && dy->ndim == 2 && dy->dtype == FP8_DT_BF16, FP8_ERR_INVALID_ARG);
   FP8_CHECK(granularity == FP8_GRAN_TENSOR || granularity == FP8_GRAN_ROW || granularity == FP8_GRAN_MX ||
                 granularity == FP8_GRAN_BLOCK_1x128,
             FP8_ERR_INVALID_ARG);

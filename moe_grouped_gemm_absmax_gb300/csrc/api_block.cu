@@ -225,7 +225,7 @@ static int check_gated(const fp8_tensor* A, const fp8_tensor* B, const fp8_tenso
     E = offsets->shape[0];
     FP8_CHECK(fp8 && E <= kMaxGatedExperts, FP8_ERR_UNSUPPORTED);
     FP8_CHECK(B->ndim == 3 && B->shape[0] == E, FP8_ERR_INVALID_ARG);
-    FP8_CHECK((reinterpret_cast<uintptr_t>(offsets->ptr) & 3u) == 0, FP8_ERR_ALIGNMENT);
+    FP8_CHECK(word_aligned({offsets}), FP8_ERR_ALIGNMENT);
   } else {
     FP8_CHECK(B->ndim == 2, FP8_ERR_INVALID_ARG);
   }
@@ -252,7 +252,7 @@ static int check_gated(const fp8_tensor* A, const fp8_tensor* B, const fp8_tenso
       FP8_CHECK((la == M || g->sa_scalar) && (lb == n * rows || g->sb_scalar), FP8_ERR_INVALID_ARG);
     }
     // read word by word: the scales of a transposed weight may follow those of the weight at any word
-    FP8_CHECK(((reinterpret_cast<uintptr_t>(sA->ptr) | reinterpret_cast<uintptr_t>(sB->ptr)) & 3u) == 0, FP8_ERR_ALIGNMENT);
+    FP8_CHECK(word_aligned({sA, sB}), FP8_ERR_ALIGNMENT);
     g->sA = static_cast<const float*>(sA->ptr);
     g->sB = static_cast<const float*>(sB->ptr);
   } else {

@@ -3,11 +3,19 @@
 
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/fp8lin.h"
 
 namespace fp8lin {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Scales, maxima and offsets (any may be null) are read and written word by word at least.
+inline bool word_aligned(std::initializer_list<const fp8_tensor*> ts) {
+  for (const fp8_tensor* t : ts)
+    if (t && (reinterpret_cast<uintptr_t>(t->ptr) & 3u) != 0) return false;
+  return true;
+}
 inline bool is_fp8(int dt) { return dt == FP8_DT_E4M3 || dt == FP8_DT_E5M2; }
 inline bool is_out(int dt) { return dt == FP8_DT_BF16 || dt == FP8_DT_F32; }
 inline int64_t numel(const fp8_tensor* t) {

@@ -96,6 +96,7 @@ extern "C" int fp8_quantize_tensor_noalloc(const fp8_tensor* x, int out_dtype, i
     inv_n *= inv_scale->shape[i];
   }
   if (inv_n != 1) return FP8_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(inv_scale->ptr) & 3u) != 0) return FP8_ERR_ALIGNMENT;
   const int64_t R = x->shape[0], C = x->shape[1];
   if (C % 8 != 0) return FP8_ERR_ALIGNMENT;
   // each extent within the limit before the product (no overflow), then the element count:
