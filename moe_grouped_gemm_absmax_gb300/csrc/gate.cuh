@@ -124,7 +124,8 @@ FP8_DEVI void gate_bwd(GuChunk& c, const float* dh, uint32_t* h) {
     const float u[2] = {__uint_as_float(c.u[i] << 16), __uint_as_float(c.u[i] & 0xFFFF0000u)};
 #pragma unroll
     for (int k = 0; k < 2; ++k) a[k] = act_bwd<ACT>(g[k], &d[k]);
-    c.g[i] = pack_bf16(dh[2 * i] * (u[0] * d[0]), dh[2 * i + 1] * (u[1] * d[1]));  // (act' is at most 1.13)
+    // dh act' first: act' is 0 where a gate is saturated, and up to 1.13, which times the largest u would be past fp32's range
+    c.g[i] = pack_bf16(dh[2 * i] * d[0] * u[0], dh[2 * i + 1] * d[1] * u[1]);
     c.u[i] = pack_bf16(dh[2 * i] * a[0], dh[2 * i + 1] * a[1]);
     h[i] = pack_bf16(a[0] * u[0], a[1] * u[1]);
   }
