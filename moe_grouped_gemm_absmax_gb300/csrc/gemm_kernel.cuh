@@ -1619,7 +1619,7 @@ int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const 
         const CUtensorMap& sfb, GemmParams p, int64_t total_tiles_hint, const Ctx& c) {
   auto kern = gemm_kernel<KIND, SCHED, A_MN, B_MN, CG, EPI, NT>;
   using C = Cfg<KIND, CG, SCHED, EPI, NT>;
-  constexpr int kThreads = C::THREADS;
+  constexpr int kThreads = C::THREADS, kEpiThreads = C::EPI_THREADS;
   const int n_arrays = is_dense(SCHED) ? 0 : (KIND == kMX && SCHED == kJagM) ? 3 : 2;
   const size_t smem = C::RING_BYTES + C::OUT_BYTES + kSharedBytes + (size_t)n_arrays * 4 * (p.E + 1) +
                      (EPI == kGate ? sizeof(AmaxShare) : EPI == kGateBwd ? sizeof(BoxBars) : 0);
@@ -1630,6 +1630,12 @@ int run(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o, const 
   if (!(done.load(std::memory_order_acquire) & bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
       return FP8_ERR_CUDA;
+    if (KIND == kBLK) {  // the promoting warps would wait without end for registers that a build did not give the block
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+          fa.numRegs * kThreads < 32 * C::EPI0 * kIssueRegs + kEpiThreads * kPromoteRegs)
+        return FP8_ERR_CUDA;
+    }
     done.fetch_or(bit, std::memory_order_release);
   }
   if (KIND == kBLK)
