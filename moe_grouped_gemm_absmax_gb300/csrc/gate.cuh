@@ -5,8 +5,9 @@
 //   act'(g) = s + g s (1 - s) w'.
 //   h = act(g) u;  given dh:  dg = dh u act'(g),  du = dh act(g).
 // All in fp32 from the fp32 accumulators, each output rounded once. The exponential and the reciprocal are the approximate
-// instructions (2 units in the last place, and |w| 2^-24 from the argument's rounding): 2^-17 of a value at |w| = 80,
-// below which s underflows to 0; a bf16 result's half step is 2^-9 of it.
+// instructions (2 units in the last place, and |w| 2^-24 from the argument's rounding): below 2^-17 of a value down to
+// w = -87.3, where 1 + e^-w passes 2^126, its reciprocal leaves the normal range and s is 0 (e^-87.3 is 1.2e-38); a bf16
+// result's half step is 2^-9 to 2^-8 of it.
 #pragma once
 
 #include "common.cuh"

@@ -108,7 +108,8 @@ int launch_gemm(const GemmArgs& g, const Ctx& c) {
   p.wide = ((reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(p.ldo * (p.out_f32 ? 4 : 2))) & 31) == 0;
   // pair tiles when there are at least ~one per SM pair. Blockwise scaling runs on single CTAs: each K block's
   // partial goes from the MMAs to the promoting warps and back, and across a pair that takes longer than
-  // the pair saves in operand traffic (8192 x 14336 x 4096: 523 us against 452).
+  // the pair saves in operand traffic (8192 x 14336 x 4096: 523 us on pairs when single CTAs took 452; since then their
+  // promotion, for a single CTA's registers, has come to 353).
   const int64_t pair_tiles = ((g.M + 255) / 256) * p.num_n * (g.mode == FP8_GROUPED_JAGGED_K ? g.E : 1);
   const bool pair = !g.blockwise && (g.mode == FP8_GROUPED_JAGGED_M ? g.M >= 2048 : pair_tiles * 2 >= c.sm_count);
   const int tile_m = pair ? 256 : 128;

@@ -185,7 +185,15 @@ struct GatedArgs {
 int launch_gated(const GatedArgs& g, const Ctx& c);
 
 // --- FP8 products of a few rows (few.cu) ---
-constexpr int64_t kFewRows = 64;  // most rows of a call that takes it
+// Most rows of a call that takes it: those of its widest tile, so that no call reads its weights twice there. us on either
+// kernel (few / tiles), gated, row scales and block scales:
+//              16 rows                 48                      64                      65                      128
+//   4096 x 14336   23 / 33, 24 / 29    23 / 31, 27 / 27        24 / 31, 28 / 27        35 / 31, 47 / 26        39 / 31, 52 / 27
+//   7168 x 2048    12 / 19, 12 / 26    16 / 19, 16 / 26        17 / 20, 17 / 27        16 / 19, 17 / 27        17 / 20, 17 / 27
+//   2048 x 1024     7 /  8,  8 / 10    11 /  8, 10 / 11        12 /  9, 11 / 11        12 /  9, 11 / 11        12 /  9, 11 / 11
+// and 8 experts' block-scaled products of 2048 x 7168: 23 / 33, 27 / 32, 27 / 27, 27 / 27, 28 / 28. The rows alone are
+// not the whole rule: with few output tiles the border lies above 128 rows, with a short contraction below 48.
+constexpr int64_t kFewRows = 64;
 int launch_few_gated(const GatedArgs& g, const Ctx& c);          // forward, FP8
 int launch_few_blockwise(const GemmArgs& g, const Ctx& c);       // jagged M, block scales
 
