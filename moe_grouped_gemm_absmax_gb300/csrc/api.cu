@@ -776,7 +776,9 @@ extern "C" int fp8_linear_fwd(const fp8_tensor* x, const fp8_tensor* w, int gran
                               fp8_linear_saved* saved, void* workspace, size_t workspace_bytes, int32_t* d_status,
                               void* stream) {
   FP8_CHECK(saved, FP8_ERR_INVALID_ARG);
-  FP8_CHECK(word_aligned({&saved->x_inv, &saved->w_inv, &saved->xt_inv, &saved->wt_inv}), FP8_ERR_ALIGNMENT);
+  // of what is saved, the scales that this granularity writes (the others may be left unset)
+  FP8_CHECK(word_aligned({&saved->x_inv, &saved->w_inv, granularity == FP8_GRAN_BLOCK_1x128 ? &saved->wt_inv : nullptr}),
+            FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   FP8_CHECK(valid_desc(x) && valid_desc(w) && valid_desc(y), FP8_ERR_INVALID_ARG);
@@ -832,7 +834,13 @@ extern "C" int fp8_linear_bwd(const fp8_tensor* dy, const fp8_linear_saved* save
                               const fp8_tensor* w, int granularity, int wgrad_mode, fp8_tensor* dx, fp8_tensor* dw,
                               void* workspace, size_t workspace_bytes, int32_t* d_status, void* stream) {
   FP8_CHECK(saved, FP8_ERR_INVALID_ARG);
-  FP8_CHECK(word_aligned({&saved->x_inv, &saved->w_inv, &saved->xt_inv, &saved->wt_inv}), FP8_ERR_ALIGNMENT);
+  // of what was saved, the scales that this call reads
+  const bool tensor_dx = granularity == FP8_GRAN_TENSOR && dx && dx->ptr;
+  const bool tensor_dw = granularity == FP8_GRAN_TENSOR && wgrad_mode == FP8_WGRAD_FP8 && dw && dw->ptr;
+  const bool block_dx = granularity == FP8_GRAN_BLOCK_1x128 && dx && dx->ptr;
+  FP8_CHECK(word_aligned({tensor_dx ? &saved->w_inv : nullptr, tensor_dw ? &saved->x_inv : nullptr,
+                          block_dx ? &saved->wt_inv : nullptr}),
+            FP8_ERR_ALIGNMENT);
   Ctx c;
   FP8_TRY(make_ctx(&c, stream, d_status));
   FP8_CHECK(valid_desc(dy) && dy->ndim == 2 && dy->dtype == FP8_DT_BF16, FP8_ERR_INVALID_ARG);
